@@ -268,6 +268,211 @@ def eagle_kv_compact(k_cache, v_cache, kv_len, path, accept_len, max_depth, dev_
         _stream(stream)))
 
 
+# ---------------------------------------------------------------- prompts and the 8-bit cache
+KV8_BLOCK = 32      # cache rows that share a scale (EAGLE_KV8_BLOCK)
+
+
+def _same_device(fn, first, tensors):
+    """Every tensor given must live on `first`'s device."""
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
+
+
+def _on(device, stream):
+    """The context a call launches in: its tensors' device and, where one is given, the
+    stream, so that scratch allocated inside belongs to that stream."""
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+
+
+def _shape(fn, t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _token_rows(fn, t, name):
+    """bf16 [T, H, d] rows whose tokens may be strided (a slice of a fused projection's
+    output); returns the token stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{fn}: {name} must be [T, H, d]")
+    T, H, d = t.shape
+    dense_heads = t.numel() == 0 or ((d == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == d))
+    if not dense_heads:
+        raise ValueError(f"{fn}: {name}'s heads must be dense within a token")
+    stride = H * d if T <= 1 else t.stride(0)
+    if T > 1 and (stride < H * d or stride % 8 != 0):
+        raise ValueError(f"{fn}: {name}'s token stride must be a multiple of 8, at least H * d")
+    return stride
+
+
+def _kv8_cache(fn, k8, v8, k_scale, v_scale, lead):
+    """Checks the four arrays of an 8-bit cache; `lead`: its leading dimensions (with
+    Hkv last).  Returns (Lmax, d)."""
+    for t, name in ((k8, "k8"), (v8, "v8")):
+        _dev(t, name, torch.float8_e4m3fn)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _dev(t, name, torch.float32)
+    Lmax, d = k8.shape[-2:]
+    _shape(fn, k8, "k8", (*lead, Lmax, d))
+    _shape(fn, v8, "v8", k8.shape)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _shape(fn, t, name, (*lead, -(-Lmax // KV8_BLOCK)))
+    return Lmax, d
+
+
+def kv8_cache(n_layers, B, Hkv, Lmax, d=128, device="cuda"):
+    """An empty 8-bit cache: (k8, v8, k_scale, v_scale) for the calls below, codes
+    [n_layers, B, Hkv, Lmax, d] and scales [n_layers, B, Hkv, ceil(Lmax / KV8_BLOCK)]."""
+    codes = [torch.zeros(n_layers, B, Hkv, Lmax, d, dtype=torch.uint8, device=device)
+             .view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones(n_layers, B, Hkv, -(-Lmax // KV8_BLOCK), device=device) for _ in range(2)]
+    return (*codes, *scales)
+
+
+def eagle_prompt_attn(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, return_lse=False,
+                      dev_status=None, stream=None):
+    """Causal attention of packed prompts.  q [Tq,Hq,d], k / v [Tk,Hkv,d] bf16 (tokens may
+    be strided), cu_q / cu_k int32 [B+1] (cu_k None: cu_q).  The queries of a sequence are
+    the last positions of its keys.  Returns out [Tq,Hq,d], or (out, lse [Tq,Hq] f32)
+    with return_lse or an lse tensor."""
+    fn = "eagle_prompt_attn"
+    sq, sk, sv = (_token_rows(fn, t, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    cu_k = cu_q if cu_k is None else cu_k
+    _dev(cu_q, "cu_q", torch.int32)
+    _dev(cu_k, "cu_k", torch.int32)
+    Tq, Hq, d = q.shape
+    Tk, Hkv = k.shape[:2]
+    B = cu_q.numel() - 1
+    if B < 0 or cu_q.dim() != 1:
+        raise ValueError(f"{fn}: cu_q must be [B + 1]")
+    _shape(fn, cu_k, "cu_k", cu_q.shape)
+    _shape(fn, k, "k", (Tk, Hkv, d))
+    _shape(fn, v, "v", k.shape)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out = torch.empty(Tq, Hq, d, dtype=q.dtype, device=q.device) if out is None else out
+    _dev(out, "out", torch.bfloat16)
+    _shape(fn, out, "out", q.shape)
+    if lse is None and return_lse:
+        lse = torch.empty(Tq, Hq, dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+        _shape(fn, lse, "lse", (Tq, Hq))
+    _same_device(fn, q, (k, v, cu_q, cu_k, out, lse, dev_status))
+    with _on(q.device, stream):
+        _check(fn, lib().eagle_prompt_attn(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(out), _ptr(lse), Tq, Tk, B, Hq,
+            Hkv, d, sq, sk, sv, float(scale), _ptr(_status(dev_status, q.device)),
+            _stream(stream)))
+    return out if lse is None else (out, lse)
+
+
+def eagle_kv8_append(k, v, cu, pos, k8, v8, k_scale, v_scale, dev_status=None, stream=None):
+    """Quantises one layer's new rows k / v [T,Hkv,d] bf16 (tokens may be strided; sequence
+    b has rows cu[b] .. cu[b+1]-1) into the cache at rows pos[b] on, in place."""
+    fn = "eagle_kv8_append"
+    sk, sv = _token_rows(fn, k, "k"), _token_rows(fn, v, "v")
+    _dev(cu, "cu", torch.int32)
+    _dev(pos, "pos", torch.int32)
+    T, Hkv, d = k.shape
+    B = pos.numel()
+    _shape(fn, pos, "pos", (B,))
+    _shape(fn, cu, "cu", (B + 1,))
+    _shape(fn, v, "v", k.shape)
+    Lmax, dc = _kv8_cache(fn, k8, v8, k_scale, v_scale, (B, Hkv))
+    if dc != d:
+        raise ValueError(f"{fn}: rows of {d} and a cache of {dc} dimensions")
+    _same_device(fn, k, (v, cu, pos, k8, v8, k_scale, v_scale, dev_status))
+    with _on(k.device, stream):
+        _check(fn, lib().eagle_kv8_append(
+            _ptr(k), _ptr(v), _ptr(cu), _ptr(pos), _ptr(k8), _ptr(v8), _ptr(k_scale),
+            _ptr(v_scale), T, B, Hkv, d, Lmax, sk, sv, _ptr(_status(dev_status, k.device)),
+            _stream(stream)))
+
+
+def eagle_kv8_commit(k_tree, v_tree, k8, v8, k_scale, v_scale, kv_len, path, accept_len, max_depth,
+                     kv_len_out=None, dev_status=None, stream=None):
+    """Quantises the accepted path's rows of the tree's K / V [n_layers,B,n,Hkv,d] bf16
+    into the cache behind kv_len; kv_len is advanced in place, or into kv_len_out."""
+    fn = "eagle_kv8_commit"
+    _dev(k_tree, "k_tree", torch.bfloat16)
+    _dev(v_tree, "v_tree", torch.bfloat16)
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    for t, name in ((kv_len, "kv_len"), (kv_len_out, "kv_len_out"), (path, "path"),
+                    (accept_len, "accept_len")):
+        _dev(t, name, torch.int32)
+    if k_tree.dim() != 5:
+        raise ValueError(f"{fn}: k_tree must be [n_layers, B, n, Hkv, d]")
+    nl, B, n, Hkv, d = k_tree.shape
+    D = int(max_depth)
+    _shape(fn, v_tree, "v_tree", k_tree.shape)
+    for t, name in ((kv_len, "kv_len"), (kv_len_out, "kv_len_out"), (accept_len, "accept_len")):
+        _shape(fn, t, name, (B,))
+    _shape(fn, path, "path", (B, D + 1))
+    Lmax, dc = _kv8_cache(fn, k8, v8, k_scale, v_scale, (nl, B, Hkv))
+    if dc != d:
+        raise ValueError(f"{fn}: rows of {d} and a cache of {dc} dimensions")
+    _same_device(fn, k_tree, (v_tree, k8, v8, k_scale, v_scale, kv_len, kv_len_out, path,
+                              accept_len, dev_status))
+    with _on(k_tree.device, stream):
+        _check(fn, lib().eagle_kv8_commit(
+            _ptr(k_tree), _ptr(v_tree), _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
+            _ptr(kv_len), _ptr(kv_len_out), _ptr(path), _ptr(accept_len), nl, B, n, Hkv, d, Lmax,
+            D, _ptr(_status(dev_status, k_tree.device)), _stream(stream)))
+    return kv_len_out
+
+
+def tree_attn_kv8_workspace_size(B, n, Hq, Hkv, head_dim, Lmax) -> int:
+    return int(lib().eagle_tree_attn_kv8_workspace_size(B, n, Hq, Hkv, head_dim, Lmax))
+
+
+def eagle_tree_attn_kv8(q, k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, parent, scale=None,
+                        out=None, workspace=None, dev_status=None, stream=None):
+    """Tree attention over the 8-bit cache of one layer.  q [B,n,Hq,d] bf16, the cache
+    [B,Hkv,Lmax,d], k_tree / v_tree [B,n,Hkv,d] bf16 (the tree's own rows), kv_len [B],
+    parent [B,n] int32.  n = 1 with parent -1 is ordinary decoding."""
+    fn = "eagle_tree_attn_kv8"
+    _dev(q, "q", torch.bfloat16)
+    _dev(k_tree, "k_tree", torch.bfloat16)
+    _dev(v_tree, "v_tree", torch.bfloat16)
+    _dev(kv_len, "kv_len", torch.int32)
+    _dev(parent, "parent", torch.int32)
+    if q.dim() != 4 or k_tree.dim() != 4:
+        raise ValueError(f"{fn}: q must be [B, n, Hq, d] and k_tree [B, n, Hkv, d]")
+    B, n, Hq, d = q.shape
+    Hkv = k_tree.shape[2]
+    _shape(fn, k_tree, "k_tree", (B, n, Hkv, d))
+    _shape(fn, v_tree, "v_tree", k_tree.shape)
+    _shape(fn, kv_len, "kv_len", (B,))
+    _shape(fn, parent, "parent", (B, n))
+    Lmax, dc = _kv8_cache(fn, k8, v8, k_scale, v_scale, (B, Hkv))
+    if dc != d:
+        raise ValueError(f"{fn}: rows of {d} and a cache of {dc} dimensions")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out = torch.empty_like(q) if out is None else out
+    _dev(out, "out", torch.bfloat16)
+    _shape(fn, out, "out", q.shape)
+    _same_device(fn, q, (k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, parent, out, workspace,
+                         dev_status))
+    with _on(q.device, stream):
+        need = tree_attn_kv8_workspace_size(B, n, Hq, Hkv, d, Lmax)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if workspace is not None:
+            _dev(workspace, "workspace")
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(fn, lib().eagle_tree_attn_kv8(
+            _ptr(q), _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale), _ptr(k_tree), _ptr(v_tree),
+            _ptr(kv_len), _ptr(parent), _ptr(out), B, n, Hq, Hkv, d, Lmax, float(scale),
+            _ptr(workspace), ws_bytes, _ptr(_status(dev_status, q.device)), _stream(stream)))
+    return out
+
+
 def expand_scratch_size(B, V, top_k) -> int:
     return int(lib().eagle2_expand_scratch_size(B, V, top_k))
 

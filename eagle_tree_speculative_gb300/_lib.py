@@ -33,6 +33,15 @@ SIGNATURES = {
     "eagle_verify_accept_d2t": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _F, _U64, _P,
                                      _P, _P, _P, _P, _P]),
     "eagle_kv_compact": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "eagle_prompt_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I64, _I64,
+                               _I64, _F, _P, _P]),
+    "eagle_kv8_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I64, _I64, _P,
+                              _P]),
+    "eagle_kv8_commit": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                              _P, _P]),
+    "eagle_tree_attn_kv8_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "eagle_tree_attn_kv8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F,
+                                 _P, _SZ, _P, _P]),
     "eagle2_tree_state_size": (_SZ, [_I, _I, _I]),
     "eagle2_expand_scratch_size": (_SZ, [_I, _I, _I]),
     "eagle2_expand": (_I, [_I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P, _SZ, _P, _P, _P,

@@ -12,7 +12,10 @@
  *                        prefix and advance the logical length
  * plus two building blocks exposed for measurement and testing
  * (eagle_softmax_stats, eagle_lmhead_gemm), and the draft head's
- * training-time-test attention (eagle_ttt_attn).
+ * training-time-test attention (eagle_ttt_attn).  What comes before and beside it:
+ *   eagle_prompt_attn    causal attention of packed prompts
+ *   eagle_kv8_append, eagle_tree_attn_kv8, eagle_kv8_commit
+ *                        the same step over a K/V cache held in 8 bits
  *
  * Pages (cited by title and section):
  *   Lesson: "推测解码与 EAGLE-3" -- "不变量：Leviathan 拒绝采样", "KV cache 回滚",
@@ -72,7 +75,7 @@ typedef enum {
 #define EAGLE_DEV_BAD_TOKEN 0x02  /* token or draft row index out of range      */
 #define EAGLE_DEV_NONFINITE 0x04  /* NaN / +inf logit, or an all -inf row        */
 #define EAGLE_DEV_DEPTH     0x08  /* tree deeper than max_depth                  */
-#define EAGLE_DEV_CAPACITY  0x10  /* kv_len[b] + n > Lmax                        */
+#define EAGLE_DEV_CAPACITY  0x10  /* kv_len[b] + n > Lmax; rows out of range     */
 #define EAGLE_DEV_TIMEOUT   0x20  /* a bounded pipeline wait gave up             */
 
 typedef void* eagle_stream_t;
@@ -284,6 +287,112 @@ eagle_status eagle_kv_compact(void* k_cache, void* v_cache, int32_t* kv_len, con
 eagle_status eagle_ttt_attn(const void* q, const void* k, const void* v, void* out, int B, int S,
                             int Hq, int Hkv, int head_dim, int R1, int r, float scale,
                             int32_t* dev_status, eagle_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * eagle_prompt_attn -- causal attention of packed prompts, one layer.
+ * Guide "一次 eagenerate 调用的完整流转": the target (and the draft head) run over
+ * the whole prompt once before the first tree.  A server packs the prompts of a
+ * batch behind one another, without padding.
+ * Sequence b: queries cu_q[b] .. cu_q[b+1]-1, keys cu_k[b] .. cu_k[b+1]-1 (counts
+ * nq and nk).  The queries are the last nq positions of the nk keys, so query i sees
+ * keys j <= nk - nq + i (a whole prompt: cu_k = cu_q; a later chunk: the keys begin
+ * with what was computed before).  For query head h (kv head h / (Hq/Hkv)):
+ *   s = scale * q . k;   out = softmax(s) . v;   lse = ln sum exp(s)
+ * in fp32, out rounded to bf16 once.  A query that sees no key (nk < nq) gets out = 0
+ * and lse = -inf.
+ *   q    bf16, token t at q + t * q_stride, [Hq, head_dim] dense within
+ *   k, v bf16, token t at k + t * k_stride (v + t * v_stride), [Hkv, head_dim] dense
+ *   cu_q, cu_k int32 [B+1], non-decreasing, within [0, Tq] and [0, Tk] (device memory)
+ *   out  bf16 [Tq, Hq, head_dim]      lse f32 [Tq, Hq] or NULL
+ * Strides are in elements: multiples of 8, at least Hq (Hkv) * head_dim; a fused
+ * projection's output can be read in place.  Bases 16-byte aligned.  Rows of out and
+ * lse that belong to no sequence are left as they are.  Hq / Hkv <= 128.  Every row
+ * of a sequence's keys must be finite (masked keys are read; a zero weight does not
+ * cancel NaN); rows of no sequence and of other sequences may hold anything.
+ * Device errors: cu_q or cu_k decreasing or out of range sets EAGLE_DEV_CAPACITY and
+ * nothing is written.
+ * ------------------------------------------------------------------------- */
+eagle_status eagle_prompt_attn(const void* q, const void* k, const void* v, const int32_t* cu_q,
+                               const int32_t* cu_k, void* out, float* lse, int Tq, int Tk, int B,
+                               int Hq, int Hkv, int head_dim, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, float scale, int32_t* dev_status,
+                               eagle_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit K/V cache.  Lesson "KV cache 回滚" (one physical cache plus a logical
+ * length), with rows held as e4m3 codes and one scale per EAGLE_KV8_BLOCK cache rows
+ * and kv head:
+ *   k8, v8            e4m3 codes [.., B, Hkv, Lmax, head_dim]
+ *   k_scale, v_scale  f32 [.., B, Hkv, ceil(Lmax / EAGLE_KV8_BLOCK)], powers of two
+ *   row r = code[r] * scale[r / EAGLE_KV8_BLOCK]
+ * Rows that need a scale get the least 2^e, e >= -64, with max |x| <= 448 * 2^e; their
+ * codes are x / 2^e rounded to the nearest e4m3 value, ties to even.  Rows that join a
+ * block which already holds rows raise its scale if they need to: the rows it holds
+ * are then brought to the new scale (exact, but for codes that become subnormal).  A
+ * block whose first row is written starts with the scale of its own rows.  The tree's
+ * rows never enter the cache: they stay in bf16 beside it until they are accepted.
+ *
+ * eagle_kv8_append -- one layer's new rows behind what the cache holds.
+ * Sequence b's rows cu[b] .. cu[b+1]-1 of k and v become cache rows pos[b] + t.  The
+ * lengths are the caller's to advance (one pos serves every layer).
+ *   k, v  bf16, token t at k + t * k_stride (elements; a multiple of 8, at least
+ *         Hkv * head_dim), [Hkv, head_dim] dense within
+ *   cu    int32 [B+1], non-decreasing, within [0, T]     pos int32 [B]
+ * Device errors: bad cu sets EAGLE_DEV_CAPACITY, nothing is written; pos[b] < 0 or
+ * pos[b] + rows > Lmax sets it and skips the sequence.  A NaN or infinite element sets
+ * EAGLE_DEV_NONFINITE and is stored as NaN, or as +-448 times the scale that the
+ * block's finite elements need.
+ *
+ * eagle_kv8_commit -- the accepted path's rows of every layer (eagle_kv_compact's
+ * counterpart).  For t = 0 .. a (a = accept_len[b]): row path[b][t] of the tree's k and
+ * v becomes cache row kv_len[b] + t; then kv_len_out[b] = kv_len[b] + a + 1.
+ *   k_tree, v_tree bf16 [n_layers, B, n, Hkv, head_dim]
+ *   k8, v8, k_scale, v_scale with a leading n_layers
+ *   kv_len int32 [B]   kv_len_out int32 [B], may be kv_len   path int32 [B, D+1]
+ *   accept_len int32 [B]
+ * Sequences with accept_len < 0 are skipped (kv_len_out = kv_len).  Device errors, the
+ * sequence being skipped: a > D or rows beyond Lmax, EAGLE_DEV_CAPACITY; a path not
+ * starting at 0, not increasing or beyond n, EAGLE_DEV_BAD_TREE; elements as above.
+ * ------------------------------------------------------------------------- */
+#define EAGLE_KV8_BLOCK 32
+
+eagle_status eagle_kv8_append(const void* k, const void* v, const int32_t* cu, const int32_t* pos,
+                              void* k8, void* v8, float* k_scale, float* v_scale, int T, int B,
+                              int Hkv, int head_dim, int Lmax, int64_t k_stride, int64_t v_stride,
+                              int32_t* dev_status, eagle_stream_t stream);
+eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, void* v8,
+                              float* k_scale, float* v_scale, const int32_t* kv_len,
+                              int32_t* kv_len_out, const int32_t* path, const int32_t* accept_len,
+                              int n_layers, int B, int n, int Hkv, int head_dim, int Lmax,
+                              int max_depth, int32_t* dev_status, eagle_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * eagle_tree_attn_kv8 -- eagle_tree_attn over the 8-bit cache, one layer.
+ * For sequence b, node i, query head h (kv head h / (Hq/Hkv)):
+ *   keys   = cache rows 0 .. L_b-1 (L_b = kv_len[b]) plus rows j of k_tree / v_tree for
+ *            every j that is i or an ancestor of i;
+ *   out    = softmax(scale * q . k) . v, fp32 accumulation, bf16 result.
+ * One node (n = 1, parent = -1) is ordinary decoding.
+ *   q        bf16 [B, n, Hq, head_dim]
+ *   k8, v8, k_scale, v_scale  the cache, [B, Hkv, ..]; scales > 0
+ *   k_tree, v_tree bf16 [B, n, Hkv, head_dim]
+ *   kv_len   int32 [B]      parent int32 [B, n]  (parent[0] = -1, parent[i] < i)
+ *   out      bf16 [B, n, Hq, head_dim]
+ *   workspace / ws_bytes: device scratch of at least
+ *            eagle_tree_attn_kv8_workspace_size(B, n, Hq, Hkv, head_dim, Lmax) bytes (may
+ *            be NULL when that size is 0), 16-byte aligned; no initialisation needed.  Two
+ *            calls that may run at the same time need one each.
+ * Cache rows from L_b on are not used, whatever they hold; 0 <= L_b <= Lmax.
+ * Device errors: an invalid tree or kv_len sets a dev_status bit and writes zeros for
+ * that sequence.
+ * ------------------------------------------------------------------------- */
+size_t eagle_tree_attn_kv8_workspace_size(int B, int n, int Hq, int Hkv, int head_dim, int Lmax);
+eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
+                                 const float* k_scale, const float* v_scale, const void* k_tree,
+                                 const void* v_tree, const int32_t* kv_len, const int32_t* parent,
+                                 void* out, int B, int n, int Hq, int Hkv, int head_dim, int Lmax,
+                                 float scale, void* workspace, size_t ws_bytes,
+                                 int32_t* dev_status, eagle_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * eagle2_expand -- one level of EAGLE-2 expansion; optionally the rerank.
