@@ -374,7 +374,8 @@ eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, 
  *   out    = softmax(scale * q . k) . v, fp32 accumulation, bf16 result.
  * One node (n = 1, parent = -1) is ordinary decoding.
  *   q        bf16 [B, n, Hq, head_dim]
- *   k8, v8, k_scale, v_scale  the cache, [B, Hkv, ..]; scales > 0
+ *   k8, v8, k_scale, v_scale  the cache, [B, Hkv, ..]; the scales of blocks with a row
+ *            below L_b are powers of two from 2^-64 on, V's at most 2^44
  *   k_tree, v_tree bf16 [B, n, Hkv, head_dim]
  *   kv_len   int32 [B]      parent int32 [B, n]  (parent[0] = -1, parent[i] < i)
  *   out      bf16 [B, n, Hq, head_dim]
@@ -384,7 +385,8 @@ eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, 
  *            calls that may run at the same time need one each.
  * Cache rows from L_b on are not used, whatever they hold; 0 <= L_b <= Lmax.
  * Device errors: an invalid tree or kv_len sets a dev_status bit and writes zeros for
- * that sequence.
+ * that sequence; a V scale above 2^44, or a tree row of V beyond 2^52, sets
+ * EAGLE_DEV_NONFINITE (the result is then not defined).
  * ------------------------------------------------------------------------- */
 size_t eagle_tree_attn_kv8_workspace_size(int B, int n, int Hq, int Hkv, int head_dim, int Lmax);
 eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
