@@ -3,9 +3,9 @@
 // cores work for one slot while the other slot's softmax runs.
 //
 // TMEM (512 columns): S of slot s at s * 128 (its P is written over the first 64 columns),
-// O of slot s at 256 + s * 128.  384 threads: warps 0-3 have single roles (loads, MMA issue,
-// scheduling, repairs), warps 4-7 and 8-11 are the softmax of slots 0 and 1, one thread per
-// query row.  The role warps give registers up to the softmax warps.
+// O of slot s at 256 + s * 128.  Warps 0-3 have single roles (loads, MMA issue, scheduling),
+// warps 4-7 and 8-11 are the softmax of slots 0 and 1, one thread per query row.  The other warps
+// give registers up to the softmax warps.
 #pragma once
 
 #include "common.cuh"
@@ -17,10 +17,7 @@ namespace attn2 {
 constexpr int kRows = 128;                        // query rows of a slot
 constexpr int kKeys = 128;                        // keys of a tile
 constexpr int kSlots = 2;
-constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-// 3 warpgroups x 168 registers x 128 threads at launch; 72 + 2 x 216 = 3 x 168
-constexpr int kRegsRole = 72, kRegsSoftmax = 216;
 
 __device__ __forceinline__ uint32_t s_col(int slot) { return (uint32_t)(slot * 128); }
 __device__ __forceinline__ uint32_t o_col(int slot) { return (uint32_t)(256 + slot * 128); }
@@ -78,6 +75,17 @@ __device__ __forceinline__ float max_of(const float* x) {
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
+// 32 columns of this thread's TMEM lane, to be waited for with tmem_wait_ld.
+__device__ __forceinline__ void load32_nowait(uint32_t addr, float (&x)[32]) {
+    uint32_t u[32];
+    tmem_ld32_nowait(addr, u);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+
 // 128 columns of this thread's TMEM lane.
 __device__ __forceinline__ void load_row(uint32_t addr, float (&x)[128]) {
     uint32_t u[4][32];
@@ -101,6 +109,14 @@ __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t 
         "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&o)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};\n" ::"r"(taddr),
+        "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]),
+        "r"(o[8]), "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
@@ -122,12 +138,7 @@ __device__ __forceinline__ void rescale_row(uint32_t addr, float alpha) {
             : "memory");
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-            "%14,%15,%16};\n" ::"r"(addr + 16 * h),
-            "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]),
-            "r"(o[8]), "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
-            : "memory");
+        tmem_st16_nowait(addr + 16 * h, o);
     }
     tmem_wait_st();
 }

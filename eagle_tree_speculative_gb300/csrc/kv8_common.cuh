@@ -21,10 +21,14 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return (uint32_t)e4m3x2(a, b) | ((uint32_t)e4m3x2(c, d) << 16);
 }
-// Two codes as floats (every e4m3 value is a half).
-__device__ __forceinline__ float2 e4m3x2_float(uint16_t c) {
+// Two codes as halves (every e4m3 value is one), and as floats.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint16_t c) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(c));
+    return h;
+}
+__device__ __forceinline__ float2 e4m3x2_float(uint16_t c) {
+    const uint32_t h = e4m3x2_half2(c);
     float2 f;
     asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
         : "=f"(f.x), "=f"(f.y)

@@ -80,7 +80,7 @@ extern "C" eagle_status eagle_prompt_attn(const void* q, const void* k, const vo
     if (cudaFuncSetAttribute(prompt_tc::prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              prompt_tc::kSmem) != cudaSuccess)
         return EAGLE_ERR_CUDA;
-    prompt_tc::prompt_attn_kernel<<<grid, attn2::kThreads, prompt_tc::kSmem,
+    prompt_tc::prompt_attn_kernel<<<grid, prompt_tc::kThreads, prompt_tc::kSmem,
                                     reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);
     EAGLE_CHECK_LAUNCH();
     return EAGLE_OK;

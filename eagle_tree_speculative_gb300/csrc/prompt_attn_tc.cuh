@@ -26,6 +26,8 @@
 // tile is written only after the same warps have read O of this one, which keeps O safe.
 #pragma once
 
+#include <type_traits>
+
 #include "attn2_common.cuh"
 
 namespace eagle {
@@ -35,6 +37,9 @@ using attn2::kKeys;
 using attn2::kRows;
 using attn2::kSlots;
 
+constexpr int kThreads = 384;
+// 3 warpgroups x 168 registers at launch; 72 + 2 x 216 = 3 x 168
+constexpr int kRegsRole = 72, kRegsSoftmax = 216;
 constexpr int kStages = 5;
 constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
@@ -161,7 +166,7 @@ __device__ __forceinline__ void find_unit(const Args& a, int64_t i, int top, Uni
     u.tiles[1] = tiles_of(u.nq, u.nk, u.pos + a.P, a.P);
 }
 
-__global__ void __launch_bounds__(attn2::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, Args a) {
     extern __shared__ uint8_t smem_raw[];
@@ -207,7 +212,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     auto unit_read = [&](int i) { mbar_arrive(s32(&sh->info_empty[i % kInfo])); };
 
     if (warp < 4) {
-        attn2::regs_dec<attn2::kRegsRole>();
+        attn2::regs_dec<kRegsRole>();
         if (warp == 0 && lane == 0) {
             // ---------------- loads ----------------
             uint32_t r = 0;                               // ring stages used so far
@@ -248,52 +253,74 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
         } else if (warp == 1 && lane == 0) {
             // ---------------- MMA issue ----------------
+            // Slots are template arguments, the ring's place is kept as (stage, phase), barrier
+            // phases as bits: nothing here may live in local memory, which has next to no L1
+            // beside this much shared memory.
             const uint64_t dq0 = sw128_desc(s32(sQ)), dk0 = sw128_desc(s32(sR));
             const uint64_t dv0 = sw128_desc_mn(s32(sR), kBox, 1024);
-            uint32_t r = 0;                               // ring stage of the unit's first K tile
-            uint32_t nqs[kSlots] = {0, 0}, nps[kSlots] = {0, 0};
+            uint32_t qph = 0, pph = 0;
+            uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // places of the next K and V tile
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && mbar_wait(s32(bar), parity & 1u, abort_flag);
                 if (ok) tc_fence_after();
                 return ok;
             };
+            auto advance = [&](uint32_t& st, uint32_t& ph) {      // K and V tiles take turns in the ring
+                st += 2;
+                if (st >= kStages) { st -= kStages; ph ^= 1u; }
+            };
+            // S of slot s = Q K^T
+            auto qk = [&](auto slot_c, bool first, bool last) {
+                constexpr int s = decltype(slot_c)::value;
+                if (first) {
+                    if (!wait(&sh->q_full[s], qph >> s)) return;
+                    qph ^= 1u << s;
+                }
+                const uint64_t dk = dk0 + (uint64_t)((ks * kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k) {
+                    const uint64_t at = (uint64_t)(((k >> 2) * kBox + (k & 3) * 32) >> 4);
+                    umma_f16(tmem + attn2::s_col(s), dq0 + (uint64_t)((s * kTile) >> 4) + at, dk + at, kIdescQK,
+                             k > 0 ? 1u : 0u);
+                }
+                umma_commit(s32(&sh->s_full[s]));
+                if (last) umma_commit(s32(&sh->q_empty[s]));
+            };
+            // O of slot s += P V
+            auto pv = [&](auto slot_c, bool first, bool last) {
+                constexpr int s = decltype(slot_c)::value;
+                if (!wait(&sh->p_full[s], pph >> s)) return;
+                pph ^= 1u << s;
+                const uint64_t dv = dv0 + (uint64_t)((vs * kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    umma_f16_ts(tmem + attn2::o_col(s), tmem + attn2::s_col(s) + k * 8,
+                                dv + (uint64_t)((k * 16 * 128) >> 4), kIdescPV, (k > 0 || !first) ? 1u : 0u);
+                if (last) umma_commit(s32(&sh->o_full[s]));
+            };
+            const std::integral_constant<int, 0> s0;
+            const std::integral_constant<int, 1> s1;
             Unit u;
             for (int i = 0; ok && next_unit(i, u); ++i) {
                 unit_read(i);
-                const int n = max(u.tiles[0], u.tiles[1]);
-                for (int j = 0; ok && j <= n; ++j) {
-                    const uint32_t ik = r + 2 * j, iv = r + 2 * j - 1;     // K of tile j, V of tile j - 1
-                    for (int s = 0; ok && s < kSlots; ++s) {
-                        if (j > 0 && j <= u.tiles[s]) {                    // O += P V(j - 1)
-                            if (!wait(&sh->full[iv % kStages], iv / kStages)) break;
-                            if (!wait(&sh->p_full[s], nps[s]++)) break;
-                            const uint64_t dv = dv0 + (uint64_t)(((iv % kStages) * kTile) >> 4);
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                umma_f16_ts(tmem + attn2::o_col(s), tmem + attn2::s_col(s) + k * 8,
-                                            dv + (uint64_t)((k * 16 * 128) >> 4), kIdescPV, (j > 1 || k > 0) ? 1u : 0u);
-                            if (j == u.tiles[s]) umma_commit(s32(&sh->o_full[s]));
-                        }
-                        if (j < u.tiles[s]) {                              // S = Q K(j)^T
-                            if (j == 0 && !wait(&sh->q_full[s], nqs[s]++)) break;
-                            if (!wait(&sh->full[ik % kStages], ik / kStages)) break;
-                            const uint64_t dq = dq0 + (uint64_t)((s * kTile) >> 4);
-                            const uint64_t dk = dk0 + (uint64_t)(((ik % kStages) * kTile) >> 4);
-#pragma unroll
-                            for (int k = 0; k < kHeadDim / 16; ++k) {
-                                const uint64_t at = (uint64_t)(((k >> 2) * kBox + (k & 3) * 32) >> 4);
-                                umma_f16(tmem + attn2::s_col(s), dq + at, dk + at, kIdescQK, k > 0 ? 1u : 0u);
-                            }
-                            umma_commit(s32(&sh->s_full[s]));
-                            if (j == u.tiles[s] - 1) umma_commit(s32(&sh->q_empty[s]));
-                        }
+                const int n0 = u.tiles[0], n1 = u.tiles[1], n = max(n0, n1);
+                for (int j = 0; ok && j <= n && n > 0; ++j) {
+                    if (j > 0 && !wait(&sh->full[vs], vp)) break;
+                    if (j > 0 && j <= n0) pv(s0, j == 1, j == n0);
+                    if (ok && j < n && !wait(&sh->full[ks], kp)) break;
+                    if (ok && j < n0) qk(s0, j == 0, j == n0 - 1);
+                    if (ok && j > 0 && j <= n1) pv(s1, j == 1, j == n1);
+                    if (ok && j > 0) {
+                        umma_commit(s32(&sh->empty[vs]));
+                        advance(vs, vp);
                     }
-                    if (!ok) break;
-                    if (j > 0) umma_commit(s32(&sh->empty[iv % kStages]));
-                    if (j < n) umma_commit(s32(&sh->empty[ik % kStages]));
+                    if (ok && j < n1) qk(s1, j == 0, j == n1 - 1);
+                    if (ok && j < n) {
+                        umma_commit(s32(&sh->empty[ks]));
+                        advance(ks, kp);
+                    }
                 }
-                r += 2 * n;
             }
             umma_commit(s32(&sh->drain));
             mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
@@ -352,7 +379,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
     } else {
         // ---------------- softmax: one thread per query row ----------------
-        attn2::regs_inc<attn2::kRegsSoftmax>();
+        attn2::regs_inc<kRegsSoftmax>();
         const int slot = (warp - 4) >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;

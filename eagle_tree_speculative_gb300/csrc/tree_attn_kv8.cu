@@ -23,11 +23,17 @@ bool code_map(CUtensorMap* map, const void* x, int Lmax, int64_t slabs) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The most positions that the cut can have, or -1 from 2^31 on.
+int64_t kv8_positions(int B, int rows, int Hkv, int Lmax) {
+    const int64_t rt = (rows + kv8_tc::kRows - 1) / kv8_tc::kRows, tiles = (Lmax + kv8_tc::kKeys - 1) / kv8_tc::kKeys + 1;
+    const int64_t units = (int64_t)B * Hkv;
+    if (units > 0x7fffffffLL || units * rt > 0x7fffffffLL || units * rt * tiles > 0x7fffffffLL) return -1;
+    return units * rt * tiles;
+}
 // CTAs: one per SM, and no more than there can be pieces.
-int kv8_grid(int B, int rows, int Hkv, int Lmax) {
+int kv8_grid(int64_t positions, int rows) {
     const int rt = (rows + kv8_tc::kRows - 1) / kv8_tc::kRows;
-    const int64_t most = (int64_t)B * Hkv * rt * ((Lmax + kv8_tc::kKeys - 1) / kv8_tc::kKeys + 1);
-    const int64_t pieces = most / (kv8_tc::kMinTiles * (rt < 2 ? rt : 2));
+    const int64_t pieces = positions / (kv8_tc::kMinTiles * (rt < 2 ? rt : 2));
     const int sms = device_sm_count();
     return (int)(pieces < 1 ? 1 : pieces < sms ? pieces : sms);
 }
@@ -48,7 +54,10 @@ extern "C" size_t eagle_tree_attn_kv8_workspace_size(int B, int n, int Hq, int H
     if (B < 1 || n < 1 || n > kMaxNodes || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || head_dim != kHeadDim ||
         Lmax < 1 || (int64_t)n * (Hq / Hkv) > 0x3fffffffLL)
         return 0;
-    const int rows = n * (Hq / Hkv), grid = kv8_grid(B, rows, Hkv, Lmax);
+    const int rows = n * (Hq / Hkv);
+    const int64_t positions = kv8_positions(B, rows, Hkv, Lmax);
+    if (positions < 0) return 0;
+    const int grid = kv8_grid(positions, rows);
     return grid > 1 ? kv8_workspace(grid, rows) : 0;
 }
 
@@ -62,13 +71,16 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
     if (B < 0 || n < 1 || Hq < 1 || Hkv < 1 || Lmax < 1 || !(scale > 0.f) || !(scale <= 3.4e38f))
         return EAGLE_ERR_INVALID_ARG;
     if (n > kMaxNodes || head_dim != kHeadDim || Hq % Hkv != 0) return EAGLE_ERR_SHAPE;
-    if ((int64_t)n * (Hq / Hkv) > 0x3fffffffLL || (int64_t)B * Hkv > 0x7fffffffLL) return EAGLE_ERR_SHAPE;
+    if ((int64_t)n * (Hq / Hkv) > 0x3fffffffLL) return EAGLE_ERR_SHAPE;
+    const int rows = n * (Hq / Hkv);
+    const int64_t positions = kv8_positions(B, rows, Hkv, Lmax);
+    if (positions < 0) return EAGLE_ERR_SHAPE;
     if (B == 0) return EAGLE_OK;                        // nothing read or written
     if (!q || !k8 || !v8 || !k_scale || !v_scale || !k_tree || !v_tree || !kv_len || !parent || !out)
         return EAGLE_ERR_INVALID_ARG;
     for (const void* p : {q, k8, v8, k_tree, v_tree, (const void*)out, (const void*)workspace})
         if (reinterpret_cast<uintptr_t>(p) & 15) return EAGLE_ERR_INVALID_ARG;
-    const int rows = n * (Hq / Hkv), grid = kv8_grid(B, rows, Hkv, Lmax);
+    const int grid = kv8_grid(positions, rows);
     if (grid > 1 && (!workspace || ws_bytes < kv8_workspace(grid, rows))) return EAGLE_ERR_CAPACITY;
     kv8_tc::Args a;
     a.q = static_cast<const uint16_t*>(q);
@@ -91,7 +103,7 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
                              kv8_tc::kSmem) != cudaSuccess)
         return EAGLE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    kv8_tc::tree_attn_kv8_kernel<<<grid, attn2::kThreads, kv8_tc::kSmem, s>>>(mk, mv, a);
+    kv8_tc::tree_attn_kv8_kernel<<<grid, kv8_tc::kThreads, kv8_tc::kSmem, s>>>(mk, mv, a);
     EAGLE_CHECK_LAUNCH();
     if (grid > 1) {
         const int y = (a.rows + kv8_tc::kMergeWarps - 1) / kv8_tc::kMergeWarps;

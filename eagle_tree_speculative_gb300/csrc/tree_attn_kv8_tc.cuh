@@ -1,21 +1,23 @@
-// Tree attention over the 8-bit K/V cache on the tensor cores (tcgen05 kind::f8f6f4, TMEM, TMA).
+// Tree attention over the 8-bit K/V cache on the tensor cores (tcgen05, TMEM, TMA).
 //
-// Digits.  The 8-bit MMA multiplies e4m3 by e4m3, and the cache's codes go into it as they lie in
-// memory.  The other operand keeps bf16's precision as two e4m3 digits: x = hi + lo with hi the
-// leading 4 bits of x's significand and lo the next 4.  Two passes over the 8-bit operand at twice
-// the bf16 rate cost what one bf16 pass costs, without a conversion of K or V.
+// QK in 8 bits, PV in 16.  The cache's K codes go into kind::f8f6f4 as they lie in memory; the
+// query keeps bf16's precision as two e4m3 digits, q = hi + lo with hi the leading 4 bits of the
+// significand and lo the next 4: two passes at twice the bf16 rate, no conversion of K.  The
+// weights change per tile and thread, so splitting them as well costs more instructions than the
+// whole softmax (it was tried: 0.56 ms at the shape below); V is widened to fp16 once per tile
+// instead (every e4m3 value is a half), for both slots, and PV runs in kind::f16.
 //   Q  per row times a power of two that brings its largest element to [128, 256): digits exact
 //      for elements within 2^-9 of the largest, the rest to 2^-17 of it.
-//   P  kept in [0, 256]: weights to 2^-8 of themselves (a bf16 P's rounding), or 2^-10 on that
-//      scale for small ones, where the largest weight is at least 2^kOffset.
-//   the tree's own rows (bf16, n <= 64): one 128-key tile with the hi digits in rows 0 .. 63 and
-//      the lo digits in rows 64 .. 127, per-row powers of two; S of key j is S[j] + S[64 + j],
-//      and both its rows get the same weight.
+//   P  fp16, between 2^-24 and 2^14: a rounding of 2^-12 on a weight, where the largest weight is
+//      at least 2^kOffset.
+//   the tree's own rows (bf16, n <= 64): K as one 128-key tile with the hi digits in rows 0 .. 63
+//      and the lo digits in rows 64 .. 127 (S of key j is S[j] + S[64 + j]), V in fp16, with a
+//      power of two per row that brings its largest element to [128, 256).
 //
 // Scales.  A block of 32 keys has K and V scales 2^ek and 2^ev.  2^ek joins the factor from S to
 // the exponent.  2^ev joins the weight, P' = 2^(s + ev - m) with m the running maximum of s + ev:
 // then O = sum P' code needs no scale, and l = sum P' 2^-ev is one factor per block.  m is the
-// running maximum of what is multiplied with the codes, so P' uses e4m3's range whatever the
+// running maximum of what is multiplied with the codes, so P' uses fp16's range whatever the
 // blocks' scales are.
 //
 // Work.  A unit is one (sequence, kv head, pair of 128-row tiles), its keys in tiles of 128, the
@@ -27,10 +29,11 @@
 // A unit that is cut leaves partial (m, l, O) in the workspace, at most two per CTA; a second
 // small kernel merges them.
 //
-// Roles: warp 0 loads K and V tiles (16 KB) through one ring, warp 1 issues the MMAs, warp 2 makes
-// the K digits of the tree's rows and zeroes V rows behind the last key (whatever bits lie there:
-// a zero weight does not cancel NaN), warp 3 cuts the work and makes the V digits, warps 4-11 are
-// the softmax, which also makes the Q digits of the next unit before it writes this one's output.
+// Roles: warp 0 loads K tiles and makes the K digits of the tree's rows, warp 1 issues the MMAs,
+// warp 2 loads V tiles, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
+// digits of the next unit before it writes this one's output, warps 12-15 widen V into a ring of
+// half tiles of 64 keys; rows behind the last key become zeros there (whatever bits lie in them:
+// a zero weight does not cancel NaN).
 #pragma once
 
 #include "attn2_common.cuh"
@@ -44,11 +47,17 @@ using attn2::kRows;
 using attn2::kSlots;
 using kv8::kKv8Block;
 
-constexpr int kStages = 7;
-constexpr int kTile = 128 * 128;                  // 16 KB: a K or V tile, a digit plane of Q
+constexpr int kThreads = 512;
+// 4 warpgroups x 128 registers at launch; 56 + 2 x 200 + 56 = 4 x 128
+constexpr int kRegsOther = 56, kRegsSoftmax = 200;
+constexpr int kKStages = 3, kVStages = 2;         // rings of raw tiles
+constexpr int kHalves = 4;                        // ring of half V tiles in fp16
+constexpr int kTile = 128 * 128;                  // 16 KB: a K or V tile, a digit plane of Q, half a V tile in fp16
+constexpr int kHalfKeys = 64, kHalfBox = kHalfKeys * 128;     // 64 keys x 64 dims of fp16
 constexpr int kInfo = 3;                          // units in flight between the roles
+constexpr int kTrees = 8;                         // trees in flight, see Shared
 constexpr int kBlocks = kKeys / kKv8Block;        // scales per tile
-constexpr float kOffset = 6.f, kRescale = 2.f;    // weights up to 2^(6 + 2) <= 448
+constexpr float kOffset = 6.f, kRescale = 8.f;    // weights up to 2^14
 constexpr int kMaxVExp = 44;                      // V scales up to 2^44, see below
 constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles
 
@@ -71,11 +80,11 @@ struct Args {
 
 // ---------------- the cut: shared by the attention and the merging kernel ----------------
 // Positions: sequence by sequence, head by head, row-tile pair by pair, tile by tile; a tile of a
-// pair counts 2, of a single row tile 1.
+// pair counts 2, of a single row tile 1.  The host refuses sizes with 2^31 positions or more.
 struct Cut {
-    int64_t total;                                // positions
+    int total;                                    // positions
     int ctas;                                     // pieces
-    __device__ int64_t begin(int c) const { return total / ctas * c + total % ctas * c / ctas; }
+    __device__ int begin(int c) const { return total / ctas * c + total % ctas * c / ctas; }
 };
 __device__ __forceinline__ int tiles_of(const Args& a, int b) {
     const int L = a.kv_len[b];
@@ -85,15 +94,13 @@ __device__ __forceinline__ int row_tiles(const Args& a) { return (a.n * a.G + kR
 
 // Warp-wide.
 __device__ __forceinline__ Cut make_cut(const Args& a, int grid) {
-    int64_t sum = 0;
+    int sum = 0;
     for (int b = threadIdx.x & 31; b < a.B; b += 32) sum += tiles_of(a, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __reduce_add_sync(0xffffffffu, sum);
     Cut c;
     const int rt = row_tiles(a);
     c.total = sum * rt * a.Hkv;
-    const int64_t most = c.total / (kMinTiles * min(rt, 2));
-    c.ctas = (int)max((int64_t)1, min((int64_t)grid, most));
+    c.ctas = max(1, min(grid, c.total / (kMinTiles * min(rt, 2))));
     return c;
 }
 
@@ -101,20 +108,23 @@ __device__ __forceinline__ Cut make_cut(const Args& a, int grid) {
 struct Segment {
     int b, head, pair, T;                         // T tiles in all, the last one the tree's
     int weight;                                   // row tiles of the pair
-    int64_t start;                                // position of its first tile
+    int start;                                    // position of its first tile
     int t0, t1;
 };
+// Tiles of a unit that begins at `start` before position pos.
+__device__ __forceinline__ int tiles_before(int start, int weight, int pos) { return (pos - start + weight - 1) >> (weight - 1); }
+
 // Warp-wide: the unit at position pos; `b`, `base`: a sequence at or before it and its first
 // position, moved on.
-__device__ __forceinline__ Segment segment_at(const Args& a, int64_t pos, int64_t end, int& b, int64_t& base) {
+__device__ __forceinline__ Segment segment_at(const Args& a, int pos, int end, int& b, int& base) {
     const int rt = row_tiles(a), lane = threadIdx.x & 31;
-    for (;;) {                                    // 32 sequences at a time; the last one holds what is left
+    for (;;) {                                    // 32 sequences at a time
         const int mine = b + lane;
-        const int64_t w = mine < a.B ? (int64_t)tiles_of(a, mine) * rt * a.Hkv : 0;
-        int64_t sum = w;
+        const int w = mine < a.B ? tiles_of(a, mine) * rt * a.Hkv : 0;
+        int sum = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
         const unsigned past = __ballot_sync(0xffffffffu, base + sum > pos);
@@ -131,16 +141,16 @@ __device__ __forceinline__ Segment segment_at(const Args& a, int64_t pos, int64_
     Segment s;
     s.b = b;
     s.T = tiles_of(a, b);
-    int64_t off = pos - base;
-    const int64_t per_head = (int64_t)s.T * rt;
-    s.head = (int)(off / per_head);
+    int off = pos - base;
+    const int per_head = s.T * rt;
+    s.head = off / per_head;
     off -= s.head * per_head;
-    s.pair = (int)(off / (2 * s.T));
-    off -= (int64_t)s.pair * 2 * s.T;
+    s.pair = off / (2 * s.T);
+    off -= s.pair * 2 * s.T;
     s.weight = min(2, rt - 2 * s.pair);
     s.start = pos - off;
-    s.t0 = (int)((off + s.weight - 1) / s.weight);
-    s.t1 = (int)min((int64_t)s.T, (end - s.start + s.weight - 1) / s.weight);
+    s.t0 = tiles_before(s.start, s.weight, pos);
+    s.t1 = min(s.T, tiles_before(s.start, s.weight, end));
     return s;
 }
 
@@ -157,28 +167,33 @@ struct Unit {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], v_last[kStages];
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t h_full[kHalves], h_empty[kHalves];
     uint64_t q_full[kSlots], s_full[kSlots], p_full[kSlots], o_full[kSlots];
-    uint64_t tree_full, tree_empty, merge_in, merge_out;
+    uint64_t tree_full[kTrees], merge_in, merge_out;
     uint64_t info_full[kInfo], info_empty[kInfo];
     uint64_t drain;
     uint32_t tmem;
     int abort_flag;
     float2 ml[kSlots][kRows];
-    float k_fac[kMaxNodes];                       // of the tree's rows: 2^ek
-    float v_exp[kMaxNodes];                       // ev
+    // factors of the tree's rows.  Their writers run ahead of the softmax by what the K ring and S
+    // hold: at most kKStages + kSlots trees, fewer than kTrees
+    float k_fac[kTrees][kMaxNodes];               // 2^ek
+    float v_exp[kTrees][kMaxNodes];               // ev
     Unit info[kInfo];
 };
+static_assert(kKStages + kSlots < kTrees && kHalves < kTrees, "trees in flight");
 
-constexpr int kSmem = kSlots * 2 * kTile + 2 * kTile + kStages * kTile + (int)sizeof(Shared) + 1024;
+constexpr int kSmem = kSlots * 2 * kTile + (kKStages + kVStages + kHalves) * kTile + (int)sizeof(Shared) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
-// tcgen05.mma kind::f8f6f4, A and B e4m3 (format 0), D fp32.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int b_mn_major) {
-    return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// tcgen05.mma kind::f8f6f4, A and B e4m3 (format 0), both K-major, D fp32.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-constexpr uint32_t kIdescQK = idesc_e4m3(128, kKeys, 0);
-constexpr uint32_t kIdescPV = idesc_e4m3(128, kHeadDim, 1);
+constexpr uint32_t kIdescQK = idesc_e4m3(128, kKeys);
+// kind::f16 with A and B fp16 (format 0), B MN-major, D fp32
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(kHeadDim >> 3) << 17) | ((128u >> 4) << 24);
 
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -188,13 +203,11 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void umma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+// Two floats as an fp16 pair (round to nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // The leading digit of x: its significand cut to 4 bits, a value that e4m3 holds exactly (for
@@ -235,68 +248,53 @@ __device__ __forceinline__ float amax8(const uint4& x) {
     return __uint_as_float(m << 16);
 }
 
-// Warp-wide: the digits of the tree's rows of one head into a tile (rows 0 .. 63 hi, 64 .. 127 lo;
-// rows from n on zero), sixteen lanes a row.  Returns the OR of status bits.
-template <class Put>
-__device__ __forceinline__ int tree_digits(const uint16_t* x, int64_t stride, int n, uint8_t* tile, int lo_exp,
-                                           int max_exp, Put put) {
-    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-    int bits = 0;
-    for (int r0 = 0; r0 < kMaxNodes; r0 += 8) {
-        uint4 v[4];
+// Warp-wide, for 8 rows r0 .. r0 + 7 of a tree's K or V of one head, sixteen lanes a row: their
+// elements (rows from n on are zero) and exponents.
+__device__ __forceinline__ void tree_rows(const uint16_t* x, int64_t stride, int n, int r0, int lo_exp, uint4 (&v)[4],
+                                          int (&e)[4]) {
+    const int half = (threadIdx.x & 31) >> 4, c = threadIdx.x & 15;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 2 * i + half;
-            v[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(x + r * stride) + c) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 2 * i + half;
-            float m = amax8(v[i]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int e = digit_exp(m, lo_exp);
-            if (e > max_exp) bits = EAGLE_DEV_NONFINITE;
-            uint32_t hi[2], lo[2];
-            digits8(v[i], kv8::exp2i(-e), hi, lo);
-            *reinterpret_cast<uint2*>(tile + swz(r, 8 * c)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + r, 8 * c)) = make_uint2(lo[0], lo[1]);
-            if (c == 0) put(r, e);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 2 * i + half;
+        v[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(x + r * stride) + c) : make_uint4(0u, 0u, 0u, 0u);
     }
-    return bits;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float m = amax8(v[i]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        e[i] = digit_exp(m, lo_exp);
+    }
 }
 
-__global__ void __launch_bounds__(attn2::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* sQ = smem;                                   // [slot][hi, lo][16 KB]
-    uint8_t* sT = sQ + kSlots * 2 * kTile;                // the tree's K tile, V tile
-    uint8_t* sR = sT + 2 * kTile;                         // [kStages][16 KB]
-    Shared* sh = reinterpret_cast<Shared*>(sR + kStages * kTile);
+    uint8_t* sK = sQ + kSlots * 2 * kTile;                // [kKStages][16 KB]
+    uint8_t* sV = sK + kKStages * kTile;                  // [kVStages][16 KB]
+    uint8_t* sH = sV + kVStages * kTile;                  // [kHalves][2 boxes of 64 dims][64 keys][128 B]
+    Shared* sh = reinterpret_cast<Shared*>(sH + kHalves * kTile);
     volatile int* abort_flag = &sh->abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(s32(&sh->full[i]), 1);
-            mbar_init(s32(&sh->empty[i]), 1);
-            mbar_init(s32(&sh->v_last[i]), 1);
-        }
+        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 1); mbar_init(s32(&sh->k_empty[i]), 1); }
+        for (int i = 0; i < kVStages; ++i) { mbar_init(s32(&sh->v_full[i]), 1); mbar_init(s32(&sh->v_empty[i]), 4); }
+        for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(s32(&sh->q_full[s]), 4);
             mbar_init(s32(&sh->s_full[s]), 1);
             mbar_init(s32(&sh->p_full[s]), 4);
             mbar_init(s32(&sh->o_full[s]), 1);
         }
-        mbar_init(s32(&sh->tree_full), 2);
-        mbar_init(s32(&sh->tree_empty), 1);
+        for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 5);       // warp 0, the widening warps
         mbar_init(s32(&sh->merge_in), 8);
         mbar_init(s32(&sh->merge_out), 8);
-        // read by the loader, the MMA thread, warp 2 and the eight softmax warps
-        for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 11); }
+        // read by warps 0 to 2, the eight softmax and the four widening warps
+        for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 15); }
         mbar_init(s32(&sh->drain), 1);
         sh->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -316,166 +314,165 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     auto unit_read = [&](int i) { mbar_arrive(s32(&sh->info_empty[i % kInfo])); };
 
     if (warp < 4) {
-        attn2::regs_dec<attn2::kRegsRole>();
-        if (warp == 0 && lane == 0) {
-            // ---------------- loads ----------------
+        attn2::regs_dec<kRegsOther>();
+        if (warp == 0) {
+            // ---------------- K tiles; K digits of the tree's rows ----------------
+            uint32_t r = 0, trees = 0;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const Unit* up = next_unit(i);
+                if (!__all_sync(0xffffffffu, up != nullptr)) break;
+                const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree;
+                __syncwarp();
+                if (lane == 0) unit_read(i);
+                if (lane == 0) {
+                    for (int j = 0; j < nc; ++j) {
+                        const int st = (r + j) % kKStages;
+                        if (!mbar_wait(s32(&sh->k_empty[st]), (((r + j) / kKStages) & 1u) ^ 1u, abort_flag)) break;
+                        mbar_expect_tx(s32(&sh->k_full[st]), kTile);
+                        tma_load_3d(s32(sK + st * kTile), &map_k, s32(&sh->k_full[st]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
+                    }
+                }
+                __syncwarp();
+                r += nc;
+                if (tree) {
+                    const int st = r % kKStages;
+                    const bool got = mbar_wait(s32(&sh->k_empty[st]), ((r / kKStages) & 1u) ^ 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    uint8_t* tile = sK + st * kTile;
+                    const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
+                    for (int r0 = 0; r0 < kMaxNodes; r0 += 8) {
+                        uint4 v[4];
+                        int e[4];
+                        tree_rows(x, (int64_t)a.Hkv * kHeadDim, a.n, r0, -40, v, e);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = r0 + 2 * k + (lane >> 4), c = lane & 15;
+                            uint32_t hi[2], lo[2];
+                            digits8(v[k], kv8::exp2i(-e[k]), hi, lo);
+                            *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
+                            if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e[k]);
+                        }
+                    }
+                    attn2::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
+                        mbar_arrive(s32(&sh->k_full[st]));
+                    }
+                    ++trees;
+                    ++r;
+                }
+            }
+        } else if (warp == 2 && lane == 0) {
+            // ---------------- V tiles ----------------
             uint32_t r = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!up) break;
-                const int t0 = up->t0, nc = up->n - up->tree, z = up->b * a.Hkv + up->head, L = up->L;
+                const int t0 = up->t0, nc = up->n - up->tree, z = up->b * a.Hkv + up->head;
                 unit_read(i);
-                for (int j = 0; ok && j < nc; ++j) {
-                    const int key0 = (t0 + j) * kKeys;
-                    for (int v = 0; v < 2; ++v, ++r) {
-                        const int st = r % kStages;
-                        ok = ok && mbar_wait(s32(&sh->empty[st]), ((r / kStages) & 1u) ^ 1u, abort_flag);
-                        if (!ok) break;
-                        // a V tile with rows behind the last key goes through warp 2 first
-                        const uint32_t bar = s32(v && key0 + kKeys > L ? &sh->v_last[st] : &sh->full[st]);
-                        mbar_expect_tx(bar, kTile);
-                        tma_load_3d(s32(sR + st * kTile), v ? &map_v : &map_k, bar, 0, key0, z);
-                    }
+                for (int j = 0; j < nc; ++j, ++r) {
+                    const int st = r % kVStages;
+                    ok = mbar_wait(s32(&sh->v_empty[st]), ((r / kVStages) & 1u) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    mbar_expect_tx(s32(&sh->v_full[st]), kTile);
+                    tma_load_3d(s32(sV + st * kTile), &map_v, s32(&sh->v_full[st]), 0, (t0 + j) * kKeys, z);
                 }
             }
         } else if (warp == 1 && lane == 0) {
             // ---------------- MMA issue ----------------
-            const uint64_t dq0 = sw128_desc(s32(sQ)), dk0 = sw128_desc(s32(sR)), dkt = sw128_desc(s32(sT));
-            const uint64_t dv0 = sw128_desc_mn(s32(sR), kTile, 1024), dvt = sw128_desc_mn(s32(sT + kTile), kTile, 1024);
-            uint32_t r = 0, trees = 0, nqs[kSlots] = {0, 0}, nps[kSlots] = {0, 0};
+            // One copy of each product's code for both slots and both ways of dealing tiles; ring
+            // places are kept as (stage, phase) and barrier phases as bits, not as arrays (see kSmem).
+            uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && mbar_wait(s32(bar), parity & 1u, abort_flag);
                 if (ok) tc_fence_after();
                 return ok;
             };
+            const uint64_t dq0 = sw128_desc(s32(sQ)), dk0 = sw128_desc(s32(sK));
+            const uint64_t dh0 = sw128_desc_mn(s32(sH), kHalfBox, 1024);
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!up) break;
-                const int n = up->n, tree = up->tree, nc = n - tree;
-                const bool alt = up->split_keys != 0;
+                const int n = up->n, nc = n - up->tree, alt = up->split_keys;
                 unit_read(i);
-                bool q_there[kSlots] = {false, false};
-                // S of slot s = Q K(t)^T, both digits of Q
-                auto qk = [&](int s, int t) {
-                    if (!q_there[s]) {
-                        if (!wait(&sh->q_full[s], nqs[s]++)) return;
-                        q_there[s] = true;
-                    }
-                    const uint32_t use = r + 2 * t;
-                    if (t < nc ? !wait(&sh->full[use % kStages], use / kStages) : !wait(&sh->tree_full, trees)) return;
-                    const uint64_t dk = t < nc ? dk0 + (uint64_t)(((use % kStages) * kTile) >> 4) : dkt;
+                // step x is slot x & 1's: O += P V of tile tp, then S = Q K^T of tile t.  Two row
+                // tiles: both slots see every tile, t = x / 2 and tp the one before.  One: tile t
+                // is slot t & 1's, t = x and tp two before.
+                const int steps = n == 0 ? 0 : alt ? n + 2 : 2 * n + 2;
+                for (int x = 0; ok && x < steps; ++x) {
+                    const int s = x & 1, t = alt ? x : x >> 1, tp = alt ? t - 2 : t - 1;
+                    const bool both_done = alt || s;
+                    const uint32_t scol = tmem + (uint32_t)(s << 7), ocol = scol + 256;
+                    if (tp >= 0 && tp < n) {
+                        if (!wait(&sh->p_full[s], pph >> s)) break;
+                        pph ^= 1u << s;
+                        const int halves = tp < nc ? 2 : 1;               // the tree's tile is one half
+                        uint32_t h = hs, ph = hp;
+                        for (int y = 0; ok && y < halves; ++y) {
+                            if (!wait(&sh->h_full[h], ph)) break;
+                            const uint64_t dv = dh0 + (uint64_t)((h * kTile) >> 4);
+                            uint32_t acc = (tp >= (alt ? 2 : 1) || y) ? 1u : 0u;
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        const uint64_t dq = dq0 + (uint64_t)(((2 * s + d) * kTile) >> 4);
-#pragma unroll
-                        for (int k = 0; k < kHeadDim / 32; ++k)
-                            umma_f8(tmem + attn2::s_col(s), dq + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
-                    }
-                    umma_commit(s32(&sh->s_full[s]));
-                };
-                // O of slot s += P V(t), both digits of P
-                auto pv = [&](int s, int t, bool first, bool last) {
-                    const uint32_t use = r + 2 * t + 1;
-                    if (t < nc && !wait(&sh->full[use % kStages], use / kStages)) return;
-                    if (!wait(&sh->p_full[s], nps[s]++)) return;
-                    const uint64_t dv = t < nc ? dv0 + (uint64_t)(((use % kStages) * kTile) >> 4) : dvt;
-#pragma unroll
-                    for (int d = 0; d < 2; ++d)
-#pragma unroll
-                        for (int k = 0; k < kKeys / 32; ++k)
-                            umma_f8_ts(tmem + attn2::o_col(s), tmem + attn2::s_col(s) + 32 * d + 8 * k,
-                                       dv + (uint64_t)((k * 32 * 128) >> 4), kIdescPV, (!first || d || k) ? 1u : 0u);
-                    if (last) umma_commit(s32(&sh->o_full[s]));
-                };
-                auto k_done = [&](int t) { if (t < nc) umma_commit(s32(&sh->empty[(r + 2 * t) % kStages])); };
-                auto v_done = [&](int t) {
-                    umma_commit(s32(t < nc ? &sh->empty[(r + 2 * t + 1) % kStages] : &sh->tree_empty));
-                };
-                if (alt) {                                // tile t is slot t & 1's
-                    for (int t = 0; ok && t < n + 2; ++t) {
-                        if (t >= 2) {
-                            pv(t & 1, t - 2, t < 4, t >= n);
-                            if (ok) v_done(t - 2);
+                            for (int k = 0; k < kHalfKeys / 16; ++k) {
+                                umma_f16_ts(ocol, scol + 32 * y + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), kIdescPV, acc);
+                                acc = 1u;
+                            }
+                            if (both_done) umma_commit(s32(&sh->h_empty[h]));
+                            if (++h == kHalves) { h = 0; ph ^= 1u; }
                         }
-                        if (ok && t < n) {
-                            qk(t & 1, t);
-                            if (ok) k_done(t);
-                        }
+                        if (!ok) break;
+                        if (both_done) { hs = h; hp = ph; }
+                        if (tp + (alt ? 2 : 1) >= n) umma_commit(s32(&sh->o_full[s]));
                     }
-                } else {
-                    for (int t = 0; ok && t <= n; ++t) {
-                        for (int s = 0; ok && s < kSlots; ++s) {
-                            if (t > 0) pv(s, t - 1, t == 1, t == n);
-                            if (ok && t < n) qk(s, t);
+                    if (t < n) {
+                        if (t < (alt ? 2 : 1)) {
+                            if (!wait(&sh->q_full[s], qph >> s)) break;
+                            qph ^= 1u << s;
                         }
-                        if (ok && t > 0) v_done(t - 1);
-                        if (ok && t < n) k_done(t);
+                        if (!wait(&sh->k_full[ks], kp)) break;
+                        const uint64_t dk = dk0 + (uint64_t)((ks * kTile) >> 4);
+                        const uint64_t dq = dq0 + (uint64_t)((2 * s * kTile) >> 4);
+#pragma unroll
+                        for (int d = 0; d < 2; ++d)                       // both digits of Q
+#pragma unroll
+                            for (int k = 0; k < kHeadDim / 32; ++k)
+                                umma_f8(scol, dq + (uint64_t)((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
+                        umma_commit(s32(&sh->s_full[s]));
+                        if (both_done) {
+                            umma_commit(s32(&sh->k_empty[ks]));
+                            if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                        }
                     }
                 }
-                r += 2 * nc;
-                trees += tree;
             }
             umma_commit(s32(&sh->drain));
             mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
-        } else if (warp == 2) {
-            // ---------------- K digits of the tree's rows; V rows behind the last key ----------------
-            uint32_t r = 0, phases = 0, trees = 0;
-            int bits = 0;
-            for (int i = 0;; ++i) {
-                const Unit* up = next_unit(i);
-                if (!__all_sync(0xffffffffu, up != nullptr)) break;
-                const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree, L = up->L;
-                __syncwarp();
-                if (lane == 0) unit_read(i);
-                if (tree) {
-                    const bool got = mbar_wait(s32(&sh->tree_empty), (trees++ & 1u) ^ 1u, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    bits |= tree_digits(a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim, (int64_t)a.Hkv * kHeadDim,
-                                        a.n, sT, -40, 120, [&](int row, int e) { sh->k_fac[row] = kv8::exp2i(e); });
-                    attn2::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s32(&sh->tree_full));
-                }
-                r += 2 * nc;
-                if (nc > 0 && (t0 + nc) * kKeys > L) {
-                    const uint32_t st = (r - 1) % kStages;
-                    const bool got = mbar_wait(s32(&sh->v_last[st]), (phases >> st) & 1u, abort_flag);
-                    phases ^= 1u << st;
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    uint8_t* v = sR + st * kTile;
-                    for (int row = L - (t0 + nc - 1) * kKeys + (lane >> 3); row < kKeys; row += 4)
-                        *reinterpret_cast<uint4*>(v + row * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    attn2::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s32(&sh->full[st]));
-                }
-            }
-            if (bits) flag_error(a.dev_status, bits);
         } else if (warp == 3) {
-            // ---------------- the cut; V digits of the tree's rows ----------------
+            // ---------------- the cut ----------------
             const Cut cut = make_cut(a, gridDim.x);
             const bool mine = (int)blockIdx.x < cut.ctas;
-            int64_t pos = mine ? cut.begin(blockIdx.x) : 0, base = 0;
-            const int64_t end = mine ? cut.begin(blockIdx.x + 1) : 0;
+            int pos = mine ? cut.begin(blockIdx.x) : 0, base = 0;
+            const int end = mine ? cut.begin(blockIdx.x + 1) : 0;
             int b = 0, anc_of = -1, bits = 0;
-            uint32_t trees = 0;
             unsigned long long anc[2] = {0, 0};           // of nodes lane and lane + 32
             bool bad_tree = false;
-            // publishes the next unit as entry i; 0: stop, 1: published (head -1: there is none)
-            auto publish = [&](int i, int& tree_b, int& tree_head) {
+            bool have = true;
+            for (int i = 0; have; ++i) {
                 Segment s;
-                bool have = false;
+                have = false;
                 while (!have && pos < end) {
                     s = segment_at(a, pos, end, b, base);
-                    pos = s.start + (int64_t)s.weight * s.T;
+                    pos = s.start + s.weight * s.T;
                     have = s.t0 < s.t1;
                 }
                 const bool got = mbar_wait(s32(&sh->info_empty[i % kInfo]), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) return false;
+                if (!__all_sync(0xffffffffu, got)) break;
                 Unit* u = &sh->info[i % kInfo];
-                tree_head = -1;
                 if (!have) {
                     if (lane == 0) u->head = -1;
                 } else {
@@ -525,36 +522,15 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         u->split_keys = s.weight == 1;
                         u->part = s.t0 == 0 && s.t1 == s.T ? -1 : (int)blockIdx.x * 2 + (s.t0 == 0);
                     }
-                    if (!zero && s.t1 == s.T) { tree_b = s.b; tree_head = s.head; }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s32(&sh->info_full[i % kInfo]));
-                return have;
-            };
-            int tb = 0, th = -1;
-            bool more = publish(0, tb, th);
-            for (int i = 1; more; ++i) {                  // one unit ahead of the digits
-                int tb1 = 0, th1 = -1;
-                const bool next = publish(i, tb1, th1);
-                if (th >= 0) {
-                    const bool got = mbar_wait(s32(&sh->tree_empty), (trees++ & 1u) ^ 1u, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    bits |= tree_digits(a.v_tree + ((int64_t)tb * a.n * a.Hkv + th) * kHeadDim, (int64_t)a.Hkv * kHeadDim,
-                                        a.n, sT + kTile, kv8::kMinExp, kMaxVExp,
-                                        [&](int row, int e) { sh->v_exp[row] = (float)e; });
-                    attn2::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s32(&sh->tree_full));
-                }
-                more = next;
-                tb = tb1;
-                th = th1;
             }
             if (bits) flag_error(a.dev_status, bits);
         }
-    } else {
+    } else if (warp < 12) {
         // ---------------- softmax: one thread per query row ----------------
-        attn2::regs_inc<attn2::kRegsSoftmax>();
+        attn2::regs_inc<kRegsSoftmax>();
         const int slot = (warp - 4) >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -615,38 +591,115 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             return true;
         };
 
-        Row w;
-        bool have = begin_unit(0, w), ok = true;
-        for (int i = 0; have; ++i) {
-            const bool idle = !__any_sync(0xffffffffu, w.r >= 0);        // rows are independent: leave P as it is
+        // Per unit: the Q digits of the next one go in, so that its first products can run during
+        // this one's output; then this one's output; then the next one's tiles.
+        Row w{};
+        bool have = true, ok = true, idle = true;
+        float mref = 0.f;
+        uint64_t l2 = 0;                                                 // two partial sums of the weights
+        int mine = 0;                                                    // tiles of this slot
+        for (int i = 0; have && ok; ++i) {
+            Row next;
+            have = begin_unit(i, next);
+            if (i > 0) {
+                if (mine > 0) {
+                    const bool got = mbar_wait(s32(&sh->o_full[slot]), units_done & 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    ++units_done;
+                    tc_fence_after();
+                }
+                float la, lb;
+                attn2::unf2(l2, la, lb);
+                float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
+                bool use0 = mine > 0, use1 = false;
+                const int c0 = w.alt ? 64 * slot : 0, c1 = w.alt ? c0 + 64 : kHeadDim;
+                uint32_t a0 = o_addr, a1 = o_addr;
+                if (w.alt) {
+                    // both slots hold this row: (m, l) change hands, each slot writes half of the columns
+                    sh->ml[slot][row] = make_float2(mref, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s32(&sh->merge_in));
+                    const bool got = mbar_wait(s32(&sh->merge_in), merges & 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    tc_fence_after();
+                    const float2 x0 = sh->ml[0][row], x1 = sh->ml[1][row];
+                    m = fmaxf(x0.x, x1.x);
+                    w0 = x0.x == -INFINITY ? 0.f : exp2f(x0.x - m);
+                    w1 = x1.x == -INFINITY ? 0.f : exp2f(x1.x - m);
+                    l = x0.y * w0 + x1.y * w1;
+                    use0 = w.n > 0;
+                    use1 = w.n > 1;
+                    a0 = tmem + lane_base + attn2::o_col(0);
+                    a1 = tmem + lane_base + attn2::o_col(1);
+                }
+                if (!idle) {
+                    const float inv = w.n == 0 || l == 0.f ? 0.f : 1.f / l;
+                    const int node = w.r < 0 ? 0 : w.r / a.G, g = w.r < 0 ? 0 : w.r % a.G;
+                    uint16_t* out = a.out + (((int64_t)w.b * a.n + node) * a.Hq + w.head * a.G + g) * kHeadDim;
+                    const int64_t place = (int64_t)w.part * a.rows + (w.r - w.pair * 2 * kRows);
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t o[32];
+                        if (use0) tmem_ld32(a0 + c, o);
+                        if (use1) {
+                            uint32_t o1[32];
+                            tmem_ld32(a1 + c, o1);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(o1[e]) * w1);
+                        }
+                        if (w.r < 0) continue;
+                        if (w.part < 0) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int d = 0; d < 4; ++d)
+                                    y[d] = use0 ? pack2(__uint_as_float(o[e + 2 * d]) * inv, __uint_as_float(o[e + 2 * d + 1]) * inv) : 0u;
+                                *reinterpret_cast<uint4*>(out + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) =
+                                    use0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (w.r >= 0 && w.part >= 0 && (!w.alt || slot == 0))
+                        a.ws_ml[place] = use0 ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+                }
+                if (w.alt) {                                                 // O and ml are free again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s32(&sh->merge_out));
+                    const bool got = mbar_wait(s32(&sh->merge_out), merges & 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    ++merges;
+                }
+            }
+            if (!have) break;
+            w = next;
+            idle = !__any_sync(0xffffffffu, w.r >= 0);        // rows are independent: leave P as it is
             const int64_t sc_at = ((int64_t)w.b * a.Hkv + w.head) * a.NB;
             const int nc = w.n - w.tree, step = w.alt ? 2 : 1;
-            float mref = -INFINITY;
-            uint64_t l2 = 0;                                             // two partial sums
-            float ks[kBlocks], vs[kBlocks];
-            // scales of blocks with a key before L; others have no key and are not read
-            auto load_scales = [&](int t) {
-#pragma unroll
-                for (int c = 0; c < kBlocks; ++c) {
-                    const int blk = (w.t0 + t) * kBlocks + c;
-                    const bool there = t < nc && blk * kKv8Block < w.L;
-                    ks[c] = there ? __ldg(a.k_scale + sc_at + blk) : 1.f;
-                    vs[c] = there ? __ldg(a.v_scale + sc_at + blk) : 1.f;
-                }
+            mref = -INFINITY;
+            l2 = 0;
+            mine = 0;
+            // lanes 0 .. 3 hold the K scales of a tile's blocks, lanes 4 .. 7 the V scales; blocks
+            // without a key before L are not read
+            const float* scales = (lane < kBlocks ? a.k_scale : a.v_scale) + sc_at + (lane & 3);
+            auto load_scale = [&](int t) {
+                const int blk = (w.t0 + t) * kBlocks;
+                return lane < 2 * kBlocks && t < nc && (blk + (lane & 3)) * kKv8Block < w.L ? __ldg(scales + blk) : 1.f;
             };
             const int first = w.alt ? slot : 0;
-            int mine = 0;                                                // tiles of this slot
-            load_scales(first);
+            float scale = load_scale(first);
             for (int t = first; t < w.n; t += step, ++mine) {
                 const bool got = mbar_wait(s32(&sh->s_full[slot]), tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
                 tc_fence_after();
                 if (!idle) {
-                    float x[kKeys];
-                    attn2::load_row(s_addr, x);
-                    uint32_t hi[32], lo[32];
-                    float mx, alpha = 1.f;
+                    float mx = -INFINITY, alpha = 1.f;
                     auto raise = [&]() {                                 // the reference maximum, if mx is far above it
                         if (mx > mref + kRescale || (mref == -INFINITY && mx > -INFINITY)) {
                             alpha = exp2f(mref - mx);                    // 0 for the first maximum
@@ -656,168 +709,193 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         // the commit behind this QK covers every PV before it: O is complete
                         if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) attn2::rescale_row(o_addr, alpha);
                     };
+                    // Both passes over the scores read them from TMEM, a block of 32 at a time in a
+                    // loop: holding all 128 in registers takes four copies of this code, and
+                    // the instruction caches are what such a kernel runs out of first.
                     if (t < nc) {
                         const int left = w.L - (w.t0 + t) * kKeys;
-                        if (left < kKeys) {
+                        const float k_fac = scale;
+                        const int ex = (int)(__float_as_uint(scale) >> 23) - 127;
+                        if (lane >= kBlocks && ex > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
+                        const float inv_ex = kv8::exp2i(min(-ex, 127));
+                        scale = load_scale(t + step);
+                        float x[32];
+                        auto mask = [&](int c) {
+                            if (left < kKv8Block * (c + 1)) {
 #pragma unroll
-                            for (int c = 0; c < kKeys; ++c) x[c] = c < left ? x[c] : -INFINITY;
-                        }
-                        float f[kBlocks], ev[kBlocks], inv[kBlocks];
-#pragma unroll
-                        for (int c = 0; c < kBlocks; ++c) {
-                            f[c] = fmaxf(ks[c] * w.sc, 1.17549435e-38f); // above 0: a masked block stays -inf
-                            const int e = (int)(__float_as_uint(vs[c]) >> 23) - 127;
-                            if (e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
-                            ev[c] = (float)e;
-                            inv[c] = kv8::exp2i(min(-e, 127));
-                        }
-                        load_scales(t + step);
-                        float mb[kBlocks];
-#pragma unroll
-                        for (int c = 0; c < kBlocks; ++c) mb[c] = fmaf(attn2::max_of<kKv8Block>(x + kKv8Block * c), f[c], ev[c]);
-                        mx = fmaxf(attn2::max3(mb[0], mb[1], mb[2]), mb[3]);
-                        raise();
-#pragma unroll
-                        for (int c = 0; c < kBlocks; ++c) {
-                            const float off = ev[c] - mref + kOffset;
-                            const uint64_t f_2 = attn2::f2(f[c], f[c]), off2 = attn2::f2(off, off);
-                            uint64_t acc[2] = {0, 0};
-#pragma unroll
-                            for (int d = 0; d < 8; ++d) {
-                                float p[4], h[4];
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const int at = 32 * c + 4 * d + 2 * y;
-                                    float s0, s1;
-                                    attn2::unf2(attn2::fma2(attn2::f2(x[at], x[at + 1]), f_2, off2), s0, s1);
-                                    p[2 * y] = ex2_approx(s0);
-                                    p[2 * y + 1] = ex2_approx(s1);
-                                    acc[y] = attn2::add2(acc[y], attn2::f2(p[2 * y], p[2 * y + 1]));
-                                }
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) h[y] = lead(p[y]);
-                                hi[8 * c + d] = kv8::e4m3x4(h[0], h[1], h[2], h[3]);
-                                lo[8 * c + d] = kv8::e4m3x4(p[0] - h[0], p[1] - h[1], p[2] - h[2], p[3] - h[3]);
+                                for (int e = 0; e < 32; ++e) x[e] = kKv8Block * c + e < left ? x[e] : -INFINITY;
                             }
-                            l2 = attn2::fma2(attn2::add2(acc[0], acc[1]), attn2::f2(inv[c], inv[c]), l2);
+                        };
+                        // above 0, so that a masked block stays -inf
+                        auto factor = [&](int c) { return fmaxf(__shfl_sync(0xffffffffu, k_fac, c) * w.sc, 1.17549435e-38f); };
+#pragma unroll 1
+                        for (int c = 0; c < kBlocks; ++c) {
+                            attn2::load32_nowait(s_addr + 32 * c, x);
+                            const float f = factor(c);
+                            const float ev = (float)__shfl_sync(0xffffffffu, ex, kBlocks + c);
+                            attn2::tmem_wait_ld();
+                            mask(c);
+                            mx = fmaxf(mx, fmaf(attn2::max_of<32>(x), f, ev));
+                        }
+                        raise();
+#pragma unroll 1
+                        for (int c = 0; c < kBlocks; ++c) {
+                            attn2::load32_nowait(s_addr + 32 * c, x);
+                            const float f = factor(c);
+                            const float off = (float)__shfl_sync(0xffffffffu, ex, kBlocks + c) - mref + kOffset;
+                            const float inv = __shfl_sync(0xffffffffu, inv_ex, kBlocks + c);
+                            const uint64_t f_2 = attn2::f2(f, f), off2 = attn2::f2(off, off);
+                            attn2::tmem_wait_ld();
+                            mask(c);
+                            uint64_t acc[2] = {0, 0};
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int d = 0; d < 16; ++d) {
+                                float s0, s1;
+                                attn2::unf2(attn2::fma2(attn2::f2(x[2 * d], x[2 * d + 1]), f_2, off2), s0, s1);
+                                const float p0 = ex2_approx(s0), p1 = ex2_approx(s1);
+                                acc[d & 1] = attn2::add2(acc[d & 1], attn2::f2(p0, p1));
+                                pk[d] = pack_half2(p0, p1);
+                            }
+                            // P over S: columns 16 c on hold scores of blocks that have been read
+                            attn2::tmem_st16_nowait(s_addr + 16 * c, pk);
+                            l2 = attn2::fma2(attn2::add2(acc[0], acc[1]), attn2::f2(inv, inv), l2);
                         }
                     } else {
-                        // the tree's tile: key j's score is the sum of its digits' columns
-                        // its factors are there: the MMA thread has seen this barrier, now this one does
-                        const bool seen = mbar_wait(s32(&sh->tree_full), trees & 1u, abort_flag);
+                        // the tree's tile, 32 keys at a time: key j's score is the sum of its digits'
+                        // columns j and 64 + j; its factors have a barrier per tree in flight
+                        const int tr = trees % kTrees;
+                        const bool seen = mbar_wait(s32(&sh->tree_full[tr]), (trees / kTrees) & 1u, abort_flag);
                         if (!__all_sync(0xffffffffu, seen)) { ok = false; break; }
-                        mx = -INFINITY;
+                        float x[32];
+                        auto scores = [&](int c) {
+                            float y[32];
+                            attn2::load32_nowait(s_addr + 32 * c, x);
+                            attn2::load32_nowait(s_addr + kMaxNodes + 32 * c, y);
+                            attn2::tmem_wait_ld();
+                            const uint32_t anc = (uint32_t)(w.anc >> (32 * c));
 #pragma unroll
-                        for (int j = 0; j < kMaxNodes; ++j) {
-                            const float f = fmaxf(sh->k_fac[j] * w.sc, 1.17549435e-38f);
-                            const bool sees = (w.anc >> j) & 1ull;
-                            x[j] = sees ? fmaf(x[j] + x[kMaxNodes + j], f, sh->v_exp[j]) : -INFINITY;
-                            mx = fmaxf(mx, x[j]);
+                            for (int j = 0; j < 32; ++j) {
+                                const float f = fmaxf(sh->k_fac[tr][32 * c + j] * w.sc, 1.17549435e-38f);
+                                x[j] = (anc >> j) & 1u ? fmaf(x[j] + y[j], f, sh->v_exp[tr][32 * c + j]) : -INFINITY;
+                            }
+                        };
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            scores(c);
+                            mx = fmaxf(mx, attn2::max_of<32>(x));
                         }
                         raise();
                         float sum = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            scores(c);
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int d = 0; d < 16; ++d) {
-                            float p[4], h[4];
+                            for (int d = 0; d < 16; ++d) {
+                                float p[2];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const int j = 4 * d + y;
-                                p[y] = ex2_approx(x[j] - mref + kOffset);
-                                sum = fmaf(p[y], kv8::exp2i(-(int)sh->v_exp[j]), sum);
-                                h[y] = lead(p[y]);
+                                for (int y = 0; y < 2; ++y) {
+                                    p[y] = ex2_approx(x[2 * d + y] - mref + kOffset);
+                                    sum = fmaf(p[y], kv8::exp2i(-(int)sh->v_exp[tr][32 * c + 2 * d + y]), sum);
+                                }
+                                pk[d] = pack_half2(p[0], p[1]);
                             }
-                            hi[d] = hi[16 + d] = kv8::e4m3x4(h[0], h[1], h[2], h[3]);
-                            lo[d] = lo[16 + d] = kv8::e4m3x4(p[0] - h[0], p[1] - h[1], p[2] - h[2], p[3] - h[3]);
+                            attn2::tmem_st16_nowait(s_addr + 16 * c, pk);
                         }
                         l2 = attn2::add2(l2, attn2::f2(sum, 0.f));
                     }
-                    attn2::tmem_st32_nowait(s_addr, hi);                 // P's digits over S
-                    attn2::tmem_st32_nowait(s_addr + 32, lo);
                     attn2::tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s32(&sh->p_full[slot]));
             }
-            if (!ok) break;
             trees += w.tree;
-            // the next unit's Q goes in now: its first products can run during this one's output
-            Row next;
-            have = begin_unit(i + 1, next);
-            if (mine > 0) {
-                const bool got = mbar_wait(s32(&sh->o_full[slot]), units_done & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) break;
-                ++units_done;
-                tc_fence_after();
-            }
-            float la, lb;
-            attn2::unf2(l2, la, lb);
-            float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
-            bool use0 = mine > 0, use1 = false;
-            const int c0 = w.alt ? 64 * slot : 0, c1 = w.alt ? c0 + 64 : kHeadDim;
-            uint32_t a0 = o_addr, a1 = o_addr;
-            if (w.alt) {
-                // both slots hold this row: (m, l) change hands, each slot writes half of the columns
-                sh->ml[slot][row] = make_float2(mref, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->merge_in));
-                const bool got = mbar_wait(s32(&sh->merge_in), merges & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) break;
-                tc_fence_after();
-                const float2 x0 = sh->ml[0][row], x1 = sh->ml[1][row];
-                m = fmaxf(x0.x, x1.x);
-                w0 = x0.x == -INFINITY ? 0.f : exp2f(x0.x - m);
-                w1 = x1.x == -INFINITY ? 0.f : exp2f(x1.x - m);
-                l = x0.y * w0 + x1.y * w1;
-                use0 = w.n > 0;
-                use1 = w.n > 1;
-                a0 = tmem + lane_base + attn2::o_col(0);
-                a1 = tmem + lane_base + attn2::o_col(1);
-            }
-            if (!idle) {
-                const float inv = w.n == 0 || l == 0.f ? 0.f : 1.f / l;
-                const int node = w.r < 0 ? 0 : w.r / a.G, g = w.r < 0 ? 0 : w.r % a.G;
-                uint16_t* out = a.out + (((int64_t)w.b * a.n + node) * a.Hq + w.head * a.G + g) * kHeadDim;
-                const int64_t place = (int64_t)w.part * a.rows + (w.r - w.pair * 2 * kRows);
-                for (int c = c0; c < c1; c += 32) {
-                    uint32_t o[32];
-                    if (use0) tmem_ld32(a0 + c, o);
-                    if (use1) {
-                        uint32_t o1[32];
-                        tmem_ld32(a1 + c, o1);
+        }
+        if (bits) flag_error(a.dev_status, bits);
+    } else {
+        // ---------------- V in fp16 ----------------
+        attn2::regs_dec<kRegsOther>();
+        const int cw = warp - 12;
+        // this lane's key of a group of eight and 16-byte chunk of four: the eight lanes of a
+        // shared-memory phase read and write all 32 banks, under both tiles' swizzles
+        const int key8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
+        uint32_t r = 0, rh = 0, trees = 0;
+        int bits = 0;
+        bool ok = true;
+        auto ready = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = mbar_wait(s32(bar), parity & 1u, abort_flag);
+            ok = ok && __all_sync(0xffffffffu, got);
+            return ok;
+        };
+        auto half_done = [&]() {
+            attn2::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s32(&sh->h_full[rh % kHalves]));
+            ++rh;
+        };
+        for (int i = 0; ok; ++i) {
+            const Unit* up = next_unit(i);
+            if (!__all_sync(0xffffffffu, up != nullptr)) break;
+            const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree, L = up->L;
+            __syncwarp();
+            if (lane == 0) unit_read(i);
+            for (int j = 0; j < nc; ++j, ++r) {
+                const int st = r % kVStages, left = L - (t0 + j) * kKeys;
+                if (!ready(&sh->v_full[st], r / kVStages)) break;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
+                    const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
+                    uint8_t* dst = sH + (rh % kHalves) * kTile;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(o1[e]) * w1);
-                    }
-                    if (w.r < 0) continue;
-                    if (w.part < 0) {
+                    for (int y = 0; y < 4; ++y) {
+                        const int key = (cw * 2 + (y >> 1)) * 8 + key8, box = y & 1;
+                        uint4 x = *reinterpret_cast<const uint4*>(src + swz(key, (4 * box + c4) * 16));
+                        if (h * kHalfKeys + key >= left) x = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t o[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t y[4];
-#pragma unroll
-                            for (int d = 0; d < 4; ++d)
-                                y[d] = use0 ? pack2(__uint_as_float(o[e + 2 * d]) * inv, __uint_as_float(o[e + 2 * d + 1]) * inv) : 0u;
-                            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            o[2 * e] = kv8::e4m3x2_half2((uint16_t)w[e]);
+                            o[2 * e + 1] = kv8::e4m3x2_half2((uint16_t)(w[e] >> 16));
                         }
-                    } else {
+                        *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    half_done();
+                }
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(s32(&sh->v_empty[st]));
+            }
+            if (ok && tree) {
+                if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
+                uint8_t* dst = sH + (rh % kHalves) * kTile;
+                const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
+                for (int r0 = cw * 16; r0 < cw * 16 + 16; r0 += 8) {
+                    uint4 v[4];
+                    int e[4];
+                    tree_rows(x, (int64_t)a.Hkv * kHeadDim, a.n, r0, kv8::kMinExp, v, e);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) =
-                                use0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = r0 + 2 * k + (lane >> 4), c = lane & 15;
+                        const float by = kv8::exp2i(-e[k]);
+                        if (e[k] > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
+                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            o[y] = pack_half2(__uint_as_float(w[y] << 16) * by, __uint_as_float(w[y] & 0xffff0000u) * by);
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBox + swz(row, (c & 7) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (c == 0) sh->v_exp[trees % kTrees][row] = (float)e[k];
                     }
                 }
-                if (w.r >= 0 && w.part >= 0 && (!w.alt || slot == 0))
-                    a.ws_ml[place] = use0 ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
-            }
-            if (w.alt) {                                                 // O and ml are free again
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->merge_out));
-                const bool got = mbar_wait(s32(&sh->merge_out), merges & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) break;
-                ++merges;
+                if (lane == 0) mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
+                ++trees;
+                half_done();
             }
-            w = next;
         }
         if (bits) flag_error(a.dev_status, bits);
     }
@@ -841,20 +919,19 @@ __global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args
     const Cut cut = make_cut(a, grid);
     const int c = blockIdx.x;
     if (c + 1 >= cut.ctas) return;                        // the last piece ends with a whole unit
-    const int64_t begin = cut.begin(c), end = cut.begin(c + 1);
-    int b = 0;
-    int64_t base = 0;
+    const int begin = cut.begin(c), end = cut.begin(c + 1);
+    int b = 0, base = 0;
     const Segment s = segment_at(a, end - 1, end, b, base);
     if (s.start < begin || s.t1 >= s.T) return;           // it begins earlier, or is whole
     const int rows = min(a.n * a.G - s.pair * 2 * kRows, 2 * kRows);
     int last = c;                                         // the piece with the unit's last tile
-    while (last + 1 < cut.ctas && (cut.begin(last + 1) - s.start + s.weight - 1) / s.weight < s.T) ++last;
+    while (last + 1 < cut.ctas && tiles_before(s.start, s.weight, cut.begin(last + 1)) < s.T) ++last;
     for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
         // part p of pieces c .. last; a piece may hold no tile of the unit
         auto place = [&](int p) -> int64_t {
             if (p == c) return ((int64_t)c * 2 + 1) * a.rows + row;
-            const int64_t t0 = (cut.begin(p) - s.start + s.weight - 1) / s.weight;
-            const int64_t t1 = p + 1 < cut.ctas ? (cut.begin(p + 1) - s.start + s.weight - 1) / s.weight : s.T;
+            const int t0 = tiles_before(s.start, s.weight, cut.begin(p));
+            const int t1 = p + 1 < cut.ctas ? tiles_before(s.start, s.weight, cut.begin(p + 1)) : s.T;
             return t0 < s.T && t0 < t1 ? (int64_t)p * 2 * a.rows + row : -1;
         };
         float m = -INFINITY, l = 0.f;
