@@ -31,6 +31,71 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// Bounded wait, in as little code as it can be: these kernels wait in many places, and their
+// speed depends on how much code goes round.  False when the abort flag is up, or after two ticks
+// of the clock's upper word (2^32 to 2^33 cycles, two to four seconds), which raises the flag.
+__device__ __forceinline__ uint32_t clock_hi() {
+    uint32_t x;
+    asm volatile("mov.u32 %0, %%clock_hi;\n" : "=r"(x));
+    return x;
+}
+__device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const uint32_t b = s32(bar), t0 = clock_hi();
+#pragma unroll 1
+    while (!mbar_try_wait(b, parity & 1u)) {
+        if (*abort_flag) return false;
+        if (clock_hi() - t0 >= 2u) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// MMA issue.  One elected lane issues, but the whole warp walks the loop, and what the loop
+// depends on is broadcast (uniform_of): the instruction takes its descriptors from uniform
+// registers, and from values that only one lane computes each of them costs a move across, 130 to
+// 160 cycles an MMA instead of 64.  A descriptor is a constant upper word and the lower word, which
+// holds the start address / 16 in its low 14 bits.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform_of(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Upper words: stride between 8-row groups 1024 bytes, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Lower words: K-major (leading offset unused), and MN-major with `lbo` between 64-element atoms.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3fffu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3fffu) | (((lbo >> 4) & 0x3fffu) << 16);
+}
+
+// D (+)= A B with A and B in shared memory (SS) or A in TMEM (TS); kind::f16 or kind::f8f6f4.
+template <bool F8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (F8)
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n"
+            " mov.b64 b, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n"
+            " mov.b64 b, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Two floats in a 64-bit register pair, and the packed operations on them.
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
     uint64_t r;
@@ -117,25 +182,36 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t 
         "r"(o[8]), "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8_nowait(uint32_t taddr, const uint32_t (&o)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(o[0]),
+        "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
+// 16 columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void load16(uint32_t addr, uint32_t (&o)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+          "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+          "=r"(o[14]), "=r"(o[15])
+        : "r"(addr)
+        : "memory");
+}
+
 // O (128 columns of this thread's lane) *= alpha.  Sixteen columns at a time in a loop that stays
-// a loop: the caller holds a row of scores in registers meanwhile, and this is rare.
+// a loop: the caller may hold a row of scores in registers meanwhile, and this is rare.
 __device__ __forceinline__ void rescale_row(uint32_t addr, float alpha) {
 #pragma unroll 1
     for (int h = 0; h < 8; ++h) {
         uint32_t o[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-            "%15}, [%16];\n"
-            "tcgen05.wait::ld.sync.aligned;\n"
-            : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-              "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-              "=r"(o[14]), "=r"(o[15])
-            : "r"(addr + 16 * h)
-            : "memory");
+        load16(addr + 16 * h, o);
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
         tmem_st16_nowait(addr + 16 * h, o);

@@ -26,8 +26,6 @@
 // tile is written only after the same warps have read O of this one, which keeps O safe.
 #pragma once
 
-#include <type_traits>
-
 #include "attn2_common.cuh"
 
 namespace eagle {
@@ -205,7 +203,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     // the i-th unit of this CTA, as the reading roles see it; false at the end (or on abort)
     auto next_unit = [&](int i, Unit& u) {
-        if (!mbar_wait(s32(&sh->info_full[i % kInfo]), ((uint32_t)i / kInfo) & 1u, abort_flag)) return false;
+        if (!attn2::wait_for(&sh->info_full[i % kInfo], ((uint32_t)i / kInfo) & 1u, abort_flag)) return false;
         u = sh->info[i % kInfo];
         return u.head >= 0;
     };
@@ -223,7 +221,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 unit_read(i);
                 auto load_q = [&](int s) {
                     if (u.tiles[s] == 0) return;
-                    ok = ok && mbar_wait(s32(&sh->q_empty[s]), (nqs[s] & 1u) ^ 1u, abort_flag);
+                    ok = ok && attn2::wait_for(&sh->q_empty[s], (nqs[s] & 1u) ^ 1u, abort_flag);
                     if (!ok) return;
                     const uint32_t bar = s32(&sh->q_full[s]);
                     mbar_expect_tx(bar, (uint32_t)(2 * a.P * a.G * 128));
@@ -234,7 +232,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 };
                 auto load_kv = [&](const CUtensorMap* map, int j, bool repair) {
                     const int st = r % kStages;
-                    ok = ok && mbar_wait(s32(&sh->empty[st]), ((r / kStages) & 1u) ^ 1u, abort_flag);
+                    ok = ok && attn2::wait_for(&sh->empty[st], ((r / kStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) return;
                     const uint32_t bar = s32(repair ? &sh->v_last[st] : &sh->full[st]);
                     mbar_expect_tx(bar, kTile);
@@ -251,79 +249,87 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     load_kv(&map_v, j, fix && j == n - 1);
                 }
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ---------------- MMA issue ----------------
-            // Slots are template arguments, the ring's place is kept as (stage, phase), barrier
-            // phases as bits: nothing here may live in local memory, which has next to no L1
-            // beside this much shared memory.
-            const uint64_t dq0 = sw128_desc(s32(sQ)), dk0 = sw128_desc(s32(sR));
-            const uint64_t dv0 = sw128_desc_mn(s32(sR), kBox, 1024);
+            // One copy of each product's code for both slots; the ring's place is kept as (stage,
+            // phase), barrier phases as bits: nothing here may live in local memory, which has next
+            // to no L1 beside this much shared memory.
+            const bool leader = attn2::elect_lane();
+            const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
+            const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sR)), dv0 = attn2::desc_lo_mn(s32(sR), kBox);
             uint32_t qph = 0, pph = 0;
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // places of the next K and V tile
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                ok = ok && mbar_wait(s32(bar), parity & 1u, abort_flag);
-                if (ok) tc_fence_after();
+                const bool got = attn2::wait_for(bar, parity, abort_flag);
+                ok = __all_sync(0xffffffffu, got);
+                tc_fence_after();
                 return ok;
             };
+            auto commit = [&](uint64_t* bar) { if (leader) umma_commit(s32(bar)); };
             auto advance = [&](uint32_t& st, uint32_t& ph) {      // K and V tiles take turns in the ring
                 st += 2;
                 if (st >= kStages) { st -= kStages; ph ^= 1u; }
             };
-            // S of slot s = Q K^T
-            auto qk = [&](auto slot_c, bool first, bool last) {
-                constexpr int s = decltype(slot_c)::value;
-                if (first) {
-                    if (!wait(&sh->q_full[s], qph >> s)) return;
-                    qph ^= 1u << s;
-                }
-                const uint64_t dk = dk0 + (uint64_t)((ks * kTile) >> 4);
+            for (int i = 0; ok; ++i) {
+                Unit u;
+                if (!__all_sync(0xffffffffu, next_unit(i, u))) break;
+                if (lane == 0) unit_read(i);
+                const int n0 = attn2::uniform_of(u.tiles[0]), n1 = attn2::uniform_of(u.tiles[1]), n = max(n0, n1);
+                // step x: slot s = x & 1, O += P V of tile j - 1, then S = Q K^T of tile j = x / 2
+                const int steps = n > 0 ? 2 * n + 2 : 0;
+                for (int x = 0; ok && x < steps; ++x) {
+                    const int s = x & 1, j = x >> 1, ns = s ? n1 : n0;
+                    const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
+                    if (j > 0) {
+                        if (!wait(&sh->full[vs], vp)) break;
+                        if (j <= ns) {
+                            if (!wait(&sh->p_full[s], pph >> s)) break;
+                            pph ^= 1u << s;
+                            const uint32_t dv = dv0 + ((vs * kTile) >> 4);
+                            const uint32_t acc = j > 1 ? 1u : 0u;
+                            if (leader) {
+                                attn2::mma_ts(ocol, scol, dv, kIdescPV, acc);
 #pragma unroll
-                for (int k = 0; k < kHeadDim / 16; ++k) {
-                    const uint64_t at = (uint64_t)(((k >> 2) * kBox + (k & 3) * 32) >> 4);
-                    umma_f16(tmem + attn2::s_col(s), dq0 + (uint64_t)((s * kTile) >> 4) + at, dk + at, kIdescQK,
-                             k > 0 ? 1u : 0u);
-                }
-                umma_commit(s32(&sh->s_full[s]));
-                if (last) umma_commit(s32(&sh->q_empty[s]));
-            };
-            // O of slot s += P V
-            auto pv = [&](auto slot_c, bool first, bool last) {
-                constexpr int s = decltype(slot_c)::value;
-                if (!wait(&sh->p_full[s], pph >> s)) return;
-                pph ^= 1u << s;
-                const uint64_t dv = dv0 + (uint64_t)((vs * kTile) >> 4);
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    umma_f16_ts(tmem + attn2::o_col(s), tmem + attn2::s_col(s) + k * 8,
-                                dv + (uint64_t)((k * 16 * 128) >> 4), kIdescPV, (k > 0 || !first) ? 1u : 0u);
-                if (last) umma_commit(s32(&sh->o_full[s]));
-            };
-            const std::integral_constant<int, 0> s0;
-            const std::integral_constant<int, 1> s1;
-            Unit u;
-            for (int i = 0; ok && next_unit(i, u); ++i) {
-                unit_read(i);
-                const int n0 = u.tiles[0], n1 = u.tiles[1], n = max(n0, n1);
-                for (int j = 0; ok && j <= n && n > 0; ++j) {
-                    if (j > 0 && !wait(&sh->full[vs], vp)) break;
-                    if (j > 0 && j <= n0) pv(s0, j == 1, j == n0);
-                    if (ok && j < n && !wait(&sh->full[ks], kp)) break;
-                    if (ok && j < n0) qk(s0, j == 0, j == n0 - 1);
-                    if (ok && j > 0 && j <= n1) pv(s1, j == 1, j == n1);
-                    if (ok && j > 0) {
-                        umma_commit(s32(&sh->empty[vs]));
-                        advance(vs, vp);
+                                for (int k = 1; k < kKeys / 16; ++k)
+                                    attn2::mma_ts(ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, 1u);
+                            }
+                            if (j == ns) commit(&sh->o_full[s]);
+                        }
+                        if (s) {
+                            commit(&sh->empty[vs]);
+                            advance(vs, vp);
+                        }
                     }
-                    if (ok && j < n1) qk(s1, j == 0, j == n1 - 1);
-                    if (ok && j < n) {
-                        umma_commit(s32(&sh->empty[ks]));
-                        advance(ks, kp);
+                    if (j < n) {
+                        if (!wait(&sh->full[ks], kp)) break;
+                        if (j < ns) {
+                            if (j == 0) {
+                                if (!wait(&sh->q_full[s], qph >> s)) break;
+                                qph ^= 1u << s;
+                            }
+                            const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((s * kTile) >> 4);
+                            if (leader) {
+#pragma unroll
+                                for (int k = 0; k < kHeadDim / 16; ++k) {
+                                    const uint32_t at = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                                    attn2::mma_ss<false>(scol, dq + at, dk + at, kIdescQK, k > 0 ? 1u : 0u);
+                                }
+                            }
+                            commit(&sh->s_full[s]);
+                            if (j == ns - 1) commit(&sh->q_empty[s]);
+                        }
+                        if (s) {
+                            commit(&sh->empty[ks]);
+                            advance(ks, kp);
+                        }
                     }
                 }
             }
-            umma_commit(s32(&sh->drain));
-            mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
+            if (leader) {
+                umma_commit(s32(&sh->drain));
+                mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
+            }
         } else if (warp == 2) {
             // ---------------- V rows behind the sequence's last key ----------------
             uint32_t r = 0, phases = 0;                   // phases: a bit per stage
@@ -335,7 +341,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 r += 2 * n;
                 if (!needs_fix(u, n)) continue;
                 const uint32_t st = (r - 1) % kStages;
-                const bool got = mbar_wait(s32(&sh->v_last[st]), (phases >> st) & 1u, abort_flag);
+                const bool got = attn2::wait_for(&sh->v_last[st], (phases >> st) & 1u, abort_flag);
                 phases ^= 1u << st;
                 if (!__all_sync(0xffffffffu, got)) break;
                 uint8_t* v = sR + st * kTile;
@@ -368,7 +374,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 Unit u{};
                 u.head = -1;
                 if (at < total) find_unit(a, at, top, u);
-                const bool got = mbar_wait(s32(&sh->info_empty[i % kInfo]), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
+                const bool got = attn2::wait_for(&sh->info_empty[i % kInfo], (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 if (lane == 0) {
                     sh->info[i % kInfo] = u;
@@ -404,7 +410,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             float mref = -INFINITY;
             uint64_t l2 = 0;                              // two partial sums
             for (int j = 0; j < n; ++j) {
-                const bool got = mbar_wait(s32(&sh->s_full[slot]), tiles_done & 1u, abort_flag);
+                const bool got = attn2::wait_for(&sh->s_full[slot], tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
                 tc_fence_after();
@@ -450,7 +456,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
             if (!ok) break;
             if (n > 0) {
-                const bool got = mbar_wait(s32(&sh->o_full[slot]), units_done & 1u, abort_flag);
+                const bool got = attn2::wait_for(&sh->o_full[slot], units_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 ++units_done;
                 tc_fence_after();

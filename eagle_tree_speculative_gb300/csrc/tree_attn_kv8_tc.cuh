@@ -180,6 +180,7 @@ struct Shared {
     // hold: at most kKStages + kSlots trees, fewer than kTrees
     float k_fac[kTrees][kMaxNodes];               // 2^ek
     float v_exp[kTrees][kMaxNodes];               // ev
+    float v_inv[kTrees][kMaxNodes];               // 2^-ev
     Unit info[kInfo];
 };
 static_assert(kKStages + kSlots < kTrees && kHalves < kTrees, "trees in flight");
@@ -195,14 +196,6 @@ constexpr uint32_t kIdescQK = idesc_e4m3(128, kKeys);
 // kind::f16 with A and B fp16 (format 0), B MN-major, D fp32
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(kHeadDim >> 3) << 17) | ((128u >> 4) << 24);
 
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // Two floats as an fp16 pair (round to nearest even), lo in the low half.
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
@@ -248,23 +241,12 @@ __device__ __forceinline__ float amax8(const uint4& x) {
     return __uint_as_float(m << 16);
 }
 
-// Warp-wide, for 8 rows r0 .. r0 + 7 of a tree's K or V of one head, sixteen lanes a row: their
-// elements (rows from n on are zero) and exponents.
-__device__ __forceinline__ void tree_rows(const uint16_t* x, int64_t stride, int n, int r0, int lo_exp, uint4 (&v)[4],
-                                          int (&e)[4]) {
-    const int half = (threadIdx.x & 31) >> 4, c = threadIdx.x & 15;
+// Warp-wide: of two rows at once, sixteen lanes a row, the exponent of each lane's row.
+__device__ __forceinline__ int row_exp(const uint4& v, int lo_exp) {
+    float m = amax8(v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 2 * i + half;
-        v[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(x + r * stride) + c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float m = amax8(v[i]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        e[i] = digit_exp(m, lo_exp);
-    }
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return digit_exp(m, lo_exp);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -307,7 +289,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 
     // the i-th unit of this CTA; nullptr at the end (or on abort)
     auto next_unit = [&](int i) -> const Unit* {
-        if (!mbar_wait(s32(&sh->info_full[i % kInfo]), ((uint32_t)i / kInfo) & 1u, abort_flag)) return nullptr;
+        if (!attn2::wait_for(&sh->info_full[i % kInfo], ((uint32_t)i / kInfo) & 1u, abort_flag)) return nullptr;
         const Unit* u = &sh->info[i % kInfo];
         return u->head >= 0 ? u : nullptr;
     };
@@ -328,7 +310,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 if (lane == 0) {
                     for (int j = 0; j < nc; ++j) {
                         const int st = (r + j) % kKStages;
-                        if (!mbar_wait(s32(&sh->k_empty[st]), (((r + j) / kKStages) & 1u) ^ 1u, abort_flag)) break;
+                        if (!attn2::wait_for(&sh->k_empty[st], (((r + j) / kKStages) & 1u) ^ 1u, abort_flag)) break;
                         mbar_expect_tx(s32(&sh->k_full[st]), kTile);
                         tma_load_3d(s32(sK + st * kTile), &map_k, s32(&sh->k_full[st]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
                     }
@@ -337,22 +319,25 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 r += nc;
                 if (tree) {
                     const int st = r % kKStages;
-                    const bool got = mbar_wait(s32(&sh->k_empty[st]), ((r / kKStages) & 1u) ^ 1u, abort_flag);
+                    const bool got = attn2::wait_for(&sh->k_empty[st], ((r / kKStages) & 1u) ^ 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     uint8_t* tile = sK + st * kTile;
                     const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
-                    for (int r0 = 0; r0 < kMaxNodes; r0 += 8) {
+#pragma unroll 1
+                    for (int r0 = lane >> 4; r0 < kMaxNodes; r0 += 8) {
                         uint4 v[4];
-                        int e[4];
-                        tree_rows(x, (int64_t)a.Hkv * kHeadDim, a.n, r0, -40, v, e);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim) + (lane & 15))
+                                                    : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int row = r0 + 2 * k + (lane >> 4), c = lane & 15;
+                            const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[k], -40);
                             uint32_t hi[2], lo[2];
-                            digits8(v[k], kv8::exp2i(-e[k]), hi, lo);
+                            digits8(v[k], kv8::exp2i(-e), hi, lo);
                             *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
                             *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
-                            if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e[k]);
+                            if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e);
                         }
                     }
                     attn2::fence_async_shared();
@@ -376,30 +361,35 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 unit_read(i);
                 for (int j = 0; j < nc; ++j, ++r) {
                     const int st = r % kVStages;
-                    ok = mbar_wait(s32(&sh->v_empty[st]), ((r / kVStages) & 1u) ^ 1u, abort_flag);
+                    ok = attn2::wait_for(&sh->v_empty[st], ((r / kVStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
                     mbar_expect_tx(s32(&sh->v_full[st]), kTile);
                     tma_load_3d(s32(sV + st * kTile), &map_v, s32(&sh->v_full[st]), 0, (t0 + j) * kKeys, z);
                 }
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ---------------- MMA issue ----------------
             // One copy of each product's code for both slots and both ways of dealing tiles; ring
-            // places are kept as (stage, phase) and barrier phases as bits, not as arrays (see kSmem).
+            // places are kept as (stage, phase) and barrier phases as bits, not as arrays.
+            const bool leader = attn2::elect_lane();
             uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                ok = ok && mbar_wait(s32(bar), parity & 1u, abort_flag);
-                if (ok) tc_fence_after();
+                const bool got = attn2::wait_for(bar, parity, abort_flag);
+                ok = __all_sync(0xffffffffu, got);
+                tc_fence_after();
                 return ok;
             };
-            const uint64_t dq0 = sw128_desc(s32(sQ)), dk0 = sw128_desc(s32(sK));
-            const uint64_t dh0 = sw128_desc_mn(s32(sH), kHalfBox, 1024);
+            auto commit = [&](uint64_t* bar) { if (leader) umma_commit(s32(bar)); };
+            const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
+            const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
-                if (!up) break;
-                const int n = up->n, nc = n - up->tree, alt = up->split_keys;
-                unit_read(i);
+                if (!__all_sync(0xffffffffu, up != nullptr)) break;
+                const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);
+                const int alt = attn2::uniform_of(up->split_keys);
+                __syncwarp();
+                if (lane == 0) unit_read(i);
                 // step x is slot x & 1's: O += P V of tile tp, then S = Q K^T of tile t.  Two row
                 // tiles: both slots see every tile, t = x / 2 and tp the one before.  One: tile t
                 // is slot t & 1's, t = x and tp two before.
@@ -407,7 +397,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 for (int x = 0; ok && x < steps; ++x) {
                     const int s = x & 1, t = alt ? x : x >> 1, tp = alt ? t - 2 : t - 1;
                     const bool both_done = alt || s;
-                    const uint32_t scol = tmem + (uint32_t)(s << 7), ocol = scol + 256;
+                    const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
                     if (tp >= 0 && tp < n) {
                         if (!wait(&sh->p_full[s], pph >> s)) break;
                         pph ^= 1u << s;
@@ -415,19 +405,20 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         uint32_t h = hs, ph = hp;
                         for (int y = 0; ok && y < halves; ++y) {
                             if (!wait(&sh->h_full[h], ph)) break;
-                            const uint64_t dv = dh0 + (uint64_t)((h * kTile) >> 4);
-                            uint32_t acc = (tp >= (alt ? 2 : 1) || y) ? 1u : 0u;
+                            const uint32_t dv = dh0 + ((h * kTile) >> 4), pcol = scol + 32 * y;
+                            const uint32_t acc = (tp >= (alt ? 2 : 1) || y) ? 1u : 0u;
+                            if (leader) {
+                                attn2::mma_ts(ocol, pcol, dv, kIdescPV, acc);
 #pragma unroll
-                            for (int k = 0; k < kHalfKeys / 16; ++k) {
-                                umma_f16_ts(ocol, scol + 32 * y + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), kIdescPV, acc);
-                                acc = 1u;
+                                for (int k = 1; k < kHalfKeys / 16; ++k)
+                                    attn2::mma_ts(ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, 1u);
                             }
-                            if (both_done) umma_commit(s32(&sh->h_empty[h]));
+                            if (both_done) commit(&sh->h_empty[h]);
                             if (++h == kHalves) { h = 0; ph ^= 1u; }
                         }
                         if (!ok) break;
                         if (both_done) { hs = h; hp = ph; }
-                        if (tp + (alt ? 2 : 1) >= n) umma_commit(s32(&sh->o_full[s]));
+                        if (tp + (alt ? 2 : 1) >= n) commit(&sh->o_full[s]);
                     }
                     if (t < n) {
                         if (t < (alt ? 2 : 1)) {
@@ -435,23 +426,26 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             qph ^= 1u << s;
                         }
                         if (!wait(&sh->k_full[ks], kp)) break;
-                        const uint64_t dk = dk0 + (uint64_t)((ks * kTile) >> 4);
-                        const uint64_t dq = dq0 + (uint64_t)((2 * s * kTile) >> 4);
+                        const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
+                        if (leader) {
 #pragma unroll
-                        for (int d = 0; d < 2; ++d)                       // both digits of Q
+                            for (int d = 0; d < 2; ++d)                   // both digits of Q
 #pragma unroll
-                            for (int k = 0; k < kHeadDim / 32; ++k)
-                                umma_f8(scol, dq + (uint64_t)((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
-                        umma_commit(s32(&sh->s_full[s]));
+                                for (int k = 0; k < kHeadDim / 32; ++k)
+                                    attn2::mma_ss<true>(scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
+                        }
+                        commit(&sh->s_full[s]);
                         if (both_done) {
-                            umma_commit(s32(&sh->k_empty[ks]));
+                            commit(&sh->k_empty[ks]);
                             if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                         }
                     }
                 }
             }
-            umma_commit(s32(&sh->drain));
-            mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
+            if (leader) {
+                umma_commit(s32(&sh->drain));
+                mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
+            }
         } else if (warp == 3) {
             // ---------------- the cut ----------------
             const Cut cut = make_cut(a, gridDim.x);
@@ -470,7 +464,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     pos = s.start + s.weight * s.T;
                     have = s.t0 < s.t1;
                 }
-                const bool got = mbar_wait(s32(&sh->info_empty[i % kInfo]), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
+                const bool got = attn2::wait_for(&sh->info_empty[i % kInfo], (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 Unit* u = &sh->info[i % kInfo];
                 if (!have) {
@@ -489,6 +483,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             anc[h] = 1ull << i2;
                         }
                         bad_tree = __any_sync(0xffffffffu, bad);
+#pragma unroll 1
                         for (int round = 0; !bad_tree && round < 6; ++round) {
                             unsigned long long add[2];
                             int up[2];
@@ -559,32 +554,32 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (lane == 0) unit_read(i);
             // a slot without a tile leaves Q (and its barrier) alone: it could be units ahead
             if (w.n <= (w.alt ? slot : 0)) return true;
-            uint4 q[16];
-            if (w.r >= 0) {
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    a.q + (((int64_t)w.b * a.n + node) * a.Hq + w.head * a.G + r % a.G) * kHeadDim);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) q[c] = __ldg(src + c);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 16; ++c) q[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            float m = 0.f;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) m = fmaxf(m, amax8(q[c]));
-            const int e = digit_exp(m, -40);
-            w.sc = a.scale_log2 * kv8::exp2i(e);
-            const float by = kv8::exp2i(-e);
-            // every QK of this slot's last unit has completed (its S was read): Q may be replaced
+            // every QK of this slot's last unit has completed (its S was read): Q may be replaced.
+            // The warp makes its 32 rows' digits together, two rows at once, sixteen lanes a row.
+            const int my_off = w.r < 0 ? -1 : node * a.Hq + (r - node * a.G);
+            const uint16_t* src = a.q + ((int64_t)w.b * a.n * a.Hq + w.head * a.G) * kHeadDim + (lane & 15) * 8;
             uint8_t* dst = sQ + slot * 2 * kTile;
+            int e_mine = 0;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                uint4 v[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint32_t h0[2], l0[2], h1[2], l1[2];
-                digits8(q[2 * c], by, h0, l0);
-                digits8(q[2 * c + 1], by, h1, l1);
-                *reinterpret_cast<uint4*>(dst + swz(row, 16 * c)) = make_uint4(h0[0], h0[1], h1[0], h1[1]);
-                *reinterpret_cast<uint4*>(dst + kTile + swz(row, 16 * c)) = make_uint4(l0[0], l0[1], l1[0], l1[1]);
+                for (int k = 0; k < 4; ++k) {
+                    const int off = __shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4));
+                    v[k] = off >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rr = r0 + 2 * k + (lane >> 4), e = row_exp(v[k], -40), at = (warp & 3) * 32 + rr;
+                    uint32_t hi[2], lo[2];
+                    digits8(v[k], kv8::exp2i(-e), hi, lo);
+                    *reinterpret_cast<uint2*>(dst + swz(at, 8 * (lane & 15))) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
+                    const int e_of = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);      // of row r0 + 2 k + (lane & 1)
+                    if ((lane >> 1) == (r0 >> 1) + k) e_mine = e_of;
+                }
             }
+            w.sc = a.scale_log2 * kv8::exp2i(e_mine);
             attn2::fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(s32(&sh->q_full[slot]));
@@ -603,7 +598,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             have = begin_unit(i, next);
             if (i > 0) {
                 if (mine > 0) {
-                    const bool got = mbar_wait(s32(&sh->o_full[slot]), units_done & 1u, abort_flag);
+                    const bool got = attn2::wait_for(&sh->o_full[slot], units_done & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     ++units_done;
                     tc_fence_after();
@@ -619,7 +614,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     sh->ml[slot][row] = make_float2(mref, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s32(&sh->merge_in));
-                    const bool got = mbar_wait(s32(&sh->merge_in), merges & 1u, abort_flag);
+                    const bool got = attn2::wait_for(&sh->merge_in, merges & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     tc_fence_after();
                     const float2 x0 = sh->ml[0][row], x1 = sh->ml[1][row];
@@ -637,31 +632,28 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     const int node = w.r < 0 ? 0 : w.r / a.G, g = w.r < 0 ? 0 : w.r % a.G;
                     uint16_t* out = a.out + (((int64_t)w.b * a.n + node) * a.Hq + w.head * a.G + g) * kHeadDim;
                     const int64_t place = (int64_t)w.part * a.rows + (w.r - w.pair * 2 * kRows);
-                    for (int c = c0; c < c1; c += 32) {
-                        uint32_t o[32];
-                        if (use0) tmem_ld32(a0 + c, o);
-                        if (use1) {
-                            uint32_t o1[32];
-                            tmem_ld32(a1 + c, o1);
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 16) {
+                        uint32_t o[16], o1[16];
+                        if (use0) attn2::load16(a0 + c, o);
+                        if (use1) attn2::load16(a1 + c, o1);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(o1[e]) * w1);
+                        for (int e = 0; e < 16; ++e) {
+                            const float x0 = use0 ? __uint_as_float(o[e]) : 0.f, x1 = use1 ? __uint_as_float(o1[e]) : 0.f;
+                            o[e] = __float_as_uint(fmaf(x0, w0, x1 * w1));
                         }
                         if (w.r < 0) continue;
                         if (w.part < 0) {
+                            uint32_t y[8];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint32_t y[4];
-#pragma unroll
-                                for (int d = 0; d < 4; ++d)
-                                    y[d] = use0 ? pack2(__uint_as_float(o[e + 2 * d]) * inv, __uint_as_float(o[e + 2 * d + 1]) * inv) : 0u;
-                                *reinterpret_cast<uint4*>(out + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                y[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + c) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) =
-                                    use0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         }
                     }
                     if (w.r >= 0 && w.part >= 0 && (!w.alt || slot == 0))
@@ -671,7 +663,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s32(&sh->merge_out));
-                    const bool got = mbar_wait(s32(&sh->merge_out), merges & 1u, abort_flag);
+                    const bool got = attn2::wait_for(&sh->merge_out, merges & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     ++merges;
                 }
@@ -694,7 +686,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             const int first = w.alt ? slot : 0;
             float scale = load_scale(first);
             for (int t = first; t < w.n; t += step, ++mine) {
-                const bool got = mbar_wait(s32(&sh->s_full[slot]), tiles_done & 1u, abort_flag);
+                const bool got = attn2::wait_for(&sh->s_full[slot], tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
                 tc_fence_after();
@@ -765,43 +757,42 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         // the tree's tile, 32 keys at a time: key j's score is the sum of its digits'
                         // columns j and 64 + j; its factors have a barrier per tree in flight
                         const int tr = trees % kTrees;
-                        const bool seen = mbar_wait(s32(&sh->tree_full[tr]), (trees / kTrees) & 1u, abort_flag);
+                        const bool seen = attn2::wait_for(&sh->tree_full[tr], (trees / kTrees) & 1u, abort_flag);
                         if (!__all_sync(0xffffffffu, seen)) { ok = false; break; }
-                        float x[32];
-                        auto scores = [&](int c) {
-                            float y[32];
-                            attn2::load32_nowait(s_addr + 32 * c, x);
-                            attn2::load32_nowait(s_addr + kMaxNodes + 32 * c, y);
-                            attn2::tmem_wait_ld();
-                            const uint32_t anc = (uint32_t)(w.anc >> (32 * c));
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float f = fmaxf(sh->k_fac[tr][32 * c + j] * w.sc, 1.17549435e-38f);
-                                x[j] = (anc >> j) & 1u ? fmaf(x[j] + y[j], f, sh->v_exp[tr][32 * c + j]) : -INFINITY;
-                            }
-                        };
+                        // first pass: scores, back into TMEM; second pass: weights
+                        uint32_t x[16], y[16];
 #pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {
-                            scores(c);
-                            mx = fmaxf(mx, attn2::max_of<32>(x));
+                        for (int c = 0; c < kMaxNodes; c += 16) {
+                            attn2::load16(s_addr + c, x);
+                            attn2::load16(s_addr + kMaxNodes + c, y);
+                            const uint32_t anc = (uint32_t)(w.anc >> c);
+                            float s[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float f = fmaxf(sh->k_fac[tr][c + j] * w.sc, 1.17549435e-38f);
+                                s[j] = (anc >> j) & 1u ? fmaf(__uint_as_float(x[j]) + __uint_as_float(y[j]), f, sh->v_exp[tr][c + j])
+                                                       : -INFINITY;
+                                x[j] = __float_as_uint(s[j]);
+                            }
+                            mx = fmaxf(mx, attn2::max_of<16>(s));
+                            attn2::tmem_st16_nowait(s_addr + c, x);
                         }
+                        attn2::tmem_wait_st();
                         raise();
                         float sum = 0.f;
+                        const float off = kOffset - mref;
 #pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {
-                            scores(c);
-                            uint32_t pk[16];
+                        for (int c = 0; c < kMaxNodes; c += 16) {
+                            attn2::load16(s_addr + c, x);
+                            uint32_t pk[8];
 #pragma unroll
-                            for (int d = 0; d < 16; ++d) {
-                                float p[2];
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    p[y] = ex2_approx(x[2 * d + y] - mref + kOffset);
-                                    sum = fmaf(p[y], kv8::exp2i(-(int)sh->v_exp[tr][32 * c + 2 * d + y]), sum);
-                                }
-                                pk[d] = pack_half2(p[0], p[1]);
+                            for (int d = 0; d < 8; ++d) {
+                                const float p0 = ex2_approx(__uint_as_float(x[2 * d]) + off);
+                                const float p1 = ex2_approx(__uint_as_float(x[2 * d + 1]) + off);
+                                sum = fmaf(p0, sh->v_inv[tr][c + 2 * d], fmaf(p1, sh->v_inv[tr][c + 2 * d + 1], sum));
+                                pk[d] = pack_half2(p0, p1);
                             }
-                            attn2::tmem_st16_nowait(s_addr + 16 * c, pk);
+                            attn2::tmem_st8_nowait(s_addr + c / 2, pk);      // over scores that have been read
                         }
                         l2 = attn2::add2(l2, attn2::f2(sum, 0.f));
                     }
@@ -825,7 +816,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         int bits = 0;
         bool ok = true;
         auto ready = [&](uint64_t* bar, uint32_t parity) {
-            const bool got = mbar_wait(s32(bar), parity & 1u, abort_flag);
+            const bool got = attn2::wait_for(bar, parity, abort_flag);
             ok = ok && __all_sync(0xffffffffu, got);
             return ok;
         };
@@ -849,7 +840,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
                     const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
                     uint8_t* dst = sH + (rh % kHalves) * kTile;
-#pragma unroll
+#pragma unroll 2
                     for (int y = 0; y < 4; ++y) {
                         const int key = (cw * 2 + (y >> 1)) * 8 + key8, box = y & 1;
                         uint4 x = *reinterpret_cast<const uint4*>(src + swz(key, (4 * box + c4) * 16));
@@ -873,22 +864,28 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
                 uint8_t* dst = sH + (rh % kHalves) * kTile;
                 const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
-                for (int r0 = cw * 16; r0 < cw * 16 + 16; r0 += 8) {
+#pragma unroll 1
+                for (int r0 = cw * 16 + (lane >> 4); r0 < cw * 16 + 16; r0 += 8) {
                     uint4 v[4];
-                    int e[4];
-                    tree_rows(x, (int64_t)a.Hkv * kHeadDim, a.n, r0, kv8::kMinExp, v, e);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim) + (lane & 15))
+                                                : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int row = r0 + 2 * k + (lane >> 4), c = lane & 15;
-                        const float by = kv8::exp2i(-e[k]);
-                        if (e[k] > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
+                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[k], kv8::kMinExp);
+                        const float by = kv8::exp2i(-e);
+                        if (e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
                         const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
                         uint32_t o[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             o[y] = pack_half2(__uint_as_float(w[y] << 16) * by, __uint_as_float(w[y] & 0xffff0000u) * by);
                         *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBox + swz(row, (c & 7) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (c == 0) sh->v_exp[trees % kTrees][row] = (float)e[k];
+                        if (c == 0) {
+                            sh->v_exp[trees % kTrees][row] = (float)e;
+                            sh->v_inv[trees % kTrees][row] = by;
+                        }
                     }
                 }
                 __syncwarp();
