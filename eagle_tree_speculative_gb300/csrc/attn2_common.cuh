@@ -40,7 +40,9 @@ __device__ __forceinline__ uint32_t clock_hi() {
     return x;
 }
 __device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const uint32_t b = s32(bar), t0 = clock_hi();
+    const uint32_t b = s32(bar);
+    if (mbar_try_wait(b, parity & 1u)) return true;
+    const uint32_t t0 = clock_hi();
 #pragma unroll 1
     while (!mbar_try_wait(b, parity & 1u)) {
         if (*abort_flag) return false;
@@ -50,6 +52,12 @@ __device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, v
         }
     }
     return true;
+}
+
+// The end of an MMA thread: its own products, which always end, have left the tensor cores.
+__device__ __forceinline__ void wait_drain(const uint64_t* bar) {
+    int never = 0;
+    mbar_wait(s32(bar), 0u, &never, /*honour_abort=*/false);
 }
 
 // MMA issue.  One elected lane issues, but the whole warp walks the loop, and what the loop
@@ -140,27 +148,27 @@ __device__ __forceinline__ float max_of(const float* x) {
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
-// 32 columns of this thread's TMEM lane, to be waited for with tmem_wait_ld.
-__device__ __forceinline__ void load32_nowait(uint32_t addr, float (&x)[32]) {
-    uint32_t u[32];
-    tmem_ld32_nowait(addr, u);
-#pragma unroll
-    for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
-}
 __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
+// 32 columns of this thread's TMEM lane and their maximum, which the load itself takes (NaN does not
+// count); both are there after tmem_wait_ld.
+__device__ __forceinline__ void load32_max_nowait(uint32_t addr, uint32_t* r, float& mx) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(mx)
+        : "r"(addr));
+}
 
-// 128 columns of this thread's TMEM lane.
-__device__ __forceinline__ void load_row(uint32_t addr, float (&x)[128]) {
-    uint32_t u[4][32];
+// 128 columns of this thread's TMEM lane, and the maximum of each 32; there after tmem_wait_ld.
+__device__ __forceinline__ void load_row_nowait(uint32_t addr, uint32_t (&u)[128], float (&mx)[4]) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) tmem_ld32_nowait(addr + 32 * h, u[h]);
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[32 * h + c] = __uint_as_float(u[h][c]);
+    for (int h = 0; h < 4; ++h) load32_max_nowait(addr + 32 * h, u + 32 * h, mx[h]);
 }
 
 __device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t (&r)[32]) {

@@ -415,14 +415,22 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 ++tiles_done;
                 tc_fence_after();
                 if (!idle) {
-                    float x[kKeys];
-                    attn2::load_row(s_addr, x);
+                    uint32_t x[kKeys];
+                    float m4[4];
+                    attn2::load_row_nowait(s_addr, x, m4);
                     const int left = seen - j * kKeys;
+                    attn2::tmem_wait_ld();
                     if (left < kKeys) {
+                        float y[kKeys];
 #pragma unroll
-                        for (int c = 0; c < kKeys; ++c) x[c] = c < left ? x[c] : -INFINITY;
+                        for (int c = 0; c < kKeys; ++c) {
+                            y[c] = c < left ? __uint_as_float(x[c]) : -INFINITY;
+                            x[c] = __float_as_uint(y[c]);
+                        }
+                        m4[0] = attn2::max_of<kKeys>(y);
+                        m4[1] = m4[2] = m4[3] = m4[0];
                     }
-                    const float mx = attn2::max_of<kKeys>(x) * sc;       // scale > 0 commutes with max
+                    const float mx = fmaxf(attn2::max3(m4[0], m4[1], m4[2]), m4[3]) * sc;    // scale > 0 commutes with max
                     float alpha = 1.f;
                     if (mx > mref + kRescale || (mref == -INFINITY && mx > -INFINITY)) {
                         alpha = exp2f(mref - mx);                        // 0 for the first maximum
@@ -440,7 +448,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             float s0, s1;
-                            attn2::unf2(attn2::fma2(attn2::f2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]), sc2, nb2), s0, s1);
+                            attn2::unf2(attn2::fma2(attn2::f2(__uint_as_float(x[64 * h + 2 * e]), __uint_as_float(x[64 * h + 2 * e + 1])), sc2, nb2), s0, s1);
                             const float p0 = ex2_approx(s0), p1 = ex2_approx(s1);
                             acc[e & 3] = attn2::add2(acc[e & 3], attn2::f2(p0, p1));
                             pk[e] = pack2(p0, p1);

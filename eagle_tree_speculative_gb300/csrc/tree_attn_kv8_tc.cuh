@@ -29,8 +29,8 @@
 // A unit that is cut leaves partial (m, l, O) in the workspace, at most two per CTA; a second
 // small kernel merges them.
 //
-// Roles: warp 0 loads K tiles and makes the K digits of the tree's rows, warp 1 issues the MMAs,
-// warp 2 loads V tiles, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
+// Roles: warp 0 loads K and V tiles and makes the K digits of the tree's rows, warps 1 and 2 issue
+// the MMAs of slots 0 and 1, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
 // digits of the next unit before it writes this one's output, warps 12-15 widen V into a ring of
 // half tiles of 64 keys; rows behind the last key become zeros there (whatever bits lie in them:
 // a zero weight does not cancel NaN).
@@ -172,7 +172,7 @@ struct Shared {
     uint64_t q_full[kSlots], s_full[kSlots], p_full[kSlots], o_full[kSlots];
     uint64_t tree_full[kTrees], merge_in, merge_out;
     uint64_t info_full[kInfo], info_empty[kInfo];
-    uint64_t drain;
+    uint64_t drain[kSlots];
     uint32_t tmem;
     int abort_flag;
     float2 ml[kSlots][kRows];
@@ -263,9 +263,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 1); mbar_init(s32(&sh->k_empty[i]), 1); }
+        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 1); mbar_init(s32(&sh->k_empty[i]), kSlots); }
         for (int i = 0; i < kVStages; ++i) { mbar_init(s32(&sh->v_full[i]), 1); mbar_init(s32(&sh->v_empty[i]), 4); }
-        for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
+        for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), kSlots); }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(s32(&sh->q_full[s]), 4);
             mbar_init(s32(&sh->s_full[s]), 1);
@@ -275,9 +275,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 5);       // warp 0, the widening warps
         mbar_init(s32(&sh->merge_in), 8);
         mbar_init(s32(&sh->merge_out), 8);
-        // read by warps 0 to 2, the eight softmax and the four widening warps
+        // read by warp 0, the two MMA, the eight softmax and the four widening warps
         for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 15); }
-        mbar_init(s32(&sh->drain), 1);
+        for (int s = 0; s < kSlots; ++s) mbar_init(s32(&sh->drain[s]), 1);
         sh->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -298,30 +298,37 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     if (warp < 4) {
         attn2::regs_dec<kRegsOther>();
         if (warp == 0) {
-            // ---------------- K tiles; K digits of the tree's rows ----------------
-            uint32_t r = 0, trees = 0;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
+            // ---------------- K and V tiles; K digits of the tree's rows ----------------
+            uint32_t ks = 0, kp = 1, vs = 0, vp = 1, trees = 0;
+            for (int i = 0;; ++i) {
                 const Unit* up = next_unit(i);
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
                 const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree;
                 __syncwarp();
                 if (lane == 0) unit_read(i);
-                if (lane == 0) {
-                    for (int j = 0; j < nc; ++j) {
-                        const int st = (r + j) % kKStages;
-                        if (!attn2::wait_for(&sh->k_empty[st], (((r + j) / kKStages) & 1u) ^ 1u, abort_flag)) break;
-                        mbar_expect_tx(s32(&sh->k_full[st]), kTile);
-                        tma_load_3d(s32(sK + st * kTile), &map_k, s32(&sh->k_full[st]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
+                bool ok = true;
+#pragma unroll 1
+                for (int j = 0; ok && j < nc; ++j) {
+                    const bool k_free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
+                    ok = __all_sync(0xffffffffu, k_free);
+                    if (ok && lane == 0) {
+                        mbar_expect_tx(s32(&sh->k_full[ks]), kTile);
+                        tma_load_3d(s32(sK + ks * kTile), &map_k, s32(&sh->k_full[ks]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
                     }
+                    if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                    const bool v_free = ok && attn2::wait_for(&sh->v_empty[vs], vp, abort_flag);
+                    ok = __all_sync(0xffffffffu, v_free);
+                    if (ok && lane == 0) {
+                        mbar_expect_tx(s32(&sh->v_full[vs]), kTile);
+                        tma_load_3d(s32(sV + vs * kTile), &map_v, s32(&sh->v_full[vs]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
+                    }
+                    if (++vs == kVStages) { vs = 0; vp ^= 1u; }
                 }
-                __syncwarp();
-                r += nc;
+                if (!ok) break;
                 if (tree) {
-                    const int st = r % kKStages;
-                    const bool got = attn2::wait_for(&sh->k_empty[st], ((r / kKStages) & 1u) ^ 1u, abort_flag);
+                    const bool got = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
-                    uint8_t* tile = sK + st * kTile;
+                    uint8_t* tile = sK + ks * kTile;
                     const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
 #pragma unroll 1
                     for (int r0 = lane >> 4; r0 < kMaxNodes; r0 += 8) {
@@ -330,49 +337,34 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         for (int k = 0; k < 4; ++k)
                             v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim) + (lane & 15))
                                                     : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
-                            const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[k], -40);
+                            const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[0], -40);
                             uint32_t hi[2], lo[2];
-                            digits8(v[k], kv8::exp2i(-e), hi, lo);
+                            digits8(v[0], kv8::exp2i(-e), hi, lo);
                             *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
                             *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
                             if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e);
+                            v[0] = v[1]; v[1] = v[2]; v[2] = v[3];       // the loop's body exists once
                         }
                     }
                     attn2::fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
-                        mbar_arrive(s32(&sh->k_full[st]));
+                        mbar_arrive(s32(&sh->k_full[ks]));
                     }
                     ++trees;
-                    ++r;
+                    if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
             }
-        } else if (warp == 2 && lane == 0) {
-            // ---------------- V tiles ----------------
-            uint32_t r = 0;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                const Unit* up = next_unit(i);
-                if (!up) break;
-                const int t0 = up->t0, nc = up->n - up->tree, z = up->b * a.Hkv + up->head;
-                unit_read(i);
-                for (int j = 0; j < nc; ++j, ++r) {
-                    const int st = r % kVStages;
-                    ok = attn2::wait_for(&sh->v_empty[st], ((r / kVStages) & 1u) ^ 1u, abort_flag);
-                    if (!ok) break;
-                    mbar_expect_tx(s32(&sh->v_full[st]), kTile);
-                    tma_load_3d(s32(sV + st * kTile), &map_v, s32(&sh->v_full[st]), 0, (t0 + j) * kKeys, z);
-                }
-            }
-        } else if (warp == 1) {
+        } else if (warp == 1 || warp == 2) {
             // ---------------- MMA issue ----------------
-            // One copy of each product's code for both slots and both ways of dealing tiles; ring
-            // places are kept as (stage, phase) and barrier phases as bits, not as arrays.
+            // Warp 1 + s issues slot s's products: one warp alone spends longer on its control than
+            // the tensor cores on the products.  Both run the same code.
+            const int s = attn2::uniform_of(warp - 1);
             const bool leader = attn2::elect_lane();
-            uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;
+            uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qp = 0, pp = 0;      // ring places and phases
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 const bool got = attn2::wait_for(bar, parity, abort_flag);
@@ -380,9 +372,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 tc_fence_after();
                 return ok;
             };
-            auto commit = [&](uint64_t* bar) { if (leader) umma_commit(s32(bar)); };
-            const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
-            const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
+            const uint32_t scol = (uint32_t)attn2::uniform_of((int)tmem) + (uint32_t)(s << 7), ocol = scol + 256;
+            const uint32_t dq = attn2::desc_lo(s32(sQ)) + ((2 * s * kTile) >> 4), dk0 = attn2::desc_lo(s32(sK));
+            const uint32_t dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
@@ -390,61 +382,65 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 const int alt = attn2::uniform_of(up->split_keys);
                 __syncwarp();
                 if (lane == 0) unit_read(i);
-                // step x is slot x & 1's: O += P V of tile tp, then S = Q K^T of tile t.  Two row
-                // tiles: both slots see every tile, t = x / 2 and tp the one before.  One: tile t
-                // is slot t & 1's, t = x and tp two before.
-                const int steps = n == 0 ? 0 : alt ? n + 2 : 2 * n + 2;
-                for (int x = 0; ok && x < steps; ++x) {
-                    const int s = x & 1, t = alt ? x : x >> 1, tp = alt ? t - 2 : t - 1;
-                    const bool both_done = alt || s;
-                    const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                    if (tp >= 0 && tp < n) {
-                        if (!wait(&sh->p_full[s], pph >> s)) break;
-                        pph ^= 1u << s;
+                // Step t: O += P V of tile t - lag, then S = Q K^T of tile t.  Two row tiles: every
+                // tile is both slots'; one: tile t is slot t & 1's, and the other slot only lets
+                // it pass.  A stage is free when both slots have said so.
+                const int lag = alt ? 2 : 1;
+#pragma unroll 1
+                for (int t = 0; ok && n > 0 && t < n + lag; ++t) {
+                    const int tp = t - lag;
+                    const bool mine = !alt || (t & 1) == s;               // tiles t and t - lag
+                    if (tp >= 0) {
                         const int halves = tp < nc ? 2 : 1;               // the tree's tile is one half
-                        uint32_t h = hs, ph = hp;
-                        for (int y = 0; ok && y < halves; ++y) {
-                            if (!wait(&sh->h_full[h], ph)) break;
-                            const uint32_t dv = dh0 + ((h * kTile) >> 4), pcol = scol + 32 * y;
-                            const uint32_t acc = (tp >= (alt ? 2 : 1) || y) ? 1u : 0u;
-                            if (leader) {
-                                attn2::mma_ts(ocol, pcol, dv, kIdescPV, acc);
+                        if (mine) {
+                            if (!wait(&sh->p_full[s], pp)) break;
+                            pp ^= 1u;
+                        }
+#pragma unroll 1
+                        for (int y = 0; y < halves; ++y) {
+                            if (!wait(&sh->h_full[hs], hp)) break;
+                            const uint32_t dv = dh0 + ((hs * kTile) >> 4), pcol = scol + 32 * y;
+                            uint32_t acc = tp >= lag || y ? 1u : 0u;
+                            if (mine && leader) {
 #pragma unroll
-                                for (int k = 1; k < kHalfKeys / 16; ++k)
-                                    attn2::mma_ts(ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, 1u);
+                                for (int k = 0; k < kHalfKeys / 16; ++k) {
+                                    attn2::mma_ts(ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
+                                    acc = 1u;
+                                }
+                                umma_commit(s32(&sh->h_empty[hs]));
+                                if (y == halves - 1 && tp + lag >= n) umma_commit(s32(&sh->o_full[s]));
+                            } else if (leader) {
+                                mbar_arrive(s32(&sh->h_empty[hs]));
                             }
-                            if (both_done) commit(&sh->h_empty[h]);
-                            if (++h == kHalves) { h = 0; ph ^= 1u; }
+                            if (++hs == kHalves) { hs = 0; hp ^= 1u; }
                         }
                         if (!ok) break;
-                        if (both_done) { hs = h; hp = ph; }
-                        if (tp + (alt ? 2 : 1) >= n) commit(&sh->o_full[s]);
                     }
                     if (t < n) {
-                        if (t < (alt ? 2 : 1)) {
-                            if (!wait(&sh->q_full[s], qph >> s)) break;
-                            qph ^= 1u << s;
+                        if (mine && t < lag) {
+                            if (!wait(&sh->q_full[s], qp)) break;
+                            qp ^= 1u;
                         }
                         if (!wait(&sh->k_full[ks], kp)) break;
-                        const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
-                        if (leader) {
+                        const uint32_t dk = dk0 + ((ks * kTile) >> 4);
+                        if (mine && leader) {
 #pragma unroll
                             for (int d = 0; d < 2; ++d)                   // both digits of Q
 #pragma unroll
                                 for (int k = 0; k < kHeadDim / 32; ++k)
                                     attn2::mma_ss<true>(scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
+                            umma_commit(s32(&sh->s_full[s]));
+                            umma_commit(s32(&sh->k_empty[ks]));
+                        } else if (leader) {
+                            mbar_arrive(s32(&sh->k_empty[ks]));
                         }
-                        commit(&sh->s_full[s]);
-                        if (both_done) {
-                            commit(&sh->k_empty[ks]);
-                            if (++ks == kKStages) { ks = 0; kp ^= 1u; }
-                        }
+                        if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                     }
                 }
             }
             if (leader) {
-                umma_commit(s32(&sh->drain));
-                mbar_wait(s32(&sh->drain), 0u, abort_flag, /*honour_abort=*/false);
+                umma_commit(s32(&sh->drain[s]));
+                attn2::wait_drain(&sh->drain[s]);
             }
         } else if (warp == 3) {
             // ---------------- the cut ----------------
@@ -534,30 +530,26 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         uint32_t tiles_done = 0, units_done = 0, merges = 0, trees = 0;
         int bits = 0;
 
-        struct Row {                                      // this thread's row of a unit
-            int b, head, pair, t0, n, tree, L, alt, part;
-            int r;                                        // row of the (sequence, head), node * G + g; -1: nobody's
-            unsigned long long anc;
-            float sc;                                     // S to log2 units, without the key's scale
-        };
-        // the i-th unit, its Q digits written; false at the end
-        auto begin_unit = [&](int i, Row& w) {
+        // Everything that a unit is stays in shared memory until its output is written; this thread
+        // keeps its row (node * G + g, -1: nobody's), the row's ancestors and its factor from S to
+        // log2 units, without the key's scale.
+        int row_of = -1, alt = 0;
+        unsigned long long anc = 0;
+        float sc = 0.f;
+        // the i-th unit: its Q digits; false at the end
+        auto begin_unit = [&](int i, int& row_next, unsigned long long& anc_next, float& sc_next) {
             const Unit* up = next_unit(i);
             if (!__all_sync(0xffffffffu, up != nullptr)) return false;
-            w.b = up->b; w.head = up->head; w.pair = up->pair; w.t0 = up->t0; w.n = up->n; w.tree = up->tree;
-            w.L = up->L; w.alt = up->split_keys; w.part = up->part;
-            const int r = w.pair * 2 * kRows + (w.alt ? 0 : slot * kRows) + row;
-            w.r = r < a.n * a.G ? r : -1;
-            const int node = w.r < 0 ? 0 : r / a.G;
-            w.anc = up->anc[node];
-            __syncwarp();
-            if (lane == 0) unit_read(i);
+            const int r = up->pair * 2 * kRows + (up->split_keys ? 0 : slot * kRows) + row;
+            row_next = r < a.n * a.G ? r : -1;
+            const int node = row_next < 0 ? 0 : r / a.G;
+            anc_next = up->anc[node];
             // a slot without a tile leaves Q (and its barrier) alone: it could be units ahead
-            if (w.n <= (w.alt ? slot : 0)) return true;
+            if (up->n <= (up->split_keys ? slot : 0)) return true;
             // every QK of this slot's last unit has completed (its S was read): Q may be replaced.
             // The warp makes its 32 rows' digits together, two rows at once, sixteen lanes a row.
-            const int my_off = w.r < 0 ? -1 : node * a.Hq + (r - node * a.G);
-            const uint16_t* src = a.q + ((int64_t)w.b * a.n * a.Hq + w.head * a.G) * kHeadDim + (lane & 15) * 8;
+            const int my_off = row_next < 0 ? -1 : node * a.Hq + (r - node * a.G);
+            const uint16_t* src = a.q + ((int64_t)up->b * a.n * a.Hq + up->head * a.G) * kHeadDim + (lane & 15) * 8;
             uint8_t* dst = sQ + slot * 2 * kTile;
             int e_mine = 0;
 #pragma unroll 1
@@ -568,18 +560,19 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     const int off = __shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4));
                     v[k] = off >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim)) : make_uint4(0u, 0u, 0u, 0u);
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
-                    const int rr = r0 + 2 * k + (lane >> 4), e = row_exp(v[k], -40), at = (warp & 3) * 32 + rr;
+                    const int rr = r0 + 2 * k + (lane >> 4), e = row_exp(v[0], -40), at = (warp & 3) * 32 + rr;
                     uint32_t hi[2], lo[2];
-                    digits8(v[k], kv8::exp2i(-e), hi, lo);
+                    digits8(v[0], kv8::exp2i(-e), hi, lo);
                     *reinterpret_cast<uint2*>(dst + swz(at, 8 * (lane & 15))) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
                     const int e_of = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);      // of row r0 + 2 k + (lane & 1)
                     if ((lane >> 1) == (r0 >> 1) + k) e_mine = e_of;
+                    v[0] = v[1]; v[1] = v[2]; v[2] = v[3];               // the loop's body exists once
                 }
             }
-            w.sc = a.scale_log2 * kv8::exp2i(e_mine);
+            sc_next = a.scale_log2 * kv8::exp2i(e_mine);
             attn2::fence_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(s32(&sh->q_full[slot]));
@@ -588,15 +581,17 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 
         // Per unit: the Q digits of the next one go in, so that its first products can run during
         // this one's output; then this one's output; then the next one's tiles.
-        Row w{};
         bool have = true, ok = true, idle = true;
         float mref = 0.f;
         uint64_t l2 = 0;                                                 // two partial sums of the weights
         int mine = 0;                                                    // tiles of this slot
         for (int i = 0; have && ok; ++i) {
-            Row next;
-            have = begin_unit(i, next);
+            int row_next = -1;
+            unsigned long long anc_next = 0;
+            float sc_next = 0.f;
+            have = begin_unit(i, row_next, anc_next, sc_next);
             if (i > 0) {
+                const Unit* u = &sh->info[(i - 1) % kInfo];
                 if (mine > 0) {
                     const bool got = attn2::wait_for(&sh->o_full[slot], units_done & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
@@ -607,9 +602,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 attn2::unf2(l2, la, lb);
                 float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
                 bool use0 = mine > 0, use1 = false;
-                const int c0 = w.alt ? 64 * slot : 0, c1 = w.alt ? c0 + 64 : kHeadDim;
+                const int c0 = alt ? 64 * slot : 0, c1 = alt ? c0 + 64 : kHeadDim;
                 uint32_t a0 = o_addr, a1 = o_addr;
-                if (w.alt) {
+                if (alt) {
                     // both slots hold this row: (m, l) change hands, each slot writes half of the columns
                     sh->ml[slot][row] = make_float2(mref, l);
                     __syncwarp();
@@ -622,16 +617,16 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     w0 = x0.x == -INFINITY ? 0.f : exp2f(x0.x - m);
                     w1 = x1.x == -INFINITY ? 0.f : exp2f(x1.x - m);
                     l = x0.y * w0 + x1.y * w1;
-                    use0 = w.n > 0;
-                    use1 = w.n > 1;
+                    use0 = u->n > 0;
+                    use1 = u->n > 1;
                     a0 = tmem + lane_base + attn2::o_col(0);
                     a1 = tmem + lane_base + attn2::o_col(1);
                 }
                 if (!idle) {
-                    const float inv = w.n == 0 || l == 0.f ? 0.f : 1.f / l;
-                    const int node = w.r < 0 ? 0 : w.r / a.G, g = w.r < 0 ? 0 : w.r % a.G;
-                    uint16_t* out = a.out + (((int64_t)w.b * a.n + node) * a.Hq + w.head * a.G + g) * kHeadDim;
-                    const int64_t place = (int64_t)w.part * a.rows + (w.r - w.pair * 2 * kRows);
+                    const float inv = u->n == 0 || l == 0.f ? 0.f : 1.f / l;
+                    const int node = row_of < 0 ? 0 : row_of / a.G, g = row_of < 0 ? 0 : row_of - node * a.G, part = u->part;
+                    uint16_t* out = a.out + (((int64_t)u->b * a.n + node) * a.Hq + u->head * a.G + g) * kHeadDim;
+                    const int64_t place = (int64_t)part * a.rows + (row_of - u->pair * 2 * kRows);
 #pragma unroll 1
                     for (int c = c0; c < c1; c += 16) {
                         uint32_t o[16], o1[16];
@@ -642,8 +637,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             const float x0 = use0 ? __uint_as_float(o[e]) : 0.f, x1 = use1 ? __uint_as_float(o1[e]) : 0.f;
                             o[e] = __float_as_uint(fmaf(x0, w0, x1 * w1));
                         }
-                        if (w.r < 0) continue;
-                        if (w.part < 0) {
+                        if (row_of < 0) continue;
+                        if (part < 0) {
                             uint32_t y[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
@@ -656,10 +651,10 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                                 *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         }
                     }
-                    if (w.r >= 0 && w.part >= 0 && (!w.alt || slot == 0))
+                    if (row_of >= 0 && part >= 0 && (!alt || slot == 0))
                         a.ws_ml[place] = use0 ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
                 }
-                if (w.alt) {                                                 // O and ml are free again
+                if (alt) {                                                   // O and ml are free again
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s32(&sh->merge_out));
@@ -668,24 +663,29 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     ++merges;
                 }
             }
+            if (i > 0) {
+                __syncwarp();
+                if (lane == 0) unit_read(i - 1);
+            }
             if (!have) break;
-            w = next;
-            idle = !__any_sync(0xffffffffu, w.r >= 0);        // rows are independent: leave P as it is
-            const int64_t sc_at = ((int64_t)w.b * a.Hkv + w.head) * a.NB;
-            const int nc = w.n - w.tree, step = w.alt ? 2 : 1;
+            row_of = row_next;
+            anc = anc_next;
+            sc = sc_next;
+            idle = !__any_sync(0xffffffffu, row_of >= 0);     // rows are independent: leave P as it is
+            const Unit* u = &sh->info[i % kInfo];
+            const int n = u->n, nc = n - u->tree, left0 = u->L - u->t0 * kKeys;     // keys from the unit's first tile on
+            alt = u->split_keys;
             mref = -INFINITY;
             l2 = 0;
             mine = 0;
-            // lanes 0 .. 3 hold the K scales of a tile's blocks, lanes 4 .. 7 the V scales; blocks
-            // without a key before L are not read
-            const float* scales = (lane < kBlocks ? a.k_scale : a.v_scale) + sc_at + (lane & 3);
-            auto load_scale = [&](int t) {
-                const int blk = (w.t0 + t) * kBlocks;
-                return lane < 2 * kBlocks && t < nc && (blk + (lane & 3)) * kKv8Block < w.L ? __ldg(scales + blk) : 1.f;
-            };
-            const int first = w.alt ? slot : 0;
+            // lanes 0 .. 3 (and every lane alike mod 8) hold the K scales of a tile's blocks, lanes
+            // 4 .. 7 the V scales, loaded a tile ahead; blocks without a key take the last one's
+            const float* scales = ((lane & 4) ? a.v_scale : a.k_scale) + ((int64_t)u->b * a.Hkv + u->head) * a.NB + u->t0 * kBlocks;
+            const int last_block = max(u->L - 1, 0) / kKv8Block - u->t0 * kBlocks;
+            auto load_scale = [&](int t) { return __ldg(scales + min(t * kBlocks + (lane & 3), last_block)); };
+            const int first = alt ? slot : 0, step = alt ? 2 : 1;
             float scale = load_scale(first);
-            for (int t = first; t < w.n; t += step, ++mine) {
+            for (int t = first; t < n; t += step, ++mine) {
                 const bool got = attn2::wait_for(&sh->s_full[slot], tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
@@ -701,56 +701,52 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         // the commit behind this QK covers every PV before it: O is complete
                         if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) attn2::rescale_row(o_addr, alpha);
                     };
-                    // Both passes over the scores read them from TMEM, a block of 32 at a time in a
-                    // loop: holding all 128 in registers takes four copies of this code, and
-                    // the instruction caches are what such a kernel runs out of first.
                     if (t < nc) {
-                        const int left = w.L - (w.t0 + t) * kKeys;
-                        const float k_fac = scale;
-                        const int ex = (int)(__float_as_uint(scale) >> 23) - 127;
-                        if (lane >= kBlocks && ex > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
-                        const float inv_ex = kv8::exp2i(min(-ex, 127));
-                        scale = load_scale(t + step);
-                        float x[32];
-                        auto mask = [&](int c) {
-                            if (left < kKv8Block * (c + 1)) {
+                        const int left = left0 - t * kKeys;
+                        uint32_t x[kKeys];
+                        float mb[kBlocks];
+                        attn2::load_row_nowait(s_addr, x, mb);
+                        // a block's factor (above 0, so that a masked block stays -inf) and exponent
+                        float f[kBlocks];
+                        int ev[kBlocks];
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = kKv8Block * c + e < left ? x[e] : -INFINITY;
-                            }
-                        };
-                        // above 0, so that a masked block stays -inf
-                        auto factor = [&](int c) { return fmaxf(__shfl_sync(0xffffffffu, k_fac, c) * w.sc, 1.17549435e-38f); };
-#pragma unroll 1
                         for (int c = 0; c < kBlocks; ++c) {
-                            attn2::load32_nowait(s_addr + 32 * c, x);
-                            const float f = factor(c);
-                            const float ev = (float)__shfl_sync(0xffffffffu, ex, kBlocks + c);
-                            attn2::tmem_wait_ld();
-                            mask(c);
-                            mx = fmaxf(mx, fmaf(attn2::max_of<32>(x), f, ev));
+                            f[c] = fmaxf(__shfl_sync(0xffffffffu, scale, c) * sc, 1.17549435e-38f);
+                            ev[c] = (int)(__float_as_uint(__shfl_sync(0xffffffffu, scale, kBlocks + c)) >> 23) - 127;
+                            if (ev[c] > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
                         }
+                        scale = load_scale(t + step);
+                        attn2::tmem_wait_ld();
+                        if (left < kKeys) {
+#pragma unroll
+                            for (int c = 0; c < kBlocks; ++c) {
+                                float y[kKv8Block];
+#pragma unroll
+                                for (int e = 0; e < kKv8Block; ++e) {
+                                    y[e] = kKv8Block * c + e < left ? __uint_as_float(x[kKv8Block * c + e]) : -INFINITY;
+                                    x[kKv8Block * c + e] = __float_as_uint(y[e]);
+                                }
+                                mb[c] = attn2::max_of<kKv8Block>(y);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < kBlocks; ++c) mx = fmaxf(mx, fmaf(mb[c], f[c], (float)ev[c]));
                         raise();
-#pragma unroll 1
+#pragma unroll
                         for (int c = 0; c < kBlocks; ++c) {
-                            attn2::load32_nowait(s_addr + 32 * c, x);
-                            const float f = factor(c);
-                            const float off = (float)__shfl_sync(0xffffffffu, ex, kBlocks + c) - mref + kOffset;
-                            const float inv = __shfl_sync(0xffffffffu, inv_ex, kBlocks + c);
-                            const uint64_t f_2 = attn2::f2(f, f), off2 = attn2::f2(off, off);
-                            attn2::tmem_wait_ld();
-                            mask(c);
+                            const float off = (float)ev[c] - mref + kOffset, inv = kv8::exp2i(min(-ev[c], 127));
+                            const uint64_t f_2 = attn2::f2(f[c], f[c]), off2 = attn2::f2(off, off);
                             uint64_t acc[2] = {0, 0};
                             uint32_t pk[16];
 #pragma unroll
                             for (int d = 0; d < 16; ++d) {
                                 float s0, s1;
-                                attn2::unf2(attn2::fma2(attn2::f2(x[2 * d], x[2 * d + 1]), f_2, off2), s0, s1);
+                                attn2::unf2(attn2::fma2(attn2::f2(__uint_as_float(x[32 * c + 2 * d]), __uint_as_float(x[32 * c + 2 * d + 1])), f_2, off2), s0, s1);
                                 const float p0 = ex2_approx(s0), p1 = ex2_approx(s1);
                                 acc[d & 1] = attn2::add2(acc[d & 1], attn2::f2(p0, p1));
                                 pk[d] = pack_half2(p0, p1);
                             }
-                            // P over S: columns 16 c on hold scores of blocks that have been read
-                            attn2::tmem_st16_nowait(s_addr + 16 * c, pk);
+                            attn2::tmem_st16_nowait(s_addr + 16 * c, pk);        // P over S
                             l2 = attn2::fma2(attn2::add2(acc[0], acc[1]), attn2::f2(inv, inv), l2);
                         }
                     } else {
@@ -765,12 +761,12 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         for (int c = 0; c < kMaxNodes; c += 16) {
                             attn2::load16(s_addr + c, x);
                             attn2::load16(s_addr + kMaxNodes + c, y);
-                            const uint32_t anc = (uint32_t)(w.anc >> c);
+                            const uint32_t sees = (uint32_t)(anc >> c);
                             float s[16];
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                const float f = fmaxf(sh->k_fac[tr][c + j] * w.sc, 1.17549435e-38f);
-                                s[j] = (anc >> j) & 1u ? fmaf(__uint_as_float(x[j]) + __uint_as_float(y[j]), f, sh->v_exp[tr][c + j])
+                                const float f = fmaxf(sh->k_fac[tr][c + j] * sc, 1.17549435e-38f);
+                                s[j] = (sees >> j) & 1u ? fmaf(__uint_as_float(x[j]) + __uint_as_float(y[j]), f, sh->v_exp[tr][c + j])
                                                        : -INFINITY;
                                 x[j] = __float_as_uint(s[j]);
                             }
@@ -802,7 +798,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s32(&sh->p_full[slot]));
             }
-            trees += w.tree;
+            trees += n - nc;
         }
         if (bits) flag_error(a.dev_status, bits);
     } else {
@@ -840,7 +836,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
                     const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
                     uint8_t* dst = sH + (rh % kHalves) * kTile;
-#pragma unroll 2
+#pragma unroll 1
                     for (int y = 0; y < 4; ++y) {
                         const int key = (cw * 2 + (y >> 1)) * 8 + key8, box = y & 1;
                         uint4 x = *reinterpret_cast<const uint4*>(src + swz(key, (4 * box + c4) * 16));
@@ -871,12 +867,12 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     for (int k = 0; k < 4; ++k)
                         v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim) + (lane & 15))
                                                 : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[k], kv8::kMinExp);
+                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[0], kv8::kMinExp);
                         const float by = kv8::exp2i(-e);
                         if (e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
-                        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
                         uint32_t o[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
@@ -886,6 +882,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             sh->v_exp[trees % kTrees][row] = (float)e;
                             sh->v_inv[trees % kTrees][row] = by;
                         }
+                        v[0] = v[1]; v[1] = v[2]; v[2] = v[3];
                     }
                 }
                 __syncwarp();
