@@ -25,7 +25,7 @@ bool code_map(CUtensorMap* map, const void* x, int Lmax, int64_t slabs) {
 
 // The most positions that the cut can have, or -1 from 2^31 on.
 int64_t kv8_positions(int B, int rows, int Hkv, int Lmax) {
-    const int64_t rt = (rows + kv8_tc::kRows - 1) / kv8_tc::kRows, tiles = (Lmax + kv8_tc::kKeys - 1) / kv8_tc::kKeys + 1;
+    const int64_t rt = (rows + kv8_tc::kRows - 1) / kv8_tc::kRows, tiles = (Lmax + kv8_tc::kKeys - 1) / kv8_tc::kKeys + 1 + kv8_tc::kUnitCost;
     const int64_t units = (int64_t)B * Hkv;
     if (units > 0x7fffffffLL || units * rt > 0x7fffffffLL || units * rt * tiles > 0x7fffffffLL) return -1;
     return units * rt * tiles;

@@ -29,8 +29,8 @@
 // A unit that is cut leaves partial (m, l, O) in the workspace, at most two per CTA; a second
 // small kernel merges them.
 //
-// Roles: warp 0 loads K and V tiles and makes the K digits of the tree's rows, warps 1 and 2 issue
-// the MMAs of slots 0 and 1, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
+// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 2 makes the K digits of the tree's
+// rows, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
 // digits of the next unit before it writes this one's output, warps 12-15 widen V into a ring of
 // half tiles of 64 keys; rows behind the last key become zeros there (whatever bits lie in them:
 // a zero weight does not cancel NaN).
@@ -57,6 +57,7 @@ constexpr int kHalfKeys = 64, kHalfBox = kHalfKeys * 128;     // 64 keys x 64 di
 constexpr int kInfo = 3;                          // units in flight between the roles
 constexpr int kTrees = 8;                         // trees in flight, see Shared
 constexpr int kBlocks = kKeys / kKv8Block;        // scales per tile
+constexpr int kUnitCost = 3;                      // what a unit costs beside its tiles, in tiles
 constexpr float kOffset = 6.f, kRescale = 8.f;    // weights up to 2^14
 constexpr int kMaxVExp = 44;                      // V scales up to 2^44, see below
 constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles
@@ -80,7 +81,8 @@ struct Args {
 
 // ---------------- the cut: shared by the attention and the merging kernel ----------------
 // Positions: sequence by sequence, head by head, row-tile pair by pair, tile by tile; a tile of a
-// pair counts 2, of a single row tile 1.  The host refuses sizes with 2^31 positions or more.
+// pair counts 2, of a single row tile 1, and a unit's first tile kUnitCost tiles more (its digits,
+// its output).  The host refuses sizes with 2^31 positions or more.
 struct Cut {
     int total;                                    // positions
     int ctas;                                     // pieces
@@ -95,7 +97,7 @@ __device__ __forceinline__ int row_tiles(const Args& a) { return (a.n * a.G + kR
 // Warp-wide.
 __device__ __forceinline__ Cut make_cut(const Args& a, int grid) {
     int sum = 0;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) sum += tiles_of(a, b);
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) sum += tiles_of(a, b) + kUnitCost;
     sum = __reduce_add_sync(0xffffffffu, sum);
     Cut c;
     const int rt = row_tiles(a);
@@ -111,8 +113,10 @@ struct Segment {
     int start;                                    // position of its first tile
     int t0, t1;
 };
-// Tiles of a unit that begins at `start` before position pos.
-__device__ __forceinline__ int tiles_before(int start, int weight, int pos) { return (pos - start + weight - 1) >> (weight - 1); }
+// Tiles of a unit that begins at `start` whose own position lies before pos.
+__device__ __forceinline__ int tiles_before(int start, int weight, int pos) {
+    return pos <= start ? 0 : max(1, ((pos - start + weight - 1) >> (weight - 1)) - kUnitCost);
+}
 
 // Warp-wide: the unit at position pos; `b`, `base`: a sequence at or before it and its first
 // position, moved on.
@@ -120,7 +124,7 @@ __device__ __forceinline__ Segment segment_at(const Args& a, int pos, int end, i
     const int rt = row_tiles(a), lane = threadIdx.x & 31;
     for (;;) {                                    // 32 sequences at a time
         const int mine = b + lane;
-        const int w = mine < a.B ? tiles_of(a, mine) * rt * a.Hkv : 0;
+        const int w = mine < a.B ? (tiles_of(a, mine) + kUnitCost) * rt * a.Hkv : 0;
         int sum = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -142,14 +146,14 @@ __device__ __forceinline__ Segment segment_at(const Args& a, int pos, int end, i
     s.b = b;
     s.T = tiles_of(a, b);
     int off = pos - base;
-    const int per_head = s.T * rt;
+    const int per_tile = s.T + kUnitCost, per_head = per_tile * rt;
     s.head = off / per_head;
     off -= s.head * per_head;
-    s.pair = off / (2 * s.T);
-    off -= s.pair * 2 * s.T;
+    s.pair = off / (2 * per_tile);
+    off -= s.pair * 2 * per_tile;
     s.weight = min(2, rt - 2 * s.pair);
     s.start = pos - off;
-    s.t0 = tiles_before(s.start, s.weight, pos);
+    s.t0 = min(s.T, tiles_before(s.start, s.weight, pos));
     s.t1 = min(s.T, tiles_before(s.start, s.weight, end));
     return s;
 }
@@ -167,12 +171,12 @@ struct Unit {
 };
 
 struct Shared {
-    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t k_full[kKStages], k_empty[kKStages], k_grant[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHalves], h_empty[kHalves];
     uint64_t q_full[kSlots], s_full[kSlots], p_full[kSlots], o_full[kSlots];
     uint64_t tree_full[kTrees], merge_in, merge_out;
     uint64_t info_full[kInfo], info_empty[kInfo];
-    uint64_t drain[kSlots];
+    uint64_t drain;
     uint32_t tmem;
     int abort_flag;
     float2 ml[kSlots][kRows];
@@ -241,6 +245,11 @@ __device__ __forceinline__ float amax8(const uint4& x) {
     return __uint_as_float(m << 16);
 }
 
+// The 256 bytes of a row, asked into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];\n prefetch.global.L2 [%0 + 128];\n" ::"l"(p) : "memory");
+}
+
 // Warp-wide: of two rows at once, sixteen lanes a row, the exponent of each lane's row.
 __device__ __forceinline__ int row_exp(const uint4& v, int lo_exp) {
     float m = amax8(v);
@@ -263,21 +272,21 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 1); mbar_init(s32(&sh->k_empty[i]), kSlots); }
+        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 1); mbar_init(s32(&sh->k_empty[i]), 1); mbar_init(s32(&sh->k_grant[i]), 1); }
         for (int i = 0; i < kVStages; ++i) { mbar_init(s32(&sh->v_full[i]), 1); mbar_init(s32(&sh->v_empty[i]), 4); }
-        for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), kSlots); }
+        for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(s32(&sh->q_full[s]), 4);
             mbar_init(s32(&sh->s_full[s]), 1);
             mbar_init(s32(&sh->p_full[s]), 4);
             mbar_init(s32(&sh->o_full[s]), 1);
         }
-        for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 5);       // warp 0, the widening warps
+        for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 5);       // warp 2, the widening warps
         mbar_init(s32(&sh->merge_in), 8);
         mbar_init(s32(&sh->merge_out), 8);
-        // read by warp 0, the two MMA, the eight softmax and the four widening warps
+        // read by warps 0 to 2, the eight softmax and the four widening warps
         for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 15); }
-        for (int s = 0; s < kSlots; ++s) mbar_init(s32(&sh->drain[s]), 1);
+        mbar_init(s32(&sh->drain), 1);
         sh->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -298,73 +307,104 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     if (warp < 4) {
         attn2::regs_dec<kRegsOther>();
         if (warp == 0) {
-            // ---------------- K and V tiles; K digits of the tree's rows ----------------
-            uint32_t ks = 0, kp = 1, vs = 0, vp = 1, trees = 0;
-            for (int i = 0;; ++i) {
+            // ---------------- K and V tiles ----------------
+            uint32_t ks = 0, kp = 1, vs = 0, vp = 1;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
-                const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree;
+                const int t0 = up->t0, nc = up->n - up->tree, tree = up->tree, z = up->b * a.Hkv + up->head;
                 __syncwarp();
                 if (lane == 0) unit_read(i);
-                bool ok = true;
 #pragma unroll 1
                 for (int j = 0; ok && j < nc; ++j) {
                     const bool k_free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
                     ok = __all_sync(0xffffffffu, k_free);
                     if (ok && lane == 0) {
                         mbar_expect_tx(s32(&sh->k_full[ks]), kTile);
-                        tma_load_3d(s32(sK + ks * kTile), &map_k, s32(&sh->k_full[ks]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
+                        tma_load_3d(s32(sK + ks * kTile), &map_k, s32(&sh->k_full[ks]), 0, (t0 + j) * kKeys, z);
                     }
                     if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                     const bool v_free = ok && attn2::wait_for(&sh->v_empty[vs], vp, abort_flag);
                     ok = __all_sync(0xffffffffu, v_free);
                     if (ok && lane == 0) {
                         mbar_expect_tx(s32(&sh->v_full[vs]), kTile);
-                        tma_load_3d(s32(sV + vs * kTile), &map_v, s32(&sh->v_full[vs]), 0, (t0 + j) * kKeys, b * a.Hkv + head);
+                        tma_load_3d(s32(sV + vs * kTile), &map_v, s32(&sh->v_full[vs]), 0, (t0 + j) * kKeys, z);
                     }
                     if (++vs == kVStages) { vs = 0; vp ^= 1u; }
                 }
-                if (!ok) break;
-                if (tree) {
-                    const bool got = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    uint8_t* tile = sK + ks * kTile;
-                    const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
-#pragma unroll 1
-                    for (int r0 = lane >> 4; r0 < kMaxNodes; r0 += 8) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim) + (lane & 15))
-                                                    : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[0], -40);
-                            uint32_t hi[2], lo[2];
-                            digits8(v[0], kv8::exp2i(-e), hi, lo);
-                            *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
-                            if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e);
-                            v[0] = v[1]; v[1] = v[2]; v[2] = v[3];       // the loop's body exists once
-                        }
-                    }
-                    attn2::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
-                        mbar_arrive(s32(&sh->k_full[ks]));
-                    }
-                    ++trees;
+                if (ok && tree) {
+                    // the tree's stage is warp 2's to fill.  It does not follow the ring, and a
+                    // parity names a phase only to a waiter that is at most one behind, so the
+                    // stage is handed over when it is free
+                    const bool free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
+                    ok = __all_sync(0xffffffffu, free);
+                    if (ok && lane == 0) mbar_arrive(s32(&sh->k_grant[ks]));
                     if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
             }
-        } else if (warp == 1 || warp == 2) {
+        } else if (warp == 2) {
+            // ---------------- K digits of the tree's rows ----------------
+            uint32_t r = 0, trees = 0, grants = 0;        // uses of the K ring before the unit; a phase bit per stage
+            for (int i = 0;; ++i) {
+                const Unit* up = next_unit(i);
+                if (!__all_sync(0xffffffffu, up != nullptr)) break;
+                const int nc = up->n - up->tree, tree = up->tree;
+                const uint16_t* x = a.k_tree + ((int64_t)up->b * a.n * a.Hkv + up->head) * kHeadDim + (lane & 15) * 8;
+                __syncwarp();
+                if (lane == 0) unit_read(i);
+                r += nc;
+                if (!tree) continue;
+                const uint32_t ks = r % kKStages;
+                uint8_t* tile = sK + ks * kTile;
+                bool free = false;
+                // rows from n on are left as they are: no key of theirs is ever seen
+#pragma unroll 1
+                for (int r0 = lane >> 4; r0 < a.n + (lane >> 4); r0 += 16) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim))
+                                                : make_uint4(0u, 0u, 0u, 0u);
+                    if (!free) {
+                        const bool got = attn2::wait_for(&sh->k_grant[ks], grants >> ks, abort_flag);
+                        if (!__all_sync(0xffffffffu, got)) break;
+                        free = true;
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[0], -40);
+                        uint32_t hi[2], lo[2];
+                        digits8(v[0], kv8::exp2i(-e), hi, lo);
+                        if (row < kMaxNodes) {
+                            *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
+                            if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 7; ++y) v[y] = v[y + 1];     // the loop's body exists once
+                    }
+                }
+                if (!free) break;
+                grants ^= 1u << ks;
+                attn2::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
+                    mbar_arrive(s32(&sh->k_full[ks]));
+                }
+                ++trees;
+                ++r;
+            }
+        } else if (warp == 1) {
             // ---------------- MMA issue ----------------
-            // Warp 1 + s issues slot s's products: one warp alone spends longer on its control than
-            // the tensor cores on the products.  Both run the same code.
-            const int s = attn2::uniform_of(warp - 1);
+            // One warp for both slots, whose products then stay together in the tensor pipe; one
+            // copy of the code for both slots and both ways of dealing tiles.  Loads are waited for
+            // before P is; from P's arrival on nothing is.
             const bool leader = attn2::elect_lane();
-            uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qp = 0, pp = 0;      // ring places and phases
+            const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
+            const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
+            uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;    // ring places, phases
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 const bool got = attn2::wait_for(bar, parity, abort_flag);
@@ -372,75 +412,77 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 tc_fence_after();
                 return ok;
             };
-            const uint32_t scol = (uint32_t)attn2::uniform_of((int)tmem) + (uint32_t)(s << 7), ocol = scol + 256;
-            const uint32_t dq = attn2::desc_lo(s32(sQ)) + ((2 * s * kTile) >> 4), dk0 = attn2::desc_lo(s32(sK));
-            const uint32_t dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
                 const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);
-                const int alt = attn2::uniform_of(up->split_keys);
+                const int alt = attn2::uniform_of(up->split_keys), lag = alt ? 2 : 1;
                 __syncwarp();
                 if (lane == 0) unit_read(i);
-                // Step t: O += P V of tile t - lag, then S = Q K^T of tile t.  Two row tiles: every
-                // tile is both slots'; one: tile t is slot t & 1's, and the other slot only lets
-                // it pass.  A stage is free when both slots have said so.
-                const int lag = alt ? 2 : 1;
+                // step x is slot x & 1's: O += P V of tile tp, then S = Q K^T of tile t.  Two row
+                // tiles: both slots see every tile, t = x / 2 and tp the one before.  One: tile t
+                // is slot t & 1's, t = x and tp two before.
+                const int steps = n == 0 ? 0 : alt ? n + 2 : 2 * n + 2;
 #pragma unroll 1
-                for (int t = 0; ok && n > 0 && t < n + lag; ++t) {
-                    const int tp = t - lag;
-                    const bool mine = !alt || (t & 1) == s;               // tiles t and t - lag
-                    if (tp >= 0) {
-                        const int halves = tp < nc ? 2 : 1;               // the tree's tile is one half
-                        if (mine) {
-                            if (!wait(&sh->p_full[s], pp)) break;
-                            pp ^= 1u;
-                        }
+                for (int x = 0; ok && x < steps; ++x) {
+                    const int s = x & 1, t = alt ? x : x >> 1, tp = t - lag;
+                    const bool pv = tp >= 0 && tp < n, qk = t < n, two = tp < nc;         // the tree's tile is one half
+                    const bool opens = alt || !s, closes = alt || s;      // the tiles' first, last use
+                    const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
+                    const uint32_t h1 = hs + 1 == kHalves ? 0 : hs + 1;
+                    if (opens) {
+                        if (pv && !wait(&sh->h_full[hs], hp)) break;
+                        if (pv && two && !wait(&sh->h_full[h1], hp ^ (h1 == 0))) break;
+                        if (qk && !wait(&sh->k_full[ks], kp)) break;
+                    }
+                    if (qk && t < lag) {
+                        if (!wait(&sh->q_full[s], qph >> s)) break;
+                        qph ^= 1u << s;
+                    }
+                    if (pv) {
+                        if (!wait(&sh->p_full[s], pph >> s)) break;
+                        pph ^= 1u << s;
+                    }
+                    if (leader) {
+                        if (pv) {
+                            uint32_t acc = tp >= lag ? 1u : 0u;
 #pragma unroll 1
-                        for (int y = 0; y < halves; ++y) {
-                            if (!wait(&sh->h_full[hs], hp)) break;
-                            const uint32_t dv = dh0 + ((hs * kTile) >> 4), pcol = scol + 32 * y;
-                            uint32_t acc = tp >= lag || y ? 1u : 0u;
-                            if (mine && leader) {
+                            for (int y = 0; y <= (int)two; ++y) {
+                                const uint32_t dv = dh0 + (((y ? h1 : hs) * kTile) >> 4), pcol = scol + 32 * y;
 #pragma unroll
                                 for (int k = 0; k < kHalfKeys / 16; ++k) {
                                     attn2::mma_ts(ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
                                     acc = 1u;
                                 }
-                                umma_commit(s32(&sh->h_empty[hs]));
-                                if (y == halves - 1 && tp + lag >= n) umma_commit(s32(&sh->o_full[s]));
-                            } else if (leader) {
-                                mbar_arrive(s32(&sh->h_empty[hs]));
                             }
-                            if (++hs == kHalves) { hs = 0; hp ^= 1u; }
                         }
-                        if (!ok) break;
-                    }
-                    if (t < n) {
-                        if (mine && t < lag) {
-                            if (!wait(&sh->q_full[s], qp)) break;
-                            qp ^= 1u;
-                        }
-                        if (!wait(&sh->k_full[ks], kp)) break;
-                        const uint32_t dk = dk0 + ((ks * kTile) >> 4);
-                        if (mine && leader) {
+                        if (qk) {
+                            const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
 #pragma unroll
                             for (int d = 0; d < 2; ++d)                   // both digits of Q
 #pragma unroll
                                 for (int k = 0; k < kHeadDim / 32; ++k)
                                     attn2::mma_ss<true>(scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
                             umma_commit(s32(&sh->s_full[s]));
-                            umma_commit(s32(&sh->k_empty[ks]));
-                        } else if (leader) {
-                            mbar_arrive(s32(&sh->k_empty[ks]));
                         }
-                        if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                        if (pv && tp + lag >= n) umma_commit(s32(&sh->o_full[s]));
+                        if (closes && pv) {
+                            umma_commit(s32(&sh->h_empty[hs]));
+                            if (two) umma_commit(s32(&sh->h_empty[h1]));
+                        }
+                        if (closes && qk) umma_commit(s32(&sh->k_empty[ks]));
                     }
+                    if (closes && pv) {
+                        if (two && h1 == 0) hp ^= 1u;
+                        hs = two ? h1 : hs;
+                        if (++hs == kHalves) { hs = 0; hp ^= 1u; }
+                    }
+                    if (closes && qk && ++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
             }
             if (leader) {
-                umma_commit(s32(&sh->drain[s]));
-                attn2::wait_drain(&sh->drain[s]);
+                umma_commit(s32(&sh->drain));
+                attn2::wait_drain(&sh->drain);
             }
         } else if (warp == 3) {
             // ---------------- the cut ----------------
@@ -457,7 +499,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 have = false;
                 while (!have && pos < end) {
                     s = segment_at(a, pos, end, b, base);
-                    pos = s.start + s.weight * s.T;
+                    pos = s.start + s.weight * (s.T + kUnitCost);
                     have = s.t0 < s.t1;
                 }
                 const bool got = attn2::wait_for(&sh->info_empty[i % kInfo], (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
@@ -496,6 +538,14 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #pragma unroll
                             for (int h = 0; h < 2; ++h) { anc[h] |= add[h]; p[h] = up[h]; }
                         }
+                    }
+                    // the unit's rows of Q and of the tree go into L2 meanwhile
+                    const char* qr = reinterpret_cast<const char*>(a.q + ((int64_t)s.b * a.n * a.Hq + s.head * a.G) * kHeadDim);
+                    const int64_t tree_at = ((int64_t)s.b * a.n * a.Hkv + s.head) * kHeadDim;
+                    for (int y = lane; y < a.n; y += 32) {
+                        prefetch_l2(a.k_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
+                        prefetch_l2(a.v_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
+                        for (int g = 0; g < a.G; ++g) prefetch_l2(qr + ((int64_t)y * a.Hq + g) * kHeadDim * 2);
                     }
                     const int L = a.kv_len[s.b];
                     const bool bad_len = L < 0 || L > a.Lmax;
@@ -552,16 +602,17 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             const uint16_t* src = a.q + ((int64_t)up->b * a.n * a.Hq + up->head * a.G) * kHeadDim + (lane & 15) * 8;
             uint8_t* dst = sQ + slot * 2 * kTile;
             int e_mine = 0;
+            const int count = __popc(__ballot_sync(0xffffffffu, row_next >= 0));   // rows of this warp that exist, its first ones
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 8) {
-                uint4 v[4];
+            for (int r0 = 0; r0 < count; r0 += 16) {
+                uint4 v[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const int off = __shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4));
                     v[k] = off >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim)) : make_uint4(0u, 0u, 0u, 0u);
                 }
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const int rr = r0 + 2 * k + (lane >> 4), e = row_exp(v[0], -40), at = (warp & 3) * 32 + rr;
                     uint32_t hi[2], lo[2];
                     digits8(v[0], kv8::exp2i(-e), hi, lo);
@@ -569,7 +620,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
                     const int e_of = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);      // of row r0 + 2 k + (lane & 1)
                     if ((lane >> 1) == (r0 >> 1) + k) e_mine = e_of;
-                    v[0] = v[1]; v[1] = v[2]; v[2] = v[3];               // the loop's body exists once
+#pragma unroll
+                    for (int y = 0; y < 7; ++y) v[y] = v[y + 1];         // the loop's body exists once
                 }
             }
             sc_next = a.scale_log2 * kv8::exp2i(e_mine);
