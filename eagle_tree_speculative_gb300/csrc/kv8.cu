@@ -39,9 +39,9 @@ __device__ __forceinline__ int write_block(const Cache& c, int kv, int64_t slab,
     uint4 x[kKv8Block / 2];
 #pragma unroll
     for (int s = 0; s < kKv8Block / 2; ++s) {
-        const int t = 2 * s + half;
-        x[s] = make_uint4(0u, 0u, 0u, 0u);
-        if (t < m) x[s] = __ldg(reinterpret_cast<const uint4*>(src(t)) + col);
+        // a row behind the last is the last one again: its magnitudes count once more, which changes
+        // nothing, and the loads need no condition (under one each waits for the one before)
+        x[s] = __ldg(reinterpret_cast<const uint4*>(src(min(2 * s + half, m - 1))) + col);
     }
     // the largest finite magnitude, as the bits of a bf16 (magnitudes order like integers);
     // an exponent of all ones is an infinity or a NaN and does not count

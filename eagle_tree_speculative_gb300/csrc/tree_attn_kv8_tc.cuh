@@ -29,10 +29,9 @@
 // A unit that is cut leaves partial (m, l, O) in the workspace, at most two per CTA; a second
 // small kernel merges them.
 //
-// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 2 makes the K digits of the tree's
-// rows, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
+// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
 // digits of the next unit before it writes this one's output, warps 12-15 widen V into a ring of
-// half tiles of 64 keys; rows behind the last key become zeros there (whatever bits lie in them:
+// half tiles of 64 keys and make the K digits of the tree's rows; rows behind the last key become zeros there (whatever bits lie in them:
 // a zero weight does not cancel NaN).
 #pragma once
 
@@ -272,7 +271,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 1); mbar_init(s32(&sh->k_empty[i]), 1); mbar_init(s32(&sh->k_grant[i]), 1); }
+        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 4); mbar_init(s32(&sh->k_empty[i]), 1); mbar_init(s32(&sh->k_grant[i]), 1); }
         for (int i = 0; i < kVStages; ++i) { mbar_init(s32(&sh->v_full[i]), 1); mbar_init(s32(&sh->v_empty[i]), 4); }
         for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
         for (int s = 0; s < kSlots; ++s) {
@@ -281,11 +280,11 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             mbar_init(s32(&sh->p_full[s]), 4);
             mbar_init(s32(&sh->o_full[s]), 1);
         }
-        for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 5);       // warp 2, the widening warps
+        for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 4);
         mbar_init(s32(&sh->merge_in), 8);
         mbar_init(s32(&sh->merge_out), 8);
-        // read by warps 0 to 2, the eight softmax and the four widening warps
-        for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 15); }
+        // read by warps 0 and 1, the eight softmax and the four widening warps
+        for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 14); }
         mbar_init(s32(&sh->drain), 1);
         sh->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -320,6 +319,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 for (int j = 0; ok && j < nc; ++j) {
                     const bool k_free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
                     ok = __all_sync(0xffffffffu, k_free);
+                    if (ok && lane > 0 && lane < 4) mbar_arrive(s32(&sh->k_full[ks]));    // four arrivals, as for the tree's
                     if (ok && lane == 0) {
                         mbar_expect_tx(s32(&sh->k_full[ks]), kTile);
                         tma_load_3d(s32(sK + ks * kTile), &map_k, s32(&sh->k_full[ks]), 0, (t0 + j) * kKeys, z);
@@ -334,67 +334,14 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     if (++vs == kVStages) { vs = 0; vp ^= 1u; }
                 }
                 if (ok && tree) {
-                    // the tree's stage is warp 2's to fill.  It does not follow the ring, and a
-                    // parity names a phase only to a waiter that is at most one behind, so the
-                    // stage is handed over when it is free
+                    // the tree's stage is the widening warps' to fill.  They do not follow this
+                    // ring, and a parity names a phase only to a waiter that is at most one
+                    // behind, so the stage is handed over when it is free
                     const bool free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
                     ok = __all_sync(0xffffffffu, free);
                     if (ok && lane == 0) mbar_arrive(s32(&sh->k_grant[ks]));
                     if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
-            }
-        } else if (warp == 2) {
-            // ---------------- K digits of the tree's rows ----------------
-            uint32_t r = 0, trees = 0, grants = 0;        // uses of the K ring before the unit; a phase bit per stage
-            for (int i = 0;; ++i) {
-                const Unit* up = next_unit(i);
-                if (!__all_sync(0xffffffffu, up != nullptr)) break;
-                const int nc = up->n - up->tree, tree = up->tree;
-                const uint16_t* x = a.k_tree + ((int64_t)up->b * a.n * a.Hkv + up->head) * kHeadDim + (lane & 15) * 8;
-                __syncwarp();
-                if (lane == 0) unit_read(i);
-                r += nc;
-                if (!tree) continue;
-                const uint32_t ks = r % kKStages;
-                uint8_t* tile = sK + ks * kTile;
-                bool free = false;
-                // rows from n on are left as they are: no key of theirs is ever seen
-#pragma unroll 1
-                for (int r0 = lane >> 4; r0 < a.n + (lane >> 4); r0 += 16) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim))
-                                                : make_uint4(0u, 0u, 0u, 0u);
-                    if (!free) {
-                        const bool got = attn2::wait_for(&sh->k_grant[ks], grants >> ks, abort_flag);
-                        if (!__all_sync(0xffffffffu, got)) break;
-                        free = true;
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[0], -40);
-                        uint32_t hi[2], lo[2];
-                        digits8(v[0], kv8::exp2i(-e), hi, lo);
-                        if (row < kMaxNodes) {
-                            *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
-                            if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e);
-                        }
-#pragma unroll
-                        for (int y = 0; y < 7; ++y) v[y] = v[y + 1];     // the loop's body exists once
-                    }
-                }
-                if (!free) break;
-                grants ^= 1u << ks;
-                attn2::fence_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
-                    mbar_arrive(s32(&sh->k_full[ks]));
-                }
-                ++trees;
-                ++r;
             }
         } else if (warp == 1) {
             // ---------------- MMA issue ----------------
@@ -608,20 +555,28 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 uint4 v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int off = __shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4));
-                    v[k] = off >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim)) : make_uint4(0u, 0u, 0u, 0u);
+                    // a row that does not exist takes the first one's place in the load: loads
+                    // under a condition each wait for the one before
+                    const int off = max(__shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4)), 0);
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim));
                 }
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
-                    const int rr = r0 + 2 * k + (lane >> 4), e = row_exp(v[0], -40), at = (warp & 3) * 32 + rr;
-                    uint32_t hi[2], lo[2];
-                    digits8(v[0], kv8::exp2i(-e), hi, lo);
-                    *reinterpret_cast<uint2*>(dst + swz(at, 8 * (lane & 15))) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
-                    const int e_of = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);      // of row r0 + 2 k + (lane & 1)
-                    if ((lane >> 1) == (r0 >> 1) + k) e_mine = e_of;
+                for (int k = 0; k < 8; k += 4) {                         // four row pairs at once, to hide their latencies
+                    int e[4];
 #pragma unroll
-                    for (int y = 0; y < 7; ++y) v[y] = v[y + 1];         // the loop's body exists once
+                    for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int rr = r0 + 2 * (k + y) + (lane >> 4), at = (warp & 3) * 32 + rr;
+                        uint32_t hi[2], lo[2];
+                        digits8(v[y], kv8::exp2i(-e[y]), hi, lo);
+                        *reinterpret_cast<uint2*>(dst + swz(at, 8 * (lane & 15))) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
+                        const int e_of = __shfl_sync(0xffffffffu, e[y], (lane & 1) << 4);   // of row r0 + 2 (k + y) + (lane & 1)
+                        if ((lane >> 1) == (r0 >> 1) + k + y) e_mine = e_of;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) v[y] = v[y + 4];         // the loop's body exists once
                 }
             }
             sc_next = a.scale_log2 * kv8::exp2i(e_mine);
@@ -860,7 +815,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         // this lane's key of a group of eight and 16-byte chunk of four: the eight lanes of a
         // shared-memory phase read and write all 32 banks, under both tiles' swizzles
         const int key8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
-        uint32_t r = 0, rh = 0, trees = 0;
+        uint32_t r = 0, rh = 0, rk = 0, trees = 0, grants = 0;   // uses of the rings; a phase bit per K stage
         int bits = 0;
         bool ok = true;
         auto ready = [&](uint64_t* bar, uint32_t parity) {
@@ -888,12 +843,15 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
                     const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
                     uint8_t* dst = sH + (rh % kHalves) * kTile;
-#pragma unroll 1
+                    uint4 x[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        x[y] = *reinterpret_cast<const uint4*>(src + swz((cw * 2 + (y >> 1)) * 8 + key8, (4 * (y & 1) + c4) * 16));
+#pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         const int key = (cw * 2 + (y >> 1)) * 8 + key8, box = y & 1;
-                        uint4 x = *reinterpret_cast<const uint4*>(src + swz(key, (4 * box + c4) * 16));
-                        if (h * kHalfKeys + key >= left) x = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        const bool there = h * kHalfKeys + key < left;
+                        const uint32_t w[4] = {there ? x[y].x : 0u, there ? x[y].y : 0u, there ? x[y].z : 0u, there ? x[y].w : 0u};
                         uint32_t o[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -908,7 +866,44 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(s32(&sh->v_empty[st]));
             }
+            rk += nc;
             if (ok && tree) {
+                const uint32_t ks = rk++ % kKStages;
+                {
+                    // K: digits.  Rows from n on are left as they are: no key of theirs is ever seen.
+                    uint8_t* tile = sK + ks * kTile;
+                    const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim + (lane & 15) * 8;
+                    const int r0 = cw * 16 + (lane >> 4);
+                    uint4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
+                    if (!ready(&sh->k_grant[ks], grants >> ks)) break;
+                    grants ^= 1u << ks;
+#pragma unroll 1
+                    for (int k = 0; k < 8; k += 4) {                     // four row pairs at once, to hide their latencies
+                        int e[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int row = r0 + 2 * (k + y), c = lane & 15;
+                            uint32_t hi[2], lo[2];
+                            digits8(v[y], kv8::exp2i(-e[y]), hi, lo);
+                            if (row < a.n) {
+                                *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
+                                *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
+                                if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e[y]);
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) v[y] = v[y + 4];     // the loop's body exists once
+                    }
+                    attn2::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s32(&sh->k_full[ks]));
+                }
+                // V
                 if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
                 uint8_t* dst = sH + (rh % kHalves) * kTile;
                 const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
@@ -917,14 +912,14 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        v[k] = r0 + 2 * k < a.n ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(r0 + 2 * k) * a.Hkv * kHeadDim) + (lane & 15))
-                                                : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
+                        v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim) + (lane & 15));
+#pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[0], kv8::kMinExp);
+                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[k], kv8::kMinExp);
                         const float by = kv8::exp2i(-e);
-                        if (e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
-                        const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                        if (row < a.n && e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
+                        const bool there = row < a.n;                    // zeros behind the tree's rows
+                        const uint32_t w[4] = {there ? v[k].x : 0u, there ? v[k].y : 0u, there ? v[k].z : 0u, there ? v[k].w : 0u};
                         uint32_t o[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
@@ -934,7 +929,6 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             sh->v_exp[trees % kTrees][row] = (float)e;
                             sh->v_inv[trees % kTrees][row] = by;
                         }
-                        v[0] = v[1]; v[1] = v[2]; v[2] = v[3];
                     }
                 }
                 __syncwarp();
