@@ -54,6 +54,21 @@ __device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, v
     return true;
 }
 
+// Arrival and commit of one lane, `on`, without a branch: warps that part for a lane's instruction
+// and meet again lose 200 to 300 cycles here.
+__device__ __forceinline__ void arrive_if(bool on, const uint64_t* bar) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(s32(bar)),
+                 "r"((uint32_t)on)
+                 : "memory");
+}
+__device__ __forceinline__ void commit_if(bool on, const uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(s32(bar)),
+        "r"((uint32_t)on)
+        : "memory");
+}
+
 // The end of an MMA thread: its own products, which always end, have left the tensor cores.
 __device__ __forceinline__ void wait_drain(const uint64_t* bar) {
     int never = 0;
@@ -80,27 +95,30 @@ __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t lbo) {
     return ((saddr >> 4) & 0x3fffu) | (((lbo >> 4) & 0x3fffu) << 16);
 }
 
-// D (+)= A B with A and B in shared memory (SS) or A in TMEM (TS); kind::f16 or kind::f8f6f4.
+// D (+)= A B with A and B in shared memory (SS) or A in TMEM (TS); kind::f16 or kind::f8f6f4.  Issued
+// by the lane that is `on`, without a branch.
 template <bool F8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     if constexpr (F8)
         asm volatile(
-            "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n"
-            " mov.b64 b, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n}\n" ::"r"(d),
-            "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate)
+            "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n"
+            " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+            " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate), "r"(on)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n"
-            " mov.b64 b, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
-            "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate)
+            "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n"
+            " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+            " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate), "r"(on)
             : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
-        "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %6, 0;\n mov.b64 b, {%2, %3};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(idesc), "r"(accumulate), "r"(on)
         : "memory");
 }
 

@@ -207,7 +207,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         u = sh->info[i % kInfo];
         return u.head >= 0;
     };
-    auto unit_read = [&](int i) { mbar_arrive(s32(&sh->info_empty[i % kInfo])); };
+    auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, &sh->info_empty[i % kInfo]); };
 
     if (warp < 4) {
         attn2::regs_dec<kRegsRole>();
@@ -255,6 +255,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // phase), barrier phases as bits: nothing here may live in local memory, which has next
             // to no L1 beside this much shared memory.
             const bool leader = attn2::elect_lane();
+            const uint32_t on = leader;
             const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
             const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sR)), dv0 = attn2::desc_lo_mn(s32(sR), kBox);
             uint32_t qph = 0, pph = 0;
@@ -266,7 +267,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tc_fence_after();
                 return ok;
             };
-            auto commit = [&](uint64_t* bar) { if (leader) umma_commit(s32(bar)); };
             auto advance = [&](uint32_t& st, uint32_t& ph) {      // K and V tiles take turns in the ring
                 st += 2;
                 if (st >= kStages) { st -= kStages; ph ^= 1u; }
@@ -274,55 +274,47 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             for (int i = 0; ok; ++i) {
                 Unit u;
                 if (!__all_sync(0xffffffffu, next_unit(i, u))) break;
-                if (lane == 0) unit_read(i);
+                unit_read(i);
                 const int n0 = attn2::uniform_of(u.tiles[0]), n1 = attn2::uniform_of(u.tiles[1]), n = max(n0, n1);
                 // step x: slot s = x & 1, O += P V of tile j - 1, then S = Q K^T of tile j = x / 2
                 const int steps = n > 0 ? 2 * n + 2 : 0;
                 for (int x = 0; ok && x < steps; ++x) {
                     const int s = x & 1, j = x >> 1, ns = s ? n1 : n0;
+                    const bool pv = j > 0 && j <= ns, qk = j < ns;
                     const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                    if (j > 0) {
-                        if (!wait(&sh->full[vs], vp)) break;
-                        if (j <= ns) {
-                            if (!wait(&sh->p_full[s], pph >> s)) break;
-                            pph ^= 1u << s;
-                            const uint32_t dv = dv0 + ((vs * kTile) >> 4);
-                            const uint32_t acc = j > 1 ? 1u : 0u;
-                            if (leader) {
-                                attn2::mma_ts(ocol, scol, dv, kIdescPV, acc);
+                    if (s == 0 && j > 0 && !wait(&sh->full[vs], vp)) break;
+                    if (pv) {
+                        if (!wait(&sh->p_full[s], pph >> s)) break;
+                        pph ^= 1u << s;
+                        const uint32_t dv = dv0 + ((vs * kTile) >> 4);
+                        uint32_t acc = j > 1 ? 1u : 0u;
 #pragma unroll
-                                for (int k = 1; k < kKeys / 16; ++k)
-                                    attn2::mma_ts(ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, 1u);
-                            }
-                            if (j == ns) commit(&sh->o_full[s]);
-                        }
-                        if (s) {
-                            commit(&sh->empty[vs]);
-                            advance(vs, vp);
+                        for (int k = 0; k < kKeys / 16; ++k) {
+                            attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
+                            acc = 1u;
                         }
                     }
-                    if (j < n) {
-                        if (!wait(&sh->full[ks], kp)) break;
-                        if (j < ns) {
-                            if (j == 0) {
-                                if (!wait(&sh->q_full[s], qph >> s)) break;
-                                qph ^= 1u << s;
-                            }
-                            const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((s * kTile) >> 4);
-                            if (leader) {
+                    if (s == 0 && j < n && !wait(&sh->full[ks], kp)) break;
+                    if (qk) {
+                        if (j == 0) {
+                            if (!wait(&sh->q_full[s], qph >> s)) break;
+                            qph ^= 1u << s;
+                        }
+                        const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((s * kTile) >> 4);
 #pragma unroll
-                                for (int k = 0; k < kHeadDim / 16; ++k) {
-                                    const uint32_t at = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                                    attn2::mma_ss<false>(scol, dq + at, dk + at, kIdescQK, k > 0 ? 1u : 0u);
-                                }
-                            }
-                            commit(&sh->s_full[s]);
-                            if (j == ns - 1) commit(&sh->q_empty[s]);
+                        for (int k = 0; k < kHeadDim / 16; ++k) {
+                            const uint32_t at = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                            attn2::mma_ss<false>(on, scol, dq + at, dk + at, kIdescQK, k > 0 ? 1u : 0u);
                         }
-                        if (s) {
-                            commit(&sh->empty[ks]);
-                            advance(ks, kp);
-                        }
+                        attn2::commit_if(leader, &sh->s_full[s]);
+                    }
+                    attn2::commit_if(leader && pv && j == ns, &sh->o_full[s]);
+                    attn2::commit_if(leader && qk && j == ns - 1, &sh->q_empty[s]);
+                    attn2::commit_if(leader && s && j > 0, &sh->empty[vs]);
+                    attn2::commit_if(leader && s && j < n, &sh->empty[ks]);
+                    if (s) {
+                        if (j > 0) advance(vs, vp);
+                        if (j < n) advance(ks, kp);
                     }
                 }
             }
@@ -336,7 +328,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             Unit u;
             for (int i = 0;; ++i) {
                 if (!__all_sync(0xffffffffu, next_unit(i, u))) break;
-                if (lane == 0) unit_read(i);
+                unit_read(i);
                 const int n = max(u.tiles[0], u.tiles[1]);
                 r += 2 * n;
                 if (!needs_fix(u, n)) continue;
@@ -350,7 +342,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         make_uint4(0u, 0u, 0u, 0u);
                 attn2::fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->full[st]));
+                attn2::arrive_if(lane == 0, &sh->full[st]);
             }
         } else if (warp == 3) {
             // ---------------- which units ----------------
@@ -400,7 +392,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         Unit u;
         for (int i = 0; ok; ++i) {
             if (!__all_sync(0xffffffffu, next_unit(i, u))) break;
-            if (lane == 0) unit_read(i);
+            unit_read(i);
             const int pos = u.pos + slot * a.P + p;
             const bool valid = in_tile && pos < u.nq;
             // keys 0 .. seen - 1 are visible; a row of nobody sees all, its result is not used
@@ -460,7 +452,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->p_full[slot]));
+                attn2::arrive_if(lane == 0, &sh->p_full[slot]);
             }
             if (!ok) break;
             if (n > 0) {

@@ -301,7 +301,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         const Unit* u = &sh->info[i % kInfo];
         return u->head >= 0 ? u : nullptr;
     };
-    auto unit_read = [&](int i) { mbar_arrive(s32(&sh->info_empty[i % kInfo])); };
+    auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, &sh->info_empty[i % kInfo]); };
 
     if (warp < 4) {
         attn2::regs_dec<kRegsOther>();
@@ -314,7 +314,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
                 const int t0 = up->t0, nc = up->n - up->tree, tree = up->tree, z = up->b * a.Hkv + up->head;
                 __syncwarp();
-                if (lane == 0) unit_read(i);
+                unit_read(i);
 #pragma unroll 1
                 for (int j = 0; ok && j < nc; ++j) {
                     const bool k_free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
@@ -349,6 +349,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             // copy of the code for both slots and both ways of dealing tiles.  Loads are waited for
             // before P is; from P's arrival on nothing is.
             const bool leader = attn2::elect_lane();
+            const uint32_t on = leader;
             const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
             const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
             uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;    // ring places, phases
@@ -365,7 +366,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);
                 const int alt = attn2::uniform_of(up->split_keys), lag = alt ? 2 : 1;
                 __syncwarp();
-                if (lane == 0) unit_read(i);
+                unit_read(i);
                 // step x is slot x & 1's: O += P V of tile tp, then S = Q K^T of tile t.  Two row
                 // tiles: both slots see every tile, t = x / 2 and tp the one before.  One: tile t
                 // is slot t & 1's, t = x and tp two before.
@@ -390,35 +391,31 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         if (!wait(&sh->p_full[s], pph >> s)) break;
                         pph ^= 1u << s;
                     }
-                    if (leader) {
-                        if (pv) {
-                            uint32_t acc = tp >= lag ? 1u : 0u;
+                    if (pv) {
+                        uint32_t acc = tp >= lag ? 1u : 0u;
 #pragma unroll 1
-                            for (int y = 0; y <= (int)two; ++y) {
-                                const uint32_t dv = dh0 + (((y ? h1 : hs) * kTile) >> 4), pcol = scol + 32 * y;
+                        for (int y = 0; y <= (int)two; ++y) {
+                            const uint32_t dv = dh0 + (((y ? h1 : hs) * kTile) >> 4), pcol = scol + 32 * y;
 #pragma unroll
-                                for (int k = 0; k < kHalfKeys / 16; ++k) {
-                                    attn2::mma_ts(ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
-                                    acc = 1u;
-                                }
+                            for (int k = 0; k < kHalfKeys / 16; ++k) {
+                                attn2::mma_ts(on, ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
+                                acc = 1u;
                             }
                         }
-                        if (qk) {
-                            const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
-#pragma unroll
-                            for (int d = 0; d < 2; ++d)                   // both digits of Q
-#pragma unroll
-                                for (int k = 0; k < kHeadDim / 32; ++k)
-                                    attn2::mma_ss<true>(scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
-                            umma_commit(s32(&sh->s_full[s]));
-                        }
-                        if (pv && tp + lag >= n) umma_commit(s32(&sh->o_full[s]));
-                        if (closes && pv) {
-                            umma_commit(s32(&sh->h_empty[hs]));
-                            if (two) umma_commit(s32(&sh->h_empty[h1]));
-                        }
-                        if (closes && qk) umma_commit(s32(&sh->k_empty[ks]));
                     }
+                    if (qk) {
+                        const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
+#pragma unroll
+                        for (int d = 0; d < 2; ++d)                       // both digits of Q
+#pragma unroll
+                            for (int k = 0; k < kHeadDim / 32; ++k)
+                                attn2::mma_ss<true>(on, scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
+                        attn2::commit_if(leader, &sh->s_full[s]);
+                    }
+                    attn2::commit_if(leader && pv && tp + lag >= n, &sh->o_full[s]);
+                    attn2::commit_if(leader && closes && pv, &sh->h_empty[hs]);
+                    attn2::commit_if(leader && closes && pv && two, &sh->h_empty[h1]);
+                    attn2::commit_if(leader && closes && qk, &sh->k_empty[ks]);
                     if (closes && pv) {
                         if (two && h1 == 0) hp ^= 1u;
                         hs = two ? h1 : hs;
@@ -512,7 +509,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->info_full[i % kInfo]));
+                attn2::arrive_if(lane == 0, &sh->info_full[i % kInfo]);
             }
             if (bits) flag_error(a.dev_status, bits);
         }
@@ -582,7 +579,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             sc_next = a.scale_log2 * kv8::exp2i(e_mine);
             attn2::fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s32(&sh->q_full[slot]));
+            attn2::arrive_if(lane == 0, &sh->q_full[slot]);
             return true;
         };
 
@@ -615,7 +612,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     // both slots hold this row: (m, l) change hands, each slot writes half of the columns
                     sh->ml[slot][row] = make_float2(mref, l);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(s32(&sh->merge_in));
+                    attn2::arrive_if(lane == 0, &sh->merge_in);
                     const bool got = attn2::wait_for(&sh->merge_in, merges & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     tc_fence_after();
@@ -664,7 +661,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 if (alt) {                                                   // O and ml are free again
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(s32(&sh->merge_out));
+                    attn2::arrive_if(lane == 0, &sh->merge_out);
                     const bool got = attn2::wait_for(&sh->merge_out, merges & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     ++merges;
@@ -672,7 +669,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             }
             if (i > 0) {
                 __syncwarp();
-                if (lane == 0) unit_read(i - 1);
+                unit_read(i - 1);
             }
             if (!have) break;
             row_of = row_next;
@@ -803,7 +800,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->p_full[slot]));
+                attn2::arrive_if(lane == 0, &sh->p_full[slot]);
             }
             trees += n - nc;
         }
@@ -826,7 +823,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         auto half_done = [&]() {
             attn2::fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s32(&sh->h_full[rh % kHalves]));
+            attn2::arrive_if(lane == 0, &sh->h_full[rh % kHalves]);
             ++rh;
         };
         for (int i = 0; ok; ++i) {
@@ -834,7 +831,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (!__all_sync(0xffffffffu, up != nullptr)) break;
             const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree, L = up->L;
             __syncwarp();
-            if (lane == 0) unit_read(i);
+            unit_read(i);
             for (int j = 0; j < nc; ++j, ++r) {
                 const int st = r % kVStages, left = L - (t0 + j) * kKeys;
                 if (!ready(&sh->v_full[st], r / kVStages)) break;
@@ -864,7 +861,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     half_done();
                 }
                 if (!ok) break;
-                if (lane == 0) mbar_arrive(s32(&sh->v_empty[st]));
+                attn2::arrive_if(lane == 0, &sh->v_empty[st]);
             }
             rk += nc;
             if (ok && tree) {
@@ -901,7 +898,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                     attn2::fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(s32(&sh->k_full[ks]));
+                    attn2::arrive_if(lane == 0, &sh->k_full[ks]);
                 }
                 // V
                 if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
@@ -932,7 +929,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(s32(&sh->tree_full[trees % kTrees]));
+                attn2::arrive_if(lane == 0, &sh->tree_full[trees % kTrees]);
                 ++trees;
                 half_done();
             }
