@@ -261,12 +261,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             uint32_t qph = 0, pph = 0;
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // places of the next K and V tile
             bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = attn2::wait_for(bar, parity, abort_flag);
-                ok = __all_sync(0xffffffffu, got);
-                tc_fence_after();
-                return ok;
-            };
+            // (a wait that gives up lets the step run on, on data that nobody will use)
+            auto wait = [&](uint64_t* bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
             auto advance = [&](uint32_t& st, uint32_t& ph) {      // K and V tiles take turns in the ring
                 st += 2;
                 if (st >= kStages) { st -= kStages; ph ^= 1u; }
@@ -278,14 +274,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int n0 = attn2::uniform_of(u.tiles[0]), n1 = attn2::uniform_of(u.tiles[1]), n = max(n0, n1);
                 // step x: slot s = x & 1, O += P V of tile j - 1, then S = Q K^T of tile j = x / 2
                 const int steps = n > 0 ? 2 * n + 2 : 0;
-                for (int x = 0; ok && x < steps; ++x) {
+#pragma unroll 1
+                for (int x = 0; x < steps && __all_sync(0xffffffffu, ok); ++x) {
                     const int s = x & 1, j = x >> 1, ns = s ? n1 : n0;
                     const bool pv = j > 0 && j <= ns, qk = j < ns;
                     const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                    if (s == 0 && j > 0 && !wait(&sh->full[vs], vp)) break;
+                    if (s == 0 && j > 0) wait(&sh->full[vs], vp);
                     if (pv) {
-                        if (!wait(&sh->p_full[s], pph >> s)) break;
+                        wait(&sh->p_full[s], pph >> s);
                         pph ^= 1u << s;
+                        tc_fence_after();
                         const uint32_t dv = dv0 + ((vs * kTile) >> 4);
                         uint32_t acc = j > 1 ? 1u : 0u;
 #pragma unroll
@@ -294,12 +292,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             acc = 1u;
                         }
                     }
-                    if (s == 0 && j < n && !wait(&sh->full[ks], kp)) break;
+                    if (s == 0 && j < n) wait(&sh->full[ks], kp);
                     if (qk) {
                         if (j == 0) {
-                            if (!wait(&sh->q_full[s], qph >> s)) break;
+                            wait(&sh->q_full[s], qph >> s);
                             qph ^= 1u << s;
                         }
+                        tc_fence_after();
                         const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((s * kTile) >> 4);
 #pragma unroll
                         for (int k = 0; k < kHeadDim / 16; ++k) {
@@ -412,7 +411,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     attn2::load_row_nowait(s_addr, x, m4);
                     const int left = seen - j * kKeys;
                     attn2::tmem_wait_ld();
-                    if (left < kKeys) {
+                    if (__any_sync(0xffffffffu, left < kKeys)) {
                         float y[kKeys];
 #pragma unroll
                         for (int c = 0; c < kKeys; ++c) {
@@ -423,14 +422,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         m4[1] = m4[2] = m4[3] = m4[0];
                     }
                     const float mx = fmaxf(attn2::max3(m4[0], m4[1], m4[2]), m4[3]) * sc;    // scale > 0 commutes with max
-                    float alpha = 1.f;
-                    if (mx > mref + kRescale || (mref == -INFINITY && mx > -INFINITY)) {
-                        alpha = exp2f(mref - mx);                        // 0 for the first maximum
-                        mref = mx;
-                        l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
-                    }
+                    // no branches of a lane; the first finite maximum is always above the reference
+                    const bool up = mx > mref + kRescale;
+                    const float alpha = up ? ex2_approx(mref - mx) : 1.f;            // 0 for the first one
+                    mref = up ? mx : mref;
+                    l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
                     // QK(j) was committed after PV(j - 1): O is complete up to tile j - 1
-                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) attn2::rescale_row(o_addr, alpha);
+                    if (j > 0 && __any_sync(0xffffffffu, up)) attn2::rescale_row(o_addr, alpha);
                     const float base = mref == -INFINITY ? 0.f : mref;
                     const uint64_t nb2 = attn2::f2(-base, -base);
                     uint64_t acc[4] = {l2, 0, 0, 0};

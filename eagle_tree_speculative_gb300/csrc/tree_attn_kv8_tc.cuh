@@ -30,8 +30,8 @@
 // small kernel merges them.
 //
 // Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
-// digits of the next unit before it writes this one's output, warps 12-15 widen V into a ring of
-// half tiles of 64 keys and make the K digits of the tree's rows; rows behind the last key become zeros there (whatever bits lie in them:
+// digits of the next unit before it writes this one's output, warps 12-15 widen V into two tiles
+// (of two halves of 64 keys) and make the K digits of the tree's rows; rows behind the last key become zeros there (whatever bits lie in them:
 // a zero weight does not cancel NaN).
 #pragma once
 
@@ -50,7 +50,7 @@ constexpr int kThreads = 512;
 // 4 warpgroups x 128 registers at launch; 56 + 2 x 200 + 56 = 4 x 128
 constexpr int kRegsOther = 56, kRegsSoftmax = 200;
 constexpr int kKStages = 3, kVStages = 2;         // rings of raw tiles
-constexpr int kHalves = 4;                        // ring of half V tiles in fp16
+constexpr int kWide = 2;                          // V tiles in fp16, two halves of 64 keys each
 constexpr int kTile = 128 * 128;                  // 16 KB: a K or V tile, a digit plane of Q, half a V tile in fp16
 constexpr int kHalfKeys = 64, kHalfBox = kHalfKeys * 128;     // 64 keys x 64 dims of fp16
 constexpr int kInfo = 3;                          // units in flight between the roles
@@ -171,7 +171,7 @@ struct Unit {
 
 struct Shared {
     uint64_t k_full[kKStages], k_empty[kKStages], k_grant[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t h_full[kHalves], h_empty[kHalves];
+    uint64_t h_full[kWide], h_empty[kWide];
     uint64_t q_full[kSlots], s_full[kSlots], p_full[kSlots], o_full[kSlots];
     uint64_t tree_full[kTrees], merge_in, merge_out;
     uint64_t info_full[kInfo], info_empty[kInfo];
@@ -186,9 +186,9 @@ struct Shared {
     float v_inv[kTrees][kMaxNodes];               // 2^-ev
     Unit info[kInfo];
 };
-static_assert(kKStages + kSlots < kTrees && kHalves < kTrees, "trees in flight");
+static_assert(kKStages + kSlots < kTrees && kWide < kTrees, "trees in flight");
 
-constexpr int kSmem = kSlots * 2 * kTile + (kKStages + kVStages + kHalves) * kTile + (int)sizeof(Shared) + 1024;
+constexpr int kSmem = kSlots * 2 * kTile + (kKStages + kVStages + 2 * kWide) * kTile + (int)sizeof(Shared) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // tcgen05.mma kind::f8f6f4, A and B e4m3 (format 0), both K-major, D fp32.
@@ -265,15 +265,15 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     uint8_t* sQ = smem;                                   // [slot][hi, lo][16 KB]
     uint8_t* sK = sQ + kSlots * 2 * kTile;                // [kKStages][16 KB]
     uint8_t* sV = sK + kKStages * kTile;                  // [kVStages][16 KB]
-    uint8_t* sH = sV + kVStages * kTile;                  // [kHalves][2 boxes of 64 dims][64 keys][128 B]
-    Shared* sh = reinterpret_cast<Shared*>(sH + kHalves * kTile);
+    uint8_t* sH = sV + kVStages * kTile;                  // [kWide][2 halves][2 boxes of 64 dims][64 keys][128 B]
+    Shared* sh = reinterpret_cast<Shared*>(sH + 2 * kWide * kTile);
     volatile int* abort_flag = &sh->abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 4); mbar_init(s32(&sh->k_empty[i]), 1); mbar_init(s32(&sh->k_grant[i]), 1); }
         for (int i = 0; i < kVStages; ++i) { mbar_init(s32(&sh->v_full[i]), 1); mbar_init(s32(&sh->v_empty[i]), 4); }
-        for (int i = 0; i < kHalves; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
+        for (int i = 0; i < kWide; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(s32(&sh->q_full[s]), 4);
             mbar_init(s32(&sh->s_full[s]), 1);
@@ -354,12 +354,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
             uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;    // ring places, phases
             bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = attn2::wait_for(bar, parity, abort_flag);
-                ok = __all_sync(0xffffffffu, got);
-                tc_fence_after();
-                return ok;
-            };
+            // (a wait that gives up lets the step run on, on data that nobody will use)
+            auto wait = [&](uint64_t* bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
@@ -372,38 +368,35 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 // is slot t & 1's, t = x and tp two before.
                 const int steps = n == 0 ? 0 : alt ? n + 2 : 2 * n + 2;
 #pragma unroll 1
-                for (int x = 0; ok && x < steps; ++x) {
+                for (int x = 0; x < steps && __all_sync(0xffffffffu, ok); ++x) {
                     const int s = x & 1, t = alt ? x : x >> 1, tp = t - lag;
-                    const bool pv = tp >= 0 && tp < n, qk = t < n, two = tp < nc;         // the tree's tile is one half
+                    const bool pv = tp >= 0 && tp < n, qk = t < n;
                     const bool opens = alt || !s, closes = alt || s;      // the tiles' first, last use
                     const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                    const uint32_t h1 = hs + 1 == kHalves ? 0 : hs + 1;
-                    if (opens) {
-                        if (pv && !wait(&sh->h_full[hs], hp)) break;
-                        if (pv && two && !wait(&sh->h_full[h1], hp ^ (h1 == 0))) break;
-                        if (qk && !wait(&sh->k_full[ks], kp)) break;
-                    }
+                    if (opens && pv) wait(&sh->h_full[hs], hp);
+                    if (opens && qk) wait(&sh->k_full[ks], kp);
                     if (qk && t < lag) {
-                        if (!wait(&sh->q_full[s], qph >> s)) break;
+                        wait(&sh->q_full[s], qph >> s);
                         qph ^= 1u << s;
                     }
                     if (pv) {
-                        if (!wait(&sh->p_full[s], pph >> s)) break;
+                        wait(&sh->p_full[s], pph >> s);
                         pph ^= 1u << s;
-                    }
-                    if (pv) {
+                        tc_fence_after();
+                        const uint32_t dv = dh0 + ((hs * 2 * kTile) >> 4);
                         uint32_t acc = tp >= lag ? 1u : 0u;
-#pragma unroll 1
-                        for (int y = 0; y <= (int)two; ++y) {
-                            const uint32_t dv = dh0 + (((y ? h1 : hs) * kTile) >> 4), pcol = scol + 32 * y;
 #pragma unroll
-                            for (int k = 0; k < kHalfKeys / 16; ++k) {
-                                attn2::mma_ts(on, ocol, pcol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
-                                acc = 1u;
-                            }
+                        for (int k = 0; k < kHalfKeys / 16; ++k) {
+                            attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
+                            acc = 1u;
                         }
+                        const uint32_t on2 = leader && tp < nc;           // the tree's tile is one half
+#pragma unroll
+                        for (int k = 0; k < kHalfKeys / 16; ++k)
+                            attn2::mma_ts(on2, ocol, scol + 32 + 8 * k, dv + ((kTile + k * 16 * 128) >> 4), kIdescPV, 1u);
                     }
                     if (qk) {
+                        tc_fence_after();
                         const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
 #pragma unroll
                         for (int d = 0; d < 2; ++d)                       // both digits of Q
@@ -414,13 +407,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                     attn2::commit_if(leader && pv && tp + lag >= n, &sh->o_full[s]);
                     attn2::commit_if(leader && closes && pv, &sh->h_empty[hs]);
-                    attn2::commit_if(leader && closes && pv && two, &sh->h_empty[h1]);
                     attn2::commit_if(leader && closes && qk, &sh->k_empty[ks]);
-                    if (closes && pv) {
-                        if (two && h1 == 0) hp ^= 1u;
-                        hs = two ? h1 : hs;
-                        if (++hs == kHalves) { hs = 0; hp ^= 1u; }
-                    }
+                    if (closes && pv) { hs ^= 1u; hp ^= hs == 0; }
                     if (closes && qk && ++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
             }
@@ -696,14 +684,15 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 tc_fence_after();
                 if (!idle) {
                     float mx = -INFINITY, alpha = 1.f;
-                    auto raise = [&]() {                                 // the reference maximum, if mx is far above it
-                        if (mx > mref + kRescale || (mref == -INFINITY && mx > -INFINITY)) {
-                            alpha = exp2f(mref - mx);                    // 0 for the first maximum
-                            mref = mx;
-                            l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
-                        }
+                    // raises the reference maximum where mx is far above it (every tile has a visible
+                    // key: mx is finite, and the first one always is above), without branches of a lane
+                    auto raise = [&]() {
+                        const bool up = mx > mref + kRescale;
+                        alpha = up ? ex2_approx(mref - mx) : 1.f;        // 0 for the first maximum
+                        mref = up ? mx : mref;
+                        l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
                         // the commit behind this QK covers every PV before it: O is complete
-                        if (mine > 0 && __any_sync(0xffffffffu, alpha != 1.f)) attn2::rescale_row(o_addr, alpha);
+                        if (mine > 0 && __any_sync(0xffffffffu, up)) attn2::rescale_row(o_addr, alpha);
                     };
                     if (t < nc) {
                         const int left = left0 - t * kKeys;
@@ -820,10 +809,10 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             ok = ok && __all_sync(0xffffffffu, got);
             return ok;
         };
-        auto half_done = [&]() {
+        auto tile_done = [&]() {
             attn2::fence_async_shared();
             __syncwarp();
-            attn2::arrive_if(lane == 0, &sh->h_full[rh % kHalves]);
+            attn2::arrive_if(lane == 0, &sh->h_full[rh % kWide]);
             ++rh;
         };
         for (int i = 0; ok; ++i) {
@@ -835,11 +824,11 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             for (int j = 0; j < nc; ++j, ++r) {
                 const int st = r % kVStages, left = L - (t0 + j) * kKeys;
                 if (!ready(&sh->v_full[st], r / kVStages)) break;
+                if (!ready(&sh->h_empty[rh % kWide], (rh / kWide) ^ 1u)) break;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
                     const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
-                    uint8_t* dst = sH + (rh % kHalves) * kTile;
+                    uint8_t* dst = sH + (rh % kWide * 2 + h) * kTile;
                     uint4 x[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
@@ -858,9 +847,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4)) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    half_done();
                 }
-                if (!ok) break;
+                tile_done();
                 attn2::arrive_if(lane == 0, &sh->v_empty[st]);
             }
             rk += nc;
@@ -901,8 +889,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     attn2::arrive_if(lane == 0, &sh->k_full[ks]);
                 }
                 // V
-                if (!ready(&sh->h_empty[rh % kHalves], (rh / kHalves) ^ 1u)) break;
-                uint8_t* dst = sH + (rh % kHalves) * kTile;
+                if (!ready(&sh->h_empty[rh % kWide], (rh / kWide) ^ 1u)) break;
+                uint8_t* dst = sH + rh % kWide * 2 * kTile;
                 const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
 #pragma unroll 1
                 for (int r0 = cw * 16 + (lane >> 4); r0 < cw * 16 + 16; r0 += 8) {
@@ -931,7 +919,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 __syncwarp();
                 attn2::arrive_if(lane == 0, &sh->tree_full[trees % kTrees]);
                 ++trees;
-                half_done();
+                tile_done();
             }
         }
         if (bits) flag_error(a.dev_status, bits);
