@@ -9,7 +9,9 @@ the optional ``dev_status`` int32 tensor (bits EAGLE_DEV_*).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -272,22 +274,19 @@ def eagle_kv_compact(k_cache, v_cache, kv_len, path, accept_len, max_depth, dev_
 KV8_BLOCK = 32      # cache rows that share a scale (EAGLE_KV8_BLOCK)
 
 
-def _same_device(fn, first, tensors):
-    """Every tensor given must live on `first`'s device."""
-    for t in tensors:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
-
-
-def _on(device, stream):
-    """The context a call launches in: its tensors' device and, where one is given, the
-    stream, so that scratch allocated inside belongs to that stream."""
-    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
-
-
-def _shape(fn, t, name, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{fn}: {name} must be {list(shape)}, got {list(t.shape)}")
+def _args(fn, dev, specs):
+    """Checks (tensor, name, dtype, shape) rows: dense CUDA tensors on device `dev`.  These calls
+    take microseconds on the GPU, so the checks are one pass of cheap tests; what is wrong
+    is worked out only when something is."""
+    for t, name, dtype, shape in specs:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+                or not t.is_contiguous()):
+            _dev(t, name, dtype)
+            if t.shape != shape:
+                raise ValueError(f"{fn}: {name} must be {list(shape)}, got {list(t.shape)}")
+            raise ValueError(f"{fn}: {name} is on {t.device}, other tensors on cuda:{dev}")
 
 
 def _token_rows(fn, t, name):
@@ -295,33 +294,41 @@ def _token_rows(fn, t, name):
     output); returns the token stride in elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{fn}: {name} must be [T, H, d]")
     T, H, d = t.shape
-    dense_heads = t.numel() == 0 or ((d == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == d))
-    if not dense_heads:
+    if t.is_contiguous():
+        return H * d
+    s0, s1, s2 = t.stride()
+    if not ((d == 1 or s2 == 1) and (H == 1 or s1 == d)):
         raise ValueError(f"{fn}: {name}'s heads must be dense within a token")
-    stride = H * d if T <= 1 else t.stride(0)
-    if T > 1 and (stride < H * d or stride % 8 != 0):
+    if T > 1 and (s0 < H * d or s0 % 8 != 0):
         raise ValueError(f"{fn}: {name}'s token stride must be a multiple of 8, at least H * d")
-    return stride
+    return s0 if T > 1 else H * d
 
 
-def _kv8_cache(fn, k8, v8, k_scale, v_scale, lead):
-    """Checks the four arrays of an 8-bit cache; `lead`: its leading dimensions (with
-    Hkv last).  Returns (Lmax, d)."""
-    for t, name in ((k8, "k8"), (v8, "v8")):
-        _dev(t, name, torch.float8_e4m3fn)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _dev(t, name, torch.float32)
-    Lmax, d = k8.shape[-2:]
-    _shape(fn, k8, "k8", (*lead, Lmax, d))
-    _shape(fn, v8, "v8", k8.shape)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _shape(fn, t, name, (*lead, -(-Lmax // KV8_BLOCK)))
-    return Lmax, d
+def _launch(fn, dev, stream, args):
+    """Calls the library on device `dev`, on `stream` or that device's current one."""
+    f = getattr(lib(), fn)
+    if torch._C._cuda_getDevice() == dev:
+        raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, _stream(stream))
+    if code != 0:
+        raise EagleError(fn, code)
+
+
+def _status_ptr(fn, dev, dev_status):
+    if dev_status is None:
+        return None
+    _dev(dev_status, "dev_status", torch.int32)
+    if dev_status.get_device() != dev:
+        raise ValueError(f"{fn}: dev_status is on {dev_status.device}, other tensors on cuda:{dev}")
+    return dev_status.data_ptr()
 
 
 def kv8_cache(n_layers, B, Hkv, Lmax, d=128, device="cuda"):
@@ -333,6 +340,18 @@ def kv8_cache(n_layers, B, Hkv, Lmax, d=128, device="cuda"):
     return (*codes, *scales)
 
 
+def _kv8_specs(k8, v8, k_scale, v_scale, lead, Lmax, d):
+    code, scale = (*lead, Lmax, d), (*lead, -(-Lmax // KV8_BLOCK))
+    return ((k8, "k8", torch.float8_e4m3fn, code), (v8, "v8", torch.float8_e4m3fn, code),
+            (k_scale, "k_scale", torch.float32, scale), (v_scale, "v_scale", torch.float32, scale))
+
+
+def _cache_rows(fn, k8):
+    if not isinstance(k8, torch.Tensor) or k8.dim() < 2:
+        raise TypeError("k8 must be a CUDA tensor")
+    return k8.shape[-2]
+
+
 def eagle_prompt_attn(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, return_lse=False,
                       dev_status=None, stream=None):
     """Causal attention of packed prompts.  q [Tq,Hq,d], k / v [Tk,Hkv,d] bf16 (tokens may
@@ -340,34 +359,32 @@ def eagle_prompt_attn(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, 
     the last positions of its keys.  Returns out [Tq,Hq,d], or (out, lse [Tq,Hq] f32)
     with return_lse or an lse tensor."""
     fn = "eagle_prompt_attn"
-    sq, sk, sv = (_token_rows(fn, t, name) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    sq, sk, sv = _token_rows(fn, q, "q"), _token_rows(fn, k, "k"), _token_rows(fn, v, "v")
     cu_k = cu_q if cu_k is None else cu_k
-    _dev(cu_q, "cu_q", torch.int32)
-    _dev(cu_k, "cu_k", torch.int32)
     Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[:2]
-    B = cu_q.numel() - 1
-    if B < 0 or cu_q.dim() != 1:
+    if k.shape != (Tk, Hkv, d) or v.shape != k.shape:
+        raise ValueError(f"{fn}: k and v must be [Tk, Hkv, {d}]")
+    dev = q.get_device()
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"{fn}: q, k and v are on different devices")
+    _dev(cu_q, "cu_q", torch.int32)
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError(f"{fn}: cu_q must be [B + 1]")
-    _shape(fn, cu_k, "cu_k", cu_q.shape)
-    _shape(fn, k, "k", (Tk, Hkv, d))
-    _shape(fn, v, "v", k.shape)
+    B = cu_q.shape[0] - 1
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    out = torch.empty(Tq, Hq, d, dtype=q.dtype, device=q.device) if out is None else out
-    _dev(out, "out", torch.bfloat16)
-    _shape(fn, out, "out", q.shape)
+        scale = d ** -0.5
+    if out is None:
+        out = torch.empty((Tq, Hq, d), dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty(Tq, Hq, dtype=torch.float32, device=q.device)
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+    _args(fn, dev, ((cu_q, "cu_q", torch.int32, cu_q.shape), (cu_k, "cu_k", torch.int32, cu_q.shape),
+                    (out, "out", torch.bfloat16, q.shape)))
     if lse is not None:
-        _dev(lse, "lse", torch.float32)
-        _shape(fn, lse, "lse", (Tq, Hq))
-    _same_device(fn, q, (k, v, cu_q, cu_k, out, lse, dev_status))
-    with _on(q.device, stream):
-        _check(fn, lib().eagle_prompt_attn(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(out), _ptr(lse), Tq, Tk, B, Hq,
-            Hkv, d, sq, sk, sv, float(scale), _ptr(_status(dev_status, q.device)),
-            _stream(stream)))
+        _args(fn, dev, ((lse, "lse", torch.float32, (Tq, Hq)),))
+    _launch(fn, dev, stream, (
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(),
+        _ptr(lse), Tq, Tk, B, Hq, Hkv, d, sq, sk, sv, scale, _status_ptr(fn, dev, dev_status)))
     return out if lse is None else (out, lse)
 
 
@@ -376,22 +393,19 @@ def eagle_kv8_append(k, v, cu, pos, k8, v8, k_scale, v_scale, dev_status=None, s
     b has rows cu[b] .. cu[b+1]-1) into the cache at rows pos[b] on, in place."""
     fn = "eagle_kv8_append"
     sk, sv = _token_rows(fn, k, "k"), _token_rows(fn, v, "v")
-    _dev(cu, "cu", torch.int32)
-    _dev(pos, "pos", torch.int32)
     T, Hkv, d = k.shape
-    B = pos.numel()
-    _shape(fn, pos, "pos", (B,))
-    _shape(fn, cu, "cu", (B + 1,))
-    _shape(fn, v, "v", k.shape)
-    Lmax, dc = _kv8_cache(fn, k8, v8, k_scale, v_scale, (B, Hkv))
-    if dc != d:
-        raise ValueError(f"{fn}: rows of {d} and a cache of {dc} dimensions")
-    _same_device(fn, k, (v, cu, pos, k8, v8, k_scale, v_scale, dev_status))
-    with _on(k.device, stream):
-        _check(fn, lib().eagle_kv8_append(
-            _ptr(k), _ptr(v), _ptr(cu), _ptr(pos), _ptr(k8), _ptr(v8), _ptr(k_scale),
-            _ptr(v_scale), T, B, Hkv, d, Lmax, sk, sv, _ptr(_status(dev_status, k.device)),
-            _stream(stream)))
+    if v.shape != k.shape:
+        raise ValueError(f"{fn}: v must be {list(k.shape)}, got {list(v.shape)}")
+    _dev(pos, "pos", torch.int32)
+    B, Lmax, dev = pos.numel(), _cache_rows(fn, k8), k.get_device()
+    if v.get_device() != dev:
+        raise ValueError(f"{fn}: k and v are on different devices")
+    _args(fn, dev, ((pos, "pos", torch.int32, (B,)), (cu, "cu", torch.int32, (B + 1,)),
+                    *_kv8_specs(k8, v8, k_scale, v_scale, (B, Hkv), Lmax, d)))
+    _launch(fn, dev, stream, (
+        k.data_ptr(), v.data_ptr(), cu.data_ptr(), pos.data_ptr(), k8.data_ptr(), v8.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), T, B, Hkv, d, Lmax, sk, sv,
+        _status_ptr(fn, dev, dev_status)))
 
 
 def eagle_kv8_commit(k_tree, v_tree, k8, v8, k_scale, v_scale, kv_len, path, accept_len, max_depth,
@@ -400,30 +414,27 @@ def eagle_kv8_commit(k_tree, v_tree, k8, v8, k_scale, v_scale, kv_len, path, acc
     into the cache behind kv_len; kv_len is advanced in place, or into kv_len_out."""
     fn = "eagle_kv8_commit"
     _dev(k_tree, "k_tree", torch.bfloat16)
-    _dev(v_tree, "v_tree", torch.bfloat16)
-    kv_len_out = kv_len if kv_len_out is None else kv_len_out
-    for t, name in ((kv_len, "kv_len"), (kv_len_out, "kv_len_out"), (path, "path"),
-                    (accept_len, "accept_len")):
-        _dev(t, name, torch.int32)
     if k_tree.dim() != 5:
         raise ValueError(f"{fn}: k_tree must be [n_layers, B, n, Hkv, d]")
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
     nl, B, n, Hkv, d = k_tree.shape
-    D = int(max_depth)
-    _shape(fn, v_tree, "v_tree", k_tree.shape)
-    for t, name in ((kv_len, "kv_len"), (kv_len_out, "kv_len_out"), (accept_len, "accept_len")):
-        _shape(fn, t, name, (B,))
-    _shape(fn, path, "path", (B, D + 1))
-    Lmax, dc = _kv8_cache(fn, k8, v8, k_scale, v_scale, (nl, B, Hkv))
-    if dc != d:
-        raise ValueError(f"{fn}: rows of {d} and a cache of {dc} dimensions")
-    _same_device(fn, k_tree, (v_tree, k8, v8, k_scale, v_scale, kv_len, kv_len_out, path,
-                              accept_len, dev_status))
-    with _on(k_tree.device, stream):
-        _check(fn, lib().eagle_kv8_commit(
-            _ptr(k_tree), _ptr(v_tree), _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
-            _ptr(kv_len), _ptr(kv_len_out), _ptr(path), _ptr(accept_len), nl, B, n, Hkv, d, Lmax,
-            D, _ptr(_status(dev_status, k_tree.device)), _stream(stream)))
+    D, Lmax, dev = int(max_depth), _cache_rows(fn, k8), k_tree.get_device()
+    i32 = torch.int32
+    _args(fn, dev, ((v_tree, "v_tree", torch.bfloat16, k_tree.shape),
+                    *_kv8_specs(k8, v8, k_scale, v_scale, (nl, B, Hkv), Lmax, d),
+                    (kv_len, "kv_len", i32, (B,)), (kv_len_out, "kv_len_out", i32, (B,)),
+                    (path, "path", i32, (B, D + 1)), (accept_len, "accept_len", i32, (B,))))
+    _launch(fn, dev, stream, (
+        k_tree.data_ptr(), v_tree.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), kv_len.data_ptr(), kv_len_out.data_ptr(), path.data_ptr(),
+        accept_len.data_ptr(), nl, B, n, Hkv, d, Lmax, D, _status_ptr(fn, dev, dev_status)))
     return kv_len_out
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_attn_kv8_workspace_size(dev, B, n, Hq, Hkv, head_dim, Lmax) -> int:
+    with torch.cuda.device(dev):
+        return int(lib().eagle_tree_attn_kv8_workspace_size(B, n, Hq, Hkv, head_dim, Lmax))
 
 
 def tree_attn_kv8_workspace_size(B, n, Hq, Hkv, head_dim, Lmax) -> int:
@@ -438,38 +449,36 @@ def eagle_tree_attn_kv8(q, k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, par
     fn = "eagle_tree_attn_kv8"
     _dev(q, "q", torch.bfloat16)
     _dev(k_tree, "k_tree", torch.bfloat16)
-    _dev(v_tree, "v_tree", torch.bfloat16)
-    _dev(kv_len, "kv_len", torch.int32)
-    _dev(parent, "parent", torch.int32)
     if q.dim() != 4 or k_tree.dim() != 4:
         raise ValueError(f"{fn}: q must be [B, n, Hq, d] and k_tree [B, n, Hkv, d]")
     B, n, Hq, d = q.shape
-    Hkv = k_tree.shape[2]
-    _shape(fn, k_tree, "k_tree", (B, n, Hkv, d))
-    _shape(fn, v_tree, "v_tree", k_tree.shape)
-    _shape(fn, kv_len, "kv_len", (B,))
-    _shape(fn, parent, "parent", (B, n))
-    Lmax, dc = _kv8_cache(fn, k8, v8, k_scale, v_scale, (B, Hkv))
-    if dc != d:
-        raise ValueError(f"{fn}: rows of {d} and a cache of {dc} dimensions")
+    Hkv, Lmax, dev = k_tree.shape[2], _cache_rows(fn, k8), q.get_device()
+    bf16, tree = torch.bfloat16, (B, n, Hkv, d)
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    out = torch.empty_like(q) if out is None else out
-    _dev(out, "out", torch.bfloat16)
-    _shape(fn, out, "out", q.shape)
-    _same_device(fn, q, (k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, parent, out, workspace,
-                         dev_status))
-    with _on(q.device, stream):
-        need = tree_attn_kv8_workspace_size(B, n, Hq, Hkv, d, Lmax)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if workspace is not None:
-            _dev(workspace, "workspace")
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(fn, lib().eagle_tree_attn_kv8(
-            _ptr(q), _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale), _ptr(k_tree), _ptr(v_tree),
-            _ptr(kv_len), _ptr(parent), _ptr(out), B, n, Hq, Hkv, d, Lmax, float(scale),
-            _ptr(workspace), ws_bytes, _ptr(_status(dev_status, q.device)), _stream(stream)))
+        scale = d ** -0.5
+    if out is None:
+        out = torch.empty_like(q)
+    _args(fn, dev, (*_kv8_specs(k8, v8, k_scale, v_scale, (B, Hkv), Lmax, d),
+                    (k_tree, "k_tree", bf16, tree), (v_tree, "v_tree", bf16, tree),
+                    (kv_len, "kv_len", torch.int32, (B,)), (parent, "parent", torch.int32, (B, n)),
+                    (out, "out", bf16, q.shape)))
+    ws_bytes = 0
+    if workspace is None:
+        ws_bytes = _tree_attn_kv8_workspace_size(dev, B, n, Hq, Hkv, d, Lmax)
+        if ws_bytes:
+            # scratch belongs to the stream that uses it
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    else:
+        _dev(workspace, "workspace")
+        if workspace.get_device() != dev:
+            raise ValueError(f"{fn}: workspace is on {workspace.device}, other tensors on cuda:{dev}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _launch(fn, dev, stream, (
+        q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        k_tree.data_ptr(), v_tree.data_ptr(), kv_len.data_ptr(), parent.data_ptr(), out.data_ptr(),
+        B, n, Hq, Hkv, d, Lmax, scale, _ptr(workspace), ws_bytes,
+        _status_ptr(fn, dev, dev_status)))
     return out
 
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "eagle.h"
 
 namespace eagle {
@@ -111,6 +113,28 @@ inline int device_sm_count() {
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
     return sms;
+}
+
+// The current device's SM count, and a kernel's shared-memory limit raised, each looked up or set
+// once per device (a limit that is set stays set): the calls of a few microseconds notice them.
+inline int cached_sm_count() {
+    static std::atomic<int> sms[16] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return device_sm_count();
+    int n = sms[dev].load(std::memory_order_relaxed);
+    if (n == 0) sms[dev].store(n = device_sm_count(), std::memory_order_relaxed);
+    return n;
+}
+template <auto Kernel>
+inline bool raise_smem_limit(int bytes) {
+    static std::atomic<bool> done[16] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const bool known = dev >= 0 && dev < 16;
+    if (known && done[dev].load(std::memory_order_relaxed)) return true;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (known) done[dev].store(true, std::memory_order_relaxed);
+    return true;
 }
 
 }  // namespace eagle

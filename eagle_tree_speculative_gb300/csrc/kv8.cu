@@ -3,15 +3,16 @@
 //
 // Method.  The unit of work is one scale: the new rows of one block of 32 cache rows, for one
 // (layer, sequence, kv head, K or V).  One warp owns it, so nothing is shared and no atomics
-// order anything: it holds the block's new rows in registers (up to 32 rows of 256 bytes, 16
-// bytes a lane and load, two rows at a time), takes their largest magnitude, the least power
-// of two 2^e with amax <= 448 * 2^e, raises it to the block's present scale if the block holds
-// rows already, and writes x * 2^-e as e4m3.  Where the scale rose, the rows held are read
-// back, multiplied by old / new and rounded again: a power of two, so a code changes only
-// where it becomes subnormal.  Scaling by a power of two is exact in fp32, so each value is
-// rounded once, by the conversion.
+// order anything: it takes the rows' largest magnitude, the least power of two 2^e with amax <=
+// 448 * 2^e, raises it to the block's present scale if the block holds rows already, and writes
+// x * 2^-e as e4m3.  Where the scale rose, the rows held are read back, multiplied by old / new and
+// rounded again: a power of two, so a code changes only where it becomes subnormal.  Scaling by
+// a power of two is exact in fp32, so each value is rounded once, by the conversion.
+// Up to 2 R rows stay in registers (16 bytes a lane and load, two rows at a time) between the
+// maximum and the conversion; more are read twice, the second time from L2.
 //
-// Bound: HBM, 2 bytes read and 1 written per value.
+// Bound: HBM, 2 bytes read and 1 written per value; in practice the latency of a warp's few dependent
+// accesses, so what counts is warps in flight.
 #include "common.cuh"
 #include "kv8_common.cuh"
 
@@ -20,53 +21,69 @@ namespace {
 
 using kv8::kKv8Block;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Cache {
-    uint8_t* code[2];                     // K, V
-    float* scale[2];
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
     int Lmax, NB;
 };
 
-// Writes rows first .. first + m - 1 (all within one block) of the head slab `slab`; `src(t)`
-// is the address of the row that becomes row first + t, 32 lanes x 16 bytes being two rows.
-template <class Src>
-__device__ __forceinline__ int write_block(const Cache& c, int kv, int64_t slab, int first, int m,
-                                           Src src) {
-    const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
-    uint4 x[kKv8Block / 2];
+// The largest finite magnitude of 8 bf16 as its bits (magnitudes order like integers); an
+// exponent of all ones is an infinity or a NaN, does not count and sets `odd`.
+__device__ __forceinline__ uint32_t top8(const uint4& x, bool& odd) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t top = 0u;
 #pragma unroll
-    for (int s = 0; s < kKv8Block / 2; ++s) {
-        // a row behind the last is the last one again: its magnitudes count once more, which changes
-        // nothing, and the loads need no condition (under one each waits for the one before)
-        x[s] = __ldg(reinterpret_cast<const uint4*>(src(min(2 * s + half, m - 1))) + col);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        odd |= max(lo, hi) >= 0x7f80u;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
     }
-    // the largest finite magnitude, as the bits of a bf16 (magnitudes order like integers);
-    // an exponent of all ones is an infinity or a NaN and does not count
+    return top;
+}
+__device__ __forceinline__ uint2 codes8(const uint4& x, float inv) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16) * inv;
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
+    }
+    return make_uint2(kv8::e4m3x4(f[0], f[1], f[2], f[3]), kv8::e4m3x4(f[4], f[5], f[6], f[7]));
+}
+
+// Writes rows first .. first + m - 1 (all within one block) of the head slab `slab`; `src(t)`
+// is the address of the row that becomes row first + t.
+template <int R, class Src>
+__device__ __forceinline__ int write_block(const Cache& c, int kv, int64_t slab, int first, int m, Src src) {
+    const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
+    const int blk = first / kKv8Block, r0 = blk * kKv8Block;
+    float* sp = (kv ? c.v_scale : c.k_scale) + slab * c.NB + blk;
+    uint8_t* rows = (kv ? c.v : c.k) + (slab * c.Lmax + r0) * kHeadDim;
+    const bool held = first > r0;         // the block holds rows r0 .. first - 1
+    const float old = held ? *sp : 0.f;
+    // a row behind the last is the last one again: its magnitudes count once more, which changes
+    // nothing, and the loads need no condition (under one each waits for the one before)
+    uint4 x[R];
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int s = 0; s < R; ++s)
+            x[s] = __ldg(reinterpret_cast<const uint4*>(src(min(t0 + 2 * s + half, m - 1))) + col);
+    };
     uint32_t top = 0u;
     bool odd = false;
+    for (int t0 = 0; t0 < m; t0 += 2 * R) {
+        load(t0);
 #pragma unroll
-    for (int s = 0; s < kKv8Block / 2; ++s) {
-        const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-            if (lo >= 0x7f80u) odd = true; else top = max(top, lo);
-            if (hi >= 0x7f80u) odd = true; else top = max(top, hi);
-        }
+        for (int s = 0; s < R; ++s) top = max(top, top8(x[s], odd));
     }
     top = __reduce_max_sync(kFull, top);
-    int e = kv8::scale_exp(__uint_as_float(top << 16));
-
-    const int blk = first / kKv8Block, r0 = blk * kKv8Block;
-    float* sp = c.scale[kv] + slab * c.NB + blk;
-    uint8_t* rows = c.code[kv] + (slab * c.Lmax + r0) * kHeadDim;
-    float scale = kv8::exp2i(e);
-    if (first > r0) {                     // the block holds rows r0 .. first - 1
-        const float old = *sp;
-        __syncwarp();                     // every lane has read it before it is replaced
+    float scale = kv8::exp2i(kv8::scale_exp(__uint_as_float(top << 16)));
+    if (held) {
+        __syncwarp();                     // every lane has read the scale before it is replaced
         if (old >= scale) {
             scale = old;
         } else {
@@ -87,28 +104,25 @@ __device__ __forceinline__ int write_block(const Cache& c, int kv, int64_t slab,
     }
     if (lane == 0) *sp = scale;
     const float inv = 1.f / scale;        // exact: a power of two
+    for (int t0 = 0; t0 < m; t0 += 2 * R) {
+        if (m > 2 * R) load(t0);
 #pragma unroll
-    for (int s = 0; s < kKv8Block / 2; ++s) {
-        const int t = 2 * s + half;
-        if (t < m) {
-            const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16) * inv;
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
-            }
-            *reinterpret_cast<uint2*>(rows + (int64_t)(first - r0 + t) * kHeadDim + col * 8) =
-                make_uint2(kv8::e4m3x4(f[0], f[1], f[2], f[3]), kv8::e4m3x4(f[4], f[5], f[6], f[7]));
+        for (int s = 0; s < R; ++s) {
+            const int t = t0 + 2 * s + half;
+            const uint2 y = codes8(x[s], inv);
+            if (t < m) *reinterpret_cast<uint2*>(rows + (int64_t)(first - r0 + t) * kHeadDim + col * 8) = y;
         }
     }
     return odd ? EAGLE_DEV_NONFINITE : 0;
 }
 
 // ---------------------------------------------------------------- append
+constexpr int kAppendWarps = 4;
+
 struct AppendArgs {
-    const uint16_t* x[2];                 // K, V rows
-    int64_t stride[2];
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_stride, v_stride;
     const int32_t* cu;
     const int32_t* pos;
     Cache c;
@@ -132,9 +146,10 @@ __device__ __forceinline__ int blocks_of(const AppendArgs& a, int b, int& err, b
     return (p + (c1 - c0) + kKv8Block - 1) / kKv8Block - p / kKv8Block;
 }
 
-// grid (touched blocks, an upper bound; groups of kWarps (head, K|V) units)
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(AppendArgs a) {
-    const int lane = threadIdx.x & 31, unit = blockIdx.y * kWarps + (threadIdx.x >> 5);
+// grid (touched blocks, an upper bound; groups of kAppendWarps (head, K|V) units).  Five CTAs per SM:
+// see the bound above
+__global__ void __launch_bounds__(kAppendWarps * 32, 5) kv8_append_kernel(AppendArgs a) {
+    const int lane = threadIdx.x & 31, unit = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
     // which (sequence, block) this is: the touched blocks counted along the sequences
     int left = (int)blockIdx.x, b = -1, at = 0, err = 0;
     bool bad_cu = false;
@@ -165,15 +180,19 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(AppendArgs a) {
     const int c0 = a.cu[b], end = a.pos[b] + (a.cu[b + 1] - c0), p = a.pos[b];
     const int blk = p / kKv8Block + at;
     const int lo = max(p, blk * kKv8Block), hi = min(end, (blk + 1) * kKv8Block);
-    const uint16_t* x = a.x[kv] + (int64_t)(c0 + lo - p) * a.stride[kv] + h * kHeadDim;
-    const int odd = write_block(a.c, kv, (int64_t)b * a.Hkv + h, lo, hi - lo,
-                                [&](int t) { return x + (int64_t)t * a.stride[kv]; });
+    const int64_t stride = kv ? a.v_stride : a.k_stride;
+    const uint16_t* x = (kv ? a.v : a.k) + (int64_t)(c0 + lo - p) * stride + h * kHeadDim;
+    const int odd = write_block<kKv8Block / 2>(a.c, kv, (int64_t)b * a.Hkv + h, lo, hi - lo,
+                                               [&](int t) { return x + t * stride; });
     if (odd) flag_error(a.dev_status, odd);
 }
 
 // ---------------------------------------------------------------- commit
+constexpr int kCommitWarps = 16;
+
 struct CommitArgs {
-    const uint16_t* x[2];                 // K, V of the tree, [n_layers, B, n, Hkv, 128]
+    const uint16_t* k;                    // of the tree, [n_layers, B, n, Hkv, 128]
+    const uint16_t* v;
     Cache c;
     const int32_t* kv_len;
     int32_t* kv_len_out;
@@ -187,7 +206,7 @@ struct CommitArgs {
 // rows in one to three blocks.  The cluster barrier at the end orders every CTA's read of
 // kv_len[b] before its update.
 template <int CS>
-__global__ void __launch_bounds__(kThreads) kv8_commit_kernel(CommitArgs a) {
+__global__ void __launch_bounds__(kCommitWarps * 32, 2) kv8_commit_kernel(CommitArgs a) {
     __shared__ int s_path[kMaxNodes + 1];
     __shared__ int s_ok;
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -213,13 +232,13 @@ __global__ void __launch_bounds__(kThreads) kv8_commit_kernel(CommitArgs a) {
     if (ok) {
         const int units = a.n_layers * 2 * a.Hkv;
         int odd = 0;
-        for (int u = rank * kWarps + warp; u < units; u += CS * kWarps) {
+        for (int u = rank * kCommitWarps + warp; u < units; u += CS * kCommitWarps) {
             const int h = u % a.Hkv, kv = (u / a.Hkv) & 1;
             const int64_t seq = (int64_t)(u / (2 * a.Hkv)) * a.B + b;          // (layer, sequence)
-            const uint16_t* x = a.x[kv] + (seq * a.n * a.Hkv + h) * kHeadDim;
+            const uint16_t* x = (kv ? a.v : a.k) + (seq * a.n * a.Hkv + h) * kHeadDim;
             for (int lo = L; lo <= L + acc;) {
                 const int hi = min(L + acc + 1, (lo / kKv8Block + 1) * kKv8Block);
-                odd |= write_block(a.c, kv, seq * a.Hkv + h, lo, hi - lo, [&](int t) {
+                odd |= write_block<4>(a.c, kv, seq * a.Hkv + h, lo, hi - lo, [&](int t) {
                     return x + (int64_t)s_path[lo - L + t] * a.Hkv * kHeadDim;
                 });
                 lo = hi;
@@ -260,16 +279,16 @@ extern "C" eagle_status eagle_kv8_append(const void* k, const void* v, const int
     if (!k || !v || !cu || !pos || !k8 || !v8 || !k_scale || !v_scale) return EAGLE_ERR_INVALID_ARG;
     if (misaligned({k, v, k8, v8})) return EAGLE_ERR_INVALID_ARG;
     AppendArgs a{};
-    a.x[0] = static_cast<const uint16_t*>(k);
-    a.x[1] = static_cast<const uint16_t*>(v);
-    a.stride[0] = k_stride; a.stride[1] = v_stride;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.k_stride = k_stride; a.v_stride = v_stride;
     a.cu = cu; a.pos = pos;
-    a.c = Cache{{static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8)}, {k_scale, v_scale}, Lmax,
+    a.c = Cache{static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8), k_scale, v_scale, Lmax,
                 (Lmax + kKv8Block - 1) / kKv8Block};
     a.T = T; a.B = B; a.Hkv = Hkv;
     a.dev_status = dev_status;
-    const dim3 grid((unsigned)blocks, (unsigned)((2 * Hkv + kWarps - 1) / kWarps));
-    kv8_append_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    const dim3 grid((unsigned)blocks, (unsigned)((2 * Hkv + kAppendWarps - 1) / kAppendWarps));
+    kv8_append_kernel<<<grid, kAppendWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     EAGLE_CHECK_LAUNCH();
     return EAGLE_OK;
 }
@@ -291,24 +310,24 @@ extern "C" eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree,
         return EAGLE_ERR_INVALID_ARG;
     if (misaligned({k_tree, v_tree, k8, v8})) return EAGLE_ERR_INVALID_ARG;
     CommitArgs a{};
-    a.x[0] = static_cast<const uint16_t*>(k_tree);
-    a.x[1] = static_cast<const uint16_t*>(v_tree);
-    a.c = Cache{{static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8)}, {k_scale, v_scale}, Lmax,
+    a.k = static_cast<const uint16_t*>(k_tree);
+    a.v = static_cast<const uint16_t*>(v_tree);
+    a.c = Cache{static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8), k_scale, v_scale, Lmax,
                 (Lmax + kKv8Block - 1) / kKv8Block};
     a.kv_len = kv_len; a.kv_len_out = kv_len_out; a.path = path; a.accept_len = accept_len;
     a.n_layers = n_layers; a.B = B; a.n = n; a.Hkv = Hkv; a.D = max_depth;
     a.dev_status = dev_status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // clusters of 8 while every CTA is resident at once, fewer for large batches
-    const int sms = device_sm_count();
+    const int sms = cached_sm_count();
     int cs = 8;
     while (cs > 1 && (int64_t)B * cs > 4LL * sms) cs >>= 1;
     cudaError_t e;
     switch (cs) {
-        case 8: e = launch_clustered(kv8_commit_kernel<8>, B, 8, kThreads, 0, s, a); break;
-        case 4: e = launch_clustered(kv8_commit_kernel<4>, B, 4, kThreads, 0, s, a); break;
-        case 2: e = launch_clustered(kv8_commit_kernel<2>, B, 2, kThreads, 0, s, a); break;
-        default: e = launch_clustered(kv8_commit_kernel<1>, B, 1, kThreads, 0, s, a); break;
+        case 8: e = launch_clustered(kv8_commit_kernel<8>, B, 8, kCommitWarps * 32, 0, s, a); break;
+        case 4: e = launch_clustered(kv8_commit_kernel<4>, B, 4, kCommitWarps * 32, 0, s, a); break;
+        case 2: e = launch_clustered(kv8_commit_kernel<2>, B, 2, kCommitWarps * 32, 0, s, a); break;
+        default: e = launch_clustered(kv8_commit_kernel<1>, B, 1, kCommitWarps * 32, 0, s, a); break;
     }
     return e == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
 }

@@ -75,10 +75,9 @@ extern "C" eagle_status eagle_prompt_attn(const void* q, const void* k, const vo
         return EAGLE_ERR_CUDA;
     // a sequence of m queries has at most m / 2P + 1 units
     const int64_t units = ((int64_t)Tq / (2 * a.P) + B) * Hkv;
-    const int sms = device_sm_count();
+    const int sms = cached_sm_count();
     const unsigned grid = (unsigned)(units < sms ? units : sms);
-    if (cudaFuncSetAttribute(prompt_tc::prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             prompt_tc::kSmem) != cudaSuccess)
+    if (!raise_smem_limit<prompt_tc::prompt_attn_kernel>(prompt_tc::kSmem))
         return EAGLE_ERR_CUDA;
     prompt_tc::prompt_attn_kernel<<<grid, prompt_tc::kThreads, prompt_tc::kSmem,
                                     reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);

@@ -34,7 +34,7 @@ int64_t kv8_positions(int B, int rows, int Hkv, int Lmax) {
 int kv8_grid(int64_t positions, int rows) {
     const int rt = (rows + kv8_tc::kRows - 1) / kv8_tc::kRows;
     const int64_t pieces = positions / (kv8_tc::kMinTiles * (rt < 2 ? rt : 2));
-    const int sms = device_sm_count();
+    const int sms = cached_sm_count();
     return (int)(pieces < 1 ? 1 : pieces < sms ? pieces : sms);
 }
 // Rows of a partial: those of a unit.
@@ -99,15 +99,14 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
     CUtensorMap mk, mv;
     if (!code_map(&mk, k8, Lmax, (int64_t)B * Hkv) || !code_map(&mv, v8, Lmax, (int64_t)B * Hkv))
         return EAGLE_ERR_CUDA;
-    if (cudaFuncSetAttribute(kv8_tc::tree_attn_kv8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kv8_tc::kSmem) != cudaSuccess)
+    if (!raise_smem_limit<kv8_tc::tree_attn_kv8_kernel>(kv8_tc::kSmem))
         return EAGLE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     kv8_tc::tree_attn_kv8_kernel<<<grid, kv8_tc::kThreads, kv8_tc::kSmem, s>>>(mk, mv, a);
     EAGLE_CHECK_LAUNCH();
     if (grid > 1) {
         const int y = (a.rows + kv8_tc::kMergeWarps - 1) / kv8_tc::kMergeWarps;
-        kv8_tc::tree_attn_kv8_merge_kernel<<<dim3(grid - 1, y < 8 ? y : 8), kv8_tc::kMergeThreads, 0, s>>>(a, grid);
+        kv8_tc::tree_attn_kv8_merge_kernel<<<dim3(grid - 1, y < 16 ? y : 16), kv8_tc::kMergeThreads, 0, s>>>(a, grid);
         EAGLE_CHECK_LAUNCH();
     }
     return EAGLE_OK;
