@@ -39,8 +39,8 @@ __device__ __forceinline__ uint32_t clock_hi() {
     asm volatile("mov.u32 %0, %%clock_hi;\n" : "=r"(x));
     return x;
 }
-__device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const uint32_t b = s32(bar);
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    const uint32_t b = bar;
     if (mbar_try_wait(b, parity & 1u)) return true;
     const uint32_t t0 = clock_hi();
 #pragma unroll 1
@@ -56,15 +56,15 @@ __device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, v
 
 // Arrival and commit of one lane, `on`, without a branch: warps that part for a lane's instruction
 // and meet again lose 200 to 300 cycles here.
-__device__ __forceinline__ void arrive_if(bool on, const uint64_t* bar) {
-    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(s32(bar)),
+__device__ __forceinline__ void arrive_if(bool on, uint32_t bar) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
                  "r"((uint32_t)on)
                  : "memory");
 }
-__device__ __forceinline__ void commit_if(bool on, const uint64_t* bar) {
+__device__ __forceinline__ void commit_if(bool on, uint32_t bar) {
     asm volatile(
         "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(s32(bar)),
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
         "r"((uint32_t)on)
         : "memory");
 }

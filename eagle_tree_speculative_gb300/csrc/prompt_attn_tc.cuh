@@ -26,6 +26,8 @@
 // tile is written only after the same warps have read O of this one, which keeps O safe.
 #pragma once
 
+#include <cstddef>
+
 #include "attn2_common.cuh"
 
 namespace eagle {
@@ -174,6 +176,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     uint8_t* sR = sQ + kSlots * kTile;                    // [kStages][32 KB]
     Shared* sh = reinterpret_cast<Shared*>(sR + kStages * kTile);
     volatile int* abort_flag = &sh->abort_flag;
+    // barriers by their 32-bit shared addresses: 64-bit pointer arithmetic in the control of the MMA
+    // warp is time that the tensor cores wait
+    const uint32_t sb = s32(sh);
+#define BAR(name) (sb + (uint32_t)offsetof(Shared, name))
+#define BAR_AT(name, i) (sb + (uint32_t)offsetof(Shared, name) + 8u * (uint32_t)(i))
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -203,11 +210,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     // the i-th unit of this CTA, as the reading roles see it; false at the end (or on abort)
     auto next_unit = [&](int i, Unit& u) {
-        if (!attn2::wait_for(&sh->info_full[i % kInfo], ((uint32_t)i / kInfo) & 1u, abort_flag)) return false;
+        if (!attn2::wait_for(BAR_AT(info_full, i % kInfo), ((uint32_t)i / kInfo) & 1u, abort_flag)) return false;
         u = sh->info[i % kInfo];
         return u.head >= 0;
     };
-    auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, &sh->info_empty[i % kInfo]); };
+    auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, BAR_AT(info_empty, i % kInfo)); };
 
     if (warp < 4) {
         attn2::regs_dec<kRegsRole>();
@@ -221,7 +228,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 unit_read(i);
                 auto load_q = [&](int s) {
                     if (u.tiles[s] == 0) return;
-                    ok = ok && attn2::wait_for(&sh->q_empty[s], (nqs[s] & 1u) ^ 1u, abort_flag);
+                    ok = ok && attn2::wait_for(BAR_AT(q_empty, s), (nqs[s] & 1u) ^ 1u, abort_flag);
                     if (!ok) return;
                     const uint32_t bar = s32(&sh->q_full[s]);
                     mbar_expect_tx(bar, (uint32_t)(2 * a.P * a.G * 128));
@@ -232,7 +239,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 };
                 auto load_kv = [&](const CUtensorMap* map, int j, bool repair) {
                     const int st = r % kStages;
-                    ok = ok && attn2::wait_for(&sh->empty[st], ((r / kStages) & 1u) ^ 1u, abort_flag);
+                    ok = ok && attn2::wait_for(BAR_AT(empty, st), ((r / kStages) & 1u) ^ 1u, abort_flag);
                     if (!ok) return;
                     const uint32_t bar = s32(repair ? &sh->v_last[st] : &sh->full[st]);
                     mbar_expect_tx(bar, kTile);
@@ -262,7 +269,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // places of the next K and V tile
             bool ok = true;
             // (a wait that gives up lets the step run on, on data that nobody will use)
-            auto wait = [&](uint64_t* bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
+            auto wait = [&](uint32_t bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
             auto advance = [&](uint32_t& st, uint32_t& ph) {      // K and V tiles take turns in the ring
                 st += 2;
                 if (st >= kStages) { st -= kStages; ph ^= 1u; }
@@ -279,9 +286,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     const int s = x & 1, j = x >> 1, ns = s ? n1 : n0;
                     const bool pv = j > 0 && j <= ns, qk = j < ns;
                     const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                    if (s == 0 && j > 0) wait(&sh->full[vs], vp);
+                    if (s == 0 && j > 0) wait(BAR_AT(full, vs), vp);
                     if (pv) {
-                        wait(&sh->p_full[s], pph >> s);
+                        wait(BAR_AT(p_full, s), pph >> s);
                         pph ^= 1u << s;
                         tc_fence_after();
                         const uint32_t dv = dv0 + ((vs * kTile) >> 4);
@@ -292,10 +299,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             acc = 1u;
                         }
                     }
-                    if (s == 0 && j < n) wait(&sh->full[ks], kp);
+                    if (s == 0 && j < n) wait(BAR_AT(full, ks), kp);
                     if (qk) {
                         if (j == 0) {
-                            wait(&sh->q_full[s], qph >> s);
+                            wait(BAR_AT(q_full, s), qph >> s);
                             qph ^= 1u << s;
                         }
                         tc_fence_after();
@@ -305,12 +312,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             const uint32_t at = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
                             attn2::mma_ss<false>(on, scol, dq + at, dk + at, kIdescQK, k > 0 ? 1u : 0u);
                         }
-                        attn2::commit_if(leader, &sh->s_full[s]);
+                        attn2::commit_if(leader, BAR_AT(s_full, s));
                     }
-                    attn2::commit_if(leader && pv && j == ns, &sh->o_full[s]);
-                    attn2::commit_if(leader && qk && j == ns - 1, &sh->q_empty[s]);
-                    attn2::commit_if(leader && s && j > 0, &sh->empty[vs]);
-                    attn2::commit_if(leader && s && j < n, &sh->empty[ks]);
+                    attn2::commit_if(leader && pv && j == ns, BAR_AT(o_full, s));
+                    attn2::commit_if(leader && qk && j == ns - 1, BAR_AT(q_empty, s));
+                    attn2::commit_if(leader && s && j > 0, BAR_AT(empty, vs));
+                    attn2::commit_if(leader && s && j < n, BAR_AT(empty, ks));
                     if (s) {
                         if (j > 0) advance(vs, vp);
                         if (j < n) advance(ks, kp);
@@ -332,7 +339,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 r += 2 * n;
                 if (!needs_fix(u, n)) continue;
                 const uint32_t st = (r - 1) % kStages;
-                const bool got = attn2::wait_for(&sh->v_last[st], (phases >> st) & 1u, abort_flag);
+                const bool got = attn2::wait_for(BAR_AT(v_last, st), (phases >> st) & 1u, abort_flag);
                 phases ^= 1u << st;
                 if (!__all_sync(0xffffffffu, got)) break;
                 uint8_t* v = sR + st * kTile;
@@ -341,7 +348,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         make_uint4(0u, 0u, 0u, 0u);
                 attn2::fence_async_shared();
                 __syncwarp();
-                attn2::arrive_if(lane == 0, &sh->full[st]);
+                attn2::arrive_if(lane == 0, BAR_AT(full, st));
             }
         } else if (warp == 3) {
             // ---------------- which units ----------------
@@ -365,7 +372,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 Unit u{};
                 u.head = -1;
                 if (at < total) find_unit(a, at, top, u);
-                const bool got = attn2::wait_for(&sh->info_empty[i % kInfo], (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
+                const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 if (lane == 0) {
                     sh->info[i % kInfo] = u;
@@ -401,7 +408,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             float mref = -INFINITY;
             uint64_t l2 = 0;                              // two partial sums
             for (int j = 0; j < n; ++j) {
-                const bool got = attn2::wait_for(&sh->s_full[slot], tiles_done & 1u, abort_flag);
+                const bool got = attn2::wait_for(BAR_AT(s_full, slot), tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
                 tc_fence_after();
@@ -450,11 +457,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 tc_fence_before();
                 __syncwarp();
-                attn2::arrive_if(lane == 0, &sh->p_full[slot]);
+                attn2::arrive_if(lane == 0, BAR_AT(p_full, slot));
             }
             if (!ok) break;
             if (n > 0) {
-                const bool got = attn2::wait_for(&sh->o_full[slot], units_done & 1u, abort_flag);
+                const bool got = attn2::wait_for(BAR_AT(o_full, slot), units_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 ++units_done;
                 tc_fence_after();
@@ -491,6 +498,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tc_fence_after();
         tmem_dealloc(tmem, attn2::kTmemCols);
     }
+#undef BAR
+#undef BAR_AT
 }
 
 }  // namespace prompt_tc

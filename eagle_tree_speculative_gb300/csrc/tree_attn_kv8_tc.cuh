@@ -35,6 +35,9 @@
 // a zero weight does not cancel NaN).
 #pragma once
 
+#include <cstddef>
+#include <type_traits>
+
 #include "attn2_common.cuh"
 #include "kv8_common.cuh"
 
@@ -268,6 +271,11 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     uint8_t* sH = sV + kVStages * kTile;                  // [kWide][2 halves][2 boxes of 64 dims][64 keys][128 B]
     Shared* sh = reinterpret_cast<Shared*>(sH + 2 * kWide * kTile);
     volatile int* abort_flag = &sh->abort_flag;
+    // barriers by their 32-bit shared addresses: 64-bit pointer arithmetic in the control of the MMA
+    // warp is time that the tensor cores wait
+    const uint32_t sb = s32(sh);
+#define BAR(name) (sb + (uint32_t)offsetof(Shared, name))
+#define BAR_AT(name, i) (sb + (uint32_t)offsetof(Shared, name) + 8u * (uint32_t)(i))
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -297,11 +305,11 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 
     // the i-th unit of this CTA; nullptr at the end (or on abort)
     auto next_unit = [&](int i) -> const Unit* {
-        if (!attn2::wait_for(&sh->info_full[i % kInfo], ((uint32_t)i / kInfo) & 1u, abort_flag)) return nullptr;
+        if (!attn2::wait_for(BAR_AT(info_full, i % kInfo), ((uint32_t)i / kInfo) & 1u, abort_flag)) return nullptr;
         const Unit* u = &sh->info[i % kInfo];
         return u->head >= 0 ? u : nullptr;
     };
-    auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, &sh->info_empty[i % kInfo]); };
+    auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, BAR_AT(info_empty, i % kInfo)); };
 
     if (warp < 4) {
         attn2::regs_dec<kRegsOther>();
@@ -317,15 +325,15 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 unit_read(i);
 #pragma unroll 1
                 for (int j = 0; ok && j < nc; ++j) {
-                    const bool k_free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
+                    const bool k_free = attn2::wait_for(BAR_AT(k_empty, ks), kp, abort_flag);
                     ok = __all_sync(0xffffffffu, k_free);
-                    if (ok && lane > 0 && lane < 4) mbar_arrive(s32(&sh->k_full[ks]));    // four arrivals, as for the tree's
+                    attn2::arrive_if(ok && lane > 0 && lane < 4, BAR_AT(k_full, ks));     // four arrivals, as for the tree's
                     if (ok && lane == 0) {
                         mbar_expect_tx(s32(&sh->k_full[ks]), kTile);
                         tma_load_3d(s32(sK + ks * kTile), &map_k, s32(&sh->k_full[ks]), 0, (t0 + j) * kKeys, z);
                     }
                     if (++ks == kKStages) { ks = 0; kp ^= 1u; }
-                    const bool v_free = ok && attn2::wait_for(&sh->v_empty[vs], vp, abort_flag);
+                    const bool v_free = ok && attn2::wait_for(BAR_AT(v_empty, vs), vp, abort_flag);
                     ok = __all_sync(0xffffffffu, v_free);
                     if (ok && lane == 0) {
                         mbar_expect_tx(s32(&sh->v_full[vs]), kTile);
@@ -337,17 +345,18 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     // the tree's stage is the widening warps' to fill.  They do not follow this
                     // ring, and a parity names a phase only to a waiter that is at most one
                     // behind, so the stage is handed over when it is free
-                    const bool free = attn2::wait_for(&sh->k_empty[ks], kp, abort_flag);
+                    const bool free = attn2::wait_for(BAR_AT(k_empty, ks), kp, abort_flag);
                     ok = __all_sync(0xffffffffu, free);
-                    if (ok && lane == 0) mbar_arrive(s32(&sh->k_grant[ks]));
+                    attn2::arrive_if(ok && lane == 0, BAR_AT(k_grant, ks));
                     if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
             }
         } else if (warp == 1) {
             // ---------------- MMA issue ----------------
-            // One warp for both slots, whose products then stay together in the tensor pipe; one
-            // copy of the code for both slots and both ways of dealing tiles.  Loads are waited for
-            // before P is; from P's arrival on nothing is.
+            // One warp for both slots, whose products then stay together in the tensor pipe (with a
+            // warp per slot they interleave, and both slots wait for both).  This warp's control
+            // is what the tensor pipe waits for: steps have their slot as a template argument, loads
+            // are waited for before P is, and no lane's instruction stands in a branch.
             const bool leader = attn2::elect_lane();
             const uint32_t on = leader;
             const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
@@ -355,62 +364,77 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;    // ring places, phases
             bool ok = true;
             // (a wait that gives up lets the step run on, on data that nobody will use)
-            auto wait = [&](uint64_t* bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
+            auto wait = [&](uint32_t bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
+            // O of slot s += P V of the tile at the ring's place, then S = Q K^T of the next tile there.
+            // opens, closes: the tiles' first, last use
+            auto step = [&](auto slot_c, bool pv, bool pv_first, bool pv_last, bool two, bool qk, bool qk_first, bool opens, bool closes) {
+                constexpr int s = decltype(slot_c)::value;
+                const uint32_t scol = tm + attn2::s_col(s), ocol = tm + attn2::o_col(s);
+                if (opens && pv) wait(BAR_AT(h_full, hs), hp);
+                if (opens && qk) wait(BAR_AT(k_full, ks), kp);
+                if (qk && qk_first) {
+                    wait(BAR_AT(q_full, s), qph >> s);
+                    qph ^= 1u << s;
+                }
+                if (pv) {
+                    wait(BAR_AT(p_full, s), pph >> s);
+                    pph ^= 1u << s;
+                    tc_fence_after();
+                    const uint32_t dv = dh0 + ((hs * 2 * kTile) >> 4);
+                    attn2::mma_ts(on, ocol, scol, dv, kIdescPV, pv_first ? 0u : 1u);
+#pragma unroll
+                    for (int k = 1; k < kHalfKeys / 16; ++k)
+                        attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, 1u);
+                    const uint32_t on2 = leader && two;
+#pragma unroll
+                    for (int k = 0; k < kHalfKeys / 16; ++k)
+                        attn2::mma_ts(on2, ocol, scol + 32 + 8 * k, dv + ((kTile + k * 16 * 128) >> 4), kIdescPV, 1u);
+                }
+                if (qk) {
+                    tc_fence_after();
+                    const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
+#pragma unroll
+                    for (int d = 0; d < 2; ++d)                           // both digits of Q
+#pragma unroll
+                        for (int k = 0; k < kHeadDim / 32; ++k)
+                            attn2::mma_ss<true>(on, scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
+                    attn2::commit_if(leader, BAR_AT(s_full, s));
+                }
+                attn2::commit_if(leader && pv && pv_last, BAR_AT(o_full, s));
+                if (closes && pv) {
+                    attn2::commit_if(leader, BAR_AT(h_empty, hs));
+                    hs ^= 1u;
+                    hp ^= hs == 0;
+                }
+                if (closes && qk) {
+                    attn2::commit_if(leader, BAR_AT(k_empty, ks));
+                    if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                }
+            };
+            const std::integral_constant<int, 0> s0;
+            const std::integral_constant<int, 1> s1;
             for (int i = 0; ok; ++i) {
                 const Unit* up = next_unit(i);
                 if (!__all_sync(0xffffffffu, up != nullptr)) break;
-                const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);
-                const int alt = attn2::uniform_of(up->split_keys), lag = alt ? 2 : 1;
+                const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);     // the tree's tile is one half
+                const int alt = attn2::uniform_of(up->split_keys);
                 __syncwarp();
                 unit_read(i);
-                // step x is slot x & 1's: O += P V of tile tp, then S = Q K^T of tile t.  Two row
-                // tiles: both slots see every tile, t = x / 2 and tp the one before.  One: tile t
-                // is slot t & 1's, t = x and tp two before.
-                const int steps = n == 0 ? 0 : alt ? n + 2 : 2 * n + 2;
+                if (n == 0) continue;
+                if (alt) {                                // tile t is slot t & 1's
 #pragma unroll 1
-                for (int x = 0; x < steps && __all_sync(0xffffffffu, ok); ++x) {
-                    const int s = x & 1, t = alt ? x : x >> 1, tp = t - lag;
-                    const bool pv = tp >= 0 && tp < n, qk = t < n;
-                    const bool opens = alt || !s, closes = alt || s;      // the tiles' first, last use
-                    const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                    if (opens && pv) wait(&sh->h_full[hs], hp);
-                    if (opens && qk) wait(&sh->k_full[ks], kp);
-                    if (qk && t < lag) {
-                        wait(&sh->q_full[s], qph >> s);
-                        qph ^= 1u << s;
+                    for (int t = 0; t < n + 2 && __all_sync(0xffffffffu, ok); t += 2) {
+                        step(s0, t >= 2, t == 2, t >= n, t - 2 < nc, t < n, t == 0, true, true);
+                        step(s1, t >= 2 && t - 1 < n, t == 2, t + 1 >= n, t - 1 < nc, t + 1 < n, t == 0, true, true);
                     }
-                    if (pv) {
-                        wait(&sh->p_full[s], pph >> s);
-                        pph ^= 1u << s;
-                        tc_fence_after();
-                        const uint32_t dv = dh0 + ((hs * 2 * kTile) >> 4);
-                        uint32_t acc = tp >= lag ? 1u : 0u;
-#pragma unroll
-                        for (int k = 0; k < kHalfKeys / 16; ++k) {
-                            attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
-                            acc = 1u;
-                        }
-                        const uint32_t on2 = leader && tp < nc;           // the tree's tile is one half
-#pragma unroll
-                        for (int k = 0; k < kHalfKeys / 16; ++k)
-                            attn2::mma_ts(on2, ocol, scol + 32 + 8 * k, dv + ((kTile + k * 16 * 128) >> 4), kIdescPV, 1u);
+                } else {                                  // every tile is both slots'
+#pragma unroll 1
+                    for (int t = 0; t <= n && __all_sync(0xffffffffu, ok); ++t) {
+                        step(s0, t > 0, t == 1, t == n, t - 1 < nc, t < n, t == 0, true, false);
+                        step(s1, t > 0, t == 1, t == n, t - 1 < nc, t < n, t == 0, false, true);
                     }
-                    if (qk) {
-                        tc_fence_after();
-                        const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
-#pragma unroll
-                        for (int d = 0; d < 2; ++d)                       // both digits of Q
-#pragma unroll
-                            for (int k = 0; k < kHeadDim / 32; ++k)
-                                attn2::mma_ss<true>(on, scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
-                        attn2::commit_if(leader, &sh->s_full[s]);
-                    }
-                    attn2::commit_if(leader && pv && tp + lag >= n, &sh->o_full[s]);
-                    attn2::commit_if(leader && closes && pv, &sh->h_empty[hs]);
-                    attn2::commit_if(leader && closes && qk, &sh->k_empty[ks]);
-                    if (closes && pv) { hs ^= 1u; hp ^= hs == 0; }
-                    if (closes && qk && ++ks == kKStages) { ks = 0; kp ^= 1u; }
                 }
+                ok = __all_sync(0xffffffffu, ok);
             }
             if (leader) {
                 umma_commit(s32(&sh->drain));
@@ -434,7 +458,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     pos = s.start + s.weight * (s.T + kUnitCost);
                     have = s.t0 < s.t1;
                 }
-                const bool got = attn2::wait_for(&sh->info_empty[i % kInfo], (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
+                const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 Unit* u = &sh->info[i % kInfo];
                 if (!have) {
@@ -497,7 +521,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                 }
                 __syncwarp();
-                attn2::arrive_if(lane == 0, &sh->info_full[i % kInfo]);
+                attn2::arrive_if(lane == 0, BAR_AT(info_full, i % kInfo));
             }
             if (bits) flag_error(a.dev_status, bits);
         }
@@ -567,7 +591,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             sc_next = a.scale_log2 * kv8::exp2i(e_mine);
             attn2::fence_async_shared();
             __syncwarp();
-            attn2::arrive_if(lane == 0, &sh->q_full[slot]);
+            attn2::arrive_if(lane == 0, BAR_AT(q_full, slot));
             return true;
         };
 
@@ -585,7 +609,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (i > 0) {
                 const Unit* u = &sh->info[(i - 1) % kInfo];
                 if (mine > 0) {
-                    const bool got = attn2::wait_for(&sh->o_full[slot], units_done & 1u, abort_flag);
+                    const bool got = attn2::wait_for(BAR_AT(o_full, slot), units_done & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     ++units_done;
                     tc_fence_after();
@@ -600,8 +624,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     // both slots hold this row: (m, l) change hands, each slot writes half of the columns
                     sh->ml[slot][row] = make_float2(mref, l);
                     __syncwarp();
-                    attn2::arrive_if(lane == 0, &sh->merge_in);
-                    const bool got = attn2::wait_for(&sh->merge_in, merges & 1u, abort_flag);
+                    attn2::arrive_if(lane == 0, BAR(merge_in));
+                    const bool got = attn2::wait_for(BAR(merge_in), merges & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     tc_fence_after();
                     const float2 x0 = sh->ml[0][row], x1 = sh->ml[1][row];
@@ -649,8 +673,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 if (alt) {                                                   // O and ml are free again
                     tc_fence_before();
                     __syncwarp();
-                    attn2::arrive_if(lane == 0, &sh->merge_out);
-                    const bool got = attn2::wait_for(&sh->merge_out, merges & 1u, abort_flag);
+                    attn2::arrive_if(lane == 0, BAR(merge_out));
+                    const bool got = attn2::wait_for(BAR(merge_out), merges & 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;
                     ++merges;
                 }
@@ -678,7 +702,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             const int first = alt ? slot : 0, step = alt ? 2 : 1;
             float scale = load_scale(first);
             for (int t = first; t < n; t += step, ++mine) {
-                const bool got = attn2::wait_for(&sh->s_full[slot], tiles_done & 1u, abort_flag);
+                const bool got = attn2::wait_for(BAR_AT(s_full, slot), tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
                 tc_fence_after();
@@ -746,7 +770,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         // the tree's tile, 32 keys at a time: key j's score is the sum of its digits'
                         // columns j and 64 + j; its factors have a barrier per tree in flight
                         const int tr = trees % kTrees;
-                        const bool seen = attn2::wait_for(&sh->tree_full[tr], (trees / kTrees) & 1u, abort_flag);
+                        const bool seen = attn2::wait_for(BAR_AT(tree_full, tr), (trees / kTrees) & 1u, abort_flag);
                         if (!__all_sync(0xffffffffu, seen)) { ok = false; break; }
                         // first pass: scores, back into TMEM; second pass: weights
                         uint32_t x[16], y[16];
@@ -789,7 +813,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 }
                 tc_fence_before();
                 __syncwarp();
-                attn2::arrive_if(lane == 0, &sh->p_full[slot]);
+                attn2::arrive_if(lane == 0, BAR_AT(p_full, slot));
             }
             trees += n - nc;
         }
@@ -804,7 +828,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         uint32_t r = 0, rh = 0, rk = 0, trees = 0, grants = 0;   // uses of the rings; a phase bit per K stage
         int bits = 0;
         bool ok = true;
-        auto ready = [&](uint64_t* bar, uint32_t parity) {
+        auto ready = [&](uint32_t bar, uint32_t parity) {
             const bool got = attn2::wait_for(bar, parity, abort_flag);
             ok = ok && __all_sync(0xffffffffu, got);
             return ok;
@@ -812,7 +836,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         auto tile_done = [&]() {
             attn2::fence_async_shared();
             __syncwarp();
-            attn2::arrive_if(lane == 0, &sh->h_full[rh % kWide]);
+            attn2::arrive_if(lane == 0, BAR_AT(h_full, rh % kWide));
             ++rh;
         };
         for (int i = 0; ok; ++i) {
@@ -823,8 +847,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             unit_read(i);
             for (int j = 0; j < nc; ++j, ++r) {
                 const int st = r % kVStages, left = L - (t0 + j) * kKeys;
-                if (!ready(&sh->v_full[st], r / kVStages)) break;
-                if (!ready(&sh->h_empty[rh % kWide], (rh / kWide) ^ 1u)) break;
+                if (!ready(BAR_AT(v_full, st), r / kVStages)) break;
+                if (!ready(BAR_AT(h_empty, rh % kWide), (rh / kWide) ^ 1u)) break;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
@@ -849,7 +873,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                 }
                 tile_done();
-                attn2::arrive_if(lane == 0, &sh->v_empty[st]);
+                attn2::arrive_if(lane == 0, BAR_AT(v_empty, st));
             }
             rk += nc;
             if (ok && tree) {
@@ -863,7 +887,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
-                    if (!ready(&sh->k_grant[ks], grants >> ks)) break;
+                    if (!ready(BAR_AT(k_grant, ks), grants >> ks)) break;
                     grants ^= 1u << ks;
 #pragma unroll 1
                     for (int k = 0; k < 8; k += 4) {                     // four row pairs at once, to hide their latencies
@@ -886,10 +910,10 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                     attn2::fence_async_shared();
                     __syncwarp();
-                    attn2::arrive_if(lane == 0, &sh->k_full[ks]);
+                    attn2::arrive_if(lane == 0, BAR_AT(k_full, ks));
                 }
                 // V
-                if (!ready(&sh->h_empty[rh % kWide], (rh / kWide) ^ 1u)) break;
+                if (!ready(BAR_AT(h_empty, rh % kWide), (rh / kWide) ^ 1u)) break;
                 uint8_t* dst = sH + rh % kWide * 2 * kTile;
                 const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
 #pragma unroll 1
@@ -917,7 +941,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                 }
                 __syncwarp();
-                attn2::arrive_if(lane == 0, &sh->tree_full[trees % kTrees]);
+                attn2::arrive_if(lane == 0, BAR_AT(tree_full, trees % kTrees));
                 ++trees;
                 tile_done();
             }
@@ -930,6 +954,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         tc_fence_after();
         tmem_dealloc(tmem, attn2::kTmemCols);
     }
+#undef BAR
+#undef BAR_AT
 }
 
 // ---------------- merging of cut units ----------------
