@@ -106,8 +106,16 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
     EAGLE_CHECK_LAUNCH();
     if (grid > 1) {
         const int y = (a.rows + kv8_tc::kMergeWarps - 1) / kv8_tc::kMergeWarps;
-        kv8_tc::tree_attn_kv8_merge_kernel<<<dim3(grid - 1, y < 16 ? y : 16), kv8_tc::kMergeThreads, 0, s>>>(a, grid);
-        EAGLE_CHECK_LAUNCH();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(y < 16 ? y : 16));
+        cfg.blockDim = dim3(kv8_tc::kMergeThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, kv8_tc::tree_attn_kv8_merge_kernel, a, grid) != cudaSuccess) return EAGLE_ERR_CUDA;
     }
     return EAGLE_OK;
 }

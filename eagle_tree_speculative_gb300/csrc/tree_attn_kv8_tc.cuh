@@ -298,6 +298,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 1) tmem_alloc(s32(&sh->tmem), attn2::kTmemCols);
+    // the merging kernel may be launched as CTAs of this one end; it waits for all of them itself
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -959,10 +961,11 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 }
 
 // ---------------- merging of cut units ----------------
-// Block (c, y): the unit whose first tile lies in piece c and whose last does not, rows y, y + 8,
-// .. one warp each; its parts are piece c's second place and the first places of the pieces
-// behind it.  m is in log2 units and a part's l and O share one factor, so a part weighs
-// 2^(m - max m).
+// Blocks (c, y): the unit whose first tile lies in piece c and whose last does not, one warp a row;
+// its parts are piece c's second place and the first places of the pieces behind it.  m is in
+// log2 units and a part's l and O share one factor, so a part weighs 2^(m - max m).  Lane p looks
+// after part p (of up to 32 at a time), so that the parts' loads do not wait for one another.  The
+// launch may begin while the attention kernel ends; the partials are awaited below.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 
 __global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args a, int grid) {
@@ -975,30 +978,41 @@ __global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args
     const Segment s = segment_at(a, end - 1, end, b, base);
     if (s.start < begin || s.t1 >= s.T) return;           // it begins earlier, or is whole
     const int rows = min(a.n * a.G - s.pair * 2 * kRows, 2 * kRows);
-    int last = c;                                         // the piece with the unit's last tile
-    while (last + 1 < cut.ctas && tiles_before(s.start, s.weight, cut.begin(last + 1)) < s.T) ++last;
+    // lane's part: piece c + lane, and whether it holds tiles of the unit
+    auto place_of = [&](int p) -> int {                   // -1: none, -2: none from here on
+        if (p == c) return c * 2 + 1;
+        if (p >= cut.ctas) return -2;
+        const int t0 = tiles_before(s.start, s.weight, cut.begin(p));
+        const int t1 = p + 1 < cut.ctas ? tiles_before(s.start, s.weight, cut.begin(p + 1)) : s.T;
+        return t0 >= s.T ? -2 : t0 < t1 ? p * 2 : -1;
+    };
+    const int first = place_of(c + lane);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
-        // part p of pieces c .. last; a piece may hold no tile of the unit
-        auto place = [&](int p) -> int64_t {
-            if (p == c) return ((int64_t)c * 2 + 1) * a.rows + row;
-            const int t0 = tiles_before(s.start, s.weight, cut.begin(p));
-            const int t1 = p + 1 < cut.ctas ? tiles_before(s.start, s.weight, cut.begin(p + 1)) : s.T;
-            return t0 < s.T && t0 < t1 ? (int64_t)p * 2 * a.rows + row : -1;
-        };
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = c; p <= last; ++p) {
-            const int64_t at = place(p);
-            if (at < 0) continue;
-            const float2 ml = a.ws_ml[at];
-            const float4 x = *reinterpret_cast<const float4*>(a.ws_o + at * kHeadDim + 4 * lane);
-            const float mn = fmaxf(m, ml.x);
-            if (mn == -INFINITY) continue;
-            const float wo = exp2f(m - mn), wx = exp2f(ml.x - mn);
+        for (int p0 = c;; p0 += 32) {
+            const int place = p0 == c ? first : place_of(p0 + lane);
+            const bool there = place >= 0;
+            const float2 ml = there ? a.ws_ml[(int64_t)place * a.rows + row] : make_float2(-INFINITY, 0.f);
+            float top = ml.x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m, top), at = mn == -INFINITY ? 0.f : mn;
+            const float w = exp2f(ml.x - at), wo = exp2f(m - at);
             m = mn;
-            l = l * wo + ml.y * wx;
-            o.x = o.x * wo + x.x * wx; o.y = o.y * wo + x.y * wx;
-            o.z = o.z * wo + x.z * wx; o.w = o.w * wo + x.w * wx;
+            l = l * wo + warp_sum(ml.y * w);
+            o.x *= wo; o.y *= wo; o.z *= wo; o.w *= wo;
+            const unsigned live = __ballot_sync(0xffffffffu, there);
+            const int parts = 32 - __clz(live);           // places up to the last one that is there
+#pragma unroll 4
+            for (int p = 0; p < parts; ++p) {
+                const int at_p = max(__shfl_sync(0xffffffffu, place, p), 0);
+                const float wp = __shfl_sync(0xffffffffu, w, p);
+                const float4 x = *reinterpret_cast<const float4*>(a.ws_o + ((int64_t)at_p * a.rows + row) * kHeadDim + 4 * lane);
+                if ((live >> p) & 1u) { o.x += x.x * wp; o.y += x.y * wp; o.z += x.z * wp; o.w += x.w * wp; }
+            }
+            if (__any_sync(0xffffffffu, place == -2)) break;
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int r = s.pair * 2 * kRows + row;
