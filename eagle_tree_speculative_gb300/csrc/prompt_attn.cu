@@ -75,6 +75,7 @@ extern "C" eagle_status eagle_prompt_attn(const void* q, const void* k, const vo
         return EAGLE_ERR_CUDA;
     // a sequence of m queries has at most m / 2P + 1 units
     const int64_t units = ((int64_t)Tq / (2 * a.P) + B) * Hkv;
+    if (units > 0x3fffffffLL || Tq > 0x3fffffff || Tk > 0x3fffffff) return EAGLE_ERR_SHAPE;      // 32-bit places
     const int sms = cached_sm_count();
     const unsigned grid = (unsigned)(units < sms ? units : sms);
     if (!raise_smem_limit<prompt_tc::prompt_attn_kernel>(prompt_tc::kSmem))

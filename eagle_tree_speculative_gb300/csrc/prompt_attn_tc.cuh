@@ -101,22 +101,22 @@ __device__ __forceinline__ int tiles_of(int nq, int nk, int p, int P) {
 __device__ __forceinline__ int units_above(int nq, int nk, int t, int W) {
     const int units = (nq + W - 1) / W;
     // unit u reaches key nk - nq + (u + 1) W; > t * kKeys  <=>  u + 1 > (t kKeys - (nk - nq)) / W
-    const int64_t x = (int64_t)t * kKeys - (nk - nq);
-    const int64_t first = x < 0 ? 0 : x / W;
-    return units - (int)min((int64_t)units, first);
+    const int x = t * kKeys - (nk - nq);
+    return units - min(units, x < 0 ? 0 : x / W);
 }
 
 // Warp-wide: the unit of rank i in order of falling key count, over all sequences.  `top`: no
-// unit has more than top tiles.
-__device__ __forceinline__ void find_unit(const Args& a, int64_t i, int top, Unit& u) {
+// unit has more than top tiles; nq0, nk0: the counts of sequence `lane`, if there is one.
+__device__ __forceinline__ void find_unit(const Args& a, int i, int top, int nq0, int nk0, Unit& u) {
     const int lane = threadIdx.x & 31, W = 2 * a.P;
-    const int head = (int)(i % a.Hkv);
-    const int rank = (int)(i / a.Hkv);
+    const int rank = i / a.Hkv, head = i - rank * a.Hkv;
+    auto queries = [&](int b) { return b < 32 ? nq0 : a.cu_q[b + 1] - a.cu_q[b]; };      // b = lane mod 32
+    auto keys = [&](int b) { return b < 32 ? nk0 : a.cu_k[b + 1] - a.cu_k[b]; };
     auto count = [&](int t) {                     // units with more than t tiles
         int c = 0;
         for (int b = lane; b < a.B; b += 32) {
-            const int nq = a.cu_q[b + 1] - a.cu_q[b];
-            if (nq > 0) c += units_above(nq, a.cu_k[b + 1] - a.cu_k[b], t, W);
+            const int nq = queries(b);
+            if (nq > 0) c += units_above(nq, keys(b), t, W);
         }
         return __reduce_add_sync(0xffffffffu, c);
     };
@@ -134,8 +134,8 @@ __device__ __forceinline__ void find_unit(const Args& a, int64_t i, int top, Uni
         const int b = b0 + lane;
         int nq = 0, nk = 0, n = 0, above = 0;
         if (b < a.B) {
-            nq = a.cu_q[b + 1] - a.cu_q[b];
-            nk = a.cu_k[b + 1] - a.cu_k[b];
+            nq = queries(b);
+            nk = keys(b);
             if (nq > 0) {
                 above = units_above(nq, nk, lo, W);
                 n = (lo == 0 ? (nq + W - 1) / W : units_above(nq, nk, lo - 1, W)) - above;
@@ -353,11 +353,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         } else if (warp == 3) {
             // ---------------- which units ----------------
             bool bad = false;
-            int top = 0, units = 0;
+            int top = 0, units = 0, nq0 = 0, nk0 = 0;
             for (int b = lane; b < a.B; b += 32) {
                 const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
                 if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) bad = true;
                 else if (q1 > q0) {
+                    if (b < 32) { nq0 = q1 - q0; nk0 = k1 - k0; }
                     units += (q1 - q0 + 2 * a.P - 1) / (2 * a.P);
                     top = max(top, (k1 - k0) / kKeys + 2 * a.P / kKeys + 2);
                 }
@@ -371,7 +372,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int64_t at = (int64_t)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 Unit u{};
                 u.head = -1;
-                if (at < total) find_unit(a, at, top, u);
+                if (at < total) find_unit(a, (int)at, top, nq0, nk0, u);
                 const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) break;
                 if (lane == 0) {

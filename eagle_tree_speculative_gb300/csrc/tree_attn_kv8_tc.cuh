@@ -497,14 +497,6 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             for (int h = 0; h < 2; ++h) { anc[h] |= add[h]; p[h] = up[h]; }
                         }
                     }
-                    // the unit's rows of Q and of the tree go into L2 meanwhile
-                    const char* qr = reinterpret_cast<const char*>(a.q + ((int64_t)s.b * a.n * a.Hq + s.head * a.G) * kHeadDim);
-                    const int64_t tree_at = ((int64_t)s.b * a.n * a.Hkv + s.head) * kHeadDim;
-                    for (int y = lane; y < a.n; y += 32) {
-                        prefetch_l2(a.k_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
-                        prefetch_l2(a.v_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
-                        for (int g = 0; g < a.G; ++g) prefetch_l2(qr + ((int64_t)y * a.Hq + g) * kHeadDim * 2);
-                    }
                     const int L = a.kv_len[s.b];
                     const bool bad_len = L < 0 || L > a.Lmax;
                     if ((bad_len || bad_tree) && s.head == 0 && s.pair == 0 && s.t0 == 0)
@@ -524,6 +516,16 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 }
                 __syncwarp();
                 attn2::arrive_if(lane == 0, BAR_AT(info_full, i % kInfo));
+                if (have) {
+                    // the unit's rows of Q and of the tree go into L2 meanwhile
+                    const char* qr = reinterpret_cast<const char*>(a.q + ((int64_t)s.b * a.n * a.Hq + s.head * a.G) * kHeadDim);
+                    const int64_t tree_at = ((int64_t)s.b * a.n * a.Hkv + s.head) * kHeadDim;
+                    for (int y = lane; y < a.n; y += 32) {
+                        prefetch_l2(a.k_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
+                        prefetch_l2(a.v_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
+                        for (int g = 0; g < a.G; ++g) prefetch_l2(qr + ((int64_t)y * a.Hq + g) * kHeadDim * 2);
+                    }
+                }
             }
             if (bits) flag_error(a.dev_status, bits);
         }
@@ -891,8 +893,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
                     if (!ready(BAR_AT(k_grant, ks), grants >> ks)) break;
                     grants ^= 1u << ks;
+                    const int pairs = min(8, (a.n - cw * 16 + 1) >> 1);
 #pragma unroll 1
-                    for (int k = 0; k < 8; k += 4) {                     // four row pairs at once, to hide their latencies
+                    for (int k = 0; k < pairs; k += 4) {                     // four row pairs at once, to hide their latencies
                         int e[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
@@ -920,6 +923,13 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
 #pragma unroll 1
                 for (int r0 = cw * 16 + (lane >> 4); r0 < cw * 16 + 16; r0 += 8) {
+                    if (r0 - (lane >> 4) >= a.n) {        // no row of the tree
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(dst + ((lane & 15) >> 3) * kHalfBox + swz(r0 + 2 * k, (lane & 7) * 16)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        continue;
+                    }
                     uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
