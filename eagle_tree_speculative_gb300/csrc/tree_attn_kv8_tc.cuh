@@ -50,8 +50,8 @@ using attn2::kSlots;
 using kv8::kKv8Block;
 
 constexpr int kThreads = 512;
-// 4 warpgroups x 128 registers at launch; 56 + 2 x 200 + 56 = 4 x 128
-constexpr int kRegsOther = 56, kRegsSoftmax = 200;
+// 4 warpgroups x 128 registers at launch; 64 + 2 x 192 + 64 = 4 x 128
+constexpr int kRegsOther = 64, kRegsSoftmax = 192;
 constexpr int kKStages = 3, kVStages = 2;         // rings of raw tiles
 constexpr int kWide = 2;                          // V tiles in fp16, two halves of 64 keys each
 constexpr int kTile = 128 * 128;                  // 16 KB: a K or V tile, a digit plane of Q, half a V tile in fp16
@@ -59,7 +59,9 @@ constexpr int kHalfKeys = 64, kHalfBox = kHalfKeys * 128;     // 64 keys x 64 di
 constexpr int kInfo = 3;                          // units in flight between the roles
 constexpr int kTrees = 8;                         // trees in flight, see Shared
 constexpr int kBlocks = kKeys / kKv8Block;        // scales per tile
-constexpr int kUnitCost = 3;                      // what a unit costs beside its tiles, in tiles
+// What a unit costs beside its tiles (digits, the tree, its output), in tiles.  3 / 6 / 8 / 12: 202 /
+// 172 / 164 / 161 us for 48 ragged sequences of one node, 273 / 275 / 277 / 281 us for 64 equal trees.
+constexpr int kUnitCost = 8;
 constexpr float kOffset = 6.f, kRescale = 8.f;    // weights up to 2^14
 constexpr int kMaxVExp = 44;                      // V scales up to 2^44, see below
 constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles
@@ -83,7 +85,7 @@ struct Args {
 
 // ---------------- the cut: shared by the attention and the merging kernel ----------------
 // Positions: sequence by sequence, head by head, row-tile pair by pair, tile by tile; a tile of a
-// pair counts 2, of a single row tile 1, and a unit's first tile kUnitCost tiles more (its digits,
+// pair counts 2, of a single row tile 1, and a unit's first tile kUnitCost more (its digits,
 // its output).  The host refuses sizes with 2^31 positions or more.
 struct Cut {
     int total;                                    // positions

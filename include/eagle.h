@@ -306,9 +306,10 @@ eagle_status eagle_ttt_attn(const void* q, const void* k, const void* v, void* o
  *   out  bf16 [Tq, Hq, head_dim]      lse f32 [Tq, Hq] or NULL
  * Strides are in elements: multiples of 8, at least Hq (Hkv) * head_dim; a fused
  * projection's output can be read in place.  Bases 16-byte aligned.  Rows of out and
- * lse that belong to no sequence are left as they are.  Hq / Hkv <= 128.  Every row
- * of a sequence's keys must be finite (masked keys are read; a zero weight does not
- * cancel NaN); rows of no sequence and of other sequences may hold anything.
+ * lse that belong to no sequence are left as they are.  Hq / Hkv <= 128; Tq and Tk
+ * below 2^30.  Every row of a sequence's keys must be finite (masked keys are read; a
+ * zero weight does not cancel NaN); rows of no sequence and of other sequences may
+ * hold anything.
  * Device errors: cu_q or cu_k decreasing or out of range sets EAGLE_DEV_CAPACITY and
  * nothing is written.
  * ------------------------------------------------------------------------- */
