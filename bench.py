@@ -1068,7 +1068,7 @@ def run_reference(args, rank, world):
 
 
 KERNEL_CASES = ("gemm", "topk", "fused", "attn", "verify", "verify_filtered", "compact",
-                "softmax", "ttt")
+                "softmax", "ttt", "prompt", "attn_kv8", "append_kv8", "commit_kv8")
 
 
 def kernel_case(name, reps):
@@ -1087,6 +1087,10 @@ def kernel_case(name, reps):
       compact  KV compaction, 32 layers, B=4 (8 kv heads, Lmax 4156)
       softmax  softmax statistics of [32, 60, 128256] target logits
       ttt      training-time-test attention, B=8, S=2048, 32/8 heads, round 7 of 8
+      prompt   attention of 8 packed prompts of 2048 tokens, 32/8 heads
+      attn_kv8 tree attention over the 8-bit cache, the shape of `attn`
+      append_kv8  those prompts' rows quantised into the 8-bit cache, one layer
+      commit_kv8  the path of `compact` committed into an 8-bit cache, 32 layers, B=4
     """
     import torch
 
@@ -1186,6 +1190,48 @@ def kernel_case(name, reps):
         q, k, v = ttt_inputs(torch, dev, t["B"], t["S"], t["Hq"], t["Hkv"], t["R1"], g)
         out = torch.empty_like(q)
         fn = lambda: E.eagle_ttt_attn(q, k, v, t["r"], out=out, dev_status=st)  # noqa: E731
+    elif name in ("prompt", "append_kv8"):
+        B, S = 8, 2048
+        cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * S
+        k, v = (normal((B * S, c.Hkv, c.head_dim), 1.0, torch.bfloat16) for _ in range(2))
+        if name == "prompt":
+            q = normal((B * S, c.Hq, c.head_dim), 1.0, torch.bfloat16)
+            out = torch.empty_like(q)
+            fn = lambda: E.eagle_prompt_attn(q, k, v, cu, out=out, dev_status=st)  # noqa: E731
+        else:
+            k8, v8, ks, vs = (x[0] for x in E.kv8_cache(1, B, c.Hkv, S, c.head_dim, dev))
+            pos = torch.zeros(B, dtype=torch.int32, device=dev)
+            fn = lambda: E.eagle_kv8_append(k, v, cu, pos, k8, v8, ks, vs, dev_status=st)  # noqa
+    elif name == "attn_kv8":
+        B = c.B
+        _, _, _, par, _ = expanded(8)
+        parent = par.repeat(B // 8, 1).contiguous()
+        k8, v8, ks, vs = (x[0] for x in E.kv8_cache(1, B, c.Hkv, c.L, c.head_dim, dev))
+        rows = normal((B * c.L, 2 * c.Hkv, c.head_dim), 1.0, torch.bfloat16)
+        cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * c.L
+        E.eagle_kv8_append(rows[:, :c.Hkv], rows[:, c.Hkv:], cu,
+                           torch.zeros(B, dtype=torch.int32, device=dev), k8, v8, ks, vs)
+        del rows
+        q = normal((B, c.n, c.Hq, c.head_dim), 1.0, torch.bfloat16)
+        kt, vt = (normal((B, c.n, c.Hkv, c.head_dim), 1.0, torch.bfloat16) for _ in range(2))
+        kv_len = torch.full((B,), c.L, dtype=torch.int32, device=dev)
+        out = torch.empty_like(q)
+        ws = E.tree_attn_kv8_workspace_size(B, c.n, c.Hq, c.Hkv, c.head_dim, c.L)
+        wsb = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+        fn = lambda: E.eagle_tree_attn_kv8(q, k8, v8, ks, vs, kt, vt, kv_len, parent,  # noqa: E731
+                                           out=out, workspace=wsb, dev_status=st)
+    elif name == "commit_kv8":
+        B = 4
+        k8, v8, ks, vs = E.kv8_cache(c.n_layers, B, c.Hkv, c.Lmax, c.head_dim, dev)
+        kt, vt = (normal((c.n_layers, B, c.n, c.Hkv, c.head_dim), 1.0, torch.bfloat16)
+                  for _ in range(2))
+        kv_len = torch.full((B,), c.L, dtype=torch.int32, device=dev)
+        new_len = torch.empty_like(kv_len)
+        path = torch.full((B, c.depth + 1), -1, dtype=torch.int32, device=dev)
+        path[:, :7] = torch.tensor([0, 2, 5, 9, 14, 20, 27], dtype=torch.int32)
+        acc = torch.full((B,), 6, dtype=torch.int32, device=dev)
+        fn = lambda: E.eagle_kv8_commit(kt, vt, k8, v8, ks, vs, kv_len, path, acc,  # noqa: E731
+                                        c.depth, kv_len_out=new_len, dev_status=st)
     else:
         raise ValueError(name)
     fn()                                   # warm-up (first-call set-up stays untimed)
