@@ -31,16 +31,21 @@ struct Cache {
     int Lmax, NB;
 };
 
-// The largest finite magnitude of 8 bf16 as its bits (magnitudes order like integers); an
-// exponent of all ones is an infinity or a NaN, does not count and sets `odd`.
-__device__ __forceinline__ uint32_t top8(const uint4& x, bool& odd) {
+// Magnitudes of bf16 order like integers: the larger ones of 8, as two packed halves, two elements
+// an instruction.
+__device__ __forceinline__ uint32_t top8(const uint4& x, uint32_t top) {
+    top = __vmaxu2(top, x.x & 0x7fff7fffu);
+    top = __vmaxu2(top, x.y & 0x7fff7fffu);
+    top = __vmaxu2(top, x.z & 0x7fff7fffu);
+    return __vmaxu2(top, x.w & 0x7fff7fffu);
+}
+// The same where infinities and NaN (exponents of all ones) do not count.
+__device__ __forceinline__ uint32_t top8_finite(const uint4& x, uint32_t top) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        odd |= max(lo, hi) >= 0x7f80u;
-        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        top = __vmaxu2(top, (lo < 0x7f80u ? lo : 0u) | ((hi < 0x7f80u ? hi : 0u) << 16));
     }
     return top;
 }
@@ -74,13 +79,22 @@ __device__ __forceinline__ int write_block(const Cache& c, int kv, int64_t slab,
             x[s] = __ldg(reinterpret_cast<const uint4*>(src(min(t0 + 2 * s + half, m - 1))) + col);
     };
     uint32_t top = 0u;
-    bool odd = false;
     for (int t0 = 0; t0 < m; t0 += 2 * R) {
         load(t0);
 #pragma unroll
-        for (int s = 0; s < R; ++s) top = max(top, top8(x[s], odd));
+        for (int s = 0; s < R; ++s) top = top8(x[s], top);
     }
-    top = __reduce_max_sync(kFull, top);
+    top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
+    const bool odd = top >= 0x7f80u;      // an infinity or a NaN: the finite ones again
+    if (odd) {
+        top = 0u;
+        for (int t0 = 0; t0 < m; t0 += 2 * R) {
+            if (m > 2 * R) load(t0);
+#pragma unroll
+            for (int s = 0; s < R; ++s) top = top8_finite(x[s], top);
+        }
+        top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
+    }
     float scale = kv8::exp2i(kv8::scale_exp(__uint_as_float(top << 16)));
     if (held) {
         __syncwarp();                     // every lane has read the scale before it is replaced
