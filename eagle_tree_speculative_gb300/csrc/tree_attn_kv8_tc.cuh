@@ -4,7 +4,7 @@
 // query keeps bf16's precision as two e4m3 digits, q = hi + lo with hi the leading 4 bits of the
 // significand and lo the next 4: two passes at twice the bf16 rate, no conversion of K.  The
 // weights change per tile and thread, so splitting them as well costs more instructions than the
-// whole softmax (it was tried: 0.56 ms at the shape below); V is widened to fp16 once per tile
+// whole softmax (0.56 ms against 0.275 ms at the first shape below); V is widened to fp16 once per tile
 // instead (every e4m3 value is a half), for both slots, and PV runs in kind::f16.
 //   Q  per row times a power of two that brings its largest element to [128, 256): digits exact
 //      for elements within 2^-9 of the largest, the rest to 2^-17 of it.
@@ -29,10 +29,17 @@
 // A unit that is cut leaves partial (m, l, O) in the workspace, at most two per CTA; a second
 // small kernel merges them.
 //
-// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 3 cuts the work, warps 4-11 are the softmax, which also makes the Q
-// digits of the next unit before it writes this one's output, warps 12-15 widen V into two tiles
-// (of two halves of 64 keys) and make the K digits of the tree's rows; rows behind the last key become zeros there (whatever bits lie in them:
-// a zero weight does not cancel NaN).
+// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 3 cuts the work, warps 4-11 are
+// the softmax, which also makes the Q digits of the next unit before it writes this one's output,
+// warps 12-15 widen V into two tiles (of two halves of 64 keys) and make the K digits of the tree's
+// rows; V rows behind the last key become zeros there (whatever bits lie in them: a zero weight
+// does not cancel NaN).
+//
+// Measured: 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 0.275 ms (the bf16 cache's kernel:
+// 0.297 ms from twice the bytes); tensor pipe 50% active, 643 MB read.  48 sequences of one node over
+// 100 .. 30 000 rows, 64 / 8 heads: 160 us, 3.8 TB/s.  Bound: the chain of QK, softmax and PV per slot
+// and the MMA warp's control, about 3 800 cycles per 256 rows x 128 keys, and 20 to 30 thousand
+// cycles at a unit's ends; neither HBM nor the tensor pipe is full.
 #pragma once
 
 #include <cstddef>
@@ -927,9 +934,12 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 for (int r0 = cw * 16 + (lane >> 4); r0 < cw * 16 + 16; r0 += 8) {
                     if (r0 - (lane >> 4) >= a.n) {        // no row of the tree
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 4; ++k) {
                             *reinterpret_cast<uint4*>(dst + ((lane & 15) >> 3) * kHalfBox + swz(r0 + 2 * k, (lane & 7) * 16)) =
                                 make_uint4(0u, 0u, 0u, 0u);
+                            // the sum multiplies it with a weight of zero, which does not cancel NaN
+                            if ((lane & 15) == 0) sh->v_inv[trees % kTrees][r0 + 2 * k] = 0.f;
+                        }
                         continue;
                     }
                     uint4 v[4];
@@ -984,11 +994,14 @@ __global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args
     const int lane = threadIdx.x & 31;
     const Cut cut = make_cut(a, grid);
     const int c = blockIdx.x;
-    if (c + 1 >= cut.ctas) return;                        // the last piece ends with a whole unit
+    // A block that has nothing to merge awaits the attention kernel too: a kernel launched next
+    // waits for this one alone.
+    auto await = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
+    if (c + 1 >= cut.ctas) { await(); return; }           // the last piece ends with a whole unit
     const int begin = cut.begin(c), end = cut.begin(c + 1);
     int b = 0, base = 0;
     const Segment s = segment_at(a, end - 1, end, b, base);
-    if (s.start < begin || s.t1 >= s.T) return;           // it begins earlier, or is whole
+    if (s.start < begin || s.t1 >= s.T) { await(); return; }   // it begins earlier, or is whole
     const int rows = min(a.n * a.G - s.pair * 2 * kRows, 2 * kRows);
     // lane's part: piece c + lane, and whether it holds tiles of the unit
     auto place_of = [&](int p) -> int {                   // -1: none, -2: none from here on
@@ -999,7 +1012,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args
         return t0 >= s.T ? -2 : t0 < t1 ? p * 2 : -1;
     };
     const int first = place_of(c + lane);
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    await();
     for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

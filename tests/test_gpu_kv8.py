@@ -451,3 +451,128 @@ def test_prompt_then_steps():
         _same(k8, kd, codes[0], scales[0])
         _same(v8, vd, codes[1], scales[1])
     assert int(st.item()) == 0 and max(L) > max(lens)
+
+
+# ---------------------------------------------------------------- further calls
+@pytest.mark.parametrize("where", [(0,), (31,), (32, 33), (70, 3, 40)])
+@pytest.mark.parametrize("value", ["inf", "nan"])
+def test_append_non_finite_rows_anywhere_in_a_block(where, value):
+    """A whole row without a finite element beside others that set the scale; a block of nothing else."""
+    x, y = _bf16((75, 1, D), 111), _bf16((75, 1, D), 112)
+    for t in where:
+        x[t] = float(value)
+    y[5:37, 0, 64:] = float(value)
+    _append(x, y, [75], [17], 1, 96, 113, status=_E().EAGLE_DEV_NONFINITE)
+
+
+@pytest.mark.parametrize("start", [0, 9, 31])
+def test_commit_non_finite_elements_of_long_paths(start):
+    """Paths longer than the rows a warp holds at once, an infinity and a NaN in them."""
+    E = _E()
+    n, depth, Lmax = 40, 30, 64
+    x = _bf16((2, 1, n, 2, D), 114)
+    x[0, 0, 3, 1, 5], x[1, 0, 25, 0, 100] = float("inf"), float("nan")
+    path = np.array([[0] + list(range(2, 32))], np.int32)
+    kc, ks = _random_cache((2, 1, 2), Lmax, 115)
+    k8, kd = _put(kc, ks)
+    v8, vd = _put(kc, ks)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    E.eagle_kv8_commit(x.cuda(), x.cuda(), k8, v8, kd, vd, _dev([start]), _dev(path), _dev([depth]), depth, dev_status=st)
+    torch.cuda.synchronize()
+    ref.kv8_commit(x.double().numpy(), [start], path, [depth], kc, ks)
+    _same(k8, kd, kc, ks)
+    _same(v8, vd, kc, ks)
+    assert int(st.item()) == E.EAGLE_DEV_NONFINITE
+
+
+def _attention_inputs(B, n, Hq, Hkv, L, Lmax, seed):
+    kc, ks = _quantised((B, Hkv), L, Lmax, seed)
+    vc, vs = _quantised((B, Hkv), L, Lmax, seed + 1)
+    parent = _dev(np.stack([W.random_tree(n, 6, seed, b) if n > 1 else np.array([-1], np.int32) for b in range(B)]))
+    q, kt, vt = (_bf16((B, n, h, D), seed + 2 + i).cuda() for i, h in enumerate((Hq, Hkv, Hkv)))
+    return (q, *sum(zip(_put(kc, ks), _put(vc, vs)), ()), kt, vt, _dev(L), parent)
+
+
+def test_tree_attention_on_two_streams_at_once():
+    """Calls of different shapes that run at the same time, a workspace each."""
+    E = _E()
+    shapes = [(3, 20, 8, 2, [1000, 300, 0], 1100), (2, 1, 16, 4, [2000, 77], 2048)]
+    args = [_attention_inputs(*s, seed=121 + 10 * i) for i, s in enumerate(shapes)]
+    want = [E.eagle_tree_attn_kv8(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    ws = [torch.empty(max(1, E.tree_attn_kv8_workspace_size(*s[:4], D, s[5])), dtype=torch.uint8, device="cuda") for s in shapes]
+    outs = [[torch.zeros_like(w) for _ in range(20)] for w in want]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i, st in enumerate(streams):
+            E.eagle_tree_attn_kv8(*args[i], out=outs[i][k], workspace=ws[i], stream=st)
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        assert all(torch.equal(o, w) for o in outs[i])
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv,L", [(1, 1, 8, 8, 2000), (2, 3, 4, 2, 5), (1, 1, 1, 1, 0), (16, 30, 8, 2, 700)])
+def test_work_queued_behind_the_attention_sees_its_output(B, n, Hq, Hkv, L):
+    """A copy right behind the call, with nothing between, and the output cleared before it."""
+    E = _E()
+    args = _attention_inputs(B, n, Hq, Hkv, [L] * B, 2048, seed=141)
+    want = E.eagle_tree_attn_kv8(*args)
+    torch.cuda.synchronize()
+    out = torch.empty_like(want)
+    got = [torch.empty_like(want) for _ in range(50)]
+    ws = torch.empty(max(1, E.tree_attn_kv8_workspace_size(B, n, Hq, Hkv, D, 2048)), dtype=torch.uint8, device="cuda")
+    for g in got:
+        out.fill_(float("nan"))
+        E.eagle_tree_attn_kv8(*args, out=out, workspace=ws)
+        g.copy_(out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_tree_attention_reports_value_scales_out_of_range():
+    """2^44 is the largest V scale; a larger one sets the status bit, in the cache or in the tree."""
+    E = _E()
+    B, n, Hq, Hkv, L, Lmax = 1, 4, 4, 1, [100], 128
+    args = list(_attention_inputs(B, n, Hq, Hkv, L, Lmax, seed=151))
+    for block, exp, bit in ((0, 44, 0), (3, 45, E.EAGLE_DEV_NONFINITE), (1, 60, E.EAGLE_DEV_NONFINITE)):
+        vd = args[4].clone()
+        vd[0, 0, block] = 2.0 ** exp
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        E.eagle_tree_attn_kv8(*args[:4], vd, *args[5:], dev_status=st)
+        assert int(st.item()) == bit
+    big = args[6].clone()
+    big[0, 2, 0, 5] = 2.0 ** 60
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    E.eagle_tree_attn_kv8(*args[:6], big, *args[7:], dev_status=st)
+    assert int(st.item()) == E.EAGLE_DEV_NONFINITE
+
+
+def _leave_nan_in_shared_memory():
+    """A prompt of nothing but NaN, on every SM: its tiles stay in shared memory and its products in TMEM."""
+    E = _E()
+    x = torch.full((400, 8, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    cu = _dev(np.arange(0, 401, 400))
+    for _ in range(4):
+        E.eagle_prompt_attn(x.repeat(16, 4, 1), x.repeat(16, 1, 1), x.repeat(16, 1, 1), _dev(np.arange(0, 6401, 400)))
+    E.eagle_prompt_attn(x, x, x, cu)
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 16, 17, 30, 40, 63, 64])
+@pytest.mark.parametrize("L", [0, 5, 130, 1000])
+def test_tree_attention_does_not_read_what_an_earlier_kernel_left(n, L):
+    B, Hq, Hkv = 40, 8, 4
+    _leave_nan_in_shared_memory()
+    _tree_check(B, n, Hq, Hkv, [L] * B, 1024, 161 + n)
+
+
+@pytest.mark.parametrize("n", [1, 5, 64, 130, 300])
+def test_prompt_attention_does_not_read_what_an_earlier_kernel_left(n):
+    E = _E()
+    B, Hq, Hkv = 50, 6, 2
+    q, k, v = _bf16((B * n, Hq, D), 171), _bf16((B * n, Hkv, D), 172), _bf16((B * n, Hkv, D), 173)
+    cu = [b * n for b in range(B + 1)]
+    _leave_nan_in_shared_memory()
+    out = E.eagle_prompt_attn(q.cuda(), k.cuda(), v.cuda(), _dev(cu))
+    torch.cuda.synchronize()
+    o, _, tol = ref.prompt_attn(q, k, v, cu, cu, D ** -0.5)
+    assert ((out.double().cpu() - o).abs() <= tol).all()
