@@ -332,7 +332,8 @@ extern "C" eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree,
     a.n_layers = n_layers; a.B = B; a.n = n; a.Hkv = Hkv; a.D = max_depth;
     a.dev_status = dev_status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // clusters of 8 while every CTA is resident at once, fewer for large batches
+    // clusters of 8 up to about two waves of CTAs, fewer for larger batches: 64 sequences of 32 layers
+    // take 31.5 us with 8, 36.5 with 4 and 43 with 2
     const int sms = cached_sm_count();
     int cs = 8;
     while (cs > 1 && (int64_t)B * cs > 4LL * sms) cs >>= 1;

@@ -24,6 +24,12 @@
 // after PV(j - 1) has read it, and the commit behind QK(j) also says that O holds PV(j - 1):
 // the softmax warps may then rescale O without a wait of its own.  P of the next unit's first
 // tile is written only after the same warps have read O of this one, which keeps O safe.
+//
+// Measured: one prompt of 16384 tokens, 32 / 8 heads, 1.51 ms = 1.45 PFLOP/s over the visible keys
+// (78% of the library GEMM's burst, 86% of its sustained rate); 8 prompts of 2048, 0.241 ms, tensor
+// pipe 53% active.  Bound: the tensor pipe and the softmax in turn (about 1450 cycles a tile), and
+// the MMA warp's control; short prompts: the ends of their units.  An MMA warp per slot took 1.72
+// against 1.61 ms: their products interleave, and both slots wait for both.
 #pragma once
 
 #include <cstddef>
