@@ -385,6 +385,8 @@ eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, 
  *            be NULL when that size is 0), 16-byte aligned; no initialisation needed.  Two
  *            calls that may run at the same time need one each.
  * Cache rows from L_b on are not used, whatever they hold; 0 <= L_b <= Lmax.
+ * Rows below L_b and the tree's n rows must be finite (a row that a node does not see is
+ * multiplied with a zero weight, which does not cancel NaN).
  * Device errors: an invalid tree or kv_len sets a dev_status bit and writes zeros for
  * that sequence; a V scale above 2^44, or a tree row of V beyond 2^52, sets
  * EAGLE_DEV_NONFINITE (the result is then not defined).
