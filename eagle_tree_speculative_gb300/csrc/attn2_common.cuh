@@ -70,9 +70,9 @@ __device__ __forceinline__ void commit_if(bool on, uint32_t bar) {
 }
 
 // The end of an MMA thread: its own products, which always end, have left the tensor cores.
-__device__ __forceinline__ void wait_drain(const uint64_t* bar) {
+__device__ __forceinline__ void wait_drain(uint32_t bar) {
     int never = 0;
-    mbar_wait(s32(bar), 0u, &never, /*honour_abort=*/false);
+    mbar_wait(bar, 0u, &never, /*honour_abort=*/false);
 }
 
 // MMA issue.  One elected lane issues, but the whole warp walks the loop, and what the loop

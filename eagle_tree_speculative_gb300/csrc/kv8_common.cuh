@@ -27,14 +27,14 @@ __device__ __forceinline__ uint32_t e4m3x2_half2(uint16_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(c));
     return h;
 }
-__device__ __forceinline__ float2 e4m3x2_float(uint16_t c) {
-    const uint32_t h = e4m3x2_half2(c);
+__device__ __forceinline__ float2 half2_float(uint32_t h) {
     float2 f;
     asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
         : "=f"(f.x), "=f"(f.y)
         : "r"(h));
     return f;
 }
+__device__ __forceinline__ float2 e4m3x2_float(uint16_t c) { return half2_float(e4m3x2_half2(c)); }
 
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }

@@ -8,8 +8,8 @@
 // instead (every e4m3 value is a half), for both slots, and PV runs in kind::f16.
 //   Q  per row times a power of two that brings its largest element to [128, 256): digits exact
 //      for elements within 2^-9 of the largest, the rest to 2^-17 of it.
-//   P  fp16, between 2^-24 and 2^14: a rounding of 2^-12 on a weight, where the largest weight is
-//      at least 2^kOffset.
+//   P  fp16, between 2^-24 and 2^14: a rounding of 2^-11 on a weight, where the largest weight is
+//      at least 2^kOffset (or bf16, see Scales).
 //   the tree's own rows (bf16, n <= 64): K as one 128-key tile with the hi digits in rows 0 .. 63
 //      and the lo digits in rows 64 .. 127 (S of key j is S[j] + S[64 + j]), V in fp16, with a
 //      power of two per row that brings its largest element to [128, 256).
@@ -18,7 +18,13 @@
 // the exponent.  2^ev joins the weight, P' = 2^(s + ev - m) with m the running maximum of s + ev:
 // then O = sum P' code needs no scale, and l = sum P' 2^-ev is one factor per block.  m is the
 // running maximum of what is multiplied with the codes, so P' uses fp16's range whatever the
-// blocks' scales are.
+// blocks' scales have in common.  What it does not hold is a wide spread: beside a block of far larger
+// scale, whose codes may well be zero in most columns, the other blocks' weights would be subnormal
+// halves or zero.  A CTA that finds the exponents of a unit's V rows spread over more than kSpread
+// goes through its units a second time, with P and V in bf16 (a rounding of 2^-8; the tree's P with
+// its remainder, its V as it is), which replaces what the first pass wrote.  Only the second
+// pass pays for that: bf16 as a case in the loops cost 5 to 10% of every call, and a copy of
+// the loops that shared values with the first ones 1 to 8%.
 //
 // Work.  A unit is one (sequence, kv head, pair of 128-row tiles), its keys in tiles of 128, the
 // tree's tile last.  With two row tiles, each slot has one and both see every key tile; a
@@ -29,7 +35,8 @@
 // A unit that is cut leaves partial (m, l, O) in the workspace, at most two per CTA; a second
 // small kernel merges them.
 //
-// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 3 cuts the work, warps 4-11 are
+// Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 2 looks for wide spreads, warp 3 cuts
+// the work, warps 4-11 are
 // the softmax, which also makes the Q digits of the next unit before it writes this one's output,
 // warps 12-15 widen V into two tiles (of two halves of 64 keys) and make the K digits of the tree's
 // rows; V rows behind the last key become zeros there (whatever bits lie in them: a zero weight
@@ -71,6 +78,10 @@ constexpr int kBlocks = kKeys / kKv8Block;        // scales per tile
 constexpr int kUnitCost = 8;
 constexpr float kOffset = 6.f, kRescale = 8.f;    // weights up to 2^14
 constexpr int kMaxVExp = 44;                      // V scales up to 2^44, see below
+// The spread of a unit's V exponents up to which its weights are fp16.  A weight that is 2^-x of the
+// largest in the product with its block's scale is off by 2^(x - 31) of itself at most, so 2^8 leaves a
+// weight of 2^-15 (one of 32k equal ones) 8 bits.
+constexpr int kSpread = 8;
 constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles
 
 struct Args {
@@ -181,15 +192,19 @@ struct Unit {
     unsigned long long anc[kMaxNodes];            // node i and its ancestors
 };
 
-struct Shared {
+struct Barriers {
     uint64_t k_full[kKStages], k_empty[kKStages], k_grant[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kWide], h_empty[kWide];
     uint64_t q_full[kSlots], s_full[kSlots], p_full[kSlots], o_full[kSlots];
     uint64_t tree_full[kTrees], merge_in, merge_out;
     uint64_t info_full[kInfo], info_empty[kInfo];
     uint64_t drain;
+};
+struct Shared {
+    Barriers bars[2];                             // of the first and the second pass
     uint32_t tmem;
     int abort_flag;
+    int wide;                                     // a unit of this CTA has a wide spread
     float2 ml[kSlots][kRows];
     // factors of the tree's rows.  Their writers run ahead of the softmax by what the K ring and S
     // hold: at most kKStages + kSlots trees, fewer than kTrees
@@ -210,12 +225,19 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
 constexpr uint32_t kIdescQK = idesc_e4m3(128, kKeys);
 // kind::f16 with A and B fp16 (format 0), B MN-major, D fp32
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(kHeadDim >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPVbf = idesc_bf16(128, kHeadDim, 0, 1);         // the same in bf16
 
 // Two floats as an fp16 pair (round to nearest even), lo in the low half.
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Two halves that hold e4m3 values as a bf16 pair (exact).
+__device__ __forceinline__ uint32_t half2_bf162(uint32_t h) {
+    const float2 f = kv8::half2_float(h);
+    return pack2(f.x, f.y);
 }
 
 // The leading digit of x: its significand cut to 4 bits, a value that e4m3 holds exactly (for
@@ -269,42 +291,54 @@ __device__ __forceinline__ int row_exp(const uint4& v, int lo_exp) {
     return digit_exp(m, lo_exp);
 }
 
+// All threads of the CTA, wherever in the roles' code they are.
+__device__ __forceinline__ void all_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kThreads) : "memory"); }
+
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, Args a) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    uint8_t* sQ = smem;                                   // [slot][hi, lo][16 KB]
-    uint8_t* sK = sQ + kSlots * 2 * kTile;                // [kKStages][16 KB]
-    uint8_t* sV = sK + kKStages * kTile;                  // [kVStages][16 KB]
-    uint8_t* sH = sV + kVStages * kTile;                  // [kWide][2 halves][2 boxes of 64 dims][64 keys][128 B]
-    Shared* sh = reinterpret_cast<Shared*>(sH + 2 * kWide * kTile);
+    uint32_t at = (0u - s32(smem_raw)) & 1023u;           // tiles begin at a multiple of 1024
+    uint8_t *sQ, *sK, *sV, *sH;
+    Shared* sh;
+    auto place = [&]() {
+        sQ = smem_raw + at;                               // [slot][hi, lo][16 KB]
+        sK = sQ + kSlots * 2 * kTile;                     // [kKStages][16 KB]
+        sV = sK + kKStages * kTile;                       // [kVStages][16 KB]
+        sH = sV + kVStages * kTile;                       // [kWide][2 halves][2 boxes of 64 dims][64 keys][128 B]
+        sh = reinterpret_cast<Shared*>(sH + 2 * kWide * kTile);
+    };
+    place();
     volatile int* abort_flag = &sh->abort_flag;
     // barriers by their 32-bit shared addresses: 64-bit pointer arithmetic in the control of the MMA
     // warp is time that the tensor cores wait
-    const uint32_t sb = s32(sh);
-#define BAR(name) (sb + (uint32_t)offsetof(Shared, name))
-#define BAR_AT(name, i) (sb + (uint32_t)offsetof(Shared, name) + 8u * (uint32_t)(i))
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t sb = s32(&sh->bars[0]);
+#define BAR(name) (sb + (uint32_t)offsetof(Barriers, name))
+#define BAR_AT(name, i) (sb + (uint32_t)offsetof(Barriers, name) + 8u * (uint32_t)(i))
+    const int tid = threadIdx.x, warp = tid >> 5;
+    int lane = tid & 31;
 
-    if (tid == 0) {
-        for (int i = 0; i < kKStages; ++i) { mbar_init(s32(&sh->k_full[i]), 4); mbar_init(s32(&sh->k_empty[i]), 1); mbar_init(s32(&sh->k_grant[i]), 1); }
-        for (int i = 0; i < kVStages; ++i) { mbar_init(s32(&sh->v_full[i]), 1); mbar_init(s32(&sh->v_empty[i]), 4); }
-        for (int i = 0; i < kWide; ++i) { mbar_init(s32(&sh->h_full[i]), 4); mbar_init(s32(&sh->h_empty[i]), 1); }
+    auto init_barriers = [&]() {
+        for (int i = 0; i < kKStages; ++i) { mbar_init(BAR_AT(k_full, i), 4); mbar_init(BAR_AT(k_empty, i), 1); mbar_init(BAR_AT(k_grant, i), 1); }
+        for (int i = 0; i < kVStages; ++i) { mbar_init(BAR_AT(v_full, i), 1); mbar_init(BAR_AT(v_empty, i), 4); }
+        for (int i = 0; i < kWide; ++i) { mbar_init(BAR_AT(h_full, i), 4); mbar_init(BAR_AT(h_empty, i), 1); }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(s32(&sh->q_full[s]), 4);
-            mbar_init(s32(&sh->s_full[s]), 1);
-            mbar_init(s32(&sh->p_full[s]), 4);
-            mbar_init(s32(&sh->o_full[s]), 1);
+            mbar_init(BAR_AT(q_full, s), 4);
+            mbar_init(BAR_AT(s_full, s), 1);
+            mbar_init(BAR_AT(p_full, s), 4);
+            mbar_init(BAR_AT(o_full, s), 1);
         }
-        for (int i = 0; i < kTrees; ++i) mbar_init(s32(&sh->tree_full[i]), 4);
-        mbar_init(s32(&sh->merge_in), 8);
-        mbar_init(s32(&sh->merge_out), 8);
-        // read by warps 0 and 1, the eight softmax and the four widening warps
-        for (int i = 0; i < kInfo; ++i) { mbar_init(s32(&sh->info_full[i]), 1); mbar_init(s32(&sh->info_empty[i]), 14); }
-        mbar_init(s32(&sh->drain), 1);
-        sh->abort_flag = 0;
+        for (int i = 0; i < kTrees; ++i) mbar_init(BAR_AT(tree_full, i), 4);
+        mbar_init(BAR(merge_in), 8);
+        mbar_init(BAR(merge_out), 8);
+        // read by warps 0, 1 and 2, the eight softmax and the four widening warps
+        for (int i = 0; i < kInfo; ++i) { mbar_init(BAR_AT(info_full, i), 1); mbar_init(BAR_AT(info_empty, i), 15); }
+        mbar_init(BAR(drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    };
+    if (tid == 0) {
+        sh->abort_flag = 0;
+        sh->wide = 0;
+        init_barriers();
     }
     if (warp == 1) tmem_alloc(s32(&sh->tmem), attn2::kTmemCols);
     // the merging kernel may be launched as CTAs of this one end; it waits for all of them itself
@@ -312,7 +346,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh->tmem;
+    uint32_t tmem = sh->tmem;
 
     // the i-th unit of this CTA; nullptr at the end (or on abort)
     auto next_unit = [&](int i) -> const Unit* {
@@ -320,47 +354,67 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         const Unit* u = &sh->info[i % kInfo];
         return u->head >= 0 ? u : nullptr;
     };
+    // Every role's end of the first pass over this CTA's units: whether a second one follows.  It has
+    // barriers of its own: arrivals that nobody awaited may still be on their way to the first ones.
+    auto again = [&]() {
+        __syncwarp();
+        tc_fence_before();
+        all_sync();
+        tc_fence_after();
+        if (!sh->wide || *abort_flag) return false;
+        sb += (uint32_t)sizeof(Barriers);
+        // values that the compiler is not to take from the first pass: it would compute there what
+        // only the second one needs, and keep it
+        asm volatile("" : "+r"(lane), "+r"(sb), "+r"(tmem), "+r"(at));
+        place();
+        if (tid == 0) init_barriers();
+        all_sync();
+        return true;
+    };
     auto unit_read = [&](int i) { attn2::arrive_if(lane == 0, BAR_AT(info_empty, i % kInfo)); };
 
     if (warp < 4) {
         attn2::regs_dec<kRegsOther>();
         if (warp == 0) {
             // ---------------- K and V tiles ----------------
-            uint32_t ks = 0, kp = 1, vs = 0, vp = 1;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                const Unit* up = next_unit(i);
-                if (!__all_sync(0xffffffffu, up != nullptr)) break;
-                const int t0 = up->t0, nc = up->n - up->tree, tree = up->tree, z = up->b * a.Hkv + up->head;
-                __syncwarp();
-                unit_read(i);
+            for (int pass = 0;; ++pass) {
+                uint32_t ks = 0, kp = 1, vs = 0, vp = 1;
+                bool ok = true;
+                for (int i = 0; ok; ++i) {
+                    const Unit* up = next_unit(i);
+                    if (!__all_sync(0xffffffffu, up != nullptr)) break;
+                    const int t0 = up->t0, nc = up->n - up->tree, tree = up->tree, z = up->b * a.Hkv + up->head;
+                    __syncwarp();
+                    unit_read(i);
 #pragma unroll 1
-                for (int j = 0; ok && j < nc; ++j) {
-                    const bool k_free = attn2::wait_for(BAR_AT(k_empty, ks), kp, abort_flag);
-                    ok = __all_sync(0xffffffffu, k_free);
-                    attn2::arrive_if(ok && lane > 0 && lane < 4, BAR_AT(k_full, ks));     // four arrivals, as for the tree's
-                    if (ok && lane == 0) {
-                        mbar_expect_tx(s32(&sh->k_full[ks]), kTile);
-                        tma_load_3d(s32(sK + ks * kTile), &map_k, s32(&sh->k_full[ks]), 0, (t0 + j) * kKeys, z);
+                    for (int j = 0; ok && j < nc; ++j) {
+                        const bool k_free = attn2::wait_for(BAR_AT(k_empty, ks), kp, abort_flag);
+                        ok = __all_sync(0xffffffffu, k_free);
+                        attn2::arrive_if(ok && lane > 0 && lane < 4, BAR_AT(k_full, ks));     // four arrivals, as for the tree's
+                        if (ok && lane == 0) {
+                            mbar_expect_tx(BAR_AT(k_full, ks), kTile);
+                            tma_load_3d(s32(sK + ks * kTile), &map_k, BAR_AT(k_full, ks), 0, (t0 + j) * kKeys, z);
+                        }
+                        if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                        const bool v_free = ok && attn2::wait_for(BAR_AT(v_empty, vs), vp, abort_flag);
+                        ok = __all_sync(0xffffffffu, v_free);
+                        if (ok && lane == 0) {
+                            mbar_expect_tx(BAR_AT(v_full, vs), kTile);
+                            tma_load_3d(s32(sV + vs * kTile), &map_v, BAR_AT(v_full, vs), 0, (t0 + j) * kKeys, z);
+                        }
+                        if (++vs == kVStages) { vs = 0; vp ^= 1u; }
                     }
-                    if (++ks == kKStages) { ks = 0; kp ^= 1u; }
-                    const bool v_free = ok && attn2::wait_for(BAR_AT(v_empty, vs), vp, abort_flag);
-                    ok = __all_sync(0xffffffffu, v_free);
-                    if (ok && lane == 0) {
-                        mbar_expect_tx(s32(&sh->v_full[vs]), kTile);
-                        tma_load_3d(s32(sV + vs * kTile), &map_v, s32(&sh->v_full[vs]), 0, (t0 + j) * kKeys, z);
+                    if (ok && tree) {
+                        // the tree's stage is the widening warps' to fill.  They do not follow this
+                        // ring, and a parity names a phase only to a waiter that is at most one
+                        // behind, so the stage is handed over when it is free
+                        const bool free = attn2::wait_for(BAR_AT(k_empty, ks), kp, abort_flag);
+                        ok = __all_sync(0xffffffffu, free);
+                        attn2::arrive_if(ok && lane == 0, BAR_AT(k_grant, ks));
+                        if (++ks == kKStages) { ks = 0; kp ^= 1u; }
                     }
-                    if (++vs == kVStages) { vs = 0; vp ^= 1u; }
                 }
-                if (ok && tree) {
-                    // the tree's stage is the widening warps' to fill.  They do not follow this
-                    // ring, and a parity names a phase only to a waiter that is at most one
-                    // behind, so the stage is handed over when it is free
-                    const bool free = attn2::wait_for(BAR_AT(k_empty, ks), kp, abort_flag);
-                    ok = __all_sync(0xffffffffu, free);
-                    attn2::arrive_if(ok && lane == 0, BAR_AT(k_grant, ks));
-                    if (++ks == kKStages) { ks = 0; kp ^= 1u; }
-                }
+                if (pass > 0 || !again()) break;
             }
         } else if (warp == 1) {
             // ---------------- MMA issue ----------------
@@ -368,609 +422,684 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             // warp per slot they interleave, and both slots wait for both).  This warp's control
             // is what the tensor pipe waits for: steps have their slot as a template argument, loads
             // are waited for before P is, and no lane's instruction stands in a branch.
-            const bool leader = attn2::elect_lane();
-            const uint32_t on = leader;
-            const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
-            const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
-            uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;    // ring places, phases
-            bool ok = true;
-            // (a wait that gives up lets the step run on, on data that nobody will use)
-            auto wait = [&](uint32_t bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
-            // O of slot s += P V of the tile at the ring's place, then S = Q K^T of the next tile there.
-            // opens, closes: the tiles' first, last use
-            auto step = [&](auto slot_c, bool pv, bool pv_first, bool pv_last, bool two, bool qk, bool qk_first, bool opens, bool closes) {
-                constexpr int s = decltype(slot_c)::value;
-                const uint32_t scol = tm + attn2::s_col(s), ocol = tm + attn2::o_col(s);
-                if (opens && pv) wait(BAR_AT(h_full, hs), hp);
-                if (opens && qk) wait(BAR_AT(k_full, ks), kp);
-                if (qk && qk_first) {
-                    wait(BAR_AT(q_full, s), qph >> s);
-                    qph ^= 1u << s;
-                }
-                if (pv) {
-                    wait(BAR_AT(p_full, s), pph >> s);
-                    pph ^= 1u << s;
-                    tc_fence_after();
-                    const uint32_t dv = dh0 + ((hs * 2 * kTile) >> 4);
-                    attn2::mma_ts(on, ocol, scol, dv, kIdescPV, pv_first ? 0u : 1u);
+            auto pass = [&](auto wide) {
+                constexpr bool kBf = decltype(wide)::value;
+                const bool leader = attn2::elect_lane();
+                const uint32_t on = leader;
+                const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
+                const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sK)), dh0 = attn2::desc_lo_mn(s32(sH), kHalfBox);
+                uint32_t ks = 0, kp = 0, hs = 0, hp = 0, qph = 0, pph = 0;    // ring places, phases
+                bool ok = true;
+                // (a wait that gives up lets the step run on, on data that nobody will use)
+                auto wait = [&](uint32_t bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
+                // O of slot s += P V of the tile at the ring's place, then S = Q K^T of the next tile there.
+                // two: a tile of 128 keys (the tree's is one half; in bf16 its weights are two parts of 64
+                // keys, both on that half's rows).  opens, closes: the tiles' first, last use
+                auto step = [&](auto slot_c, bool pv, bool pv_first, bool pv_last, bool two, bool qk, bool qk_first, bool opens, bool closes) {
+                    constexpr int s = decltype(slot_c)::value;
+                    const uint32_t scol = tm + attn2::s_col(s), ocol = tm + attn2::o_col(s);
+                    if (opens && pv) wait(BAR_AT(h_full, hs), hp);
+                    if (opens && qk) wait(BAR_AT(k_full, ks), kp);
+                    if (qk && qk_first) {
+                        wait(BAR_AT(q_full, s), qph >> s);
+                        qph ^= 1u << s;
+                    }
+                    if (pv) {
+                        wait(BAR_AT(p_full, s), pph >> s);
+                        pph ^= 1u << s;
+                        tc_fence_after();
+                        constexpr uint32_t id = kBf ? kIdescPVbf : kIdescPV;
+                        const uint32_t dv = dh0 + ((hs * 2 * kTile) >> 4), dv2 = dv + (kBf && !two ? 0 : kTile >> 4);
+                        attn2::mma_ts(on, ocol, scol, dv, id, pv_first ? 0u : 1u);
 #pragma unroll
-                    for (int k = 1; k < kHalfKeys / 16; ++k)
-                        attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, 1u);
-                    const uint32_t on2 = leader && two;
+                        for (int k = 1; k < kHalfKeys / 16; ++k)
+                            attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), id, 1u);
+                        const uint32_t on2 = leader && (kBf || two);
 #pragma unroll
-                    for (int k = 0; k < kHalfKeys / 16; ++k)
-                        attn2::mma_ts(on2, ocol, scol + 32 + 8 * k, dv + ((kTile + k * 16 * 128) >> 4), kIdescPV, 1u);
-                }
-                if (qk) {
-                    tc_fence_after();
-                    const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
+                        for (int k = 0; k < kHalfKeys / 16; ++k)
+                            attn2::mma_ts(on2, ocol, scol + 32 + 8 * k, dv2 + ((k * 16 * 128) >> 4), id, 1u);
+                    }
+                    if (qk) {
+                        tc_fence_after();
+                        const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((2 * s * kTile) >> 4);
 #pragma unroll
-                    for (int d = 0; d < 2; ++d)                           // both digits of Q
+                        for (int d = 0; d < 2; ++d)                           // both digits of Q
 #pragma unroll
-                        for (int k = 0; k < kHeadDim / 32; ++k)
-                            attn2::mma_ss<true>(on, scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
-                    attn2::commit_if(leader, BAR_AT(s_full, s));
+                            for (int k = 0; k < kHeadDim / 32; ++k)
+                                attn2::mma_ss<true>(on, scol, dq + ((d * kTile) >> 4) + 2 * k, dk + 2 * k, kIdescQK, (d | k) ? 1u : 0u);
+                        attn2::commit_if(leader, BAR_AT(s_full, s));
+                    }
+                    attn2::commit_if(leader && pv && pv_last, BAR_AT(o_full, s));
+                    if (closes && pv) {
+                        attn2::commit_if(leader, BAR_AT(h_empty, hs));
+                        hs ^= 1u;
+                        hp ^= hs == 0;
+                    }
+                    if (closes && qk) {
+                        attn2::commit_if(leader, BAR_AT(k_empty, ks));
+                        if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                    }
+                };
+                const std::integral_constant<int, 0> s0;
+                const std::integral_constant<int, 1> s1;
+                for (int i = 0; ok; ++i) {
+                    const Unit* up = next_unit(i);
+                    if (!__all_sync(0xffffffffu, up != nullptr)) break;
+                    const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);     // the tree's tile is one half
+                    const int alt = attn2::uniform_of(up->split_keys);
+                    __syncwarp();
+                    unit_read(i);
+                    if (n == 0) continue;
+                    if (alt) {                                // tile t is slot t & 1's
+#pragma unroll 1
+                        for (int t = 0; t < n + 2 && __all_sync(0xffffffffu, ok); t += 2) {
+                            step(s0, t >= 2, t == 2, t >= n, t - 2 < nc, t < n, t == 0, true, true);
+                            step(s1, t >= 2 && t - 1 < n, t == 2, t + 1 >= n, t - 1 < nc, t + 1 < n, t == 0, true, true);
+                        }
+                    } else {                                  // every tile is both slots'
+#pragma unroll 1
+                        for (int t = 0; t <= n && __all_sync(0xffffffffu, ok); ++t) {
+                            step(s0, t > 0, t == 1, t == n, t - 1 < nc, t < n, t == 0, true, false);
+                            step(s1, t > 0, t == 1, t == n, t - 1 < nc, t < n, t == 0, false, true);
+                        }
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
                 }
-                attn2::commit_if(leader && pv && pv_last, BAR_AT(o_full, s));
-                if (closes && pv) {
-                    attn2::commit_if(leader, BAR_AT(h_empty, hs));
-                    hs ^= 1u;
-                    hp ^= hs == 0;
-                }
-                if (closes && qk) {
-                    attn2::commit_if(leader, BAR_AT(k_empty, ks));
-                    if (++ks == kKStages) { ks = 0; kp ^= 1u; }
+                if (leader) {
+                    umma_commit(BAR(drain));
+                    attn2::wait_drain(BAR(drain));
                 }
             };
-            const std::integral_constant<int, 0> s0;
-            const std::integral_constant<int, 1> s1;
-            for (int i = 0; ok; ++i) {
-                const Unit* up = next_unit(i);
-                if (!__all_sync(0xffffffffu, up != nullptr)) break;
-                const int n = attn2::uniform_of(up->n), nc = n - attn2::uniform_of(up->tree);     // the tree's tile is one half
-                const int alt = attn2::uniform_of(up->split_keys);
-                __syncwarp();
-                unit_read(i);
-                if (n == 0) continue;
-                if (alt) {                                // tile t is slot t & 1's
-#pragma unroll 1
-                    for (int t = 0; t < n + 2 && __all_sync(0xffffffffu, ok); t += 2) {
-                        step(s0, t >= 2, t == 2, t >= n, t - 2 < nc, t < n, t == 0, true, true);
-                        step(s1, t >= 2 && t - 1 < n, t == 2, t + 1 >= n, t - 1 < nc, t + 1 < n, t == 0, true, true);
+            pass(std::false_type{});
+            if (again()) pass(std::true_type{});
+        } else if (warp == 2) {
+            // ---------------- the spread of each unit's V exponents ----------------
+            for (int pass = 0;; ++pass) {
+                for (int i = 0;; ++i) {
+                    const Unit* u = next_unit(i);
+                    if (!__all_sync(0xffffffffu, u != nullptr)) break;
+                    int top = 0, low = 255;               // exponents as stored
+                    const int end = min((u->L + kKv8Block - 1) / kKv8Block, (u->t0 + u->n) * kBlocks);
+                    const float* scales = a.v_scale + ((int64_t)u->b * a.Hkv + u->head) * a.NB;
+                    for (int y = u->t0 * kBlocks; y < end; y += 128)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e = (int)(__float_as_uint(__ldg(scales + min(y + 32 * k + lane, end - 1))) >> 23);
+                            top = max(top, e);
+                            low = min(low, e);
+                        }
+                    const uint16_t* x = a.v_tree + ((int64_t)u->b * a.n * a.Hkv + u->head) * kHeadDim + (lane & 15) * 8;
+                    for (int r0 = lane >> 4; u->tree && r0 - (lane >> 4) < a.n; r0 += 4) {
+                        uint4 v[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int e = row_exp(v[k], -127) + 127;
+                            if (e == 0) continue;         // below 2^-120: a row of zeros, or as good as one
+                            top = max(top, e);
+                            low = min(low, e);
+                        }
                     }
-                } else {                                  // every tile is both slots'
-#pragma unroll 1
-                    for (int t = 0; t <= n && __all_sync(0xffffffffu, ok); ++t) {
-                        step(s0, t > 0, t == 1, t == n, t - 1 < nc, t < n, t == 0, true, false);
-                        step(s1, t > 0, t == 1, t == n, t - 1 < nc, t < n, t == 0, false, true);
-                    }
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    low = __reduce_min_sync(0xffffffffu, low);
+                    if (lane == 0 && (top - low > kSpread || low < kv8::kMinExp + 127)) sh->wide = 1;
+                    unit_read(i);
                 }
-                ok = __all_sync(0xffffffffu, ok);
-            }
-            if (leader) {
-                umma_commit(s32(&sh->drain));
-                attn2::wait_drain(&sh->drain);
+                if (pass > 0 || !again()) break;
             }
         } else if (warp == 3) {
             // ---------------- the cut ----------------
-            const Cut cut = make_cut(a, gridDim.x);
-            const bool mine = (int)blockIdx.x < cut.ctas;
-            int pos = mine ? cut.begin(blockIdx.x) : 0, base = 0;
-            const int end = mine ? cut.begin(blockIdx.x + 1) : 0;
-            int b = 0, anc_of = -1, bits = 0;
-            unsigned long long anc[2] = {0, 0};           // of nodes lane and lane + 32
-            bool bad_tree = false;
-            bool have = true;
-            for (int i = 0; have; ++i) {
-                Segment s;
-                have = false;
-                while (!have && pos < end) {
-                    s = segment_at(a, pos, end, b, base);
-                    pos = s.start + s.weight * (s.T + kUnitCost);
-                    have = s.t0 < s.t1;
-                }
-                const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) break;
-                Unit* u = &sh->info[i % kInfo];
-                if (!have) {
-                    if (lane == 0) u->head = -1;
-                } else {
-                    if (s.b != anc_of) {
-                        // anc: each round doubles how far up a node's set reaches
-                        anc_of = s.b;
-                        int p[2];
-                        bool bad = false;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int i2 = lane + 32 * h;
-                            p[h] = i2 < a.n ? a.parent[(int64_t)s.b * a.n + i2] : -1;
-                            if (i2 < a.n && (i2 == 0 ? p[h] != -1 : (p[h] < 0 || p[h] >= i2))) bad = true;
-                            anc[h] = 1ull << i2;
-                        }
-                        bad_tree = __any_sync(0xffffffffu, bad);
-#pragma unroll 1
-                        for (int round = 0; !bad_tree && round < 6; ++round) {
-                            unsigned long long add[2];
-                            int up[2];
+            for (int pass = 0;; ++pass) {
+                const Cut cut = make_cut(a, gridDim.x);
+                const bool mine = (int)blockIdx.x < cut.ctas;
+                int pos = mine ? cut.begin(blockIdx.x) : 0, base = 0;
+                const int end = mine ? cut.begin(blockIdx.x + 1) : 0;
+                int b = 0, anc_of = -1, bits = 0;
+                unsigned long long anc[2] = {0, 0};           // of nodes lane and lane + 32
+                bool bad_tree = false;
+                bool have = true;
+                for (int i = 0; have; ++i) {
+                    Segment s;
+                    have = false;
+                    while (!have && pos < end) {
+                        s = segment_at(a, pos, end, b, base);
+                        pos = s.start + s.weight * (s.T + kUnitCost);
+                        have = s.t0 < s.t1;
+                    }
+                    const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    Unit* u = &sh->info[i % kInfo];
+                    if (!have) {
+                        if (lane == 0) u->head = -1;
+                    } else {
+                        if (s.b != anc_of) {
+                            // anc: each round doubles how far up a node's set reaches
+                            anc_of = s.b;
+                            int p[2];
+                            bool bad = false;
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const int src = p[h] < 0 ? 0 : p[h];
-                                const unsigned long long x0 = __shfl_sync(0xffffffffu, anc[0], src & 31);
-                                const unsigned long long x1 = __shfl_sync(0xffffffffu, anc[1], src & 31);
-                                const int y0 = __shfl_sync(0xffffffffu, p[0], src & 31);
-                                const int y1 = __shfl_sync(0xffffffffu, p[1], src & 31);
-                                add[h] = p[h] < 0 ? 0ull : (src < 32 ? x0 : x1);
-                                up[h] = p[h] < 0 ? -1 : (src < 32 ? y0 : y1);
+                                const int i2 = lane + 32 * h;
+                                p[h] = i2 < a.n ? a.parent[(int64_t)s.b * a.n + i2] : -1;
+                                if (i2 < a.n && (i2 == 0 ? p[h] != -1 : (p[h] < 0 || p[h] >= i2))) bad = true;
+                                anc[h] = 1ull << i2;
                             }
+                            bad_tree = __any_sync(0xffffffffu, bad);
+#pragma unroll 1
+                            for (int round = 0; !bad_tree && round < 6; ++round) {
+                                unsigned long long add[2];
+                                int up[2];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) { anc[h] |= add[h]; p[h] = up[h]; }
+                                for (int h = 0; h < 2; ++h) {
+                                    const int src = p[h] < 0 ? 0 : p[h];
+                                    const unsigned long long x0 = __shfl_sync(0xffffffffu, anc[0], src & 31);
+                                    const unsigned long long x1 = __shfl_sync(0xffffffffu, anc[1], src & 31);
+                                    const int y0 = __shfl_sync(0xffffffffu, p[0], src & 31);
+                                    const int y1 = __shfl_sync(0xffffffffu, p[1], src & 31);
+                                    add[h] = p[h] < 0 ? 0ull : (src < 32 ? x0 : x1);
+                                    up[h] = p[h] < 0 ? -1 : (src < 32 ? y0 : y1);
+                                }
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) { anc[h] |= add[h]; p[h] = up[h]; }
+                            }
+                        }
+                        const int L = a.kv_len[s.b];
+                        const bool bad_len = L < 0 || L > a.Lmax;
+                        if ((bad_len || bad_tree) && s.head == 0 && s.pair == 0 && s.t0 == 0)
+                            bits |= (bad_len ? EAGLE_DEV_CAPACITY : 0) | (bad_tree ? EAGLE_DEV_BAD_TREE : 0);
+                        const bool zero = bad_len || bad_tree;
+                        u->anc[lane] = anc[0];
+                        u->anc[lane + 32] = anc[1];
+                        if (lane == 0) {
+                            u->b = s.b; u->head = s.head; u->pair = s.pair;
+                            u->t0 = s.t0;
+                            u->n = zero ? 0 : s.t1 - s.t0;
+                            u->tree = !zero && s.t1 == s.T;
+                            u->L = zero ? 0 : L;
+                            u->split_keys = s.weight == 1;
+                            u->part = s.t0 == 0 && s.t1 == s.T ? -1 : (int)blockIdx.x * 2 + (s.t0 == 0);
                         }
                     }
-                    const int L = a.kv_len[s.b];
-                    const bool bad_len = L < 0 || L > a.Lmax;
-                    if ((bad_len || bad_tree) && s.head == 0 && s.pair == 0 && s.t0 == 0)
-                        bits |= (bad_len ? EAGLE_DEV_CAPACITY : 0) | (bad_tree ? EAGLE_DEV_BAD_TREE : 0);
-                    const bool zero = bad_len || bad_tree;
-                    u->anc[lane] = anc[0];
-                    u->anc[lane + 32] = anc[1];
-                    if (lane == 0) {
-                        u->b = s.b; u->head = s.head; u->pair = s.pair;
-                        u->t0 = s.t0;
-                        u->n = zero ? 0 : s.t1 - s.t0;
-                        u->tree = !zero && s.t1 == s.T;
-                        u->L = zero ? 0 : L;
-                        u->split_keys = s.weight == 1;
-                        u->part = s.t0 == 0 && s.t1 == s.T ? -1 : (int)blockIdx.x * 2 + (s.t0 == 0);
+                    __syncwarp();
+                    attn2::arrive_if(lane == 0, BAR_AT(info_full, i % kInfo));
+                    if (have) {
+                        // the unit's rows of Q and of the tree go into L2 meanwhile
+                        const char* qr = reinterpret_cast<const char*>(a.q + ((int64_t)s.b * a.n * a.Hq + s.head * a.G) * kHeadDim);
+                        const int64_t tree_at = ((int64_t)s.b * a.n * a.Hkv + s.head) * kHeadDim;
+                        for (int y = lane; y < a.n; y += 32) {
+                            prefetch_l2(a.k_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
+                            prefetch_l2(a.v_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
+                            for (int g = 0; g < a.G; ++g) prefetch_l2(qr + ((int64_t)y * a.Hq + g) * kHeadDim * 2);
+                        }
                     }
                 }
-                __syncwarp();
-                attn2::arrive_if(lane == 0, BAR_AT(info_full, i % kInfo));
-                if (have) {
-                    // the unit's rows of Q and of the tree go into L2 meanwhile
-                    const char* qr = reinterpret_cast<const char*>(a.q + ((int64_t)s.b * a.n * a.Hq + s.head * a.G) * kHeadDim);
-                    const int64_t tree_at = ((int64_t)s.b * a.n * a.Hkv + s.head) * kHeadDim;
-                    for (int y = lane; y < a.n; y += 32) {
-                        prefetch_l2(a.k_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
-                        prefetch_l2(a.v_tree + tree_at + (int64_t)y * a.Hkv * kHeadDim);
-                        for (int g = 0; g < a.G; ++g) prefetch_l2(qr + ((int64_t)y * a.Hq + g) * kHeadDim * 2);
-                    }
-                }
+                if (bits) flag_error(a.dev_status, bits);
+                if (pass > 0 || !again()) break;
             }
-            if (bits) flag_error(a.dev_status, bits);
         }
     } else if (warp < 12) {
         // ---------------- softmax: one thread per query row ----------------
         attn2::regs_inc<kRegsSoftmax>();
-        const int slot = (warp - 4) >> 2;
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lane_base + attn2::s_col(slot);
-        const uint32_t o_addr = tmem + lane_base + attn2::o_col(slot);
-        uint32_t tiles_done = 0, units_done = 0, merges = 0, trees = 0;
-        int bits = 0;
+        auto pass = [&](auto wide) {
+            constexpr bool kBf = decltype(wide)::value;
+            const int slot = (warp - 4) >> 2;
+            const int row = (warp & 3) * 32 + lane;
+            const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_addr = tmem + lane_base + attn2::s_col(slot);
+            const uint32_t o_addr = tmem + lane_base + attn2::o_col(slot);
+            uint32_t tiles_done = 0, units_done = 0, merges = 0, trees = 0;
+            int bits = 0;
 
-        // Everything that a unit is stays in shared memory until its output is written; this thread
-        // keeps its row (node * G + g, -1: nobody's), the row's ancestors and its factor from S to
-        // log2 units, without the key's scale.
-        int row_of = -1, alt = 0;
-        unsigned long long anc = 0;
-        float sc = 0.f;
-        // the i-th unit: its Q digits; false at the end
-        auto begin_unit = [&](int i, int& row_next, unsigned long long& anc_next, float& sc_next) {
-            const Unit* up = next_unit(i);
-            if (!__all_sync(0xffffffffu, up != nullptr)) return false;
-            const int r = up->pair * 2 * kRows + (up->split_keys ? 0 : slot * kRows) + row;
-            row_next = r < a.n * a.G ? r : -1;
-            const int node = row_next < 0 ? 0 : r / a.G;
-            anc_next = up->anc[node];
-            // a slot without a tile leaves Q (and its barrier) alone: it could be units ahead
-            if (up->n <= (up->split_keys ? slot : 0)) return true;
-            // every QK of this slot's last unit has completed (its S was read): Q may be replaced.
-            // The warp makes its 32 rows' digits together, two rows at once, sixteen lanes a row.
-            const int my_off = row_next < 0 ? -1 : node * a.Hq + (r - node * a.G);
-            const uint16_t* src = a.q + ((int64_t)up->b * a.n * a.Hq + up->head * a.G) * kHeadDim + (lane & 15) * 8;
-            uint8_t* dst = sQ + slot * 2 * kTile;
-            int e_mine = 0;
-            const int count = __popc(__ballot_sync(0xffffffffu, row_next >= 0));   // rows of this warp that exist, its first ones
+            // Everything that a unit is stays in shared memory until its output is written; this thread
+            // keeps its row (node * G + g, -1: nobody's), the row's ancestors and its factor from S to
+            // log2 units, without the key's scale.
+            int row_of = -1, alt = 0;
+            unsigned long long anc = 0;
+            float sc = 0.f;
+            // the i-th unit: its Q digits; false at the end
+            auto begin_unit = [&](int i, int& row_next, unsigned long long& anc_next, float& sc_next) {
+                const Unit* up = next_unit(i);
+                if (!__all_sync(0xffffffffu, up != nullptr)) return false;
+                const int r = up->pair * 2 * kRows + (up->split_keys ? 0 : slot * kRows) + row;
+                row_next = r < a.n * a.G ? r : -1;
+                const int node = row_next < 0 ? 0 : r / a.G;
+                anc_next = up->anc[node];
+                // a slot without a tile leaves Q (and its barrier) alone: it could be units ahead
+                if (up->n <= (up->split_keys ? slot : 0)) return true;
+                // every QK of this slot's last unit has completed (its S was read): Q may be replaced.
+                // The warp makes its 32 rows' digits together, two rows at once, sixteen lanes a row.
+                const int my_off = row_next < 0 ? -1 : node * a.Hq + (r - node * a.G);
+                const uint16_t* src = a.q + ((int64_t)up->b * a.n * a.Hq + up->head * a.G) * kHeadDim + (lane & 15) * 8;
+                uint8_t* dst = sQ + slot * 2 * kTile;
+                int e_mine = 0;
+                const int count = __popc(__ballot_sync(0xffffffffu, row_next >= 0));   // rows of this warp that exist, its first ones
 #pragma unroll 1
-            for (int r0 = 0; r0 < count; r0 += 16) {
-                uint4 v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    // a row that does not exist takes the first one's place in the load: loads
-                    // under a condition each wait for the one before
-                    const int off = max(__shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4)), 0);
-                    v[k] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim));
-                }
-#pragma unroll 1
-                for (int k = 0; k < 8; k += 4) {                         // four row pairs at once, to hide their latencies
-                    int e[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int rr = r0 + 2 * (k + y) + (lane >> 4), at = (warp & 3) * 32 + rr;
-                        uint32_t hi[2], lo[2];
-                        digits8(v[y], kv8::exp2i(-e[y]), hi, lo);
-                        *reinterpret_cast<uint2*>(dst + swz(at, 8 * (lane & 15))) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
-                        const int e_of = __shfl_sync(0xffffffffu, e[y], (lane & 1) << 4);   // of row r0 + 2 (k + y) + (lane & 1)
-                        if ((lane >> 1) == (r0 >> 1) + k + y) e_mine = e_of;
-                    }
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) v[y] = v[y + 4];         // the loop's body exists once
-                }
-            }
-            sc_next = a.scale_log2 * kv8::exp2i(e_mine);
-            attn2::fence_async_shared();
-            __syncwarp();
-            attn2::arrive_if(lane == 0, BAR_AT(q_full, slot));
-            return true;
-        };
-
-        // Per unit: the Q digits of the next one go in, so that its first products can run during
-        // this one's output; then this one's output; then the next one's tiles.
-        bool have = true, ok = true, idle = true;
-        float mref = 0.f;
-        uint64_t l2 = 0;                                                 // two partial sums of the weights
-        int mine = 0;                                                    // tiles of this slot
-        for (int i = 0; have && ok; ++i) {
-            int row_next = -1;
-            unsigned long long anc_next = 0;
-            float sc_next = 0.f;
-            have = begin_unit(i, row_next, anc_next, sc_next);
-            if (i > 0) {
-                const Unit* u = &sh->info[(i - 1) % kInfo];
-                if (mine > 0) {
-                    const bool got = attn2::wait_for(BAR_AT(o_full, slot), units_done & 1u, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    ++units_done;
-                    tc_fence_after();
-                }
-                float la, lb;
-                attn2::unf2(l2, la, lb);
-                float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
-                bool use0 = mine > 0, use1 = false;
-                const int c0 = alt ? 64 * slot : 0, c1 = alt ? c0 + 64 : kHeadDim;
-                uint32_t a0 = o_addr, a1 = o_addr;
-                if (alt) {
-                    // both slots hold this row: (m, l) change hands, each slot writes half of the columns
-                    sh->ml[slot][row] = make_float2(mref, l);
-                    __syncwarp();
-                    attn2::arrive_if(lane == 0, BAR(merge_in));
-                    const bool got = attn2::wait_for(BAR(merge_in), merges & 1u, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    tc_fence_after();
-                    const float2 x0 = sh->ml[0][row], x1 = sh->ml[1][row];
-                    m = fmaxf(x0.x, x1.x);
-                    w0 = x0.x == -INFINITY ? 0.f : exp2f(x0.x - m);
-                    w1 = x1.x == -INFINITY ? 0.f : exp2f(x1.x - m);
-                    l = x0.y * w0 + x1.y * w1;
-                    use0 = u->n > 0;
-                    use1 = u->n > 1;
-                    a0 = tmem + lane_base + attn2::o_col(0);
-                    a1 = tmem + lane_base + attn2::o_col(1);
-                }
-                if (!idle) {
-                    const float inv = u->n == 0 || l == 0.f ? 0.f : 1.f / l;
-                    const int node = row_of < 0 ? 0 : row_of / a.G, g = row_of < 0 ? 0 : row_of - node * a.G, part = u->part;
-                    uint16_t* out = a.out + (((int64_t)u->b * a.n + node) * a.Hq + u->head * a.G + g) * kHeadDim;
-                    const int64_t place = (int64_t)part * a.rows + (row_of - u->pair * 2 * kRows);
-#pragma unroll 1
-                    for (int c = c0; c < c1; c += 16) {
-                        uint32_t o[16], o1[16];
-                        if (use0) attn2::load16(a0 + c, o);
-                        if (use1) attn2::load16(a1 + c, o1);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float x0 = use0 ? __uint_as_float(o[e]) : 0.f, x1 = use1 ? __uint_as_float(o1[e]) : 0.f;
-                            o[e] = __float_as_uint(fmaf(x0, w0, x1 * w1));
-                        }
-                        if (row_of < 0) continue;
-                        if (part < 0) {
-                            uint32_t y[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                y[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                            *reinterpret_cast<uint4*>(out + c) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                        }
-                    }
-                    if (row_of >= 0 && part >= 0 && (!alt || slot == 0))
-                        a.ws_ml[place] = use0 ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
-                }
-                if (alt) {                                                   // O and ml are free again
-                    tc_fence_before();
-                    __syncwarp();
-                    attn2::arrive_if(lane == 0, BAR(merge_out));
-                    const bool got = attn2::wait_for(BAR(merge_out), merges & 1u, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) break;
-                    ++merges;
-                }
-            }
-            if (i > 0) {
-                __syncwarp();
-                unit_read(i - 1);
-            }
-            if (!have) break;
-            row_of = row_next;
-            anc = anc_next;
-            sc = sc_next;
-            idle = !__any_sync(0xffffffffu, row_of >= 0);     // rows are independent: leave P as it is
-            const Unit* u = &sh->info[i % kInfo];
-            const int n = u->n, nc = n - u->tree, left0 = u->L - u->t0 * kKeys;     // keys from the unit's first tile on
-            alt = u->split_keys;
-            mref = -INFINITY;
-            l2 = 0;
-            mine = 0;
-            // lanes 0 .. 3 (and every lane alike mod 8) hold the K scales of a tile's blocks, lanes
-            // 4 .. 7 the V scales, loaded a tile ahead; blocks without a key take the last one's
-            const float* scales = ((lane & 4) ? a.v_scale : a.k_scale) + ((int64_t)u->b * a.Hkv + u->head) * a.NB + u->t0 * kBlocks;
-            const int last_block = max(u->L - 1, 0) / kKv8Block - u->t0 * kBlocks;
-            auto load_scale = [&](int t) { return __ldg(scales + min(t * kBlocks + (lane & 3), last_block)); };
-            const int first = alt ? slot : 0, step = alt ? 2 : 1;
-            float scale = load_scale(first);
-            for (int t = first; t < n; t += step, ++mine) {
-                const bool got = attn2::wait_for(BAR_AT(s_full, slot), tiles_done & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                ++tiles_done;
-                tc_fence_after();
-                if (!idle) {
-                    float mx = -INFINITY, alpha = 1.f;
-                    // raises the reference maximum where mx is far above it (every tile has a visible
-                    // key: mx is finite, and the first one always is above), without branches of a lane
-                    auto raise = [&]() {
-                        const bool up = mx > mref + kRescale;
-                        alpha = up ? ex2_approx(mref - mx) : 1.f;        // 0 for the first maximum
-                        mref = up ? mx : mref;
-                        l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
-                        // the commit behind this QK covers every PV before it: O is complete
-                        if (mine > 0 && __any_sync(0xffffffffu, up)) attn2::rescale_row(o_addr, alpha);
-                    };
-                    if (t < nc) {
-                        const int left = left0 - t * kKeys;
-                        uint32_t x[kKeys];
-                        float mb[kBlocks];
-                        attn2::load_row_nowait(s_addr, x, mb);
-                        // a block's factor (above 0, so that a masked block stays -inf) and exponent
-                        float f[kBlocks];
-                        int ev[kBlocks];
-#pragma unroll
-                        for (int c = 0; c < kBlocks; ++c) {
-                            f[c] = fmaxf(__shfl_sync(0xffffffffu, scale, c) * sc, 1.17549435e-38f);
-                            ev[c] = (int)(__float_as_uint(__shfl_sync(0xffffffffu, scale, kBlocks + c)) >> 23) - 127;
-                            if (ev[c] > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
-                        }
-                        scale = load_scale(t + step);
-                        attn2::tmem_wait_ld();
-                        if (left < kKeys) {
-#pragma unroll
-                            for (int c = 0; c < kBlocks; ++c) {
-                                float y[kKv8Block];
-#pragma unroll
-                                for (int e = 0; e < kKv8Block; ++e) {
-                                    y[e] = kKv8Block * c + e < left ? __uint_as_float(x[kKv8Block * c + e]) : -INFINITY;
-                                    x[kKv8Block * c + e] = __float_as_uint(y[e]);
-                                }
-                                mb[c] = attn2::max_of<kKv8Block>(y);
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < kBlocks; ++c) mx = fmaxf(mx, fmaf(mb[c], f[c], (float)ev[c]));
-                        raise();
-#pragma unroll
-                        for (int c = 0; c < kBlocks; ++c) {
-                            const float off = (float)ev[c] - mref + kOffset, inv = kv8::exp2i(min(-ev[c], 127));
-                            const uint64_t f_2 = attn2::f2(f[c], f[c]), off2 = attn2::f2(off, off);
-                            uint64_t acc[2] = {0, 0};
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int d = 0; d < 16; ++d) {
-                                float s0, s1;
-                                attn2::unf2(attn2::fma2(attn2::f2(__uint_as_float(x[32 * c + 2 * d]), __uint_as_float(x[32 * c + 2 * d + 1])), f_2, off2), s0, s1);
-                                const float p0 = ex2_approx(s0), p1 = ex2_approx(s1);
-                                acc[d & 1] = attn2::add2(acc[d & 1], attn2::f2(p0, p1));
-                                pk[d] = pack_half2(p0, p1);
-                            }
-                            attn2::tmem_st16_nowait(s_addr + 16 * c, pk);        // P over S
-                            l2 = attn2::fma2(attn2::add2(acc[0], acc[1]), attn2::f2(inv, inv), l2);
-                        }
-                    } else {
-                        // the tree's tile, 32 keys at a time: key j's score is the sum of its digits'
-                        // columns j and 64 + j; its factors have a barrier per tree in flight
-                        const int tr = trees % kTrees;
-                        const bool seen = attn2::wait_for(BAR_AT(tree_full, tr), (trees / kTrees) & 1u, abort_flag);
-                        if (!__all_sync(0xffffffffu, seen)) { ok = false; break; }
-                        // first pass: scores, back into TMEM; second pass: weights
-                        uint32_t x[16], y[16];
-#pragma unroll 1
-                        for (int c = 0; c < kMaxNodes; c += 16) {
-                            attn2::load16(s_addr + c, x);
-                            attn2::load16(s_addr + kMaxNodes + c, y);
-                            const uint32_t sees = (uint32_t)(anc >> c);
-                            float s[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float f = fmaxf(sh->k_fac[tr][c + j] * sc, 1.17549435e-38f);
-                                s[j] = (sees >> j) & 1u ? fmaf(__uint_as_float(x[j]) + __uint_as_float(y[j]), f, sh->v_exp[tr][c + j])
-                                                       : -INFINITY;
-                                x[j] = __float_as_uint(s[j]);
-                            }
-                            mx = fmaxf(mx, attn2::max_of<16>(s));
-                            attn2::tmem_st16_nowait(s_addr + c, x);
-                        }
-                        attn2::tmem_wait_st();
-                        raise();
-                        float sum = 0.f;
-                        const float off = kOffset - mref;
-#pragma unroll 1
-                        for (int c = 0; c < kMaxNodes; c += 16) {
-                            attn2::load16(s_addr + c, x);
-                            uint32_t pk[8];
-#pragma unroll
-                            for (int d = 0; d < 8; ++d) {
-                                const float p0 = ex2_approx(__uint_as_float(x[2 * d]) + off);
-                                const float p1 = ex2_approx(__uint_as_float(x[2 * d + 1]) + off);
-                                sum = fmaf(p0, sh->v_inv[tr][c + 2 * d], fmaf(p1, sh->v_inv[tr][c + 2 * d + 1], sum));
-                                pk[d] = pack_half2(p0, p1);
-                            }
-                            attn2::tmem_st8_nowait(s_addr + c / 2, pk);      // over scores that have been read
-                        }
-                        l2 = attn2::add2(l2, attn2::f2(sum, 0.f));
-                    }
-                    attn2::tmem_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                attn2::arrive_if(lane == 0, BAR_AT(p_full, slot));
-            }
-            trees += n - nc;
-        }
-        if (bits) flag_error(a.dev_status, bits);
-    } else {
-        // ---------------- V in fp16 ----------------
-        attn2::regs_dec<kRegsOther>();
-        const int cw = warp - 12;
-        // this lane's key of a group of eight and 16-byte chunk of four: the eight lanes of a
-        // shared-memory phase read and write all 32 banks, under both tiles' swizzles
-        const int key8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
-        uint32_t r = 0, rh = 0, rk = 0, trees = 0, grants = 0;   // uses of the rings; a phase bit per K stage
-        int bits = 0;
-        bool ok = true;
-        auto ready = [&](uint32_t bar, uint32_t parity) {
-            const bool got = attn2::wait_for(bar, parity, abort_flag);
-            ok = ok && __all_sync(0xffffffffu, got);
-            return ok;
-        };
-        auto tile_done = [&]() {
-            attn2::fence_async_shared();
-            __syncwarp();
-            attn2::arrive_if(lane == 0, BAR_AT(h_full, rh % kWide));
-            ++rh;
-        };
-        for (int i = 0; ok; ++i) {
-            const Unit* up = next_unit(i);
-            if (!__all_sync(0xffffffffu, up != nullptr)) break;
-            const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree, L = up->L;
-            __syncwarp();
-            unit_read(i);
-            for (int j = 0; j < nc; ++j, ++r) {
-                const int st = r % kVStages, left = L - (t0 + j) * kKeys;
-                if (!ready(BAR_AT(v_full, st), r / kVStages)) break;
-                if (!ready(BAR_AT(h_empty, rh % kWide), (rh / kWide) ^ 1u)) break;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
-                    uint8_t* dst = sH + (rh % kWide * 2 + h) * kTile;
-                    uint4 x[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        x[y] = *reinterpret_cast<const uint4*>(src + swz((cw * 2 + (y >> 1)) * 8 + key8, (4 * (y & 1) + c4) * 16));
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int key = (cw * 2 + (y >> 1)) * 8 + key8, box = y & 1;
-                        const bool there = h * kHalfKeys + key < left;
-                        const uint32_t w[4] = {there ? x[y].x : 0u, there ? x[y].y : 0u, there ? x[y].z : 0u, there ? x[y].w : 0u};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[2 * e] = kv8::e4m3x2_half2((uint16_t)w[e]);
-                            o[2 * e + 1] = kv8::e4m3x2_half2((uint16_t)(w[e] >> 16));
-                        }
-                        *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                }
-                tile_done();
-                attn2::arrive_if(lane == 0, BAR_AT(v_empty, st));
-            }
-            rk += nc;
-            if (ok && tree) {
-                const uint32_t ks = rk++ % kKStages;
-                {
-                    // K: digits.  Rows from n on are left as they are: no key of theirs is ever seen.
-                    uint8_t* tile = sK + ks * kTile;
-                    const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim + (lane & 15) * 8;
-                    const int r0 = cw * 16 + (lane >> 4);
+                for (int r0 = 0; r0 < count; r0 += 16) {
                     uint4 v[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
-                    if (!ready(BAR_AT(k_grant, ks), grants >> ks)) break;
-                    grants ^= 1u << ks;
-                    const int pairs = min(8, (a.n - cw * 16 + 1) >> 1);
+                    for (int k = 0; k < 8; ++k) {
+                        // a row that does not exist takes the first one's place in the load: loads
+                        // under a condition each wait for the one before
+                        const int off = max(__shfl_sync(0xffffffffu, my_off, r0 + 2 * k + (lane >> 4)), 0);
+                        v[k] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)off * kHeadDim));
+                    }
 #pragma unroll 1
-                    for (int k = 0; k < pairs; k += 4) {                     // four row pairs at once, to hide their latencies
+                    for (int k = 0; k < 8; k += 4) {                         // four row pairs at once, to hide their latencies
                         int e[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const int row = r0 + 2 * (k + y), c = lane & 15;
+                            const int rr = r0 + 2 * (k + y) + (lane >> 4), at = (warp & 3) * 32 + rr;
                             uint32_t hi[2], lo[2];
                             digits8(v[y], kv8::exp2i(-e[y]), hi, lo);
-                            if (row < a.n) {
-                                *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
-                                *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
-                                if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e[y]);
+                            *reinterpret_cast<uint2*>(dst + swz(at, 8 * (lane & 15))) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(dst + kTile + swz(at, 8 * (lane & 15))) = make_uint2(lo[0], lo[1]);
+                            const int e_of = __shfl_sync(0xffffffffu, e[y], (lane & 1) << 4);   // of row r0 + 2 (k + y) + (lane & 1)
+                            if ((lane >> 1) == (r0 >> 1) + k + y) e_mine = e_of;
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) v[y] = v[y + 4];         // the loop's body exists once
+                    }
+                }
+                sc_next = a.scale_log2 * kv8::exp2i(e_mine);
+                attn2::fence_async_shared();
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR_AT(q_full, slot));
+                return true;
+            };
+
+            // Per unit: the Q digits of the next one go in, so that its first products can run during
+            // this one's output; then this one's output; then the next one's tiles.
+            bool have = true, ok = true, idle = true;
+            float mref = 0.f;
+            uint64_t l2 = 0;                                                 // two partial sums of the weights
+            int mine = 0;                                                    // tiles of this slot
+            for (int i = 0; have && ok; ++i) {
+                int row_next = -1;
+                unsigned long long anc_next = 0;
+                float sc_next = 0.f;
+                have = begin_unit(i, row_next, anc_next, sc_next);
+                if (i > 0) {
+                    const Unit* u = &sh->info[(i - 1) % kInfo];
+                    if (mine > 0) {
+                        const bool got = attn2::wait_for(BAR_AT(o_full, slot), units_done & 1u, abort_flag);
+                        if (!__all_sync(0xffffffffu, got)) break;
+                        ++units_done;
+                        tc_fence_after();
+                    }
+                    float la, lb;
+                    attn2::unf2(l2, la, lb);
+                    float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
+                    bool use0 = mine > 0, use1 = false;
+                    const int c0 = alt ? 64 * slot : 0, c1 = alt ? c0 + 64 : kHeadDim;
+                    uint32_t a0 = o_addr, a1 = o_addr;
+                    if (alt) {
+                        // both slots hold this row: (m, l) change hands, each slot writes half of the columns
+                        sh->ml[slot][row] = make_float2(mref, l);
+                        __syncwarp();
+                        attn2::arrive_if(lane == 0, BAR(merge_in));
+                        const bool got = attn2::wait_for(BAR(merge_in), merges & 1u, abort_flag);
+                        if (!__all_sync(0xffffffffu, got)) break;
+                        tc_fence_after();
+                        const float2 x0 = sh->ml[0][row], x1 = sh->ml[1][row];
+                        m = fmaxf(x0.x, x1.x);
+                        w0 = x0.x == -INFINITY ? 0.f : exp2f(x0.x - m);
+                        w1 = x1.x == -INFINITY ? 0.f : exp2f(x1.x - m);
+                        l = x0.y * w0 + x1.y * w1;
+                        use0 = u->n > 0;
+                        use1 = u->n > 1;
+                        a0 = tmem + lane_base + attn2::o_col(0);
+                        a1 = tmem + lane_base + attn2::o_col(1);
+                    }
+                    if (!idle) {
+                        const float inv = u->n == 0 || l == 0.f ? 0.f : 1.f / l;
+                        const int node = row_of < 0 ? 0 : row_of / a.G, g = row_of < 0 ? 0 : row_of - node * a.G, part = u->part;
+                        uint16_t* out = a.out + (((int64_t)u->b * a.n + node) * a.Hq + u->head * a.G + g) * kHeadDim;
+                        const int64_t place = (int64_t)part * a.rows + (row_of - u->pair * 2 * kRows);
+#pragma unroll 1
+                        for (int c = c0; c < c1; c += 16) {
+                            uint32_t o[16], o1[16];
+                            if (use0) attn2::load16(a0 + c, o);
+                            if (use1) attn2::load16(a1 + c, o1);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float x0 = use0 ? __uint_as_float(o[e]) : 0.f, x1 = use1 ? __uint_as_float(o1[e]) : 0.f;
+                                o[e] = __float_as_uint(fmaf(x0, w0, x1 * w1));
+                            }
+                            if (row_of < 0) continue;
+                            if (part < 0) {
+                                uint32_t y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    y[e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                                *reinterpret_cast<uint4*>(out + c) = make_uint4(y[0], y[1], y[2], y[3]);
+                                *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 16; e += 4)
+                                    *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                             }
                         }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) v[y] = v[y + 4];     // the loop's body exists once
+                        if (row_of >= 0 && part >= 0 && (!alt || slot == 0))
+                            a.ws_ml[place] = use0 ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
                     }
-                    attn2::fence_async_shared();
-                    __syncwarp();
-                    attn2::arrive_if(lane == 0, BAR_AT(k_full, ks));
+                    if (alt) {                                                   // O and ml are free again
+                        tc_fence_before();
+                        __syncwarp();
+                        attn2::arrive_if(lane == 0, BAR(merge_out));
+                        const bool got = attn2::wait_for(BAR(merge_out), merges & 1u, abort_flag);
+                        if (!__all_sync(0xffffffffu, got)) break;
+                        ++merges;
+                    }
                 }
-                // V
-                if (!ready(BAR_AT(h_empty, rh % kWide), (rh / kWide) ^ 1u)) break;
-                uint8_t* dst = sH + rh % kWide * 2 * kTile;
-                const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
+                if (i > 0) {
+                    __syncwarp();
+                    unit_read(i - 1);
+                }
+                if (!have) break;
+                row_of = row_next;
+                anc = anc_next;
+                sc = sc_next;
+                idle = !__any_sync(0xffffffffu, row_of >= 0);     // rows are independent: leave P as it is
+                const Unit* u = &sh->info[i % kInfo];
+                const int n = u->n, nc = n - u->tree, left0 = u->L - u->t0 * kKeys;     // keys from the unit's first tile on
+                alt = u->split_keys;
+                mref = -INFINITY;
+                l2 = 0;
+                mine = 0;
+                // lanes 0 .. 3 (and every lane alike mod 8) hold the K scales of a tile's blocks, lanes
+                // 4 .. 7 the V scales, loaded a tile ahead; blocks without a key take the last one's
+                const float* scales = ((lane & 4) ? a.v_scale : a.k_scale) + ((int64_t)u->b * a.Hkv + u->head) * a.NB + u->t0 * kBlocks;
+                const int last_block = max(u->L - 1, 0) / kKv8Block - u->t0 * kBlocks;
+                auto load_scale = [&](int t) { return __ldg(scales + min(t * kBlocks + (lane & 3), last_block)); };
+                const int first = alt ? slot : 0, step = alt ? 2 : 1;
+                float scale = load_scale(first);
+                for (int t = first; t < n; t += step, ++mine) {
+                    const bool got = attn2::wait_for(BAR_AT(s_full, slot), tiles_done & 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    ++tiles_done;
+                    tc_fence_after();
+                    if (!idle) {
+                        float mx = -INFINITY, alpha = 1.f;
+                        // raises the reference maximum where mx is far above it (every tile has a visible
+                        // key: mx is finite, and the first one always is above), without branches of a lane
+                        auto raise = [&]() {
+                            const bool up = mx > mref + kRescale;
+                            alpha = up ? ex2_approx(mref - mx) : 1.f;        // 0 for the first maximum
+                            mref = up ? mx : mref;
+                            l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
+                            // the commit behind this QK covers every PV before it: O is complete
+                            if (mine > 0 && __any_sync(0xffffffffu, up)) attn2::rescale_row(o_addr, alpha);
+                        };
+                        if (t < nc) {
+                            const int left = left0 - t * kKeys;
+                            uint32_t x[kKeys];
+                            float mb[kBlocks];
+                            attn2::load_row_nowait(s_addr, x, mb);
+                            // a block's factor (above 0, so that a masked block stays -inf) and exponent
+                            float f[kBlocks];
+                            int ev[kBlocks];
+#pragma unroll
+                            for (int c = 0; c < kBlocks; ++c) {
+                                f[c] = fmaxf(__shfl_sync(0xffffffffu, scale, c) * sc, 1.17549435e-38f);
+                                ev[c] = (int)(__float_as_uint(__shfl_sync(0xffffffffu, scale, kBlocks + c)) >> 23) - 127;
+                                if (ev[c] > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
+                            }
+                            scale = load_scale(t + step);
+                            attn2::tmem_wait_ld();
+                            if (left < kKeys) {
+#pragma unroll
+                                for (int c = 0; c < kBlocks; ++c) {
+                                    float y[kKv8Block];
+#pragma unroll
+                                    for (int e = 0; e < kKv8Block; ++e) {
+                                        y[e] = kKv8Block * c + e < left ? __uint_as_float(x[kKv8Block * c + e]) : -INFINITY;
+                                        x[kKv8Block * c + e] = __float_as_uint(y[e]);
+                                    }
+                                    mb[c] = attn2::max_of<kKv8Block>(y);
+                                }
+                            }
+#pragma unroll
+                            for (int c = 0; c < kBlocks; ++c) mx = fmaxf(mx, fmaf(mb[c], f[c], (float)ev[c]));
+                            raise();
+#pragma unroll
+                            for (int c = 0; c < kBlocks; ++c) {
+                                const float off = (float)ev[c] - mref + kOffset, inv = kv8::exp2i(min(-ev[c], 127));
+                                const uint64_t f_2 = attn2::f2(f[c], f[c]), off2 = attn2::f2(off, off);
+                                uint64_t acc[2] = {0, 0};
+                                uint32_t pk[16];
+#pragma unroll
+                                for (int d = 0; d < 16; ++d) {
+                                    float s0, s1;
+                                    attn2::unf2(attn2::fma2(attn2::f2(__uint_as_float(x[32 * c + 2 * d]), __uint_as_float(x[32 * c + 2 * d + 1])), f_2, off2), s0, s1);
+                                    const float p0 = ex2_approx(s0), p1 = ex2_approx(s1);
+                                    acc[d & 1] = attn2::add2(acc[d & 1], attn2::f2(p0, p1));
+                                    pk[d] = kBf ? pack2(p0, p1) : pack_half2(p0, p1);
+                                }
+                                attn2::tmem_st16_nowait(s_addr + 16 * c, pk);        // P over S
+                                l2 = attn2::fma2(attn2::add2(acc[0], acc[1]), attn2::f2(inv, inv), l2);
+                            }
+                        } else {
+                            // the tree's tile, 32 keys at a time: key j's score is the sum of its digits'
+                            // columns j and 64 + j; its factors have a barrier per tree in flight
+                            const int tr = trees % kTrees;
+                            const bool seen = attn2::wait_for(BAR_AT(tree_full, tr), (trees / kTrees) & 1u, abort_flag);
+                            if (!__all_sync(0xffffffffu, seen)) { ok = false; break; }
+                            // first pass: scores, back into TMEM; second pass: weights.  In bf16 (V as it is):
+                            // a weight and its remainder, the scores meanwhile where the lo digits' were.
+                            constexpr int kAt = kBf ? kMaxNodes : 0;
+                            uint32_t x[16], y[16];
 #pragma unroll 1
-                for (int r0 = cw * 16 + (lane >> 4); r0 < cw * 16 + 16; r0 += 8) {
-                    if (r0 - (lane >> 4) >= a.n) {        // no row of the tree
+                            for (int c = 0; c < kMaxNodes; c += 16) {
+                                attn2::load16(s_addr + c, x);
+                                attn2::load16(s_addr + kMaxNodes + c, y);
+                                const uint32_t sees = (uint32_t)(anc >> c);
+                                float s[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            *reinterpret_cast<uint4*>(dst + ((lane & 15) >> 3) * kHalfBox + swz(r0 + 2 * k, (lane & 7) * 16)) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                            // the sum multiplies it with a weight of zero, which does not cancel NaN
-                            if ((lane & 15) == 0) sh->v_inv[trees % kTrees][r0 + 2 * k] = 0.f;
+                                for (int j = 0; j < 16; ++j) {
+                                    const float f = fmaxf(sh->k_fac[tr][c + j] * sc, 1.17549435e-38f);
+                                    s[j] = (sees >> j) & 1u ? fmaf(__uint_as_float(x[j]) + __uint_as_float(y[j]), f, kBf ? 0.f : sh->v_exp[tr][c + j])
+                                                           : -INFINITY;
+                                    x[j] = __float_as_uint(s[j]);
+                                }
+                                mx = fmaxf(mx, attn2::max_of<16>(s));
+                                attn2::tmem_st16_nowait(s_addr + kAt + c, x);
+                            }
+                            attn2::tmem_wait_st();
+                            raise();
+                            float sum = 0.f;
+                            const float off = kOffset - mref;
+#pragma unroll 1
+                            for (int c = 0; c < kMaxNodes; c += 16) {
+                                attn2::load16(s_addr + kAt + c, x);
+                                uint32_t pk[8], lo[8];
+#pragma unroll
+                                for (int d = 0; d < 8; ++d) {
+                                    const float p0 = ex2_approx(__uint_as_float(x[2 * d]) + off);
+                                    const float p1 = ex2_approx(__uint_as_float(x[2 * d + 1]) + off);
+                                    if constexpr (kBf) {
+                                        sum += p0 + p1;
+                                        pk[d] = pack2(p0, p1);
+                                        lo[d] = pack2(p0 - __uint_as_float(pk[d] << 16), p1 - __uint_as_float(pk[d] & 0xffff0000u));
+                                    } else {
+                                        sum = fmaf(p0, sh->v_inv[tr][c + 2 * d], fmaf(p1, sh->v_inv[tr][c + 2 * d + 1], sum));
+                                        pk[d] = pack_half2(p0, p1);
+                                    }
+                                }
+                                attn2::tmem_st8_nowait(s_addr + c / 2, pk);      // over scores that have been read
+                                if constexpr (kBf) attn2::tmem_st8_nowait(s_addr + kMaxNodes / 2 + c / 2, lo);
+                            }
+                            l2 = attn2::add2(l2, attn2::f2(sum, 0.f));
                         }
-                        continue;
+                        attn2::tmem_wait_st();
                     }
-                    uint4 v[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim) + (lane & 15));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int row = r0 + 2 * k, c = lane & 15, e = row_exp(v[k], kv8::kMinExp);
-                        const float by = kv8::exp2i(-e);
-                        if (row < a.n && e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
-                        const bool there = row < a.n;                    // zeros behind the tree's rows
-                        const uint32_t w[4] = {there ? v[k].x : 0u, there ? v[k].y : 0u, there ? v[k].z : 0u, there ? v[k].w : 0u};
-                        uint32_t o[4];
+                    tc_fence_before();
+                    __syncwarp();
+                    attn2::arrive_if(lane == 0, BAR_AT(p_full, slot));
+                }
+                trees += n - nc;
+            }
+            if (bits) flag_error(a.dev_status, bits);
+        };
+        pass(std::false_type{});
+        if (again()) pass(std::true_type{});
+    } else {
+        // ---------------- V in fp16 ----------------
+        attn2::regs_dec<kRegsOther>();
+        auto pass = [&](auto wide) {
+            constexpr bool kBf = decltype(wide)::value;
+            const int cw = warp - 12;
+            // this lane's key of a group of eight and 16-byte chunk of four: the eight lanes of a
+            // shared-memory phase read and write all 32 banks, under both tiles' swizzles
+            const int key8 = (lane >> 3) ^ ((lane & 4) ? 5 : 0), c4 = lane & 3;
+            uint32_t r = 0, rh = 0, rk = 0, trees = 0, grants = 0;   // uses of the rings; a phase bit per K stage
+            int bits = 0;
+            bool ok = true;
+            auto ready = [&](uint32_t bar, uint32_t parity) {
+                const bool got = attn2::wait_for(bar, parity, abort_flag);
+                ok = ok && __all_sync(0xffffffffu, got);
+                return ok;
+            };
+            auto tile_done = [&]() {
+                attn2::fence_async_shared();
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR_AT(h_full, rh % kWide));
+                ++rh;
+            };
+            for (int i = 0; ok; ++i) {
+                const Unit* up = next_unit(i);
+                if (!__all_sync(0xffffffffu, up != nullptr)) break;
+                const int b = up->b, head = up->head, t0 = up->t0, nc = up->n - up->tree, tree = up->tree, L = up->L;
+                __syncwarp();
+                unit_read(i);
+                for (int j = 0; j < nc; ++j, ++r) {
+                    const int st = r % kVStages, left = L - (t0 + j) * kKeys;
+                    if (!ready(BAR_AT(v_full, st), r / kVStages)) break;
+                    if (!ready(BAR_AT(h_empty, rh % kWide), (rh / kWide) ^ 1u)) break;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const uint8_t* src = sV + st * kTile + h * kHalfKeys * 128;
+                        uint8_t* dst = sH + (rh % kWide * 2 + h) * kTile;
+                        uint4 x[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            o[y] = pack_half2(__uint_as_float(w[y] << 16) * by, __uint_as_float(w[y] & 0xffff0000u) * by);
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBox + swz(row, (c & 7) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (c == 0) {
-                            sh->v_exp[trees % kTrees][row] = (float)e;
-                            sh->v_inv[trees % kTrees][row] = by;
+                            x[y] = *reinterpret_cast<const uint4*>(src + swz((cw * 2 + (y >> 1)) * 8 + key8, (4 * (y & 1) + c4) * 16));
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int key = (cw * 2 + (y >> 1)) * 8 + key8, box = y & 1;
+                            const bool there = h * kHalfKeys + key < left;
+                            const uint32_t w[4] = {there ? x[y].x : 0u, there ? x[y].y : 0u, there ? x[y].z : 0u, there ? x[y].w : 0u};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[2 * e] = kv8::e4m3x2_half2((uint16_t)w[e]);
+                                o[2 * e + 1] = kv8::e4m3x2_half2((uint16_t)(w[e] >> 16));
+                            }
+                            if constexpr (kBf)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) o[e] = half2_bf162(o[e]);
+                            *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(dst + box * kHalfBox + swz(key, 32 * c4 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
+                    tile_done();
+                    attn2::arrive_if(lane == 0, BAR_AT(v_empty, st));
                 }
-                __syncwarp();
-                attn2::arrive_if(lane == 0, BAR_AT(tree_full, trees % kTrees));
-                ++trees;
-                tile_done();
+                rk += nc;
+                if (ok && tree) {
+                    const uint32_t ks = rk++ % kKStages;
+                    {
+                        // K: digits.  Rows from n on are left as they are: no key of theirs is ever seen.
+                        uint8_t* tile = sK + ks * kTile;
+                        const uint16_t* x = a.k_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim + (lane & 15) * 8;
+                        const int r0 = cw * 16 + (lane >> 4);
+                        uint4 v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
+                        if (!ready(BAR_AT(k_grant, ks), grants >> ks)) break;
+                        grants ^= 1u << ks;
+                        const int pairs = min(8, (a.n - cw * 16 + 1) >> 1);
+#pragma unroll 1
+                        for (int k = 0; k < pairs; k += 4) {                     // four row pairs at once, to hide their latencies
+                            int e[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int row = r0 + 2 * (k + y), c = lane & 15;
+                                uint32_t hi[2], lo[2];
+                                digits8(v[y], kv8::exp2i(-e[y]), hi, lo);
+                                if (row < a.n) {
+                                    *reinterpret_cast<uint2*>(tile + swz(row, 8 * c)) = make_uint2(hi[0], hi[1]);
+                                    *reinterpret_cast<uint2*>(tile + swz(kMaxNodes + row, 8 * c)) = make_uint2(lo[0], lo[1]);
+                                    if (c == 0) sh->k_fac[trees % kTrees][row] = kv8::exp2i(e[y]);
+                                }
+                            }
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) v[y] = v[y + 4];     // the loop's body exists once
+                        }
+                        attn2::fence_async_shared();
+                        __syncwarp();
+                        attn2::arrive_if(lane == 0, BAR_AT(k_full, ks));
+                    }
+                    // V
+                    if (!ready(BAR_AT(h_empty, rh % kWide), (rh / kWide) ^ 1u)) break;
+                    uint8_t* dst = sH + rh % kWide * 2 * kTile;
+                    const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim;
+#pragma unroll 1
+                    for (int r0 = cw * 16 + (lane >> 4); r0 < cw * 16 + 16; r0 += 8) {
+                        if (r0 - (lane >> 4) >= a.n) {        // no row of the tree
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                *reinterpret_cast<uint4*>(dst + ((lane & 15) >> 3) * kHalfBox + swz(r0 + 2 * k, (lane & 7) * 16)) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                                // the sum multiplies it with a weight of zero, which does not cancel NaN
+                                if ((lane & 15) == 0) sh->v_inv[trees % kTrees][r0 + 2 * k] = 0.f;
+                            }
+                            continue;
+                        }
+                        uint4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim) + (lane & 15));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = r0 + 2 * k, c = lane & 15;
+                            const bool there = row < a.n;                    // zeros behind the tree's rows
+                            if constexpr (kBf) {
+                                *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBox + swz(row, (c & 7) * 16)) =
+                                    there ? v[k] : make_uint4(0u, 0u, 0u, 0u);
+                                continue;
+                            }
+                            const int e = row_exp(v[k], kv8::kMinExp);
+                            const float by = kv8::exp2i(-e);
+                            if (there && e > kMaxVExp) bits = EAGLE_DEV_NONFINITE;
+                            const uint32_t w[4] = {there ? v[k].x : 0u, there ? v[k].y : 0u, there ? v[k].z : 0u, there ? v[k].w : 0u};
+                            uint32_t o[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                o[y] = pack_half2(__uint_as_float(w[y] << 16) * by, __uint_as_float(w[y] & 0xffff0000u) * by);
+                            *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBox + swz(row, (c & 7) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (c == 0) {
+                                sh->v_exp[trees % kTrees][row] = (float)e;
+                                sh->v_inv[trees % kTrees][row] = by;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    attn2::arrive_if(lane == 0, BAR_AT(tree_full, trees % kTrees));
+                    ++trees;
+                    tile_done();
+                }
             }
-        }
-        if (bits) flag_error(a.dev_status, bits);
+            if (bits) flag_error(a.dev_status, bits);
+        };
+        pass(std::false_type{});
+        if (again()) pass(std::true_type{});
     }
     __syncthreads();
     if (tid == 0 && *abort_flag) flag_error(a.dev_status, EAGLE_DEV_TIMEOUT);

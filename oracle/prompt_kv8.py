@@ -135,11 +135,29 @@ def kv8_commit(x, kv_len, path, acc, codes, scales):
                     write_rows(rows[:, h], int(kv_len[b]), codes[layer, b, h], scales[layer, b, h])
 
 
+def _tree_sees(n, L, parent):
+    """bool [n, L + n]: the cache's L rows, then the tree's."""
+    sees = torch.zeros(n, L + n, dtype=torch.bool)
+    sees[:, :L] = True
+    for i in range(n):
+        j = i
+        while j >= 0:
+            sees[i, L + j] = True
+            j = int(parent[j])
+    return sees
+
+
+def _key_rows(codes, scales, tree, b, h, L):
+    """float64 [L + n, d]: rows of the cache, then the tree's."""
+    blk = np.arange(L) // KV8_BLOCK
+    return torch.cat([torch.from_numpy(_value(codes[b, h, :L]) * scales[b, h][blk][:, None]), tree[b, :, h]])
+
+
 def tree_attn_kv8(q, codes, scales, v_codes, v_scales, k_tree, v_tree, kv_len, parent, scale):
     """q [B, n, Hq, d], k_tree / v_tree [B, n, Hkv, d] (bf16 values); codes uint8 [B, Hkv, Lmax,
-    d], scales float64.  Weights may be rounded to two e4m3 digits: 2^-8 of the weight, and for
-    small ones 2^-10 on a scale where the largest weight is at least 2^6; the query's and the
-    tree rows' digits leave at most 2^-17 of their row's largest magnitude."""
+    d], scales float64.  The tolerance is a loose one, that of weights held in two 4-bit digits
+    (2^-8 of the weight, and for small ones 2^-10 on a scale where the largest is at least 2^6);
+    tree_attn_kv8_tight has the kernel's own."""
     q, kt, vt = (t.double().cpu() for t in (q, k_tree, v_tree))
     B, n, Hq, d = q.shape
     Hkv = kt.shape[2]
@@ -148,22 +166,85 @@ def tree_attn_kv8(q, codes, scales, v_codes, v_scales, k_tree, v_tree, kv_len, p
     tol = torch.zeros(B, n, Hq, d).double()
     for b in range(B):
         L = int(kv_len[b])
-        sees = torch.zeros(n, L + n, dtype=torch.bool)
-        sees[:, :L] = True
-        for i in range(n):
-            j = i
-            while j >= 0:
-                sees[i, L + j] = True
-                j = int(parent[b][j])
-        blk = np.arange(L) // KV8_BLOCK
+        sees = _tree_sees(n, L, parent[b])
         for h in range(Hkv):
-            rows = lambda c, s, t: torch.cat([torch.from_numpy(_value(c[b, h, :L]) * s[b, h][blk][:, None]),  # noqa: E731
-                                              t[b, :, h]])
-            k, v = rows(codes, scales, kt), rows(v_codes, v_scales, vt)
-            top = v[L:].abs().amax(1, keepdim=True) * 2.0 ** -17           # the tree rows' digits
+            k, v = _key_rows(codes, scales, kt, b, h, L), _key_rows(v_codes, v_scales, vt, b, h, L)
+            top = v[L:].abs().amax(1, keepdim=True) * 2.0 ** -17
             slack = torch.cat([torch.zeros(L, 1), top]).double()
             for g in range(G):
                 o, _, t = _softmax_rows(q[b, :, h * G + g], k, v, sees, scale, HALF_BF16, 2.0 ** -16,
                                         extra=2.0 ** -16)
                 out[b, :, h * G + g], tol[b, :, h * G + g] = o, t + slack.max()
+    return out, tol
+
+
+KV8_SPREAD = 8        # a larger spread of V exponents: weights in bf16
+
+
+def _row_exponents(v):
+    """The exponents e that bring each row's largest magnitude to [128, 256); NaN for a row below
+    2^-120, which counts as zeros."""
+    top = v.abs().amax(1)
+    e = torch.floor(torch.log2(torch.where(top >= 2.0 ** -120, top, torch.nan))) - 7
+    return e
+
+
+def tree_attn_kv8_tight(q, codes, scales, v_codes, v_scales, k_tree, v_tree, kv_len, parent, scale):
+    """As tree_attn_kv8, with the tolerance of the roundings that the kernel makes.  With scores s
+    in log2 units, weights p = 2^(s - max s) and ev the exponent of a V row (its block's scale, or that
+    which brings a tree row's largest magnitude to [128, 256)):
+
+      query    two 4-bit digits of each element on a scale where the row's largest is in [128, 256).
+               Elements from 2^-2 on are exact; below, each digit is off by half a step of 2^-9 at
+               most: together 2^-16 of the row's largest.  The tree's keys the same.
+      scores   256 products (two digits), each addition off by 2^-24 of the sum of magnitudes A:
+               2^-16 A; the factor, the product with it and the subtraction of the maximum: 2^-22 of
+               the largest A.
+      weights  fp16 P = 2^(s + ev - m + 6 or more), m at most the largest s + ev: half a step is 2^-11
+               of P, and 2^-25 where P is below 2^-14, which is 2^(m - max s - ev - 31) of p.  Where the
+               exponents spread over more than KV8_SPREAD (or one is below -64), bf16: 2^-8 of P; a
+               part of the keys may still be within the spread and in fp16, off by 2^(KV8_SPREAD - 31).
+      V        codes are exact; of the tree's rows elements far below the largest are fp16 subnormals:
+               2^-25 on the scale 2^ev.
+      sums, exponential, output  as above, and 2^-8 of the result."""
+    q, kt, vt = (t.double().cpu() for t in (q, k_tree, v_tree))
+    B, n, Hq, d = q.shape
+    Hkv = kt.shape[2]
+    G = Hq // Hkv
+    log2e = 1.4426950408889634
+    out = torch.zeros(B, n, Hq, d).double()
+    tol = torch.zeros(B, n, Hq, d).double()
+    for b in range(B):
+        L = int(kv_len[b])
+        sees = _tree_sees(n, L, parent[b])
+        blk = np.arange(L) // KV8_BLOCK
+        tree = torch.arange(L + n) >= L
+        for h in range(Hkv):
+            k, v = _key_rows(codes, scales, kt, b, h, L), _key_rows(v_codes, v_scales, vt, b, h, L)
+            ev = torch.cat([torch.from_numpy(np.log2(v_scales[b, h][blk])), _row_exponents(v[L:])])
+            known = ev[~torch.isnan(ev)]
+            wide = known.numel() > 0 and (float(known.max() - known.min()) > KV8_SPREAD or float(known.min()) < E_MIN)
+            ev = torch.where(torch.isnan(ev), float(E_MIN), ev)
+            v_off = torch.where(tree, torch.exp2(ev - 25), 0.0)[:, None]
+            for g in range(G):
+                x = q[b, :, h * G + g]
+                s = torch.where(sees, (x @ k.T) * (scale * log2e), -torch.inf)
+                top = s.amax(1, keepdim=True)
+                p = torch.exp2(s - top)
+                l = p.sum(1, keepdim=True)
+                A = (x.abs() @ k.abs().T) * scale
+                xm, km = x.abs().amax(1)[:, None], k.abs().amax(1)[None]
+                ds = 2.0 ** -16 * A + 2.0 ** -16 * scale * (xm * k.abs().sum(1)[None] + torch.where(
+                    tree, x.abs().sum(1)[:, None] * km + 2.0 ** -16 * d * xm * km, 0.0))
+                ds = torch.where(sees, ds, 0.0).amax(1, keepdim=True)
+                ds = ds + 2.0 ** -22 * torch.where(sees, A, 0.0).amax(1, keepdim=True)
+                c = 2.0 * (torch.expm1(ds) + 2.0 ** -21 + sees.sum(1, keepdim=True).double() * 2.0 ** -24)
+                if wide:
+                    w = 2.0 ** -8 * p + 2.0 ** (KV8_SPREAD - 31) * sees
+                else:
+                    m = (s + ev).amax(1, keepdim=True)
+                    w = torch.maximum(2.0 ** -11 * p, torch.exp2(m - top - ev - 31) * sees)
+                o = (p @ v) / l
+                out[b, :, h * G + g] = o
+                tol[b, :, h * G + g] = HALF_BF16 * o.abs() + ((w + c * p) @ v.abs() + p @ v_off.expand(-1, d)) / l
     return out, tol

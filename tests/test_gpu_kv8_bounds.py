@@ -1,0 +1,109 @@
+"""GPU checks of the 8-bit cache's tree attention to the tolerance of its own roundings
+(oracle/prompt_kv8.py, tree_attn_kv8_tight), per output element."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from oracle import prompt_kv8 as ref
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+def _E():
+    import eagle_tree_speculative_gb300 as E
+    return E
+
+
+def _bf16(shape, seed, gain=0.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * torch.exp(gain * torch.randn(shape[-1], generator=g))).bfloat16()
+
+
+def _dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x)).to(dtype).cuda().contiguous()
+
+
+def _quantise(x, L):
+    """x [B, Hkv, Lmax, D] float64, rows below L[b] written as the calls write them."""
+    B, Hkv, Lmax = x.shape[:3]
+    codes = np.full(x.shape, 0x7F, np.uint8)
+    scales = np.full((B, Hkv, -(-Lmax // ref.KV8_BLOCK)), np.nan)
+    for b in range(B):
+        for h in range(Hkv):
+            ref.write_rows(x[b, h, :L[b]], 0, codes[b, h], scales[b, h])
+    return codes, scales
+
+
+def _cache(B, Hkv, L, Lmax, seed):
+    return _quantise(_bf16((B, Hkv, Lmax, D), seed).double().numpy(), L)
+
+
+def _trees(B, n, seed):
+    return np.stack([W.random_tree(n, 12, seed, b) if n > 1 else np.array([-1], np.int32) for b in range(B)])
+
+
+def _check(q, k, v, kt, vt, L, parent, scale=None):
+    """k, v: (codes, scales) of the cache."""
+    E = _E()
+    put = lambda c: (torch.from_numpy(c[0].copy()).cuda().view(torch.float8_e4m3fn), torch.from_numpy(c[1]).float().cuda())  # noqa: E731
+    (k8, ks), (v8, vs) = put(k), put(v)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = E.eagle_tree_attn_kv8(q.cuda(), k8, v8, ks, vs, kt.cuda(), vt.cuda(), _dev(L), _dev(parent), scale=scale, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    o, tol = ref.tree_attn_kv8_tight(q, *k, *v, kt, vt, L, parent, scale or D ** -0.5)
+    worst = float(((out.double().cpu() - o).abs() / (tol + 1e-300)).max())
+    assert worst <= 1.0, f"output off by {worst:.3g} times the bound"
+
+
+# ---------------------------------------------------------------- V of very different size
+@pytest.mark.parametrize("n,Hq", [(1, 2), (5, 2), (48, 4)])
+@pytest.mark.parametrize("at", [0, 500, 998])
+@pytest.mark.parametrize("power", [8, 16, 24, 30, 40, 51])
+def test_one_large_value_leaves_other_columns_alone(power, at, n, Hq):
+    """One element of V is 2^power, all others are around one: in the other 127 columns its block
+    holds (nearly) zeros, and the other blocks' weights are the whole output."""
+    L = [999]
+    x = _bf16((1, 1, 1024, D), 3).double().numpy()
+    x[0, 0, at, 17] = 2.0 ** power
+    q, kt, vt = _bf16((1, n, Hq, D), 1), _bf16((1, n, 1, D), 4), _bf16((1, n, 1, D), 5)
+    _check(q, _cache(1, 1, L, 1024, 2), _quantise(x, L), kt, vt, L, _trees(1, n, 6))
+
+
+@pytest.mark.parametrize("n,Hq", [(2, 2), (20, 2), (64, 4)])
+@pytest.mark.parametrize("power", [12, 30, 50])
+def test_one_large_value_of_the_tree_leaves_other_columns_alone(power, n, Hq):
+    """The same with the large element in the tree's root, which every node sees."""
+    L = [130]
+    q, kt, vt = _bf16((1, n, Hq, D), 11), _bf16((1, n, 1, D), 14), _bf16((1, n, 1, D), 15)
+    vt[0, 0] = 0
+    vt[0, 0, 0, 17] = 2.0 ** power
+    _check(q, _cache(1, 1, L, 160, 12), _cache(1, 1, L, 160, 13), kt, vt, L, _trees(1, n, 16))
+
+
+@pytest.mark.parametrize("n,Hq,Hkv", [(1, 8, 2), (9, 4, 2), (60, 8, 2)])
+def test_blocks_of_any_scale(n, Hq, Hkv):
+    """V blocks from 2^-60 to 2^44; the ones from 2^-10 on have no value in half of the columns."""
+    L, Lmax = [3000, 40], 95 * 32
+    codes, _ = _cache(2, Hkv, L, Lmax, 22)
+    scales = np.exp2(np.random.default_rng(7).integers(-60, 45, (2, Hkv, 95)).astype(np.float64))
+    blocks = codes.reshape(2, Hkv, 95, 32, D)
+    blocks[..., :64] = np.where(scales[..., None, None] >= 2.0 ** -10, 0, blocks[..., :64])
+    q, kt, vt = _bf16((2, n, Hq, D), 21), _bf16((2, n, Hkv, D), 24), _bf16((2, n, Hkv, D), 25)
+    vt[..., :64] = 0
+    _check(q, _cache(2, Hkv, L, Lmax, 23), (codes, scales), kt, vt, L, _trees(2, n, 26))
+
+
+def test_wide_units_beside_ordinary_ones():
+    """More units than SMs, heads of a wide spread among others, in every third sequence."""
+    B, Hkv, n = 24, 8, 3
+    L = [100 + 37 * b for b in range(B)]
+    x = _bf16((B, Hkv, 1000, D), 33).double().numpy()
+    x[::3, ::2, 70, 5] = 2.0 ** 33
+    x[1, 3, 40:70] *= 2.0 ** -30
+    q, kt, vt = _bf16((B, n, 16, D), 31), _bf16((B, n, Hkv, D), 34), _bf16((B, n, Hkv, D), 35)
+    vt[5, 1] = 0
+    vt[6, 2] *= 2.0 ** -40
+    _check(q, _cache(B, Hkv, L, 1000, 32), _quantise(x, L), kt, vt, L, _trees(B, n, 36))
