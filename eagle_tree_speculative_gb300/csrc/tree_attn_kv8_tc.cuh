@@ -244,6 +244,11 @@ __device__ __forceinline__ uint32_t half2_bf162(uint32_t h) {
 // |x| in [2^-6, 448]; smaller ones are rounded to its 2^-9 grid when they are converted).
 __device__ __forceinline__ float lead(float x) { return __uint_as_float(__float_as_uint(x) & 0xfff00000u); }
 
+// The least exponent of a row's digits.  Their factor with the softmax's, scale log2 e 2^e, keeps 16 bits
+// and more down to 2^-133, and a key's scale joins it afterwards: small queries may meet keys as large
+// as bf16 and the cache hold them.
+constexpr int kLowExp = -126;
+
 // Exponent e that brings a row with the given largest magnitude to [128, 256), within [lo, 120].
 __device__ __forceinline__ int digit_exp(float amax, int lo) {
     const int E = (int)(__float_as_uint(amax) >> 23) - 127;
@@ -689,7 +694,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     for (int k = 0; k < 8; k += 4) {                         // four row pairs at once, to hide their latencies
                         int e[4];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
+                        for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], kLowExp);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             const int rr = r0 + 2 * (k + y) + (lane >> 4), at = (warp & 3) * 32 + rr;
@@ -1027,7 +1032,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         for (int k = 0; k < pairs; k += 4) {                     // four row pairs at once, to hide their latencies
                             int e[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], -40);
+                            for (int y = 0; y < 4; ++y) e[y] = row_exp(v[y], kLowExp);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
                                 const int row = r0 + 2 * (k + y), c = lane & 15;

@@ -375,7 +375,7 @@ eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, 
  *   out    = softmax(scale * q . k) . v, fp32 accumulation, bf16 result.
  * One node (n = 1, parent = -1) is ordinary decoding.
  * Roundings on the way: elements of a query or of a tree's K row to 2^-16 of their row's
- * largest; weights to fp16 (2^-11 of the weight), or, where the exponents of the V scales that
+ * largest (and no finer than 2^-135); weights to fp16 (2^-11 of the weight), or, where the exponents of the V scales that
  * a sequence and head sees spread over more than 8, to bf16 (2^-8; such calls take twice
  * as long).
  *   q        bf16 [B, n, Hq, head_dim]
