@@ -9,7 +9,6 @@ the optional ``dev_status`` int32 tensor (bits EAGLE_DEV_*).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -72,6 +71,18 @@ def _stream(stream):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on `stream` writes.  It comes from that stream's pool (memory from the
+    current stream's may still be in use there when another stream writes it), and the pool gets
+    it back only when the current stream, where the caller goes on with it, is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _status(dev_status, device):
     if dev_status is None:
         return None
@@ -101,11 +112,11 @@ def eagle_tree_attn(q, k_cache, v_cache, kv_len, parent, scale=None, out=None, w
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _dev(out, "out", torch.bfloat16)
     need = tree_attn_workspace_size(B, n, Hq, Hkv, d, Lmax)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("eagle_tree_attn", lib().eagle_tree_attn(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_len), _ptr(parent), _ptr(out),
@@ -128,7 +139,7 @@ def eagle_ttt_attn(q, k, v, r, scale=None, out=None, dev_status=None, stream=Non
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _dev(out, "out", torch.bfloat16)
     _check("eagle_ttt_attn", lib().eagle_ttt_attn(
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), B, S, Hq, Hkv, d, R1, int(r), float(scale),
@@ -143,7 +154,7 @@ def verify_filter_workspace_size(B, n, R) -> int:
 def eagle_d2t_inverse(d2t, V, t2d=None, dev_status=None, stream=None):
     """t2d int32 [V]: the draft id of each target id (d + d2t[d] -> d), -1 where none."""
     _dev(d2t, "d2t", torch.int32)
-    t2d = torch.empty(V, dtype=torch.int32, device=d2t.device) if t2d is None else t2d
+    t2d = _empty(V, torch.int32, d2t.device, stream) if t2d is None else t2d
     _dev(t2d, "t2d", torch.int32)
     _check("eagle_d2t_inverse", lib().eagle_d2t_inverse(
         _ptr(d2t), d2t.numel(), int(V), _ptr(t2d), _ptr(_status(dev_status, d2t.device)),
@@ -173,9 +184,9 @@ def eagle_verify_accept(target_logits, draft_logits, tokens, parent, max_depth, 
         _dev(draft_row, "draft_row", torch.int32)
     dev = tokens.device
     D = int(max_depth)
-    accept_len = torch.empty(B, dtype=torch.int32, device=dev) if accept_len is None else accept_len
-    path = torch.empty(B, D + 1, dtype=torch.int32, device=dev) if path is None else path
-    emit = torch.empty(B, D + 1, dtype=torch.int32, device=dev) if emit is None else emit
+    accept_len = _empty(B, torch.int32, dev, stream) if accept_len is None else accept_len
+    path = _empty((B, D + 1), torch.int32, dev, stream) if path is None else path
+    emit = _empty((B, D + 1), torch.int32, dev, stream) if emit is None else emit
     if row_stats is not None:
         _dev(row_stats, "row_stats", torch.float32)
     if (top_k or top_p) and temperature > 0:
@@ -183,7 +194,7 @@ def eagle_verify_accept(target_logits, draft_logits, tokens, parent, max_depth, 
             raise ValueError("top-k / top-p filtering with a draft vocabulary is not offered")
         need = int(lib().eagle_verify_filter_workspace_size(B, n, R))
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            workspace = _empty(max(need, 1), torch.uint8, dev, stream)
         _dev(workspace, "workspace")
         _check("eagle_verify_accept_filtered", lib().eagle_verify_accept_filtered(
             _ptr(target_logits), _ptr(draft_logits), _ptr(draft_row), _ptr(tokens), _ptr(parent),
@@ -243,9 +254,9 @@ def eagle_verify_accept_sharded(target_shards, draft_shards, shard_begin, tokens
         _dev(draft_row, "draft_row", torch.int32)
     dev = tokens.device
     D = int(max_depth)
-    accept_len = torch.empty(B, dtype=torch.int32, device=dev) if accept_len is None else accept_len
-    path = torch.empty(B, D + 1, dtype=torch.int32, device=dev) if path is None else path
-    emit = torch.empty(B, D + 1, dtype=torch.int32, device=dev) if emit is None else emit
+    accept_len = _empty(B, torch.int32, dev, stream) if accept_len is None else accept_len
+    path = _empty((B, D + 1), torch.int32, dev, stream) if path is None else path
+    emit = _empty((B, D + 1), torch.int32, dev, stream) if emit is None else emit
     if row_stats is not None:
         _dev(row_stats, "row_stats", torch.float32)
     _check("eagle_verify_accept_sharded", lib().eagle_verify_accept_sharded(
@@ -375,9 +386,9 @@ def eagle_prompt_attn(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, 
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty((Tq, Hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((Tq, Hq, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((Tq, Hq), torch.float32, q.device, stream)
     _args(fn, dev, ((cu_q, "cu_q", torch.int32, cu_q.shape), (cu_k, "cu_k", torch.int32, cu_q.shape),
                     (out, "out", torch.bfloat16, q.shape)))
     if lse is not None:
@@ -457,7 +468,7 @@ def eagle_tree_attn_kv8(q, k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, par
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _args(fn, dev, (*_kv8_specs(k8, v8, k_scale, v_scale, (B, Hkv), Lmax, d),
                     (k_tree, "k_tree", bf16, tree), (v_tree, "v_tree", bf16, tree),
                     (kv_len, "kv_len", torch.int32, (B,)), (parent, "parent", torch.int32, (B, n)),
@@ -466,9 +477,7 @@ def eagle_tree_attn_kv8(q, k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, par
     if workspace is None:
         ws_bytes = _tree_attn_kv8_workspace_size(dev, B, n, Hq, Hkv, d, Lmax)
         if ws_bytes:
-            # scratch belongs to the stream that uses it
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _empty(ws_bytes, torch.uint8, q.device, stream)
     else:
         _dev(workspace, "workspace")
         if workspace.get_device() != dev:
@@ -535,9 +544,9 @@ def eagle2_tree_candidates(tree_state, B, top_k, depth, stream=None):
     _dev(tree_state, "tree_state")
     C = 1 + top_k + (depth - 1) * top_k * top_k
     dev = tree_state.device
-    out = {"value": torch.empty(B, C, device=dev), "conf": torch.empty(B, C, device=dev)}
+    out = {name: _empty((B, C), torch.float32, dev, stream) for name in ("value", "conf")}
     for name in ("token", "parent", "depth", "draft_row"):
-        out[name] = torch.empty(B, C, dtype=torch.int32, device=dev)
+        out[name] = _empty((B, C), torch.int32, dev, stream)
     nbytes = tree_state.numel() * tree_state.element_size()
     _check("eagle2_tree_candidates", lib().eagle2_tree_candidates(
         _ptr(tree_state), nbytes, B, top_k, depth, _ptr(out["value"]), _ptr(out["conf"]),
@@ -617,10 +626,10 @@ def eagle_softmax_stats(logits, temperature, row_max=None, row_sum=None, row_arg
     dev = logits.device
     shp = logits.shape[:-1]
     if temperature > 0:
-        row_max = torch.empty(shp, dtype=torch.float32, device=dev) if row_max is None else row_max
-        row_sum = torch.empty(shp, dtype=torch.float32, device=dev) if row_sum is None else row_sum
+        row_max = _empty(shp, torch.float32, dev, stream) if row_max is None else row_max
+        row_sum = _empty(shp, torch.float32, dev, stream) if row_sum is None else row_sum
     if row_argmax is None and (argmax or temperature <= 0):
-        row_argmax = torch.empty(shp, dtype=torch.int32, device=dev)
+        row_argmax = _empty(shp, torch.int32, dev, stream)
     _check("eagle_softmax_stats", lib().eagle_softmax_stats(
         _ptr(logits), rows, V, float(temperature), _ptr(row_max), _ptr(row_sum), _ptr(row_argmax),
         _ptr(_status(dev_status, dev)), _stream(stream)))
@@ -637,7 +646,7 @@ def eagle_lmhead_gemm(hidden, w, out=None, ldo=None, rows_per_group=None, group_
     M, K = hidden.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty(M, N, dtype=torch.float32, device=hidden.device)
+        out = _empty((M, N), torch.float32, hidden.device, stream)
     _dev(out, "out", torch.float32)
     ldo = N if ldo is None else ldo
     rpg = M if rows_per_group is None else rows_per_group
