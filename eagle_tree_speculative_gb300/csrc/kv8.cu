@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kCommitWarps * 32, 2) kv8_commit_kernel(Commit
     __shared__ int s_path[kMaxNodes + 1];
     __shared__ int s_ok;
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
+    const int rank = (int)cg::this_cluster().block_rank();
     const int b = blockIdx.x / CS;
     const int acc = a.accept_len[b];
     const int L = a.kv_len[b];
@@ -261,8 +261,7 @@ __global__ void __launch_bounds__(kCommitWarps * 32, 2) kv8_commit_kernel(Commit
         }
         if (odd) flag_error(a.dev_status, odd);
     }
-    if constexpr (CS > 1) cg::this_cluster().sync();
-    else __syncthreads();
+    cg::this_cluster().sync();
     if (rank == 0 && tid == 0) a.kv_len_out[b] = ok ? L + acc + 1 : L;
 }
 
@@ -333,17 +332,10 @@ extern "C" eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree,
     a.n_layers = n_layers; a.B = B; a.n = n; a.Hkv = Hkv; a.D = max_depth;
     a.dev_status = dev_status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // clusters of 8 up to about two waves of CTAs, fewer for larger batches: 64 sequences of 32 layers
-    // take 31.5 us with 8, 36.5 with 4 and 43 with 2
-    const int sms = cached_sm_count();
-    int cs = 8;
-    while (cs > 1 && (int64_t)B * cs > 4LL * sms) cs >>= 1;
-    cudaError_t e;
-    switch (cs) {
-        case 8: e = launch_clustered(kv8_commit_kernel<8>, B, 8, kCommitWarps * 32, 0, s, a); break;
-        case 4: e = launch_clustered(kv8_commit_kernel<4>, B, 4, kCommitWarps * 32, 0, s, a); break;
-        case 2: e = launch_clustered(kv8_commit_kernel<2>, B, 2, kCommitWarps * 32, 0, s, a); break;
-        default: e = launch_clustered(kv8_commit_kernel<1>, B, 1, kCommitWarps * 32, 0, s, a); break;
-    }
+    // Clusters of 8 for up to a sequence an SM, of 4 for more.  us with 8 / 4 / 2 / 1, 32 layers: 1 sequence
+    // 16 / 23 / 39 / 53, 64: 35 / 37 / 57 / 86, 100: 51 / 57 / 72 / 90, 153: 70 / 68 / 76 / 92, 305: 127 / 117 /
+    // 127 / 137, 400: 160 / 148 / 156 / 166.
+    const cudaError_t e = B <= cached_sm_count() ? launch_clustered(kv8_commit_kernel<8>, B, 8, kCommitWarps * 32, 0, s, a)
+                                                 : launch_clustered(kv8_commit_kernel<4>, B, 4, kCommitWarps * 32, 0, s, a);
     return e == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
 }
