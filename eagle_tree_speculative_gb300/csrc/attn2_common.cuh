@@ -32,26 +32,30 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 // Bounded wait, in as little code as it can be: these kernels wait in many places, and their
-// speed depends on how much code goes round.  False when the abort flag is up, or after two ticks
-// of the clock's upper word (2^32 to 2^33 cycles, two to four seconds), which raises the flag.
+// speed depends on how much code goes round.  False when the abort flag is up, or after `limit`
+// ticks of the clock, which raises the flag.  wait_for: two ticks of the clock's upper word (2^32 to
+// 2^33 cycles, two to four seconds).
 __device__ __forceinline__ uint32_t clock_hi() {
     uint32_t x;
     asm volatile("mov.u32 %0, %%clock_hi;\n" : "=r"(x));
     return x;
 }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    const uint32_t b = bar;
-    if (mbar_try_wait(b, parity & 1u)) return true;
-    const uint32_t t0 = clock_hi();
+template <class Clock>
+__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volatile int* abort_flag, Clock clock, uint32_t limit) {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    const uint32_t t0 = clock();
 #pragma unroll 1
-    while (!mbar_try_wait(b, parity & 1u)) {
+    while (!mbar_try_wait(bar, parity & 1u)) {
         if (*abort_flag) return false;
-        if (clock_hi() - t0 >= 2u) {
+        if (clock() - t0 >= limit) {
             *abort_flag = 1;
             return false;
         }
     }
     return true;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return wait_until(bar, parity, abort_flag, [] { return clock_hi(); }, 2u);
 }
 
 // Arrival and commit of one lane, `on`, without a branch: warps that part for a lane's instruction

@@ -29,6 +29,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "attn2_common.cuh"
 #include "tc_common.cuh"
 
 namespace eagle {
@@ -306,17 +307,33 @@ extern "C" int eagle_abi_version(void) { return 100; }
 namespace eagle {
 namespace {
 
+// Warp 0 polls as mbar_wait does, warp 1 with attn2's loop, both for max_cycles; warp 2 waits as the
+// two-slot attention kernels do, and leaves when warp 1 raises the flag.
 __global__ void wait_selftest_kernel(int32_t* dev_status, long long max_cycles) {
     __shared__ uint64_t bar;
-    if (threadIdx.x != 0) return;
-    mbar_init(s32(&bar), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    const long long t0 = clock64();
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait(s32(&bar), 0u)) return;            // never: no arrival
-        if ((it & 127u) == 127u && clock64() - t0 > max_cycles) break;
+    __shared__ int abort_flag, given_up;
+    if (threadIdx.x == 0) {
+        mbar_init(s32(&bar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        abort_flag = given_up = 0;
     }
-    flag_error(dev_status, EAGLE_DEV_TIMEOUT);
+    __syncthreads();
+    const int warp = threadIdx.x >> 5;
+    bool over = false;                                       // nothing arrives: every wait gives up
+    if (warp == 0) {
+        const long long t0 = clock64();
+        for (uint32_t it = 0; !over; ++it) {
+            if (mbar_try_wait(s32(&bar), 0u)) break;
+            over = (it & 127u) == 127u && clock64() - t0 > max_cycles;
+        }
+    } else if (warp == 1) {
+        over = !attn2::wait_until(s32(&bar), 0u, &abort_flag, [] { return (uint32_t)clock64(); }, (uint32_t)max_cycles);
+    } else {
+        over = !attn2::wait_for(s32(&bar), 0u, &abort_flag);
+    }
+    if (over && (threadIdx.x & 31) == 0) atomicAdd(&given_up, 1);
+    __syncthreads();
+    if (threadIdx.x == 0 && given_up == 3 && abort_flag) flag_error(dev_status, EAGLE_DEV_TIMEOUT);
 }
 
 }  // namespace
@@ -325,7 +342,7 @@ __global__ void wait_selftest_kernel(int32_t* dev_status, long long max_cycles) 
 extern "C" eagle_status eagle_wait_selftest(int32_t* dev_status, int64_t max_cycles,
                                             eagle_stream_t stream) {
     if (!dev_status || max_cycles < 1 || max_cycles > eagle::kTimeoutCycles) return EAGLE_ERR_INVALID_ARG;
-    eagle::wait_selftest_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+    eagle::wait_selftest_kernel<<<1, 96, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
         dev_status, (long long)max_cycles);
     EAGLE_CHECK_LAUNCH();
     return EAGLE_OK;

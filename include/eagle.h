@@ -587,9 +587,10 @@ eagle_status eagle_lmhead_gemm(const void* hidden, const void* w, float* out, in
 /* Human-readable name of a status code (static string). */
 /* ---------------------------------------------------------------------------
  * eagle_wait_selftest -- exercises the bounded-wait path of the pipelined
- * kernels.  No counterpart in the paper.  One thread waits on an mbarrier that
- * nothing completes, polling it exactly as the pipelines do, for at most
- * max_cycles SM clock cycles (1 .. 4e9), then ORs EAGLE_DEV_TIMEOUT into
+ * kernels.  No counterpart in the paper.  Three warps wait on an mbarrier that
+ * nothing completes, polling it exactly as the pipelines do: two, one with each form of
+ * the loop, for at most max_cycles SM clock cycles (1 .. 4e9), the third until
+ * another wait has given up.  When all three have, ORs EAGLE_DEV_TIMEOUT into
  * *dev_status (required, device memory) and returns.  Lets a caller (or a test)
  * check that an expired wait reports a status and leaves the context usable.
  * ------------------------------------------------------------------------- */
