@@ -107,3 +107,42 @@ def test_wide_units_beside_ordinary_ones():
     vt[5, 1] = 0
     vt[6, 2] *= 2.0 ** -40
     _check(q, _cache(B, Hkv, L, 1000, 32), _quantise(x, L), kt, vt, L, _trees(B, n, 36))
+
+
+# ---------------------------------------------------------------- ordinary rows
+def _plain_check(B, n, Hq, Hkv, L, Lmax, seed, scale=None):
+    q, kt, vt = _bf16((B, n, Hq, D), seed), _bf16((B, n, Hkv, D), seed + 1), _bf16((B, n, Hkv, D), seed + 2)
+    _check(q, _cache(B, Hkv, L, Lmax, seed + 3), _cache(B, Hkv, L, Lmax, seed + 4), kt, vt, L, _trees(B, n, seed), scale)
+
+
+@pytest.mark.parametrize("L", [0, 1, 33, 128, 129, 300, 1000])
+@pytest.mark.parametrize("n,Hq,Hkv", [(1, 4, 2), (17, 6, 2), (64, 8, 1)])
+def test_every_length(L, n, Hq, Hkv):
+    _plain_check(1, n, Hq, Hkv, [L], max(L, 1) + L % 5, 100 + L + n)
+
+
+def test_ragged_batch():
+    L = [0, 1, 700, 64, 129, 31, 2000, 513]
+    _plain_check(8, 11, 8, 2, L, 2048, 141)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-3])
+def test_sharp_and_flat_softmax(scale):
+    _plain_check(1, 20, 4, 1, [900], 1000, 147, scale)
+
+
+def cancelling_rows(seed):
+    """Two cache rows whose values cancel but for the weights' difference, for 64 nodes whose own
+    values are zero: what is left of an output is the weights' rounding errors."""
+    n, Hq = 64, 4
+    q, kt = _bf16((1, n, Hq, D), seed) * 0.02, _bf16((1, n, 1, D), seed + 1) * 0.02
+    k = _cache(1, 1, [2], 32, seed + 2)
+    a = torch.randint(8, 16, (D,), generator=torch.Generator().manual_seed(seed + 3)).double().numpy() / 8
+    x = np.zeros((1, 1, 32, D))
+    x[0, 0, 0], x[0, 0, 1] = a, -a
+    return q, k, _quantise(x, [2]), kt, torch.zeros(1, n, 1, D).bfloat16(), [2], W.random_tree(n, 12, seed, 0)[None]
+
+
+@pytest.mark.parametrize("seed", [161, 171, 181])
+def test_weights_keep_eleven_bits(seed):
+    _check(*cancelling_rows(seed))
