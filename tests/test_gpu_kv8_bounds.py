@@ -131,6 +131,12 @@ def test_sharp_and_flat_softmax(scale):
     _plain_check(1, 20, 4, 1, [900], 1000, 147, scale)
 
 
+@pytest.mark.parametrize("n,Hq", [(1, 1), (1, 8), (30, 4)])
+def test_one_long_sequence_of_one_head(n, Hq):
+    """30 000 rows of one kv head: more parts of a unit than a warp has lanes to merge."""
+    _plain_check(1, n, Hq, 1, [30000], 30016, 151)
+
+
 def cancelling_rows(seed):
     """Two cache rows whose values cancel but for the weights' difference, for 64 nodes whose own
     values are zero: what is left of an output is the weights' rounding errors."""
