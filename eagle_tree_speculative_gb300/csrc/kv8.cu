@@ -282,7 +282,7 @@ extern "C" eagle_status eagle_kv8_append(const void* k, const void* v, const int
                                          int Lmax, int64_t k_stride, int64_t v_stride,
                                          int32_t* dev_status, eagle_stream_t stream) {
     if (T < 0 || B < 0 || Hkv < 1 || Lmax < 1) return EAGLE_ERR_INVALID_ARG;
-    if (head_dim != kHeadDim || Hkv > 65535) return EAGLE_ERR_SHAPE;
+    if (head_dim != kHeadDim || Hkv > 65535 || Lmax > kv8::kMaxRows) return EAGLE_ERR_SHAPE;
     const int64_t row = (int64_t)Hkv * kHeadDim;
     if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
         return EAGLE_ERR_INVALID_ARG;
@@ -315,7 +315,7 @@ extern "C" eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree,
                                          int32_t* dev_status, eagle_stream_t stream) {
     if (n_layers < 0 || B < 0 || n < 1 || Hkv < 1 || Lmax < 1 || max_depth < 0)
         return EAGLE_ERR_INVALID_ARG;
-    if (head_dim != kHeadDim || n > kMaxNodes || max_depth > kMaxNodes ||
+    if (head_dim != kHeadDim || n > kMaxNodes || max_depth > kMaxNodes || Lmax > kv8::kMaxRows ||
         (int64_t)n_layers * 2 * Hkv > 0x3fffffffLL)
         return EAGLE_ERR_SHAPE;
     if (B == 0 || n_layers == 0) return EAGLE_OK;       // nothing read or written

@@ -9,6 +9,7 @@ namespace kv8 {
 
 constexpr int kKv8Block = EAGLE_KV8_BLOCK;
 constexpr int kMinExp = -64;              // the smallest scale is 2^-64
+constexpr int kMaxRows = 0x7fffffff - 127;  // of a cache: its last tile of 128 ends within 32 bits
 
 // Two floats as e4m3 codes (nearest, ties to even, saturating; NaN stays NaN), lo in the
 // low byte.

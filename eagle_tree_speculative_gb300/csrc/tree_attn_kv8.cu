@@ -52,7 +52,7 @@ using namespace eagle;
 extern "C" size_t eagle_tree_attn_kv8_workspace_size(int B, int n, int Hq, int Hkv, int head_dim,
                                                      int Lmax) {
     if (B < 1 || n < 1 || n > kMaxNodes || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || head_dim != kHeadDim ||
-        Lmax < 1 || (int64_t)n * (Hq / Hkv) > 0x3fffffffLL)
+        Lmax < 1 || Lmax > kv8::kMaxRows || (int64_t)n * (Hq / Hkv) > 0x3fffffffLL)
         return 0;
     const int rows = n * (Hq / Hkv);
     const int64_t positions = kv8_positions(B, rows, Hkv, Lmax);
@@ -70,7 +70,7 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
                                             int32_t* dev_status, eagle_stream_t stream) {
     if (B < 0 || n < 1 || Hq < 1 || Hkv < 1 || Lmax < 1 || !(scale > 0.f) || !(scale <= 3.4e38f))
         return EAGLE_ERR_INVALID_ARG;
-    if (n > kMaxNodes || head_dim != kHeadDim || Hq % Hkv != 0) return EAGLE_ERR_SHAPE;
+    if (n > kMaxNodes || head_dim != kHeadDim || Hq % Hkv != 0 || Lmax > kv8::kMaxRows) return EAGLE_ERR_SHAPE;
     if ((int64_t)n * (Hq / Hkv) > 0x3fffffffLL) return EAGLE_ERR_SHAPE;
     const int rows = n * (Hq / Hkv);
     const int64_t positions = kv8_positions(B, rows, Hkv, Lmax);

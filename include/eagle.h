@@ -325,7 +325,7 @@ eagle_status eagle_prompt_attn(const void* q, const void* k, const void* v, cons
  * and kv head:
  *   k8, v8            e4m3 codes [.., B, Hkv, Lmax, head_dim]
  *   k_scale, v_scale  f32 [.., B, Hkv, ceil(Lmax / EAGLE_KV8_BLOCK)], powers of two
- *   row r = code[r] * scale[r / EAGLE_KV8_BLOCK]
+ *   row r = code[r] * scale[r / EAGLE_KV8_BLOCK],   Lmax <= 2^31 - 128
  * Rows that need a scale get the least 2^e, e >= -64, with max |x| <= 448 * 2^e; their
  * codes are x / 2^e rounded to the nearest e4m3 value, ties to even.  Rows that join a
  * block which already holds rows raise its scale if they need to: the rows it holds

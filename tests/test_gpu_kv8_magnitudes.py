@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv8_bounds import D, _bf16, _cache, _check, _trees
+from tests.test_gpu_kv8_bounds import D, _bf16, _cache, _check, _trees
 
 pytestmark = pytest.mark.gpu
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import prompt_kv8 as ref
-from test_gpu_kv8_bounds import D, cancelling_rows
+from tests.test_gpu_kv8_bounds import D, cancelling_rows
 
 
 def _with_rounded_weights(q, k, v, kt, vt, L, parent, dtype):
