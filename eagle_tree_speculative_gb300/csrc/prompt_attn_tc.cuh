@@ -51,6 +51,9 @@ constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
 constexpr int kInfo = 3;                          // units in flight between the roles
 constexpr float kRescale = 8.f;                   // log2 units the maximum may grow by
+// Keys of a sequence: a unit goes through them in 2^20 tiles of 3 300 cycles at most, during which the
+// roles that are done with it wait for the next one.  Waits give up from 2^32 cycles on.
+constexpr int kMaxKeys = 1 << 27;
 
 struct Args {
     const int32_t* cu_q;
@@ -362,7 +365,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             int top = 0, units = 0, nq0 = 0, nk0 = 0;
             for (int b = lane; b < a.B; b += 32) {
                 const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-                if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) bad = true;
+                if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk || k1 - k0 > kMaxKeys) bad = true;
                 else if (q1 > q0) {
                     if (b < 32) { nq0 = q1 - q0; nk0 = k1 - k0; }
                     units += (q1 - q0 + 2 * a.P - 1) / (2 * a.P);

@@ -310,8 +310,8 @@ eagle_status eagle_ttt_attn(const void* q, const void* k, const void* v, void* o
  * below 2^30.  Every row of a sequence's keys must be finite (masked keys are read; a
  * zero weight does not cancel NaN); rows of no sequence and of other sequences may
  * hold anything.
- * Device errors: cu_q or cu_k decreasing or out of range sets EAGLE_DEV_CAPACITY and
- * nothing is written.
+ * Device errors: cu_q or cu_k decreasing or out of range, or a sequence of more than 2^27
+ * keys, sets EAGLE_DEV_CAPACITY and nothing is written.
  * ------------------------------------------------------------------------- */
 eagle_status eagle_prompt_attn(const void* q, const void* k, const void* v, const int32_t* cu_q,
                                const int32_t* cu_k, void* out, float* lse, int Tq, int Tk, int B,
