@@ -1090,7 +1090,8 @@ def kernel_case(name, reps):
       prompt   attention of 8 packed prompts of 2048 tokens, 32/8 heads
       attn_kv8 tree attention over the 8-bit cache, the shape of `attn`
       append_kv8  those prompts' rows quantised into the 8-bit cache, one layer
-      commit_kv8  the path of `compact` committed into an 8-bit cache, 32 layers, B=4
+      commit_kv8  the path of `compact` committed into an 8-bit cache, 32 layers, B=4, lengths
+               inside blocks that hold rows (from the second repetition on at their final scale)
     """
     import torch
 
@@ -1225,7 +1226,13 @@ def kernel_case(name, reps):
         k8, v8, ks, vs = E.kv8_cache(c.n_layers, B, c.Hkv, c.Lmax, c.head_dim, dev)
         kt, vt = (normal((c.n_layers, B, c.n, c.Hkv, c.head_dim), 1.0, torch.bfloat16)
                   for _ in range(2))
-        kv_len = torch.full((B,), c.L, dtype=torch.int32, device=dev)
+        pos = torch.full((B,), c.L, dtype=torch.int32, device=dev)
+        held = torch.tensor([5, 17, 30, 11], dtype=torch.int32, device=dev)
+        kv_len = pos + held                    # rows c.L .. kv_len - 1 are there
+        cu = torch.cat([held.new_zeros(1), held.cumsum(0).int()])
+        rows = normal((int(cu[-1]), 2 * c.Hkv, c.head_dim), 1.0, torch.bfloat16)
+        for i in range(c.n_layers):
+            E.eagle_kv8_append(rows[:, :c.Hkv], rows[:, c.Hkv:], cu, pos, k8[i], v8[i], ks[i], vs[i])
         new_len = torch.empty_like(kv_len)
         path = torch.full((B, c.depth + 1), -1, dtype=torch.int32, device=dev)
         path[:, :7] = torch.tensor([0, 2, 5, 9, 14, 20, 27], dtype=torch.int32)
