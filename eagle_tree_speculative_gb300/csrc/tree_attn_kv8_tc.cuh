@@ -519,6 +519,8 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (again()) pass(std::true_type{});
         } else if (warp == 2) {
             // ---------------- the spread of each unit's V exponents ----------------
+            // Scales 512 at a time, so that a long piece waits for few loads: in fours of 32, one sequence of
+            // 30 000 rows and one head took 36.5 us instead of 33.4.
             for (int pass = 0;; ++pass) {
                 for (int i = 0;; ++i) {
                     const Unit* u = next_unit(i);
@@ -526,9 +528,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     int top = 0, low = 255;               // exponents as stored
                     const int end = min((u->L + kKv8Block - 1) / kKv8Block, (u->t0 + u->n) * kBlocks);
                     const float* scales = a.v_scale + ((int64_t)u->b * a.Hkv + u->head) * a.NB;
-                    for (int y = u->t0 * kBlocks; y < end; y += 128)
+                    for (int y = u->t0 * kBlocks; y < end; y += 512)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 16; ++k) {
                             const int e = (int)(__float_as_uint(__ldg(scales + min(y + 32 * k + lane, end - 1))) >> 23);
                             top = max(top, e);
                             low = min(low, e);
