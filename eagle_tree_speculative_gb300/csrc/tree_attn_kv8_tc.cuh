@@ -73,8 +73,10 @@ constexpr int kHalfKeys = 64, kHalfBox = kHalfKeys * 128;     // 64 keys x 64 di
 constexpr int kInfo = 3;                          // units in flight between the roles
 constexpr int kTrees = 8;                         // trees in flight, see Shared
 constexpr int kBlocks = kKeys / kKv8Block;        // scales per tile
-// What a unit costs beside its tiles (digits, the tree, its output), in tiles.  3 / 6 / 8 / 12: 202 /
-// 172 / 164 / 161 us for 48 ragged sequences of one node, 273 / 275 / 277 / 281 us for 64 equal trees.
+// What a unit costs beside its tiles (digits, the tree, its output), in tiles.  us with 3 / 6 / 8 / 12: 48
+// ragged sequences of one node 183 / 150 / 139 / 139, 16 ragged trees of 48 nodes 109 / 108 / 109 / 106, 64 equal
+// trees 270 / 271 / 273 / 274; few units: one sequence of 40 heads 28.3 / 29.8 / 29.3 / 29.3, 4 trees of 60 nodes
+// 51.9 / 51.9 / 51.9 / 53.9.
 constexpr int kUnitCost = 8;
 constexpr float kOffset = 6.f, kRescale = 8.f;    // weights up to 2^14
 constexpr int kMaxVExp = 44;                      // V scales up to 2^44, see below
@@ -82,7 +84,10 @@ constexpr int kMaxVExp = 44;                      // V scales up to 2^44, see be
 // largest in the product with its block's scale is off by 2^(x - 31) of itself at most, so 2^8 leaves a
 // weight of 2^-15 (one of 32k equal ones) 8 bits.
 constexpr int kSpread = 8;
-constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles
+// A CTA's piece is at least so many tiles (and fixed costs in tiles).  us with 1 / 2 / 3 / 4 / 6: one sequence,
+// 8 heads, 2048 rows 22.7 / 23.7 / 23.2 / 25.2 / 27.8; one head, 30 000 rows 41.6 / 37 / 35.5 / 31.4 / 31; two trees of
+// 12 nodes 23.2 / 27.3 / 25.7 / 26.2 / 29.3; large batches alike.
+constexpr int kMinTiles = 3;
 
 struct Args {
     const uint16_t* q;
