@@ -109,6 +109,50 @@ def test_wide_units_beside_ordinary_ones():
     _check(q, _cache(B, Hkv, L, 1000, 32), _quantise(x, L), kt, vt, L, _trees(B, n, 36))
 
 
+@pytest.mark.parametrize("Hq,Hkv,n", [(6, 2, 43), (8, 1, 64), (5, 1, 26), (130, 1, 1), (2, 2, 60), (1, 1, 1)])
+def test_wide_units_of_every_shape(Hq, Hkv, n):
+    """Rows that end inside a tile, one and two pairs of row tiles, one row."""
+    L = [300, 0, 61]
+    x = _bf16((3, Hkv, 320, D), 73).double().numpy()
+    x[:, :, 50, 9] = 2.0 ** 28
+    q, kt, vt = _bf16((3, n, Hq, D), 71), _bf16((3, n, Hkv, D), 74), _bf16((3, n, Hkv, D), 75)
+    vt[1, -1] *= 2.0 ** -20
+    _check(q, _cache(3, Hkv, L, 320, 72), _quantise(x, L), kt, vt, L, _trees(3, n, 76))
+
+
+def test_a_replayed_graph_follows_the_spread():
+    """The same captured call on a narrow cache, a wide one and the narrow one again equals eager calls."""
+    E = _E()
+    B, n, Hq, Hkv, L = 3, 7, 8, 2, [500, 300, 64]
+    x = _bf16((B, Hkv, 512, D), 83).double().numpy()
+    narrow = _quantise(x, L)
+    x[1, 0, 100, 3] = 2.0 ** 30
+    wide = _quantise(x, L)
+    k = _cache(B, Hkv, L, 512, 82)
+    put = lambda c: (torch.from_numpy(c[0].copy()).cuda().view(torch.float8_e4m3fn), torch.from_numpy(c[1]).float().cuda())  # noqa: E731
+    (k8, ks), (v8, vs) = put(k), put(narrow)
+    q, kt, vt = _bf16((B, n, Hq, D), 81).cuda(), _bf16((B, n, Hkv, D), 84).cuda(), _bf16((B, n, Hkv, D), 85).cuda()
+    args = (q, k8, v8, ks, vs, kt, vt, _dev(L), _dev(_trees(B, n, 86)))
+    ws = [torch.empty(max(1, E.tree_attn_kv8_workspace_size(B, n, Hq, Hkv, D, 512)), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = torch.empty_like(q)
+    E.eagle_tree_attn_kv8(*args, out=out, workspace=ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        E.eagle_tree_attn_kv8(*args, out=out, workspace=ws[0])
+    got = []
+    for c in (narrow, wide, narrow):
+        new = put(c)
+        v8.view(torch.uint8).copy_(new[0].view(torch.uint8))
+        vs.copy_(new[1])
+        graph.replay()
+        want = E.eagle_tree_attn_kv8(*args, workspace=ws[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        got.append(out.clone())
+    assert torch.equal(got[0], got[2]) and not torch.equal(got[0], got[1])
+
+
 # ---------------------------------------------------------------- ordinary rows
 def _plain_check(B, n, Hq, Hkv, L, Lmax, seed, scale=None):
     q, kt, vt = _bf16((B, n, Hq, D), seed), _bf16((B, n, Hkv, D), seed + 1), _bf16((B, n, Hkv, D), seed + 2)

@@ -100,3 +100,21 @@ def test_a_result_on_a_side_stream_leaves_memory_in_use_alone(name):
         other = [torch.zeros_like(want) for _ in range(2)]
     torch.cuda.synchronize()
     assert torch.equal(y, want) and len(other) == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["prompt", "tree", "tree_kv8"])
+def test_a_captured_call_on_a_forked_stream(name):
+    call = _calls()[name]
+    want = call(None)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
