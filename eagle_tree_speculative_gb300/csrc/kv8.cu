@@ -13,7 +13,7 @@
 //
 // Bound: HBM, 2 bytes read and 1 written per value; in practice the latency of a warp's few dependent
 // accesses, so what counts is warps in flight.  Append, 8 x 2048 rows of 8 heads: 18.4 us, 5.5 TB/s (81% of
-// a copy's rate); commit, 32 layers: 4 sequences 15.8 us, 64 sequences 32 us (its floor is 10 us).
+// a copy's rate); commit, 32 layers: 4 sequences 15.1 us, 64 sequences 35 us (its floor is 10 us).
 #include "common.cuh"
 #include "kv8_common.cuh"
 

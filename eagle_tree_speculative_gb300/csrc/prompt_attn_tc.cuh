@@ -25,8 +25,8 @@
 // the softmax warps may then rescale O without a wait of its own.  P of the next unit's first
 // tile is written only after the same warps have read O of this one, which keeps O safe.
 //
-// Measured: one prompt of 16384 tokens, 32 / 8 heads, 1.51 ms = 1.45 PFLOP/s over the visible keys
-// (78% of the library GEMM's burst, 86% of its sustained rate); 8 prompts of 2048, 0.241 ms, tensor
+// Measured: one prompt of 16384 tokens, 32 / 8 heads, 1.50 ms = 1.47 PFLOP/s over the visible keys
+// (79% of the library GEMM's burst, 87% of its sustained rate); 8 prompts of 2048, 0.239 ms, tensor
 // pipe 53% active.  Bound: the tensor pipe and the softmax in turn (about 1450 cycles a tile), and
 // the MMA warp's control; short prompts: the ends of their units.  An MMA warp per slot took 1.72
 // against 1.61 ms: their products interleave, and both slots wait for both.
@@ -269,7 +269,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // ---------------- MMA issue ----------------
             // One copy of each product's code for both slots; the ring's place is kept as (stage,
             // phase), barrier phases as bits: nothing here may live in local memory, which has next
-            // to no L1 beside this much shared memory.
+            // to no L1 beside this much shared memory.  (The kernel's 32 bytes of stack are the softmax
+            // warps' unit, whose tiles they take by slot, once a unit; there are no spills.)
             const bool leader = attn2::elect_lane();
             const uint32_t on = leader;
             const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);

@@ -7,7 +7,7 @@
 // whole softmax (0.56 ms against 0.275 ms at the first shape below); V is widened to fp16 once per tile
 // instead (every e4m3 value is a half), for both slots, and PV runs in kind::f16.
 //   Q  per row times a power of two that brings its largest element to [128, 256): digits exact
-//      for elements within 2^-9 of the largest, the rest to 2^-17 of it.
+//      for elements within 2^-9 of the largest, the rest to 2^-16 of it.
 //   P  fp16, between 2^-24 and 2^14: a rounding of 2^-11 on a weight, where the largest weight is
 //      at least 2^kOffset (or bf16, see Scales).
 //   the tree's own rows (bf16, n <= 64): K as one 128-key tile with the hi digits in rows 0 .. 63
@@ -43,10 +43,12 @@
 // does not cancel NaN).
 //
 // Measured: 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 0.275 ms (the bf16 cache's kernel:
-// 0.297 ms from twice the bytes); tensor pipe 50% active, 643 MB read.  48 sequences of one node over
-// 100 .. 30 000 rows, 64 / 8 heads: 160 us, 3.8 TB/s.  Bound: the chain of QK, softmax and PV per slot
-// and the MMA warp's control, about 3 800 cycles per 256 rows x 128 keys, and 20 to 30 thousand
-// cycles at a unit's ends; neither HBM nor the tensor pipe is full.
+// 0.296 ms from twice the bytes); tensor pipe 50% active, 644 MB read.  48 sequences of one node over
+// 100 .. 30 000 rows, 64 / 8 heads: 162 us, 3.8 TB/s.  With a second pass in every CTA 0.60 ms and 369 us.
+// Bound: the chain of QK, softmax and PV per slot and the MMA warp's control, about 3 800 cycles per 256
+// rows x 128 keys, and 20 to 30 thousand cycles at a unit's ends; neither HBM nor the tensor pipe is full.
+// ptxas: 548 bytes of spill stores, 620 of loads, 192 bytes of stack, most of them in the warps of 64
+// registers and in the second pass.
 #pragma once
 
 #include <cstddef>

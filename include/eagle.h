@@ -45,8 +45,10 @@
  *     EAGLE_DEV_* bit into *dev_status (an int32 in device memory the caller
  *     zeroes and reads when it synchronises).  dev_status may be NULL.
  *   - No global mutable state, except the fixed tree-state array behind
- *     eagle2_expand_static_state; other calls on different streams are
- *     independent unless they share output buffers.
+ *     eagle2_expand_static_state and what is looked up once (the driver's tensor-map
+ *     encoder; per device, its SM count and that a kernel's shared-memory limit has
+ *     been raised); other calls on different streams are independent unless they
+ *     share output buffers.
  *   - Shapes: n (tree nodes, root included) <= 64; head_dim == 128;
  *     Hq % Hkv == 0; temperature == 0 selects greedy decoding.
  */
@@ -306,7 +308,10 @@ eagle_status eagle_ttt_attn(const void* q, const void* k, const void* v, void* o
  *   out  bf16 [Tq, Hq, head_dim]      lse f32 [Tq, Hq] or NULL
  * Strides are in elements: multiples of 8, at least Hq (Hkv) * head_dim; a fused
  * projection's output can be read in place.  Bases 16-byte aligned.  Rows of out and
- * lse that belong to no sequence are left as they are.  Hq / Hkv <= 128; Tq and Tk
+ * lse that belong to no sequence are left as they are.  A chunk's keys and values, the ones
+ * computed before it included, are packed rows as well: the caches of eagle_tree_attn and
+ * eagle_kv8_append are not read here, so a prompt that is computed in chunks keeps its
+ * bf16 rows until it is done.  P (the softmax weights) is rounded to bf16.  Hq / Hkv <= 128; Tq and Tk
  * below 2^30.  Every row of a sequence's keys must be finite (masked keys are read; a
  * zero weight does not cancel NaN); rows of no sequence and of other sequences may
  * hold anything.
