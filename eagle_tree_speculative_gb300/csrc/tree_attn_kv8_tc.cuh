@@ -21,7 +21,7 @@
 // blocks' scales have in common.  What it does not hold is a wide spread: beside a block of far larger
 // scale, whose codes may well be zero in most columns, the other blocks' weights would be subnormal
 // halves or zero.  A CTA that finds the exponents of a unit's V rows spread over more than kSpread
-// goes through its units a second time, with P and V in bf16 (a rounding of 2^-8; the tree's P with
+// goes through these units a second time, with P and V in bf16 (a rounding of 2^-8; the tree's P with
 // its remainder, its V as it is), which replaces what the first pass wrote.  Only the second
 // pass pays for that: bf16 as a case in the loops cost 5 to 10% of every call, and a copy of
 // the loops that shared values with the first ones 1 to 8%.
@@ -44,10 +44,10 @@
 //
 // Measured: 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 0.275 ms (the bf16 cache's kernel:
 // 0.296 ms from twice the bytes); tensor pipe 50% active, 644 MB read.  48 sequences of one node over
-// 100 .. 30 000 rows, 64 / 8 heads: 162 us, 3.8 TB/s.  With a second pass in every CTA 0.60 ms and 369 us.
+// 100 .. 30 000 rows, 64 / 8 heads: 162 us, 3.8 TB/s.  With a second pass over every unit 0.58 ms and 350 us.
 // Bound: the chain of QK, softmax and PV per slot and the MMA warp's control, about 3 800 cycles per 256
 // rows x 128 keys, and 20 to 30 thousand cycles at a unit's ends; neither HBM nor the tensor pipe is full.
-// ptxas: 548 bytes of spill stores, 620 of loads, 192 bytes of stack, most of them in the warps of 64
+// ptxas: 616 bytes of spill stores, 700 of loads, 200 bytes of stack, most of them in the warps of 64
 // registers and in the second pass.
 #pragma once
 
@@ -303,6 +303,41 @@ __device__ __forceinline__ int row_exp(const uint4& v, int lo_exp) {
     return digit_exp(m, lo_exp);
 }
 
+// Warp-wide: whether the exponents of the V rows in tiles [t0, t1) of a (sequence, kv head) spread over more
+// than kSpread, or one is below the least of the cache.  Scales are loaded 512 at a time, so that a long
+// piece waits for few loads: in fours of 32, one sequence of 30 000 rows and one head took 36.5 us instead
+// of 33.4.
+__device__ __forceinline__ bool wide_spread(const Args& a, int b, int head, int t0, int t1, bool tree, int L) {
+    const int lane = threadIdx.x & 31;
+    int top = 0, low = 255;                       // exponents as stored
+    const int end = min((L + kKv8Block - 1) / kKv8Block, t1 * kBlocks);
+    const float* scales = a.v_scale + ((int64_t)b * a.Hkv + head) * a.NB;
+    for (int y = t0 * kBlocks; y < end; y += 512)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int e = (int)(__float_as_uint(__ldg(scales + min(y + 32 * k + lane, end - 1))) >> 23);
+            top = max(top, e);
+            low = min(low, e);
+        }
+    const uint16_t* x = a.v_tree + ((int64_t)b * a.n * a.Hkv + head) * kHeadDim + (lane & 15) * 8;
+    for (int r0 = lane >> 4; tree && r0 - (lane >> 4) < a.n; r0 += 4) {
+        uint4 v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = row_exp(v[k], -127) + 127;
+            if (e == 0) continue;                 // below 2^-120: a row of zeros, or as good as one
+            top = max(top, e);
+            low = min(low, e);
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, low);
+    return top - low > kSpread || low < kv8::kMinExp + 127;
+}
+
 // All threads of the CTA, wherever in the roles' code they are.
 __device__ __forceinline__ void all_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kThreads) : "memory"); }
 
@@ -525,40 +560,13 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             pass(std::false_type{});
             if (again()) pass(std::true_type{});
         } else if (warp == 2) {
-            // ---------------- the spread of each unit's V exponents ----------------
-            // Scales 512 at a time, so that a long piece waits for few loads: in fours of 32, one sequence of
-            // 30 000 rows and one head took 36.5 us instead of 33.4.
+            // ---------------- which units have a wide spread ----------------
             for (int pass = 0;; ++pass) {
                 for (int i = 0;; ++i) {
                     const Unit* u = next_unit(i);
                     if (!__all_sync(0xffffffffu, u != nullptr)) break;
-                    int top = 0, low = 255;               // exponents as stored
-                    const int end = min((u->L + kKv8Block - 1) / kKv8Block, (u->t0 + u->n) * kBlocks);
-                    const float* scales = a.v_scale + ((int64_t)u->b * a.Hkv + u->head) * a.NB;
-                    for (int y = u->t0 * kBlocks; y < end; y += 512)
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int e = (int)(__float_as_uint(__ldg(scales + min(y + 32 * k + lane, end - 1))) >> 23);
-                            top = max(top, e);
-                            low = min(low, e);
-                        }
-                    const uint16_t* x = a.v_tree + ((int64_t)u->b * a.n * a.Hkv + u->head) * kHeadDim + (lane & 15) * 8;
-                    for (int r0 = lane >> 4; u->tree && r0 - (lane >> 4) < a.n; r0 += 4) {
-                        uint4 v[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            v[k] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(r0 + 2 * k, a.n - 1) * a.Hkv * kHeadDim));
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int e = row_exp(v[k], -127) + 127;
-                            if (e == 0) continue;         // below 2^-120: a row of zeros, or as good as one
-                            top = max(top, e);
-                            low = min(low, e);
-                        }
-                    }
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    low = __reduce_min_sync(0xffffffffu, low);
-                    if (lane == 0 && (top - low > kSpread || low < kv8::kMinExp + 127)) sh->wide = 1;
+                    if (pass == 0 && wide_spread(a, u->b, u->head, u->t0, u->t0 + u->n, u->tree, u->L) && lane == 0) sh->wide = 1;
+                    __syncwarp();
                     unit_read(i);
                 }
                 if (pass > 0 || !again()) break;
@@ -581,6 +589,10 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         s = segment_at(a, pos, end, b, base);
                         pos = s.start + s.weight * (s.T + kUnitCost);
                         have = s.t0 < s.t1;
+                        if (pass > 0 && have) {           // the second pass: units of a wide spread alone
+                            const int L = a.kv_len[s.b];
+                            have = L >= 0 && L <= a.Lmax && wide_spread(a, s.b, s.head, s.t0, s.t1, s.t1 == s.T, L);
+                        }
                     }
                     const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) break;

@@ -381,8 +381,8 @@ eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, 
  * One node (n = 1, parent = -1) is ordinary decoding.
  * Roundings on the way: elements of a query or of a tree's K row to 2^-16 of their row's
  * largest (and no finer than 2^-135); weights to fp16 (2^-11 of the weight), or, where the exponents of the V scales that
- * a sequence and head sees spread over more than 8, to bf16 (2^-8; such calls take twice
- * as long).
+ * a sequence and head sees spread over more than 8, to bf16 (2^-8; those sequences and
+ * heads, or the parts of them that see the spread, are computed twice).
  *   q        bf16 [B, n, Hq, head_dim]
  *   k8, v8, k_scale, v_scale  the cache, [B, Hkv, ..]; the scales of blocks with a row
  *            below L_b are powers of two from 2^-64 on, V's at most 2^44

@@ -196,3 +196,27 @@ def cancelling_rows(seed):
 @pytest.mark.parametrize("seed", [161, 171, 181])
 def test_weights_keep_eleven_bits(seed):
     _check(*cancelling_rows(seed))
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv,L", [(3, 1, 2, 1, 20), (4, 5, 8, 2, 300), (40, 9, 8, 8, 200), (400, 1, 8, 8, 40)])
+def test_a_wide_spread_leaves_the_other_sequences_and_heads_alone(B, n, Hq, Hkv, L):
+    """Bit-equal outputs of every other (sequence, head), whether or not one has a wide spread."""
+    E = _E()
+    g = torch.Generator(device="cuda").manual_seed(91)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    k8, v8, ks, vs = (t[0] for t in E.kv8_cache(1, B, Hkv, L))
+    rows = mk(B * L, 2 * Hkv, D)
+    E.eagle_kv8_append(rows[:, :Hkv], rows[:, Hkv:], _dev(np.arange(B + 1) * L), _dev(np.zeros(B)), k8, v8, ks, vs)
+    args = lambda scales, tree: (q, k8, v8, ks, scales, kt, tree, _dev([L] * B), _dev(_trees(B, n, 96)))  # noqa: E731
+    q, kt, vt = mk(B, n, Hq, D), mk(B, n, Hkv, D), mk(B, n, Hkv, D)
+    want = E.eagle_tree_attn_kv8(*args(vs, vt))
+    wide, tree = vs.clone(), vt.clone()
+    wide[B // 2, Hkv - 1, 0] *= 2.0 ** 12
+    tree[0, 0, 0] *= 2.0 ** 12
+    got = E.eagle_tree_attn_kv8(*args(wide, tree))
+    torch.cuda.synchronize()
+    G = Hq // Hkv
+    same = torch.ones(B, Hkv, dtype=torch.bool)
+    same[B // 2, Hkv - 1] = same[0, 0] = False
+    equal = (got == want).view(B, n, Hkv, G * D).all(-1).all(1).cpu()
+    assert equal[same].all() and not equal[~same].any()
