@@ -45,8 +45,8 @@
  *     EAGLE_DEV_* bit into *dev_status (an int32 in device memory the caller
  *     zeroes and reads when it synchronises).  dev_status may be NULL.
  *   - No global mutable state, except the fixed tree-state array behind
- *     eagle2_expand_static_state and what is looked up once (the driver's tensor-map
- *     encoder; per device, its SM count and that a kernel's shared-memory limit has
+ *     eagle2_expand_static_state and what is looked up once (CUDA's tensor-map encoder;
+ *     per device, its SM count and that a kernel's shared-memory limit has
  *     been raised); other calls on different streams are independent unless they
  *     share output buffers.
  *   - Shapes: n (tree nodes, root included) <= 64; head_dim == 128;
@@ -382,7 +382,8 @@ eagle_status eagle_kv8_commit(const void* k_tree, const void* v_tree, void* k8, 
  * Roundings on the way: elements of a query or of a tree's K row to 2^-16 of their row's
  * largest (and no finer than 2^-135); weights to fp16 (2^-11 of the weight), or, where the exponents of the V scales that
  * a sequence and head sees spread over more than 8, to bf16 (2^-8; those sequences and
- * heads, or the parts of them that see the spread, are computed twice).
+ * heads, or the parts of them that see the spread, are computed twice).  A tree's V row
+ * below 2^-120 may count as zeros.
  *   q        bf16 [B, n, Hq, head_dim]
  *   k8, v8, k_scale, v_scale  the cache, [B, Hkv, ..]; the scales of blocks with a row
  *            below L_b are powers of two from 2^-64 on, V's at most 2^44
