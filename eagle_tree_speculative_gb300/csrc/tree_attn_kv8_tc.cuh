@@ -36,10 +36,9 @@
 // small kernel merges them.
 //
 // Roles: warp 0 loads K and V tiles, warp 1 issues the MMAs, warp 2 looks for wide spreads, warp 3 cuts
-// the work, warps 4-11 are
-// the softmax, which also makes the Q digits of the next unit before it writes this one's output,
-// warps 12-15 widen V into two tiles (of two halves of 64 keys) and make the K digits of the tree's
-// rows; V rows behind the last key become zeros there (whatever bits lie in them: a zero weight
+// the work, warps 4-11 are the softmax, which also makes the Q digits of the next unit before it
+// writes this one's output, warps 12-15 widen V into two tiles (of two halves of 64 keys) and make the K
+// digits of the tree's rows; V rows behind the last key become zeros there (whatever bits lie in them: a zero weight
 // does not cancel NaN).
 //
 // Measured: 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 0.275 ms (the bf16 cache's kernel:
