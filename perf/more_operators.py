@@ -349,8 +349,10 @@ def _plain_assign(s):
     first = torch.full((B,), B, device="cuda").scatter_reduce(0, of, torch.where(src < 0, B, key), "amin")
     stays = (key == first[of]) & (refs[last.clamp(min=0)] <= 1)
     copy = (src >= 0) & (part > 0) & ~stays
-    kept = torch.where(src < 0, 0, full + ((part > 0) & ~copy))
-    fresh = (col >= kept[:, None]) & (col < need[:, None])
+    # a slot that continues itself keeps what it holds behind its rows, unless it is shared
+    more = (src == me)[:, None] & (col >= full[:, None]) & (col < s["held"][:, None]) & (refs[theirs.clamp(min=0)] <= 1)
+    there = (src >= 0)[:, None] & ((col < full[:, None]) | ((col == full[:, None]) & ((part > 0) & ~copy)[:, None]) | more)
+    fresh = (col < need[:, None]) & ~there
     free = torch.argsort((refs != 0).int(), stable=True)                            # free pages first, by number
     rank = (fresh.view(-1).cumsum(0) - 1).view_as(fresh).clamp(0, N - 1)
     now = torch.where(fresh, free[rank], theirs)
@@ -467,7 +469,7 @@ def _exact_attn(s, c):
 
 
 def _exact_assign(s, c):
-    """Slot by slot, with sets of pages."""
+    """Slot by slot, page by page."""
     B, page, old = s["B"], s["page"], s["page_table"].tolist()
     refs, held = s["refs"].tolist(), s["held"].tolist()
     free = sorted(p for p, r in enumerate(refs) if r == 0)
@@ -478,14 +480,16 @@ def _exact_assign(s, c):
         L = c["L"][t] if t >= 0 else 0
         need = -(-(L + c["grow"][b]) // page)
         row = old[t][:L // page] if t >= 0 else []
-        if L % page:
-            heirs = [x for x in range(B) if c["src"][x] == t]
-            if b == (t if t in heirs else heirs[0]) and refs[old[t][L // page]] == 1:
-                row = row + [old[t][L // page]]
+        for x in range(L // page, need):
+            alone = t >= 0 and x < held[t] and refs[old[t][x]] == 1
+            if x == L // page and L % page:                       # the page that the rows end in
+                heirs = [y for y in range(B) if c["src"][y] == t]
+                stays = alone and b == (t if t in heirs else heirs[0])
+                if not stays:
+                    moves.append((old[t][x], free[0], L % page))
             else:
-                moves.append((old[t][L // page], free[0], L % page))
-        while len(row) < need:
-            row = row + [free.pop(0)]
+                stays = alone and t == b
+            row = row + [old[t][x] if stays else free.pop(0)]
         table.append(row + [-1 if x < held[b] else old[b][x] for x in range(need, len(old[b]))])
         lengths.append(L)
     for a, z, r in moves:
