@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "attn2_common.cuh"
+#include "attn2_cut.cuh"
 #include "kv8_common.cuh"
 
 namespace eagle {
@@ -105,86 +106,25 @@ struct Args {
     int rows;                                     // n G, at most 2 kRows of a unit are counted
     float scale_log2;
     int32_t* dev_status;
-};
 
-// ---------------- the cut: shared by the attention and the merging kernel ----------------
-// Positions: sequence by sequence, head by head, row-tile pair by pair, tile by tile; a tile of a
-// pair counts 2, of a single row tile 1, and a unit's first tile kUnitCost more (its digits,
-// its output).  The host refuses sizes with 2^31 positions or more.
-struct Cut {
-    int total;                                    // positions
-    int ctas;                                     // pieces
-    __device__ int begin(int c) const { return total / ctas * c + total % ctas * c / ctas; }
-};
-__device__ __forceinline__ int tiles_of(const Args& a, int b) {
-    const int L = a.kv_len[b];
-    return (L < 0 || L > a.Lmax) ? 1 : (L + kKeys - 1) / kKeys + 1;
-}
-__device__ __forceinline__ int row_tiles(const Args& a) { return (a.n * a.G + kRows - 1) / kRows; }
-
-// Warp-wide.
-__device__ __forceinline__ Cut make_cut(const Args& a, int grid) {
-    int sum = 0;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) sum += tiles_of(a, b) + kUnitCost;
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    Cut c;
-    const int rt = row_tiles(a);
-    c.total = sum * rt * a.Hkv;
-    c.ctas = max(1, min(grid, c.total / (kMinTiles * min(rt, 2))));
-    return c;
-}
-
-// A unit and the tiles of it that lie in [pos, end).
-struct Segment {
-    int b, head, pair, T;                         // T tiles in all, the last one the tree's
-    int weight;                                   // row tiles of the pair
-    int start;                                    // position of its first tile
-    int t0, t1;
-};
-// Tiles of a unit that begins at `start` whose own position lies before pos.
-__device__ __forceinline__ int tiles_before(int start, int weight, int pos) {
-    return pos <= start ? 0 : max(1, ((pos - start + weight - 1) >> (weight - 1)) - kUnitCost);
-}
-
-// Warp-wide: the unit at position pos; `b`, `base`: a sequence at or before it and its first
-// position, moved on.
-__device__ __forceinline__ Segment segment_at(const Args& a, int pos, int end, int& b, int& base) {
-    const int rt = row_tiles(a), lane = threadIdx.x & 31;
-    for (;;) {                                    // 32 sequences at a time
-        const int mine = b + lane;
-        const int w = mine < a.B ? (tiles_of(a, mine) + kUnitCost) * rt * a.Hkv : 0;
-        int sum = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, base + sum > pos);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            base += __shfl_sync(0xffffffffu, sum - w, l);
-            b += l;
-            break;
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
-        b += 32;
-        if (b >= a.B) { b = a.B - 1; break; }     // not reached: pos < total
+    // what the cut and the merging kernel ask for
+    static constexpr int kUnitCost = kv8_tc::kUnitCost, kMinTiles = kv8_tc::kMinTiles;
+    __device__ int tiles_of(int b) const {        // key tiles of a sequence, the tree's the last
+        const int L = kv_len[b];
+        return (L < 0 || L > Lmax) ? 1 : (L + kKeys - 1) / kKeys + 1;
     }
-    Segment s;
-    s.b = b;
-    s.T = tiles_of(a, b);
-    int off = pos - base;
-    const int per_tile = s.T + kUnitCost, per_head = per_tile * rt;
-    s.head = off / per_head;
-    off -= s.head * per_head;
-    s.pair = off / (2 * per_tile);
-    off -= s.pair * 2 * per_tile;
-    s.weight = min(2, rt - 2 * s.pair);
-    s.start = pos - off;
-    s.t0 = min(s.T, tiles_before(s.start, s.weight, pos));
-    s.t1 = min(s.T, tiles_before(s.start, s.weight, end));
-    return s;
-}
+    __device__ int row_tiles() const { return (n * G + kRows - 1) / kRows; }
+    __device__ int unit_rows(int pair) const { return min(n * G - pair * 2 * kRows, 2 * kRows); }
+    __device__ int64_t out_row(int b, int head, int pair, int row) const {
+        const int r = pair * 2 * kRows + row;
+        return ((int64_t)b * n + r / G) * Hq + head * G + r % G;
+    }
+};
+
+using attn2::Cut;
+using attn2::make_cut;
+using attn2::Segment;
+using attn2::segment_at;
 
 // ---------------- the attention kernel ----------------
 struct Unit {
@@ -1136,69 +1076,9 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #undef BAR_AT
 }
 
-// ---------------- merging of cut units ----------------
-// Blocks (c, y): the unit whose first tile lies in piece c and whose last does not, one warp a row;
-// its parts are piece c's second place and the first places of the pieces behind it.  m is in
-// log2 units and a part's l and O share one factor, so a part weighs 2^(m - max m).  Lane p looks
-// after part p (of up to 32 at a time), so that the parts' loads do not wait for one another.  The
-// launch may begin while the attention kernel ends; the partials are awaited below.
-constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-
-__global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args a, int grid) {
-    const int lane = threadIdx.x & 31;
-    const Cut cut = make_cut(a, grid);
-    const int c = blockIdx.x;
-    // A block that has nothing to merge awaits the attention kernel too: a kernel launched next
-    // waits for this one alone.
-    auto await = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
-    if (c + 1 >= cut.ctas) { await(); return; }           // the last piece ends with a whole unit
-    const int begin = cut.begin(c), end = cut.begin(c + 1);
-    int b = 0, base = 0;
-    const Segment s = segment_at(a, end - 1, end, b, base);
-    if (s.start < begin || s.t1 >= s.T) { await(); return; }   // it begins earlier, or is whole
-    const int rows = min(a.n * a.G - s.pair * 2 * kRows, 2 * kRows);
-    // lane's part: piece c + lane, and whether it holds tiles of the unit
-    auto place_of = [&](int p) -> int {                   // -1: none, -2: none from here on
-        if (p == c) return c * 2 + 1;
-        if (p >= cut.ctas) return -2;
-        const int t0 = tiles_before(s.start, s.weight, cut.begin(p));
-        const int t1 = p + 1 < cut.ctas ? tiles_before(s.start, s.weight, cut.begin(p + 1)) : s.T;
-        return t0 >= s.T ? -2 : t0 < t1 ? p * 2 : -1;
-    };
-    const int first = place_of(c + lane);
-    await();
-    for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = c;; p0 += 32) {
-            const int place = p0 == c ? first : place_of(p0 + lane);
-            const bool there = place >= 0;
-            const float2 ml = there ? a.ws_ml[(int64_t)place * a.rows + row] : make_float2(-INFINITY, 0.f);
-            float top = ml.x;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float mn = fmaxf(m, top), at = mn == -INFINITY ? 0.f : mn;
-            const float w = exp2f(ml.x - at), wo = exp2f(m - at);
-            m = mn;
-            l = l * wo + warp_sum(ml.y * w);
-            o.x *= wo; o.y *= wo; o.z *= wo; o.w *= wo;
-            const unsigned live = __ballot_sync(0xffffffffu, there);
-            const int parts = 32 - __clz(live);           // places up to the last one that is there
-#pragma unroll 4
-            for (int p = 0; p < parts; ++p) {
-                const int at_p = max(__shfl_sync(0xffffffffu, place, p), 0);
-                const float wp = __shfl_sync(0xffffffffu, w, p);
-                const float4 x = *reinterpret_cast<const float4*>(a.ws_o + ((int64_t)at_p * a.rows + row) * kHeadDim + 4 * lane);
-                if ((live >> p) & 1u) { o.x += x.x * wp; o.y += x.y * wp; o.z += x.z * wp; o.w += x.w * wp; }
-            }
-            if (__any_sync(0xffffffffu, place == -2)) break;
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int r = s.pair * 2 * kRows + row;
-        uint16_t* out = a.out + (((int64_t)s.b * a.n + r / a.G) * a.Hq + s.head * a.G + r % a.G) * kHeadDim;
-        reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-    }
-}
+using attn2::kMergeThreads;
+using attn2::kMergeWarps;
+__global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args a, int grid) { attn2::merge_parts(a, grid); }
 
 }  // namespace kv8_tc
 }  // namespace eagle
