@@ -491,6 +491,184 @@ def eagle_tree_attn_kv8(q, k8, v8, k_scale, v_scale, k_tree, v_tree, kv_len, par
     return out
 
 
+# ---------------------------------------------------------------- the paged cache
+def paged_cache(n_layers, n_pages, Hkv, page, B, max_pages, d=128, device="cuda"):
+    """An empty paged cache: (k_pages, v_pages, page_table, held, refs) for the calls below, pages
+    [n_layers, n_pages, Hkv, page, d] and, for B sequences, a table [B, max_pages]."""
+    pages = [torch.zeros(n_layers, n_pages, Hkv, page, d, dtype=torch.bfloat16, device=device)
+             for _ in range(2)]
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device=device)
+    return (*pages, table, *(torch.zeros(m, dtype=torch.int32, device=device) for m in (B, n_pages)))
+
+
+def _page_shape(fn, k_pages, dims):
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise TypeError("k_pages must be a CUDA tensor")
+    if k_pages.dim() != dims:
+        raise ValueError(f"{fn}: k_pages must be {'[n_layers, ' if dims == 5 else '['}N, Hkv, page, d]")
+    return k_pages.shape
+
+
+def _table_shape(fn, page_table):
+    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
+        raise TypeError("page_table must be a CUDA tensor")
+    if page_table.dim() != 2:
+        raise ValueError(f"{fn}: page_table must be [B, P]")
+    return page_table.shape
+
+
+def _workspace(fn, dev, workspace, need, stream, device):
+    """(tensor or None, bytes): the caller's workspace, or one of `need` bytes."""
+    if workspace is None:
+        return (_empty(need, torch.uint8, device, stream) if need else None), need
+    _dev(workspace, "workspace")
+    if workspace.get_device() != dev:
+        raise ValueError(f"{fn}: workspace is on {workspace.device}, other tensors on cuda:{dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def pages_workspace_size(B, N, P) -> int:
+    return int(lib().eagle_pages_workspace_size(B, N, P))
+
+
+def eagle_pages_assign(k_pages, v_pages, page_table, held, refs, kv_len, grow, src=None,
+                       workspace=None, dev_status=None, stream=None):
+    """Room for grow [B] rows behind each sequence's kv_len [B], after slot b went on with what
+    slot src[b] held (None: its own; -1: nothing).  page_table [B,P], held [B], refs [N] and kv_len
+    (int32) are updated in place; rows of pages that are shared no longer are copied in every
+    layer of k_pages / v_pages [n_layers,N,Hkv,page,d] bf16.  All or nothing: see dev_status."""
+    fn = "eagle_pages_assign"
+    nl, N, Hkv, page, d = _page_shape(fn, k_pages, 5)
+    B, P = _table_shape(fn, page_table)
+    dev, i32, bf16 = k_pages.get_device(), torch.int32, torch.bfloat16
+    _args(fn, dev, ((k_pages, "k_pages", bf16, k_pages.shape), (v_pages, "v_pages", bf16, k_pages.shape),
+                    (page_table, "page_table", i32, (B, P)), (held, "held", i32, (B,)),
+                    (refs, "refs", i32, (N,)), (kv_len, "kv_len", i32, (B,)), (grow, "grow", i32, (B,))))
+    if src is not None:
+        _args(fn, dev, ((src, "src", i32, (B,)),))
+    need = pages_workspace_size(B, N, P) if workspace is None else 0
+    workspace, ws_bytes = _workspace(fn, dev, workspace, need, stream, k_pages.device)
+    _launch(fn, dev, stream, (
+        k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), held.data_ptr(), refs.data_ptr(),
+        kv_len.data_ptr(), grow.data_ptr(), _ptr(src), nl, B, N, Hkv, page, d, P, _ptr(workspace), ws_bytes,
+        _status_ptr(fn, dev, dev_status)))
+
+
+def eagle_pages_commit(k_pages, v_pages, page_table, kv_len, path, accept_len, max_depth,
+                       kv_len_out=None, dev_status=None, stream=None):
+    """Moves the accepted path's rows behind the committed ones in every layer of the pages
+    [n_layers,N,Hkv,page,d] bf16; kv_len is advanced in place, or into kv_len_out."""
+    fn = "eagle_pages_commit"
+    nl, N, Hkv, page, d = _page_shape(fn, k_pages, 5)
+    B, P = _table_shape(fn, page_table)
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    D, dev, i32, bf16 = int(max_depth), k_pages.get_device(), torch.int32, torch.bfloat16
+    _args(fn, dev, ((k_pages, "k_pages", bf16, k_pages.shape), (v_pages, "v_pages", bf16, k_pages.shape),
+                    (page_table, "page_table", i32, (B, P)), (kv_len, "kv_len", i32, (B,)),
+                    (kv_len_out, "kv_len_out", i32, (B,)), (path, "path", i32, (B, D + 1)),
+                    (accept_len, "accept_len", i32, (B,))))
+    _launch(fn, dev, stream, (
+        k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+        kv_len_out.data_ptr(), path.data_ptr(), accept_len.data_ptr(), nl, B, N, Hkv, page, d, P, D,
+        _status_ptr(fn, dev, dev_status)))
+    return kv_len_out
+
+
+def eagle_qkv_rope(q, k, v, inv_freq, pos, cu=None, parent=None, q_weight=None, k_weight=None,
+                   eps=1e-6, interleaved=False, k_pages=None, v_pages=None, page_table=None,
+                   q_out=None, k_out=None, dev_status=None, stream=None):
+    """Norms of q's and k's heads (where weights [d] bf16 are given) and their rotation by
+    position, and k and v into the cache's pages (one layer, [N,Hkv,page,d] bf16) where those are
+    given.  q [T,Hq,d], k / v [T,Hkv,d] bf16 (tokens may be strided), inv_freq f32
+    [rot_dim / 2], pos int32 [B]: the rows that each sequence holds.  The tokens are packed by cu
+    [B+1], or the nodes of trees with parent [B,n] (T = B * n).  Returns (q_out [T,Hq,d], k_out
+    [T,Hkv,d]); with pages, k_out is written only if it is given."""
+    fn = "eagle_qkv_rope"
+    sq, sk = _token_rows(fn, q, "q"), _token_rows(fn, k, "k")
+    T, Hq, d = q.shape
+    Hkv, dev, i32, bf16 = k.shape[1], q.get_device(), torch.int32, torch.bfloat16
+    if k.shape != (T, Hkv, d):
+        raise ValueError(f"{fn}: k must be [{T}, Hkv, {d}], got {list(k.shape)}")
+    if (cu is None) == (parent is None):
+        raise ValueError(f"{fn}: either cu or parent")
+    _dev(pos, "pos", i32)
+    _dev(inv_freq, "inv_freq", torch.float32)
+    B, n = pos.numel(), 0
+    if parent is not None:
+        _dev(parent, "parent", i32)
+        n = T // B if B else 0
+    specs = [(pos, "pos", i32, (B,)), (inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),)),
+             (cu, "cu", i32, (B + 1,)) if parent is None else (parent, "parent", i32, (B, n))]
+    N = page = P = sv = 0
+    pages = k_pages is not None or v_pages is not None or page_table is not None
+    if pages:
+        N, _, page, _ = _page_shape(fn, k_pages, 4)
+        P = _table_shape(fn, page_table)[1]
+        sv = _token_rows(fn, v, "v")
+        if v.shape != k.shape or v.get_device() != dev:
+            raise ValueError(f"{fn}: v must be like k")
+        specs += [(k_pages, "k_pages", bf16, (N, Hkv, page, d)), (v_pages, "v_pages", bf16, (N, Hkv, page, d)),
+                  (page_table, "page_table", i32, (B, P))]
+    elif k_out is None:
+        k_out = _empty((T, Hkv, d), bf16, q.device, stream)
+    if k.get_device() != dev:
+        raise ValueError(f"{fn}: q and k are on different devices")
+    if q_out is None:
+        q_out = _empty((T, Hq, d), bf16, q.device, stream)
+    specs.append((q_out, "q_out", bf16, (T, Hq, d)))
+    if k_out is not None:
+        specs.append((k_out, "k_out", bf16, (T, Hkv, d)))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            specs.append((w, name, bf16, (d,)))
+    _args(fn, dev, specs)
+    _launch(fn, dev, stream, (
+        q.data_ptr(), k.data_ptr(), v.data_ptr() if pages else None, _ptr(q_weight), _ptr(k_weight),
+        inv_freq.data_ptr(), _ptr(cu), _ptr(parent), pos.data_ptr(), q_out.data_ptr(), _ptr(k_out),
+        _ptr(k_pages), _ptr(v_pages), _ptr(page_table), T, B, n, Hq, Hkv, d, 2 * inv_freq.numel(),
+        bool(interleaved), eps, sq, sk, sv, N, page, P, _status_ptr(fn, dev, dev_status)))
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_attn_paged_workspace_size(dev, B, n, Hq, Hkv, head_dim, page, P) -> int:
+    with torch.cuda.device(dev):
+        return tree_attn_paged_workspace_size(B, n, Hq, Hkv, head_dim, page, P)
+
+
+def tree_attn_paged_workspace_size(B, n, Hq, Hkv, head_dim, page, P) -> int:
+    return int(lib().eagle_tree_attn_paged_workspace_size(B, n, Hq, Hkv, head_dim, page, P))
+
+
+def eagle_tree_attn_paged(q, k_pages, v_pages, page_table, kv_len, parent, scale=None, out=None,
+                          workspace=None, dev_status=None, stream=None):
+    """Tree attention over the pages of one layer [N,Hkv,page,d] bf16, the tree's rows in them
+    behind kv_len.  q [B,n,Hq,d] bf16, page_table [B,P], kv_len [B], parent [B,n] int32.  n = 1 with
+    parent -1 is ordinary decoding."""
+    fn = "eagle_tree_attn_paged"
+    _dev(q, "q", torch.bfloat16)
+    if q.dim() != 4:
+        raise ValueError(f"{fn}: q must be [B, n, Hq, d]")
+    B, n, Hq, d = q.shape
+    N, Hkv, page, _ = _page_shape(fn, k_pages, 4)
+    P, dev = _table_shape(fn, page_table)[1], q.get_device()
+    bf16, i32 = torch.bfloat16, torch.int32
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    _args(fn, dev, ((k_pages, "k_pages", bf16, (N, Hkv, page, d)), (v_pages, "v_pages", bf16, (N, Hkv, page, d)),
+                    (page_table, "page_table", i32, (B, P)), (kv_len, "kv_len", i32, (B,)),
+                    (parent, "parent", i32, (B, n)), (out, "out", bf16, q.shape)))
+    need = _tree_attn_paged_workspace_size(dev, B, n, Hq, Hkv, d, page, P) if workspace is None else 0
+    workspace, ws_bytes = _workspace(fn, dev, workspace, need, stream, q.device)
+    _launch(fn, dev, stream, (
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+        parent.data_ptr(), out.data_ptr(), B, n, Hq, Hkv, d, N, page, P, scale, _ptr(workspace), ws_bytes,
+        _status_ptr(fn, dev, dev_status)))
+    return out
+
+
 def expand_scratch_size(B, V, top_k) -> int:
     return int(lib().eagle2_expand_scratch_size(B, V, top_k))
 

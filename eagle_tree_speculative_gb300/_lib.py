@@ -42,6 +42,15 @@ SIGNATURES = {
     "eagle_tree_attn_kv8_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "eagle_tree_attn_kv8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F,
                                  _P, _SZ, _P, _P]),
+    "eagle_pages_workspace_size": (_SZ, [_I, _I, _I]),
+    "eagle_pages_assign": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _SZ,
+                                _P, _P]),
+    "eagle_pages_commit": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "eagle_qkv_rope": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
+                            _I, _I, _I, _I, _F, _I64, _I64, _I64, _I, _I, _I, _P, _P]),
+    "eagle_tree_attn_paged_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "eagle_tree_attn_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F,
+                                   _P, _SZ, _P, _P]),
     "eagle2_tree_state_size": (_SZ, [_I, _I, _I]),
     "eagle2_expand_scratch_size": (_SZ, [_I, _I, _I]),
     "eagle2_expand": (_I, [_I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P, _SZ, _P, _P, _P,

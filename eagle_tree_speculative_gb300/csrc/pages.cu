@@ -1,0 +1,406 @@
+// The pages of the K/V cache: which pages a sequence holds (eagle_pages_assign), and the accepted
+// path's rows brought behind the committed ones (eagle_pages_commit).
+//
+// Assignment.  Everything is decided from the state before the call and nothing is written until it is
+// known that the call can be carried out, in three steps of one cluster with a barrier between
+// them: (1) per slot, a warp each: what it keeps, how many fresh pages it needs, whether all numbers
+// are in range; per part of refs: how many pages are free; (2) the free pages that are needed, by
+// number; (3) per slot: its table, and the differences in refs (integer atomics: their order does
+// not matter).  A fresh page had refs = 0, so no slot that is still being read holds it, and what a call
+// gives back is free for the next one only: no copy's source is another's destination.
+// A second kernel copies the rows of pages that sequences share no longer, in every layer.
+//
+// Commit.  The path is strictly increasing from 0, so path[t] >= t: rows are moved in rounds of rising t, a
+// round's rows all read before any of it is written.  A write to row t of one round is below every
+// path[t'] of the rounds after it, and no earlier round wrote a row of this one's sources.
+#include "paged_common.cuh"
+
+namespace eagle {
+namespace {
+
+// ---------------- assignment ----------------
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+
+// The workspace, in 32-bit words: per slot (kSlotWords), per CTA of the cluster (the free pages of
+// its part), fresh page numbers, and a table of what slots keep.
+struct Slot {
+    int fresh;                                    // pages it needs
+    int from, rows;                               // a page to copy, how many rows of it; rows = 0: none
+    int to;
+    int length;                                   // its rows
+    int bad;
+};
+constexpr int kMaxCluster = 8;
+
+struct AssignArgs {
+    int32_t *table, *held, *refs, *kv_len;
+    const int32_t *grow, *src;
+    Slot* slots;
+    int32_t* free_count;                          // [kMaxCluster]
+    int32_t* free_ids;                            // [min(N, B P)]
+    int32_t* kept;                                // [B][P]
+    int B, N, P, shift;
+    int32_t* dev_status;
+};
+
+size_t assign_words(int B, int N, int P) {
+    const int64_t cells = (int64_t)B * P;
+    return (size_t)B * (sizeof(Slot) / 4) + kMaxCluster + (size_t)(N < cells ? N : cells) + (size_t)cells;
+}
+
+// Warp-wide: the slot that goes on in the page in which s's rows end: s itself, else the first of those that
+// go on with s.
+__device__ __forceinline__ bool goes_on(const AssignArgs& a, int b, int s) {
+    if (!a.src || b == s) return true;
+    const int lane = threadIdx.x & 31;
+    if (__ldcg(a.src + s) == s) return false;
+    for (int x0 = 0; x0 < b; x0 += 32) {
+        const int x = x0 + lane;
+        if (__any_sync(0xffffffffu, x < b && __ldcg(a.src + x) == s)) return false;
+    }
+    return true;
+}
+
+template <int CS>
+__global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) {
+    __shared__ int s_sum[kPlanWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
+    const int page = 1 << a.shift;
+    auto all_sync = [] {
+        if constexpr (CS > 1) cg::this_cluster().sync();
+        else __syncthreads();
+    };
+    auto block_sum = [&](int x) {                 // of every thread; for every thread
+        x = __reduce_add_sync(0xffffffffu, x);
+        __syncthreads();
+        if (lane == 0) s_sum[warp] = x;
+        __syncthreads();
+        int t = 0;
+        for (int w = 0; w < kPlanWarps; ++w) t += s_sum[w];
+        return t;
+    };
+
+    // ---- (1) what each slot keeps and needs; how many pages are free ----
+    for (int b = rank * kPlanWarps + warp; b < a.B; b += CS * kPlanWarps) {
+        const int s = a.src ? a.src[b] : b;
+        Slot y = {};
+        const int had = a.held[b], grow = a.grow[b];
+        bool bad = s < -1 || s >= a.B || had < 0 || had > a.P || grow < 0;
+        int theirs = 0;
+        if (!bad && s >= 0) {
+            y.length = a.kv_len[s];
+            theirs = a.held[s];
+            bad = y.length < 0 || theirs < 0 || theirs > a.P || (int64_t)y.length > (int64_t)theirs << a.shift;
+        }
+        const int full = y.length >> a.shift, part = y.length & (page - 1);
+        const int64_t need64 = ((int64_t)y.length + grow + page - 1) >> a.shift;
+        bad = bad || need64 > a.P;
+        if (!bad) {
+            const int need = (int)need64;
+            const int32_t* old = a.table + (int64_t)b * a.P;
+            const int32_t* from = a.table + (int64_t)max(s, 0) * a.P;
+            int32_t* kept = a.kept + (int64_t)b * a.P;
+            if (s != b) {
+                // its own pages are all given back or found again; those of s up to the full ones are shared
+                for (int t = lane; t < had; t += 32) {
+                    const int id = old[t];
+                    bad |= id < 0 || id >= a.N;
+                }
+                for (int t = lane; t < full; t += 32) {
+                    const int id = from[t];
+                    bad |= id < 0 || id >= a.N;
+                    kept[t] = id;
+                }
+                y.fresh = need - full;
+            } else {
+                for (int t0 = full; t0 < max(need, had); t0 += 32) {
+                    const int t = t0 + lane;
+                    int id = -1;
+                    if (t < had) {
+                        id = old[t];
+                        bad |= id < 0 || id >= a.N;
+                        if (id >= 0 && id < a.N && a.refs[id] > 1) id = -1;
+                    }
+                    if (t < need) kept[t] = id;
+                    y.fresh += __popc(__ballot_sync(0xffffffffu, t < need && id < 0));
+                }
+                // full pages that stay are not looked at
+            }
+            if (part) {
+                const int id = from[full];
+                bad |= id < 0 || id >= a.N;
+                const bool alone = !bad && a.refs[id] <= 1;
+                const bool goes = goes_on(a, b, s);
+                if (alone && goes) {
+                    if (s != b) {
+                        if (lane == 0) kept[full] = id;
+                        --y.fresh;
+                    }
+                } else {
+                    if (s != b && lane == 0) kept[full] = -1;
+                    y.from = id;
+                    y.rows = part;
+                }
+            }
+        }
+        y.bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) a.slots[b] = y;
+    }
+    const int per = (a.N + CS - 1) / CS, r0 = min(a.N, rank * per), r1 = min(a.N, r0 + per);
+    int mine = 0;
+    for (int p = r0 + tid; p < r1; p += kPlanThreads) mine += a.refs[p] == 0;
+    const int frees = block_sum(mine);
+    if (tid == 0) a.free_count[rank] = frees;
+    all_sync();
+
+    // ---- can it be done? ----
+    bool bad = false;
+    int64_t fresh = 0;                            // at most B * P < 2^31, see the host side
+    for (int b = tid; b < a.B; b += kPlanThreads) {
+        bad |= __ldcg(&a.slots[b].bad) != 0;
+        fresh += __ldcg(&a.slots[b].fresh);
+    }
+    const int total = block_sum((int)fresh);
+    int before = 0, there = 0;                    // free pages of lower parts, of all
+    for (int r = 0; r < CS; ++r) {
+        const int x = __ldcg(a.free_count + r);
+        before += r < rank ? x : 0;
+        there += x;
+    }
+    if (__syncthreads_or(bad) || total > there) {       // alike in every CTA
+        if (rank == 0 && tid == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
+        // no copies: the second kernel reads the slots
+        all_sync();
+        for (int b = rank * kPlanThreads + tid; b < a.B; b += CS * kPlanThreads) a.slots[b].rows = 0;
+        return;
+    }
+
+    // ---- (2) the first `total` free pages ----
+    for (int p0 = r0; p0 < r1 && before < total; p0 += kPlanThreads) {
+        const int p = p0 + tid;
+        const bool is = p < r1 && a.refs[p] == 0;
+        const unsigned who = __ballot_sync(0xffffffffu, is);
+        __syncthreads();
+        if (lane == 0) s_sum[warp] = __popc(who);
+        __syncthreads();
+        int at = before + __popc(who & ((1u << lane) - 1u)), all = 0;
+        for (int w = 0; w < kPlanWarps; ++w) {
+            at += w < warp ? s_sum[w] : 0;
+            all += s_sum[w];
+        }
+        if (is && at < total) a.free_ids[at] = p;
+        before += all;
+    }
+    all_sync();
+
+    // ---- (3) tables and counts ----
+    for (int b = rank * kPlanWarps + warp; b < a.B; b += CS * kPlanWarps) {
+        int at = 0;                               // fresh pages of the slots before
+        for (int x = lane; x < b; x += 32) at += __ldcg(&a.slots[x].fresh);
+        at = __reduce_add_sync(0xffffffffu, at);
+        const int s = a.src ? a.src[b] : b;
+        const int length = __ldcg(&a.slots[b].length), had = a.held[b], full = length >> a.shift;
+        const int need = (int)(((int64_t)length + a.grow[b] + page - 1) >> a.shift);
+        // (the pages of s from full on are this slot's only where `kept` says so)
+        const int known = s == b ? need : min(need, full + ((length & (page - 1)) != 0));
+        const int32_t* kept = a.kept + (int64_t)b * a.P;
+        int32_t* row = a.table + (int64_t)b * a.P;
+        for (int t0 = s == b ? full : 0; t0 < max(need, had); t0 += 32) {
+            const int t = t0 + lane;
+            int id = t < known ? __ldcg(kept + t) : -1;
+            const bool fresh_page = t < need && id < 0;
+            const unsigned who = __ballot_sync(0xffffffffu, fresh_page);
+            if (fresh_page) id = __ldcg(a.free_ids + at + __popc(who & ((1u << lane) - 1u)));
+            at += __popc(who);
+            const int was = t < had ? row[t] : -1;
+            if (t < max(need, had) && id != was) {
+                row[t] = id;
+                if (id >= 0) atomicAdd(a.refs + id, 1);
+                if (was >= 0) atomicAdd(a.refs + was, -1);
+            }
+            if (t == full && t < need) a.slots[b].to = id;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            a.held[b] = need;
+            a.kv_len[b] = length;
+        }
+    }
+}
+
+constexpr int kCopyThreads = 256;
+
+// One unit is a slot's page in one layer, K or V: the first `rows` rows of each head.
+__global__ void __launch_bounds__(kCopyThreads)
+pages_copy_kernel(uint16_t* k, uint16_t* v, const Slot* slots, int n_layers, int B, int N, int Hkv, int shift) {
+    const int64_t units = (int64_t)B * n_layers * 2;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int b = (int)(u % B);
+        const int rows = slots[b].rows;
+        if (rows == 0) continue;
+        const int layer = (int)(u / (2 * B)), from = slots[b].from, to = slots[b].to;
+        uint16_t* base = ((u / B) & 1 ? v : k) + (((int64_t)layer * N * Hkv) << shift) * kHeadDim;
+        const uint4* src = reinterpret_cast<const uint4*>(base + paged::row_at(from, 0, 0, Hkv, shift));
+        uint4* dst = reinterpret_cast<uint4*>(base + paged::row_at(to, 0, 0, Hkv, shift));
+        const int chunks = rows * (kHeadDim / 8), per = (kHeadDim / 8) << shift;
+        for (int h = 0; h < Hkv; ++h)
+            for (int c = threadIdx.x; c < chunks; c += kCopyThreads) dst[h * per + c] = src[h * per + c];
+    }
+}
+
+// ---------------- commit ----------------
+constexpr int kCommitThreads = 256, kCommitWarps = kCommitThreads / 32;
+
+struct CommitArgs {
+    uint16_t *k, *v;
+    const int32_t *table, *kv_len, *path, *accept_len;
+    int32_t* kv_len_out;
+    int n_layers, B, N, Hkv, shift, P, D;
+    int32_t* dev_status;
+};
+
+template <int CS>
+__global__ void __launch_bounds__(kCommitThreads) pages_commit_kernel(CommitArgs a) {
+    __shared__ int s_from[kMaxNodes + 1], s_to[kMaxNodes + 1];      // row of a head's slab, all pages one behind the other
+    __shared__ int s_moves, s_ok;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
+    const int b = blockIdx.x / CS;
+    const int acc = a.accept_len[b], L = a.kv_len[b];
+    if (warp == 0) {
+        int err = 0, moves = 0;
+        if (acc >= 0) {
+            if (acc > a.D || L < 0 || (int64_t)L + acc + 1 > (int64_t)a.P << a.shift) err = EAGLE_DEV_CAPACITY;
+            for (int t0 = 0; err == 0 && t0 <= acc; t0 += 32) {
+                const int t = t0 + lane;
+                const bool on = t <= acc;
+                const int p = on ? a.path[(int64_t)b * (a.D + 1) + t] : 0;
+                const int q = on && t > 0 ? a.path[(int64_t)b * (a.D + 1) + t - 1] : -1;
+                int e = 0, from = 0, to = 0;
+                if (on && (t == 0 ? p != 0 : p <= q)) e = EAGLE_DEV_BAD_TREE;
+                else if (on && (int64_t)L + p >= (int64_t)a.P << a.shift) e = EAGLE_DEV_CAPACITY;
+                else if (on && p != t) {
+                    from = a.table[(int64_t)b * a.P + ((L + p) >> a.shift)];
+                    to = a.table[(int64_t)b * a.P + ((L + t) >> a.shift)];
+                    if (from < 0 || from >= a.N || to < 0 || to >= a.N) e = EAGLE_DEV_CAPACITY;
+                }
+                err = __reduce_or_sync(0xffffffffu, e);
+                // the rows that move, in order
+                const unsigned who = __ballot_sync(0xffffffffu, on && p != t);
+                if (on && p != t) {
+                    const int at = moves + __popc(who & ((1u << lane) - 1u)), mask = (1 << a.shift) - 1;
+                    s_from[at] = ((from * a.Hkv) << a.shift) + ((L + p) & mask);
+                    s_to[at] = ((to * a.Hkv) << a.shift) + ((L + t) & mask);
+                }
+                moves += __popc(who);
+            }
+        }
+        if (lane == 0) {
+            if (err && rank == 0) flag_error(a.dev_status, err);
+            s_moves = err ? 0 : moves;
+            s_ok = acc >= 0 && err == 0;
+        }
+    }
+    __syncthreads();
+    const int moves = s_moves;
+    const int units = moves ? a.n_layers * 2 * a.Hkv : 0;            // (layer, K|V, kv head)
+    for (int u = rank * kCommitWarps + warp; u < units; u += CS * kCommitWarps) {
+        const int h = u % a.Hkv, layer = u / (2 * a.Hkv);
+        uint4* base = reinterpret_cast<uint4*>(((u / a.Hkv) & 1 ? a.v : a.k)) +
+                      ((((int64_t)layer * a.N * a.Hkv + h) << a.shift) * (kHeadDim / 8)) + (lane & 15);
+        for (int m0 = 0; m0 < moves; m0 += 8) {                      // four pairs of rows a round
+            uint4 x[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int m = m0 + 2 * y + (lane >> 4);
+                if (m < moves) x[y] = base[(int64_t)s_from[m] * (kHeadDim / 8)];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int m = m0 + 2 * y + (lane >> 4);
+                if (m < moves) base[(int64_t)s_to[m] * (kHeadDim / 8)] = x[y];
+            }
+            __syncwarp();
+        }
+    }
+    // every CTA has read kv_len[b] before it changes
+    if constexpr (CS > 1) cg::this_cluster().sync();
+    else __syncthreads();
+    if (rank == 0 && tid == 0) a.kv_len_out[b] = s_ok ? L + acc + 1 : L;
+}
+
+eagle_status check_pages(int n_layers, int B, int N, int Hkv, int page, int head_dim, int P) {
+    if (n_layers < 0 || B < 0 || N < 1 || Hkv < 1 || P < 1) return EAGLE_ERR_INVALID_ARG;
+    if (head_dim != kHeadDim || !paged::page_ok(page) || (int64_t)N * Hkv * page > paged::kMaxPool ||
+        (int64_t)P * page > paged::kMaxRows || (int64_t)B * P > 0x3fffffff)
+        return EAGLE_ERR_SHAPE;
+    return EAGLE_OK;
+}
+
+}  // namespace
+}  // namespace eagle
+
+using namespace eagle;
+
+extern "C" size_t eagle_pages_workspace_size(int B, int N, int P) {
+    if (B < 1 || N < 1 || P < 1 || (int64_t)B * P > 0x3fffffff) return 0;
+    return assign_words(B, N, P) * 4;
+}
+
+extern "C" eagle_status eagle_pages_assign(void* k_pages, void* v_pages, int32_t* page_table, int32_t* held,
+                                           int32_t* refs, int32_t* kv_len, const int32_t* grow,
+                                           const int32_t* src, int n_layers, int B, int N, int Hkv, int page,
+                                           int head_dim, int P, void* workspace, size_t ws_bytes,
+                                           int32_t* dev_status, eagle_stream_t stream) {
+    const eagle_status ok = check_pages(n_layers, B, N, Hkv, page, head_dim, P);
+    if (ok != EAGLE_OK || B == 0) return ok;
+    if (!page_table || !held || !refs || !kv_len || !grow || (n_layers > 0 && (!k_pages || !v_pages)))
+        return EAGLE_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)k_pages, (const void*)v_pages, (const void*)workspace})
+        if (reinterpret_cast<uintptr_t>(p) & 15) return EAGLE_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < assign_words(B, N, P) * 4) return EAGLE_ERR_CAPACITY;
+    AssignArgs a;
+    a.table = page_table; a.held = held; a.refs = refs; a.kv_len = kv_len;
+    a.grow = grow; a.src = src;
+    a.slots = static_cast<Slot*>(workspace);
+    a.free_count = reinterpret_cast<int32_t*>(a.slots + B);
+    a.free_ids = a.free_count + kMaxCluster;
+    a.kept = a.free_ids + (N < (int64_t)B * P ? N : (int64_t)B * P);
+    a.B = B; a.N = N; a.P = P; a.shift = paged::page_shift(page);
+    a.dev_status = dev_status;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_clustered(pages_plan_kernel<kMaxCluster>, 1, kMaxCluster, kPlanThreads, 0, s, a);
+    if (e != cudaSuccess) return EAGLE_ERR_CUDA;
+    if (n_layers > 0) {
+        const int64_t units = (int64_t)B * n_layers * 2, most = 8LL * cached_sm_count();
+        pages_copy_kernel<<<(unsigned)(units < most ? units : most), kCopyThreads, 0, s>>>(
+            static_cast<uint16_t*>(k_pages), static_cast<uint16_t*>(v_pages), a.slots, n_layers, B, N, Hkv, a.shift);
+        EAGLE_CHECK_LAUNCH();
+    }
+    return EAGLE_OK;
+}
+
+extern "C" eagle_status eagle_pages_commit(void* k_pages, void* v_pages, const int32_t* page_table,
+                                           const int32_t* kv_len, int32_t* kv_len_out, const int32_t* path,
+                                           const int32_t* accept_len, int n_layers, int B, int N, int Hkv,
+                                           int page, int head_dim, int P, int max_depth, int32_t* dev_status,
+                                           eagle_stream_t stream) {
+    const eagle_status ok = check_pages(n_layers, B, N, Hkv, page, head_dim, P);
+    if (ok != EAGLE_OK) return ok;
+    if (max_depth < 0) return EAGLE_ERR_INVALID_ARG;
+    if (max_depth > kMaxNodes) return EAGLE_ERR_SHAPE;
+    if (B == 0 || n_layers == 0) return EAGLE_OK;       // nothing read or written
+    if (!k_pages || !v_pages || !page_table || !kv_len || !kv_len_out || !path || !accept_len) return EAGLE_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)k_pages, (const void*)v_pages})
+        if (reinterpret_cast<uintptr_t>(p) & 15) return EAGLE_ERR_INVALID_ARG;
+    CommitArgs a;
+    a.k = static_cast<uint16_t*>(k_pages); a.v = static_cast<uint16_t*>(v_pages);
+    a.table = page_table; a.kv_len = kv_len; a.path = path; a.accept_len = accept_len;
+    a.kv_len_out = kv_len_out;
+    a.n_layers = n_layers; a.B = B; a.N = N; a.Hkv = Hkv; a.shift = paged::page_shift(page); a.P = P; a.D = max_depth;
+    a.dev_status = dev_status;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return launch_clustered(pages_commit_kernel<8>, B, 8, kCommitThreads, 0, s, a) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+}

@@ -1,0 +1,559 @@
+// Tree attention over the paged K/V cache on the tensor cores (tcgen05, TMEM, TMA).
+//
+// Mathematics: out = softmax(scale q k^T) v per row with the running maximum and sum of the softmax in
+// fp32, in the exp2 domain; P is rounded to bf16 for the PV product (2^-8 of each weight, as the output's
+// own rounding), sums use the unrounded weights.
+//
+// Rows.  A row tile is P = 128 / G nodes x G query heads that share a kv head (row p * G + g), so a
+// kv head's K/V tile serves the whole group.  A unit is one (sequence, kv head, pair of row tiles), its
+// keys in tiles of 128 rows, 128 / page pages each.  With two row tiles each softmax slot has one and both
+// see every key tile: its bytes cross into the SM once for 256 rows.  A single row tile (decoding,
+// small trees) has its key tiles dealt to the slots in turn, merged at the end.
+// All tiles of all units are cut into one equal piece per CTA (attn2_cut.cuh): ragged batches and few long
+// sequences balance alike.
+//
+// Roles: warp 0 loads (Q, then K and V tiles through one ring of 32 KB stages; a lane per page and half of
+// the head dimension, the page numbers a tile ahead), warp 1 issues the MMAs, warp 2 zeroes V rows behind the
+// tree's last (never written: a zero weight does not cancel NaN), warp 3 cuts the work, warps 4-11 are the
+// softmax.
+//
+// MMA order and barriers are those of prompt_attn_tc.cuh: PV of a slot's last tile, then its next QK, whose
+// commit also says that O holds that PV.
+#pragma once
+
+#include <cstddef>
+#include <type_traits>
+
+#include "attn2_common.cuh"
+#include "attn2_cut.cuh"
+#include "paged_common.cuh"
+
+namespace eagle {
+namespace paged_tc {
+
+using attn2::kKeys;
+using attn2::kRows;
+using attn2::kSlots;
+
+constexpr int kThreads = 384;
+// 3 warpgroups x 168 registers at launch; 72 + 2 x 216 = 3 x 168
+constexpr int kRegsRole = 72, kRegsSoftmax = 216;
+constexpr int kStages = 5;
+constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
+constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
+constexpr int kInfo = 3;                          // units in flight between the roles
+constexpr int kUnitCost = 2;                      // what a unit costs beside its tiles, in tiles
+constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles (and unit costs)
+constexpr float kRescale = 8.f;                   // log2 units the maximum may grow by
+
+struct Args {
+    const int32_t* table;
+    const int32_t* kv_len;
+    const int32_t* parent;
+    uint16_t* out;
+    float* ws_o;                                  // [grid][2][rows][128]
+    float2* ws_ml;                                // [grid][2][rows]
+    int B, n, Hq, Hkv, G, P;                      // P: nodes of a row tile
+    int N, shift, width;                          // pages; log2 of a page's rows; entries of a table row
+    int rows;                                     // rows of a part
+    float scale_log2;
+    int32_t* dev_status;
+
+    // what the cut and the merging kernel ask for
+    static constexpr int kUnitCost = paged_tc::kUnitCost, kMinTiles = paged_tc::kMinTiles;
+    __device__ bool bad_length(int L) const { return L < 0 || L + (int64_t)n > (int64_t)width << shift; }
+    __device__ int tiles_of(int b) const {        // a sequence that is refused has one, of zeros
+        const int L = kv_len[b];
+        return bad_length(L) ? 1 : (L + n + kKeys - 1) / kKeys;
+    }
+    __device__ int row_tiles() const { return (n + P - 1) / P; }
+    __device__ int unit_rows(int pair) const {
+        const int left = n - pair * 2 * P;        // nodes from the pair's first on
+        return left > P ? kRows + min(left - P, P) * G : left * G;
+    }
+    __device__ int64_t out_row(int b, int head, int pair, int row) const {
+        const int slot = row >= kRows, r = row - slot * kRows, p = r / G;
+        if (p >= P) return -1;
+        return ((int64_t)b * n + (pair * 2 + slot) * P + p) * Hq + head * G + (r - p * G);
+    }
+};
+
+struct Unit {
+    int b, head, pair;                            // head -1: no more units
+    int t0, n;                                    // first tile, number of tiles (0: write zeros)
+    int L;
+    int split;                                    // one row tile: its key tiles alternate between the slots
+    int part;                                     // -1: whole, else the part's place
+    uint8_t parent[kMaxNodes];
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];       // K/V ring
+    uint64_t v_last[kStages];                     // a V tile that needs repair has landed
+    uint64_t q_full[kSlots], q_empty[kSlots];
+    uint64_t s_full[kSlots], p_full[kSlots], o_full[kSlots];
+    uint64_t merge_in, merge_out;
+    uint64_t info_full[kInfo], info_empty[kInfo];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort_flag;
+    float2 ml[kRows];                             // slot 1's maximum and sum of each row
+    Unit info[kInfo];
+};
+
+constexpr int kSmem = kSlots * kTile + kStages * kTile + (int)sizeof(Shared) + 1024;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+constexpr uint32_t kIdescQK = idesc_bf16(128, kKeys, 0, 0);
+constexpr uint32_t kIdescPV = idesc_bf16(128, kHeadDim, 0, 1);
+
+// Whether a unit's last tile of the cut reaches behind the last row.  Its V tile then lands on the
+// stage's v_last, and the repair warp completes the stage's own barrier once the rows are zero.
+__device__ __forceinline__ bool needs_fix(const Unit& u, int n) { return u.n > 0 && (u.t0 + u.n) * kKeys > u.L + n; }
+
+// What a row with ancestors `anc` sees of 32 keys from the one `at` rows behind L on (at < 0: before L).
+__device__ __forceinline__ uint32_t sees32(unsigned long long anc, int at) {
+    if (at <= -32) return 0xffffffffu;
+    if (at < 0) return ((1u << -at) - 1u) | ((uint32_t)anc << -at);
+    return at < kMaxNodes ? (uint32_t)(anc >> at) : 0u;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((0u - s32(smem_raw)) & 1023u);
+    uint8_t* sQ = smem;                                   // [kSlots][32 KB]
+    uint8_t* sR = sQ + kSlots * kTile;                    // [kStages][32 KB]
+    Shared* sh = reinterpret_cast<Shared*>(sR + kStages * kTile);
+    volatile int* abort_flag = &sh->abort_flag;
+    const uint32_t sb = s32(sh);
+#define BAR(name) (sb + (uint32_t)offsetof(Shared, name))
+#define BAR_AT(name, i) (sb + (uint32_t)offsetof(Shared, name) + 8u * (uint32_t)(i))
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(BAR_AT(full, i), 1);
+            mbar_init(BAR_AT(empty, i), 1);
+            mbar_init(BAR_AT(v_last, i), 1);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(BAR_AT(q_full, s), 1);
+            mbar_init(BAR_AT(q_empty, s), 1);
+            mbar_init(BAR_AT(s_full, s), 1);
+            mbar_init(BAR_AT(p_full, s), 4);
+            mbar_init(BAR_AT(o_full, s), 1);
+        }
+        mbar_init(BAR(merge_in), 4);
+        mbar_init(BAR(merge_out), 4);
+        // read by the loading, the MMA and the repair warp and the eight softmax warps
+        for (int i = 0; i < kInfo; ++i) { mbar_init(BAR_AT(info_full, i), 1); mbar_init(BAR_AT(info_empty, i), 11); }
+        mbar_init(BAR(drain), 1);
+        sh->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(s32(&sh->tmem), attn2::kTmemCols);
+    // the merging kernel may be launched as CTAs of this one end; it waits for all of them itself
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+
+    // the i-th unit of this CTA; nullptr at the end (or on abort).  Warp-wide.
+    auto next_unit = [&](int i) -> const Unit* {
+        const bool got = attn2::wait_for(BAR_AT(info_full, i % kInfo), ((uint32_t)i / kInfo) & 1u, abort_flag);
+        const Unit* u = &sh->info[i % kInfo];
+        return __all_sync(0xffffffffu, got) && u->head >= 0 ? u : nullptr;
+    };
+    auto unit_read = [&](int i) {
+        __syncwarp();
+        attn2::arrive_if(lane == 0, BAR_AT(info_empty, i % kInfo));
+    };
+
+    if (warp < 4) {
+        attn2::regs_dec<kRegsRole>();
+        if (warp == 0) {
+            // ---------------- loads ----------------
+            const int per = kKeys >> a.shift;             // pages of a tile
+            const int pg = lane >> 1, half = lane & 1;    // this lane's box of a tile, if there are so many
+            const uint32_t box_bytes = 128u << a.shift;
+            uint32_t st = 0, ph = 1;                      // place in the ring, its phase
+            uint32_t qph = 3;                             // a bit per slot
+            int bits = 0;
+            bool ok = true;
+            const Unit* u;
+            for (int i = 0; ok && (u = next_unit(i)); ++i) {
+                const int b = u->b, head = u->head, pair = u->pair, t0 = u->t0, n = u->n, end = u->L + a.n, split = u->split;
+                const bool fix = needs_fix(*u, a.n);
+                unit_read(i);
+                if (n == 0) continue;
+                auto load_q = [&](int s) {
+                    const bool free = attn2::wait_for(BAR_AT(q_empty, s), qph >> s, abort_flag);
+                    ok = ok && __all_sync(0xffffffffu, free);
+                    qph ^= 1u << s;
+                    if (!ok || lane != 0) return;
+                    mbar_expect_tx(BAR_AT(q_full, s), (uint32_t)(2 * a.P * a.G * 128));
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_4d(s32(sQ + s * kTile + x * kBox), &map_q, BAR_AT(q_full, s), 64 * x, 0, head,
+                                    b * a.n + (pair * 2 + s) * a.P);
+                };
+                const int32_t* ids = a.table + (int64_t)b * a.width;
+                const int pages = (end + (1 << a.shift) - 1) >> a.shift;
+                auto load_id = [&](int j) {               // of this lane's page in tile j
+                    const int x = (t0 + j) * per + pg;
+                    return pg < per && x < pages ? __ldg(ids + x) : -1;
+                };
+                int id = load_id(0);
+                auto load_kv = [&](const CUtensorMap* map, int boxes, int z, int y, bool repair) {
+                    const bool free = attn2::wait_for(BAR_AT(empty, st), ph, abort_flag);
+                    ok = ok && __all_sync(0xffffffffu, free);
+                    if (ok) {
+                        const uint32_t bar = repair ? BAR_AT(v_last, st) : BAR_AT(full, st);
+                        if (lane == 0) mbar_expect_tx(bar, box_bytes * (uint32_t)boxes);
+                        __syncwarp();
+                        if (lane < boxes) tma_load_3d(s32(sR + st * kTile + half * kBox) + (pg << (7 + a.shift)), map, bar, 64 * half, y, z);
+                    }
+                    if (++st == kStages) { st = 0; ph ^= 1u; }
+                };
+                load_q(0);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int boxes = 2 * min(per, pages - (t0 + j) * per);
+                    const bool bad = id < 0 || id >= a.N;
+                    if (bad && lane < boxes) bits = EAGLE_DEV_CAPACITY;
+                    // a page that does not exist: the place behind a page's last row, which reads as zeros
+                    const int z = bad ? 0 : id * a.Hkv + head, y = bad ? 1 << a.shift : 0;
+                    if (j + 1 < n) id = load_id(j + 1);
+                    load_kv(&map_k, boxes, z, y, false);
+                    if (j == 0 && !split) load_q(1);
+                    load_kv(&map_v, boxes, z, y, fix && j == n - 1);
+                }
+            }
+            if (bits) flag_error(a.dev_status, bits);
+        } else if (warp == 1) {
+            // ---------------- MMA issue ----------------
+            const bool leader = attn2::elect_lane();
+            const uint32_t on = leader;
+            const uint32_t tm = (uint32_t)attn2::uniform_of((int)tmem);
+            const uint32_t dq0 = attn2::desc_lo(s32(sQ)), dk0 = attn2::desc_lo(s32(sR)), dv0 = attn2::desc_lo_mn(s32(sR), kBox);
+            uint32_t qph = 0, pph = 0;
+            uint32_t ks = 0, kp = 0, vs = 1, vp = 0;      // places of the next K and V tile
+            bool ok = true;
+            // (a wait that gives up lets the step run on, on data that nobody will use)
+            auto wait = [&](uint32_t bar, uint32_t parity) { ok &= attn2::wait_for(bar, parity, abort_flag); };
+            auto advance = [&](uint32_t& st, uint32_t& ph) {      // K and V tiles take turns in the ring
+                st += 2;
+                if (st >= kStages) { st -= kStages; ph ^= 1u; }
+            };
+            // O of slot s += P V of the next V tile, then S = Q K^T of the next K tile.  opens, closes: the
+            // tiles' first, last use; qs: the slot whose Q it is
+            auto step = [&](int s, int qs, bool pv, bool pv_first, bool pv_last, bool qk, bool qk_first, bool qk_last, bool opens, bool closes) {
+                const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
+                if (pv) {
+                    if (opens) wait(BAR_AT(full, vs), vp);
+                    wait(BAR_AT(p_full, s), pph >> s);
+                    pph ^= 1u << s;
+                    tc_fence_after();
+                    const uint32_t dv = dv0 + ((vs * kTile) >> 4);
+                    uint32_t acc = pv_first ? 0u : 1u;
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
+                        acc = 1u;
+                    }
+                }
+                if (qk) {
+                    if (opens) wait(BAR_AT(full, ks), kp);
+                    if (qk_first) {
+                        wait(BAR_AT(q_full, qs), qph >> qs);
+                        qph ^= 1u << qs;
+                    }
+                    tc_fence_after();
+                    const uint32_t dk = dk0 + ((ks * kTile) >> 4), dq = dq0 + ((qs * kTile) >> 4);
+#pragma unroll
+                    for (int k = 0; k < kHeadDim / 16; ++k) {
+                        const uint32_t at = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                        attn2::mma_ss<false>(on, scol, dq + at, dk + at, kIdescQK, k > 0 ? 1u : 0u);
+                    }
+                    attn2::commit_if(leader, BAR_AT(s_full, s));
+                }
+                attn2::commit_if(leader && pv && pv_last, BAR_AT(o_full, s));
+                attn2::commit_if(leader && qk && qk_last, BAR_AT(q_empty, qs));
+                attn2::commit_if(leader && pv && closes, BAR_AT(empty, vs));
+                attn2::commit_if(leader && qk && closes, BAR_AT(empty, ks));
+                if (pv && closes) advance(vs, vp);
+                if (qk && closes) advance(ks, kp);
+            };
+            const Unit* u;
+            for (int i = 0; ok && (u = next_unit(i)); ++i) {
+                const int n = attn2::uniform_of(u->n), split = attn2::uniform_of(u->split);
+                unit_read(i);
+                if (n == 0) continue;
+                // step x.  Both slots see every tile: slot x & 1, PV of tile x / 2 - 1, QK of tile x / 2.
+                // Tiles in turn: PV of tile x - 2, QK of tile x, both slot x & 1's.
+                const int steps = split ? n + 2 : 2 * n + 2;
+#pragma unroll 1
+                for (int x = 0; x < steps && __all_sync(0xffffffffu, ok); ++x) {
+                    const int s = x & 1, j = split ? x : x >> 1, back = split ? 2 : 1;
+                    const bool pv = j >= back && j - back < n, qk = j < n;
+                    // (a slot's first PV is that of its first tile, its last that behind which it has no QK)
+                    step(s, split ? 0 : s, pv, j < 2 * back, j >= n, qk, j == 0, j == n - 1, split || s == 0, split || s == 1);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (leader) {
+                umma_commit(BAR(drain));
+                attn2::wait_drain(BAR(drain));
+            }
+        } else if (warp == 2) {
+            // ---------------- V rows behind the tree's last ----------------
+            uint32_t r = 0, phases = 0;                   // phases: a bit per stage
+            const Unit* u;
+            for (int i = 0; (u = next_unit(i)); ++i) {
+                const int n = u->n, first = u->L + a.n - (u->t0 + n - 1) * kKeys;
+                const bool fix = needs_fix(*u, a.n);
+                unit_read(i);
+                r += 2 * n;
+                if (!fix) continue;
+                const uint32_t st = (r - 1) % kStages;
+                const bool got = attn2::wait_for(BAR_AT(v_last, st), (phases >> st) & 1u, abort_flag);
+                phases ^= 1u << st;
+                if (!__all_sync(0xffffffffu, got)) break;
+                uint8_t* v = sR + st * kTile;
+                for (int row = first + (lane >> 4); row < kKeys; row += 2)
+                    *reinterpret_cast<uint4*>(v + ((lane >> 3) & 1) * kBox + row * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                attn2::fence_async_shared();
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR_AT(full, st));
+            }
+        } else {
+            // ---------------- the cut ----------------
+            const attn2::Cut cut = attn2::make_cut(a, gridDim.x);
+            const bool mine = (int)blockIdx.x < cut.ctas;
+            int pos = mine ? cut.begin(blockIdx.x) : 0, base = 0, b = 0;
+            const int end = mine ? cut.begin(blockIdx.x + 1) : 0;
+            int tree_of = -1, bits = 0, parent[2] = {-1, -1};         // of nodes lane and lane + 32
+            bool bad_tree = false, have = true;
+            for (int i = 0; have; ++i) {
+                attn2::Segment s;
+                have = false;
+                while (!have && pos < end) {
+                    s = attn2::segment_at(a, pos, end, b, base);
+                    pos = s.start + s.weight * (s.T + kUnitCost);
+                    have = s.t0 < s.t1;
+                }
+                if (have && s.b != tree_of) {
+                    tree_of = s.b;
+                    bool bad = false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int x = lane + 32 * h;
+                        parent[h] = x < a.n ? a.parent[(int64_t)s.b * a.n + x] : 0;
+                        bad |= x < a.n && (x == 0 ? parent[h] != -1 : (parent[h] < 0 || parent[h] >= x));
+                    }
+                    bad_tree = __any_sync(0xffffffffu, bad);
+                }
+                const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) break;
+                Unit* u = &sh->info[i % kInfo];
+                if (!have) {
+                    if (lane == 0) u->head = -1;
+                } else {
+                    const int L = a.kv_len[s.b];
+                    const bool bad_len = a.bad_length(L), zero = bad_len || bad_tree;
+                    if (zero && s.head == 0 && s.pair == 0 && s.t0 == 0)
+                        bits |= (bad_len ? EAGLE_DEV_CAPACITY : 0) | (bad_tree ? EAGLE_DEV_BAD_TREE : 0);
+                    u->parent[lane] = (uint8_t)parent[0];
+                    u->parent[lane + 32] = (uint8_t)parent[1];
+                    if (lane == 0) {
+                        u->b = s.b; u->head = s.head; u->pair = s.pair;
+                        u->t0 = s.t0;
+                        u->n = zero ? 0 : s.t1 - s.t0;
+                        u->L = zero ? 0 : L;
+                        u->split = s.weight == 1;
+                        u->part = s.t0 == 0 && s.t1 == s.T ? -1 : (int)blockIdx.x * 2 + (s.t0 == 0);
+                    }
+                }
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR_AT(info_full, i % kInfo));
+            }
+            if (bits && lane == 0) flag_error(a.dev_status, bits);
+        }
+    } else {
+        // ---------------- softmax: one thread per query row ----------------
+        attn2::regs_inc<kRegsSoftmax>();
+        const int slot = (warp - 4) >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + attn2::s_col(slot);
+        const uint32_t o_addr = tmem + lane_base + attn2::o_col(slot);
+        const int p = row / a.G, g = row % a.G;
+        const float sc = a.scale_log2;
+        const uint64_t sc2 = attn2::f2(sc, sc);
+        uint32_t tiles_done = 0, units_done = 0, merges = 0;
+        bool ok = true;
+        const Unit* u;
+        for (int i = 0; ok && (u = next_unit(i)); ++i) {
+            const int n = u->n, split = u->split, t0 = u->t0, part = u->part, L = u->L;
+            const int row_tile = u->pair * 2 + (split ? 0 : slot), node = row_tile * a.P + p;
+            const bool valid = p < a.P && node < a.n;
+            unsigned long long anc = 0;                   // the node and its ancestors
+            if (valid && n > 0)
+                for (int x = node;; x = u->parent[x]) {
+                    anc |= 1ull << x;
+                    if (x == 0) break;
+                }
+            const int64_t at = ((int64_t)u->b * a.n + node) * a.Hq + u->head * a.G + g;
+            const int64_t place = (int64_t)part * a.rows + (split ? 0 : slot * kRows) + row;
+            unit_read(i);
+            const bool idle = !__any_sync(0xffffffffu, valid);       // rows are independent: leave P as it is
+            float mref = -INFINITY;
+            uint64_t l2 = 0;                              // two partial sums
+            int mine = 0;                                 // tiles of this slot
+            for (int t = split ? slot : 0; t < n; t += split ? 2 : 1, ++mine) {
+                const bool got = attn2::wait_for(BAR_AT(s_full, slot), tiles_done & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                ++tiles_done;
+                tc_fence_after();
+                if (!idle) {
+                    uint32_t x[kKeys];
+                    float m4[4];
+                    attn2::load_row_nowait(s_addr, x, m4);
+                    const int first = (t0 + t) * kKeys - L;          // rows from L on to the tile's first key
+                    attn2::tmem_wait_ld();
+                    if (first > -kKeys) {
+                        float y[kKeys];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t sees = sees32(anc, first + 32 * w);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                y[32 * w + c] = (sees >> c) & 1u ? __uint_as_float(x[32 * w + c]) : -INFINITY;
+                                x[32 * w + c] = __float_as_uint(y[32 * w + c]);
+                            }
+                        }
+                        m4[0] = attn2::max_of<kKeys>(y);
+                        m4[1] = m4[2] = m4[3] = m4[0];
+                    }
+                    const float mx = fmaxf(attn2::max3(m4[0], m4[1], m4[2]), m4[3]) * sc;    // scale > 0 commutes with max
+                    // no branches of a lane; the first finite maximum is always above the reference
+                    const bool up = mx > mref + kRescale;
+                    const float alpha = up ? ex2_approx(mref - mx) : 1.f;            // 0 for the first one
+                    mref = up ? mx : mref;
+                    l2 = attn2::mul2(l2, attn2::f2(alpha, alpha));
+                    // this QK was committed after the slot's last PV: O is complete
+                    if (mine > 0 && __any_sync(0xffffffffu, up)) attn2::rescale_row(o_addr, alpha);
+                    const float base = mref == -INFINITY ? 0.f : mref;
+                    const uint64_t nb2 = attn2::f2(-base, -base);
+                    uint64_t acc[4] = {l2, 0, 0, 0};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float s0, s1;
+                            attn2::unf2(attn2::fma2(attn2::f2(__uint_as_float(x[64 * h + 2 * e]), __uint_as_float(x[64 * h + 2 * e + 1])), sc2, nb2), s0, s1);
+                            const float p0 = ex2_approx(s0), p1 = ex2_approx(s1);
+                            acc[e & 3] = attn2::add2(acc[e & 3], attn2::f2(p0, p1));
+                            pk[e] = pack2(p0, p1);
+                        }
+                        attn2::tmem_st32_nowait(s_addr + 32 * h, pk);    // P over S
+                    }
+                    l2 = attn2::add2(attn2::add2(acc[0], acc[1]), attn2::add2(acc[2], acc[3]));
+                    attn2::tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR_AT(p_full, slot));
+            }
+            if (!ok) break;
+            if (mine > 0) {
+                const bool got = attn2::wait_for(BAR_AT(o_full, slot), units_done & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) break;
+                ++units_done;
+                tc_fence_after();
+            }
+            float la, lb;
+            attn2::unf2(l2, la, lb);
+            float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
+            if (split && n > 1) {
+                // the row's other tiles are slot 1's: (m, l) go to slot 0, which writes both
+                if (slot == 1) {
+                    sh->ml[row] = make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    attn2::arrive_if(lane == 0, BAR(merge_in));
+                    const bool got = attn2::wait_for(BAR(merge_out), merges & 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    ++merges;
+                    continue;
+                }
+                const bool got = attn2::wait_for(BAR(merge_in), merges & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) break;
+                ++merges;
+                tc_fence_after();
+                const float2 other = sh->ml[row];
+                m = fmaxf(mref, other.x);
+                const float mb = m == -INFINITY ? 0.f : m;
+                w0 = exp2f(mref - mb);
+                w1 = exp2f(other.x - mb);
+                l = l * w0 + other.y * w1;
+            } else if (split && slot == 1) {
+                continue;
+            }
+            if (!idle) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int c = 0; c < kHeadDim; c += 32) {
+                    uint32_t o[32];
+                    if (n > 0) tmem_ld32(o_addr + c, o);
+                    else
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    if (split && n > 1) {
+                        uint32_t o1[32];
+                        tmem_ld32(o_addr + 128 + c, o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), w0, __uint_as_float(o1[e]) * w1));
+                    }
+                    if (valid && part < 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kHeadDim + c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = pack2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (valid && part >= 0) a.ws_ml[place] = make_float2(m, l);
+            }
+            if (split && n > 1) {                         // O of slot 1 and ml are free again
+                tc_fence_before();
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR(merge_out));
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0 && *abort_flag) flag_error(a.dev_status, EAGLE_DEV_TIMEOUT);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, attn2::kTmemCols);
+    }
+#undef BAR
+#undef BAR_AT
+}
+
+__global__ void __launch_bounds__(attn2::kMergeThreads) tree_attn_paged_merge_kernel(Args a, int grid) { attn2::merge_parts(a, grid); }
+
+}  // namespace paged_tc
+}  // namespace eagle

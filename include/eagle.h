@@ -16,6 +16,9 @@
  *   eagle_prompt_attn    causal attention of packed prompts
  *   eagle_kv8_append, eagle_tree_attn_kv8, eagle_kv8_commit
  *                        the same step over a K/V cache held in 8 bits
+ *   eagle_pages_assign, eagle_qkv_rope, eagle_tree_attn_paged, eagle_pages_commit
+ *                        the same step over a K/V cache cut into pages, with the norms and
+ *                        the rotation that come before the attention
  *
  * Pages (cited by title and section):
  *   Lesson: "推测解码与 EAGLE-3" -- "不变量：Leviathan 拒绝采样", "KV cache 回滚",
@@ -408,6 +411,129 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
                                  void* out, int B, int n, int Hq, int Hkv, int head_dim, int Lmax,
                                  float scale, void* workspace, size_t ws_bytes,
                                  int32_t* dev_status, eagle_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged K/V cache.  Lesson "KV cache 回滚" (one physical cache plus a logical
+ * length), with the physical cache cut into pages that sequences hold as they grow and
+ * may share:
+ *   k_pages, v_pages bf16 [n_layers, N, Hkv, page, head_dim]   (the calls of one layer
+ *            take [N, Hkv, page, head_dim]); page is 16, 32, 64 or 128 rows
+ *   page_table int32 [B, P]: row r of sequence b lies in page page_table[b][r / page],
+ *            row r % page, in every layer.  Entries behind the pages that a sequence
+ *            holds may hold anything.
+ * N * Hkv * page below 2^31, P * page up to 2^30, B * P below 2^30.
+ *
+ * eagle_pages_assign -- which pages each of B slots holds, and the rows that this needs
+ * copied: room for new rows, forks, reorders, ends.  Slot b goes on with what slot
+ * s = src[b] held (src NULL: every slot with its own; src[b] = -1: with nothing), and
+ * has room for grow[b] rows more:
+ *   kv_len[b] = L = kv_len[s] (0 for -1),   held[b] = ceil((L + grow[b]) / page)
+ *   - The L / page full pages of s are shared, not copied.
+ *   - The page in which the L rows end, if they end inside one: if no slot but s holds it,
+ *     one of the slots that go on with s (s itself, else the first) takes it as it is.
+ *     The others take a fresh page and its L % page rows are copied, in every layer.
+ *   - A slot that goes on with its own keeps the pages it holds behind its rows, as far as
+ *     it needs them and no other slot holds them.
+ *   - All else is fresh pages: those with refs = 0 before the call, by rising number, slot
+ *     by slot.  Pages that a call gives back can be taken from the next call on.
+ *   - Entries of pages given back become -1 where no other page takes their place.
+ *   held   int32 [B]  pages that each slot holds (entries 0 .. held - 1), updated
+ *   refs   int32 [N]  how many slots hold each page, updated (all 0: an empty cache)
+ *   kv_len int32 [B]  committed rows, updated      grow int32 [B], >= 0
+ *   src    int32 [B] or NULL
+ *   workspace / ws_bytes: device scratch of at least eagle_pages_workspace_size(B, N, P)
+ *            bytes; no initialisation needed.  Two calls that may run at the same time
+ *            need one each.
+ * All or nothing: too few free pages (EAGLE_DEV_CAPACITY), or src outside [-1, B), kv_len
+ * or grow negative, kv_len beyond the pages held, more than P pages needed, or a page
+ * outside [0, N) among those looked at (EAGLE_DEV_CAPACITY as well) leave everything as it
+ * was.  refs and the table have to agree; that is not checked.
+ *
+ * eagle_pages_commit -- eagle_kv_compact over pages.  For t = 0 .. a (a = accept_len[b]):
+ * row L + path[b][t] moves to row L + t (L = kv_len[b]) in every layer and kv head, for K
+ * and V, all rows read before any is written; then kv_len_out[b] = L + a + 1.  The pages
+ * of the rows that are written must be the sequence's own (eagle_pages_assign with grow
+ * of at least the tree's nodes before the step).
+ *   kv_len int32 [B]   kv_len_out int32 [B], may be kv_len   path int32 [B, D+1]
+ *   accept_len int32 [B]
+ * Sequences with accept_len < 0 are skipped (kv_len_out = kv_len).  Device errors, the
+ * sequence being skipped: a > D, rows beyond P * page or a page outside [0, N),
+ * EAGLE_DEV_CAPACITY; a path not starting at 0 or not increasing, EAGLE_DEV_BAD_TREE.
+ *
+ * eagle_qkv_rope -- from a layer's projections to its attention: norms of the queries' and
+ * keys' heads, the rotation by position, and the rows into pages, in one pass.
+ * For a head x of q or k (w = q_weight or k_weight):
+ *   y = w * x / sqrt(mean x^2 + eps)          (y = x where w is NULL)
+ *   the pairs (y_i, y_{i + r/2}), or (y_2i, y_{2i+1}) with `interleaved`, i < r/2 = rot_dim/2,
+ *   are turned by the angle position * inv_freq[i]; elements from rot_dim on stay.
+ * One rounding, to bf16, at the end.  Sequence b holds pos[b] rows already.  Its new tokens
+ * are either rows cu[b] .. cu[b+1]-1 (packed, positions pos[b] + t) or, with parent, the n
+ * nodes of a draft tree (T = B * n; position pos[b] + depth of the node: nodes of one depth
+ * share it).  Token t of a sequence is cache row pos[b] + t in either case.
+ *   q        bf16, token t at q + t * q_stride, [Hq, head_dim] dense within
+ *   k, v     bf16, likewise with [Hkv, head_dim]; v may be NULL without pages
+ *   q_weight, k_weight bf16 [head_dim], each may be NULL;   eps > 0
+ *   inv_freq f32 [rot_dim / 2], finite       rot_dim a multiple of 16, at most head_dim
+ *   cu       int32 [B+1], non-decreasing, within [0, T]; exactly one of cu and parent
+ *   parent   int32 [B, n]  (parent[0] = -1, parent[i] < i), n <= 64
+ *   pos      int32 [B]
+ *   q_out    bf16 [T, Hq, head_dim]; may be q where q is dense
+ *   k_out    bf16 [T, Hkv, head_dim] or NULL; may be k where k is dense
+ *   k_pages, v_pages, page_table   one layer, or all NULL (then k_out is needed)
+ * Strides are in elements: multiples of 8, at least Hq (Hkv) * head_dim.  Tokens of no
+ * sequence are left out.  NaN and infinities come out as the formulas make them.
+ * Device errors: bad cu sets EAGLE_DEV_CAPACITY and nothing is written; pos[b] < 0, or rows
+ * beyond P * page (without pages: beyond 2^31 - 1) set it, an invalid tree sets
+ * EAGLE_DEV_BAD_TREE, and the sequence is skipped; a page outside [0, N) sets
+ * EAGLE_DEV_CAPACITY and its rows are not stored in the cache.
+ *
+ * eagle_tree_attn_paged -- eagle_tree_attn over pages, one layer.  For sequence b, node i,
+ * query head h (kv head h / (Hq/Hkv)):
+ *   keys   = cache rows 0 .. L-1 (L = kv_len[b]) plus rows L + j for every j that is i or an
+ *            ancestor of i (the tree's rows, as eagle_qkv_rope stores them);
+ *   out    = softmax(scale * q . k) . v, fp32 accumulation, bf16 result.
+ * One node (n = 1, parent = -1) is ordinary decoding.  The softmax weights are rounded to
+ * bf16 (2^-8 of each) before they are multiplied with V, their sum is not.
+ *   q      bf16 [B, n, Hq, head_dim]        k_pages, v_pages bf16 [N, Hkv, page, head_dim]
+ *   kv_len int32 [B]      parent int32 [B, n]  (parent[0] = -1, parent[i] < i)
+ *   out    bf16 [B, n, Hq, head_dim]
+ *   workspace / ws_bytes: device scratch of at least
+ *          eagle_tree_attn_paged_workspace_size(B, n, Hq, Hkv, head_dim, page, P) bytes (may
+ *          be NULL when that size is 0), 16-byte aligned; no initialisation needed.  Two
+ *          calls that may run at the same time need one each.
+ * Rows 0 .. L + n - 1 must be finite (a row that a node does not see is multiplied with a
+ * zero weight, which does not cancel NaN); what lies behind them in a page is not used,
+ * whatever it holds.  Hq / Hkv <= 128.
+ * Device errors: an invalid tree, kv_len[b] < 0 or kv_len[b] + n > P * page sets a
+ * dev_status bit and writes zeros for that sequence; a page outside [0, N) sets
+ * EAGLE_DEV_CAPACITY and its rows count as zeros.
+ * ------------------------------------------------------------------------- */
+size_t eagle_pages_workspace_size(int B, int N, int P);
+eagle_status eagle_pages_assign(void* k_pages, void* v_pages, int32_t* page_table, int32_t* held,
+                                int32_t* refs, int32_t* kv_len, const int32_t* grow,
+                                const int32_t* src, int n_layers, int B, int N, int Hkv, int page,
+                                int head_dim, int P, void* workspace, size_t ws_bytes,
+                                int32_t* dev_status, eagle_stream_t stream);
+eagle_status eagle_pages_commit(void* k_pages, void* v_pages, const int32_t* page_table,
+                                const int32_t* kv_len, int32_t* kv_len_out, const int32_t* path,
+                                const int32_t* accept_len, int n_layers, int B, int N, int Hkv,
+                                int page, int head_dim, int P, int max_depth, int32_t* dev_status,
+                                eagle_stream_t stream);
+eagle_status eagle_qkv_rope(const void* q, const void* k, const void* v, const void* q_weight,
+                            const void* k_weight, const float* inv_freq, const int32_t* cu,
+                            const int32_t* parent, const int32_t* pos, void* q_out, void* k_out,
+                            void* k_pages, void* v_pages, const int32_t* page_table, int T, int B,
+                            int n, int Hq, int Hkv, int head_dim, int rot_dim, int interleaved,
+                            float eps, int64_t q_stride, int64_t k_stride, int64_t v_stride, int N,
+                            int page, int P, int32_t* dev_status, eagle_stream_t stream);
+size_t eagle_tree_attn_paged_workspace_size(int B, int n, int Hq, int Hkv, int head_dim, int page,
+                                            int P);
+eagle_status eagle_tree_attn_paged(const void* q, const void* k_pages, const void* v_pages,
+                                   const int32_t* page_table, const int32_t* kv_len,
+                                   const int32_t* parent, void* out, int B, int n, int Hq, int Hkv,
+                                   int head_dim, int N, int page, int P, float scale,
+                                   void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                   eagle_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * eagle2_expand -- one level of EAGLE-2 expansion; optionally the rerank.
