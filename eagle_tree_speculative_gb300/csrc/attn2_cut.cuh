@@ -89,16 +89,84 @@ __device__ __forceinline__ Segment segment_at(const A& a, int pos, int end, int&
 }
 
 // ---------------- merging of cut units ----------------
-// Blocks (c, y): the unit whose first tile lies in piece c and whose last does not, one warp a row;
-// its parts are piece c's second place and the first places of the pieces behind it.  m is in
-// log2 units and a part's l and O share one factor, so a part weighs 2^(m - max m).  Lane p looks
-// after part p (of up to 32 at a time), so that the parts' loads do not wait for one another.  The
-// launch may begin while the attention kernel ends; the partials are awaited below.
+// Blocks (c, y): the unit whose first tile lies in piece c and whose last does not; its parts are piece c's
+// second place and the first places of the pieces behind it.  m is in log2 units and a part's l and O share one
+// factor, so a part weighs 2^(m - max m).  kLanes lanes look after a row, 32 / kLanes float4 of its O each, and in
+// the same way after 32 parts at a time, so that the parts' loads do not wait for one another: a warp
+// a row where there are few, else eight lanes (4 rows a warp: 151 units of 256 rows and two parts took 24 us with
+// a warp a row).  The launch may begin while the attention kernel ends; the partials are awaited below.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeFewRows = 64;                 // rows of a part up to which a warp takes one
+constexpr int kMergeMaxParts = 1024;              // at most one per CTA of the attention kernel
+
+template <int kLanes, class A>
+__device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const int* places, int parts) {
+    constexpr int kEach = 32 / kLanes;
+    const int lane = threadIdx.x & 31, l = lane % kLanes;
+    const int rows = a.unit_rows(s.pair), per_block = kMergeWarps * kEach;
+    for (int row0 = blockIdx.y * per_block + (threadIdx.x >> 5) * kEach; row0 < rows; row0 += gridDim.y * per_block) {
+        const int row = min(row0 + lane / kLanes, rows - 1);          // (the last row more than once)
+        float m = -INFINITY, sum = 0.f;
+        float4 o[kEach] = {};
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            float2 ml[kEach];
+            float top = -INFINITY, w[kEach], y[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int p = p0 + l + kLanes * k, place = p < parts ? places[p] : -1;
+                ml[k] = place >= 0 ? a.ws_ml[(int64_t)place * a.rows + row] : make_float2(-INFINITY, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) top = fmaxf(top, ml[k].x);
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m, top), at = mn == -INFINITY ? 0.f : mn, wo = exp2f(m - at);
+            m = mn;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                w[k] = exp2f(ml[k].x - at);
+                y[k] = ml[k].y * w[k];
+            }
+#pragma unroll
+            for (int h = kEach / 2; h > 0; h >>= 1)
+#pragma unroll
+                for (int k = 0; k < h; ++k) y[k] += y[k + h];
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d >>= 1) y[0] += __shfl_xor_sync(0xffffffffu, y[0], d);
+            sum = sum * wo + y[0];
+#pragma unroll
+            for (int c = 0; c < kEach; ++c) { o[c].x *= wo; o[c].y *= wo; o[c].z *= wo; o[c].w *= wo; }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int first = p0 + k * kLanes, count = min(kLanes, parts - first);
+#pragma unroll 4
+                for (int p = 0; p < count; ++p) {
+                    const float wp = __shfl_sync(0xffffffffu, w[k], p, kLanes);
+                    const int place = places[first + p];
+                    if (place < 0) continue;
+                    const float4* x = reinterpret_cast<const float4*>(a.ws_o + ((int64_t)place * a.rows + row) * kHeadDim) + l;
+#pragma unroll
+                    for (int c = 0; c < kEach; ++c) {
+                        const float4 z = x[c * kLanes];
+                        o[c].x += z.x * wp; o[c].y += z.y * wp; o[c].z += z.z * wp; o[c].w += z.w * wp;
+                    }
+                }
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t to = a.out_row(s.b, s.head, s.pair, row);
+        if (to < 0) continue;                             // nobody's row
+#pragma unroll
+        for (int c = 0; c < kEach; ++c)
+            reinterpret_cast<uint2*>(a.out + to * kHeadDim)[l + c * kLanes] =
+                make_uint2(pack2(o[c].x * inv, o[c].y * inv), pack2(o[c].z * inv, o[c].w * inv));
+    }
+}
 
 template <class A>
 __device__ __forceinline__ void merge_parts(const A& a, int grid) {
-    const int lane = threadIdx.x & 31;
+    __shared__ int s_place[kMergeMaxParts];
+    __shared__ int s_parts;
     const Cut cut = make_cut(a, grid);
     const int c = blockIdx.x;
     // A block that has nothing to merge awaits the attention kernel too: a kernel launched next
@@ -109,48 +177,25 @@ __device__ __forceinline__ void merge_parts(const A& a, int grid) {
     int b = 0, base = 0;
     const Segment s = segment_at(a, end - 1, end, b, base);
     if (s.start < begin || s.t1 >= s.T) { await(); return; }   // it begins earlier, or is whole
-    const int rows = a.unit_rows(s.pair);
-    // lane's part: piece c + lane, and whether it holds tiles of the unit
-    auto place_of = [&](int p) -> int {                   // -1: none, -2: none from here on
-        if (p == c) return c * 2 + 1;
-        if (p >= cut.ctas) return -2;
-        const int t0 = tiles_before<A>(s.start, s.weight, cut.begin(p));
+    if (threadIdx.x == 0) s_parts = cut.ctas - c;
+    __syncthreads();
+    for (int p = c + threadIdx.x; p < cut.ctas; p += kMergeThreads) {
+        // piece p's part of the unit, whose first tile is piece c's; -1: it holds none of its tiles
+        const int t0 = p == c ? 0 : tiles_before<A>(s.start, s.weight, cut.begin(p));
         const int t1 = p + 1 < cut.ctas ? tiles_before<A>(s.start, s.weight, cut.begin(p + 1)) : s.T;
-        return t0 >= s.T ? -2 : t0 < t1 ? p * 2 : -1;
-    };
-    const int first = place_of(c + lane);
-    await();
-    for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = c;; p0 += 32) {
-            const int place = p0 == c ? first : place_of(p0 + lane);
-            const bool there = place >= 0;
-            const float2 ml = there ? a.ws_ml[(int64_t)place * a.rows + row] : make_float2(-INFINITY, 0.f);
-            float top = ml.x;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float mn = fmaxf(m, top), at = mn == -INFINITY ? 0.f : mn;
-            const float w = exp2f(ml.x - at), wo = exp2f(m - at);
-            m = mn;
-            l = l * wo + warp_sum(ml.y * w);
-            o.x *= wo; o.y *= wo; o.z *= wo; o.w *= wo;
-            const unsigned live = __ballot_sync(0xffffffffu, there);
-            const int parts = 32 - __clz(live);           // places up to the last one that is there
-#pragma unroll 4
-            for (int p = 0; p < parts; ++p) {
-                const int at_p = max(__shfl_sync(0xffffffffu, place, p), 0);
-                const float wp = __shfl_sync(0xffffffffu, w, p);
-                const float4 x = *reinterpret_cast<const float4*>(a.ws_o + ((int64_t)at_p * a.rows + row) * kHeadDim + 4 * lane);
-                if ((live >> p) & 1u) { o.x += x.x * wp; o.y += x.y * wp; o.z += x.z * wp; o.w += x.w * wp; }
-            }
-            if (__any_sync(0xffffffffu, place == -2)) break;
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t to = a.out_row(s.b, s.head, s.pair, row);
-        if (to < 0) continue;                             // nobody's row
-        reinterpret_cast<uint2*>(a.out + to * kHeadDim)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+        s_place[p - c] = t0 < min(t1, s.T) ? p * 2 + (p == c) : -1;
+        if (t0 >= s.T) atomicMin(&s_parts, p - c);
     }
+    __syncthreads();
+    await();
+    if (a.rows <= kMergeFewRows) merge_rows<32>(a, s, s_place, s_parts);
+    else merge_rows<8>(a, s, s_place, s_parts);
+}
+
+// Blocks a piece takes for the rows of a part.
+inline int merge_blocks(int rows) {
+    const int per = kMergeWarps * (rows <= kMergeFewRows ? 1 : 4), y = (rows + per - 1) / per;
+    return y < 16 ? y : 16;
 }
 
 }  // namespace attn2

@@ -105,10 +105,9 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
     kv8_tc::tree_attn_kv8_kernel<<<grid, kv8_tc::kThreads, kv8_tc::kSmem, s>>>(mk, mv, a);
     EAGLE_CHECK_LAUNCH();
     if (grid > 1) {
-        const int y = (a.rows + kv8_tc::kMergeWarps - 1) / kv8_tc::kMergeWarps;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(y < 16 ? y : 16));
-        cfg.blockDim = dim3(kv8_tc::kMergeThreads);
+        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)attn2::merge_blocks(a.rows));
+        cfg.blockDim = dim3(attn2::kMergeThreads);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

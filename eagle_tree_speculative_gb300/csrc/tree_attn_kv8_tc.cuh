@@ -1076,9 +1076,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #undef BAR_AT
 }
 
-using attn2::kMergeThreads;
-using attn2::kMergeWarps;
-__global__ void __launch_bounds__(kMergeThreads) tree_attn_kv8_merge_kernel(Args a, int grid) { attn2::merge_parts(a, grid); }
+__global__ void __launch_bounds__(attn2::kMergeThreads) tree_attn_kv8_merge_kernel(Args a, int grid) { attn2::merge_parts(a, grid); }
 
 }  // namespace kv8_tc
 }  // namespace eagle

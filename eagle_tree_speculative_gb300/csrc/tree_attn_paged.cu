@@ -119,9 +119,8 @@ extern "C" eagle_status eagle_tree_attn_paged(const void* q, const void* k_pages
     paged_tc::tree_attn_paged_kernel<<<grid, paged_tc::kThreads, paged_tc::kSmem, s>>>(mq, mk, mv, a);
     EAGLE_CHECK_LAUNCH();
     if (grid > 1) {
-        const int y = (a.rows + attn2::kMergeWarps - 1) / attn2::kMergeWarps;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(y < 16 ? y : 16));
+        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)attn2::merge_blocks(a.rows));
         cfg.blockDim = dim3(attn2::kMergeThreads);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
