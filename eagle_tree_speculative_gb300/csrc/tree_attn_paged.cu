@@ -39,7 +39,7 @@ bool page_map(CUtensorMap* map, const void* x, int page, int64_t slabs) {
 // Row tiles of a sequence and kv head; rows of a part: those of a unit.
 int paged_row_tiles(int n, int G) {
     const int P = paged_tc::kRows / G;
-    return (n + P - 1) / P;
+    return n <= P ? 1 : (n + 2 * P - 1) / (2 * P) * 2;    // as the cut counts them
 }
 int paged_part_rows(int n, int G) {
     const int rt = paged_row_tiles(n, G);

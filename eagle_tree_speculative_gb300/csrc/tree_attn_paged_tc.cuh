@@ -66,7 +66,9 @@ struct Args {
         const int L = kv_len[b];
         return bad_length(L) ? 1 : (L + n + kKeys - 1) / kKeys;
     }
-    __device__ int row_tiles() const { return (n + P - 1) / P; }
+    // a pair's missing row tile counts too: its key tiles take as long as two row tiles' (a tile's bytes, not its
+    // products, are what a single row tile waits for; 16 ragged trees of 48 nodes, 64 / 8 heads: 67 against 87 us)
+    __device__ int row_tiles() const { return n <= P ? 1 : (n + 2 * P - 1) / (2 * P) * 2; }
     __device__ int unit_rows(int pair) const {
         const int left = n - pair * 2 * P;        // nodes from the pair's first on
         return left > P ? kRows + min(left - P, P) * G : left * G;
@@ -371,7 +373,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                         u->t0 = s.t0;
                         u->n = zero ? 0 : s.t1 - s.t0;
                         u->L = zero ? 0 : L;
-                        u->split = s.weight == 1;
+                        u->split = s.pair * 2 * a.P + a.P >= a.n;
                         u->part = s.t0 == 0 && s.t1 == s.T ? -1 : (int)blockIdx.x * 2 + (s.t0 == 0);
                     }
                 }
