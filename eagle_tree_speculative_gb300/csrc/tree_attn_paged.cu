@@ -114,9 +114,14 @@ extern "C" eagle_status eagle_tree_attn_paged(const void* q, const void* k_pages
     if (!paged_q_map(&mq, q, G, a.P, Hkv, (int64_t)B * n) || !page_map(&mk, k_pages, page, (int64_t)N * Hkv) ||
         !page_map(&mv, v_pages, page, (int64_t)N * Hkv))
         return EAGLE_ERR_CUDA;
-    if (!raise_smem_limit<paged_tc::tree_attn_paged_kernel>(paged_tc::kSmem)) return EAGLE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    paged_tc::tree_attn_paged_kernel<<<grid, paged_tc::kThreads, paged_tc::kSmem, s>>>(mq, mk, mv, a);
+    if (n <= a.P) {
+        if (!raise_smem_limit<paged_tc::tree_attn_paged_kernel<true>>(paged_tc::kSmem)) return EAGLE_ERR_CUDA;
+        paged_tc::tree_attn_paged_kernel<true><<<grid, paged_tc::kThreads, paged_tc::kSmem, s>>>(mq, mk, mv, a);
+    } else {
+        if (!raise_smem_limit<paged_tc::tree_attn_paged_kernel<false>>(paged_tc::kSmem)) return EAGLE_ERR_CUDA;
+        paged_tc::tree_attn_paged_kernel<false><<<grid, paged_tc::kThreads, paged_tc::kSmem, s>>>(mq, mk, mv, a);
+    }
     EAGLE_CHECK_LAUNCH();
     if (grid > 1) {
         cudaLaunchConfig_t cfg = {};

@@ -12,10 +12,10 @@
 // All tiles of all units are cut into one equal piece per CTA (attn2_cut.cuh): ragged batches and few long
 // sequences balance alike.
 //
-// Roles: warp 0 loads (Q, then K and V tiles through one ring of 32 KB stages; a lane per page and half of
-// the head dimension, the page numbers a tile ahead), warp 1 issues the MMAs, warp 2 zeroes V rows behind the
-// tree's last (never written: a zero weight does not cancel NaN), warp 3 cuts the work, warps 4-11 are the
-// softmax.
+// Roles: warp 0 loads Q and K, warp 2 V (tiles through one ring of 32 KB stages, page numbers a tile ahead; a
+// page of 16 rows is a box of 2 KB, 32 of them a tile of K and V), warp 1 issues the MMAs, warp 3 cuts the work
+// and zeroes V rows behind the tree's last (never written: a zero weight does not cancel NaN), warps 4-11
+// are the softmax.
 //
 // MMA order and barriers are those of prompt_attn_tc.cuh: PV of a slot's last tile, then its next QK, whose
 // commit also says that O holds that PV.
@@ -38,7 +38,9 @@ using attn2::kSlots;
 constexpr int kThreads = 384;
 // 3 warpgroups x 168 registers at launch; 72 + 2 x 216 = 3 x 168
 constexpr int kRegsRole = 72, kRegsSoftmax = 216;
-constexpr int kStages = 5;
+// Tiles in shared memory: Q, and the stages of the ring.  A launch whose units are single row tiles has Q once.
+constexpr int kTiles = 7, kMaxStages = kTiles - 1;
+template <bool kSingle> constexpr int kQTiles = kSingle ? 1 : kSlots;
 constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
 constexpr int kInfo = 3;                          // units in flight between the roles
@@ -90,8 +92,8 @@ struct Unit {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];       // K/V ring
-    uint64_t v_last[kStages];                     // a V tile that needs repair has landed
+    uint64_t full[kMaxStages], empty[kMaxStages]; // K/V ring
+    uint64_t v_last[kMaxStages];                  // a V tile that needs repair has landed
     uint64_t q_full[kSlots], q_empty[kSlots];
     uint64_t s_full[kSlots], p_full[kSlots], o_full[kSlots];
     uint64_t merge_in, merge_out;
@@ -103,7 +105,7 @@ struct Shared {
     Unit info[kInfo];
 };
 
-constexpr int kSmem = kSlots * kTile + kStages * kTile + (int)sizeof(Shared) + 1024;
+constexpr int kSmem = kTiles * kTile + (int)sizeof(Shared) + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 constexpr uint32_t kIdescQK = idesc_bf16(128, kKeys, 0, 0);
@@ -120,13 +122,15 @@ __device__ __forceinline__ uint32_t sees32(unsigned long long anc, int at) {
     return at < kMaxNodes ? (uint32_t)(anc >> at) : 0u;
 }
 
+template <bool kSingle>                           // every unit is a single row tile
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, Args a) {
+    constexpr int kStages = kTiles - kQTiles<kSingle>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((0u - s32(smem_raw)) & 1023u);
-    uint8_t* sQ = smem;                                   // [kSlots][32 KB]
-    uint8_t* sR = sQ + kSlots * kTile;                    // [kStages][32 KB]
+    uint8_t* sQ = smem;                                   // [kQTiles][32 KB]
+    uint8_t* sR = sQ + kQTiles<kSingle> * kTile;          // [kStages][32 KB]
     Shared* sh = reinterpret_cast<Shared*>(sR + kStages * kTile);
     volatile int* abort_flag = &sh->abort_flag;
     const uint32_t sb = s32(sh);
@@ -149,13 +153,18 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         }
         mbar_init(BAR(merge_in), 4);
         mbar_init(BAR(merge_out), 4);
-        // read by the loading, the MMA and the repair warp and the eight softmax warps
-        for (int i = 0; i < kInfo; ++i) { mbar_init(BAR_AT(info_full, i), 1); mbar_init(BAR_AT(info_empty, i), 11); }
+        // read by the four single warps and the eight softmax warps
+        for (int i = 0; i < kInfo; ++i) { mbar_init(BAR_AT(info_full, i), 1); mbar_init(BAR_AT(info_empty, i), 12); }
         mbar_init(BAR(drain), 1);
         sh->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 1) tmem_alloc(s32(&sh->tmem), attn2::kTmemCols);
+    if (warp == 2 && lane == 0) {
+        prefetch_map(&map_q);
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+    }
     // the merging kernel may be launched as CTAs of this one end; it waits for all of them itself
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     tc_fence_before();
@@ -176,19 +185,25 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 
     if (warp < 4) {
         attn2::regs_dec<kRegsRole>();
-        if (warp == 0) {
-            // ---------------- loads ----------------
+        if (warp == 0 || warp == 2) {
+            // ---------------- loads: warp 0 Q and K, warp 2 V ----------------
+            // K and V tiles take turns in the ring: K's at even places, V's at odd ones.  (A stage's uses may alternate
+            // between the warps.  Neither can be two uses ahead on one, which its parity would not show: a
+            // place two before has been waited for, and the products that freed it come behind the older use's.)
+            const bool is_v = warp == 2;
+            const CUtensorMap* map = is_v ? &map_v : &map_k;
             const int per = kKeys >> a.shift;             // pages of a tile
-            const int pg = lane >> 1, half = lane & 1;    // this lane's box of a tile, if there are so many
-            const uint32_t box_bytes = 128u << a.shift;
-            uint32_t st = 0, ph = 1;                      // place in the ring, its phase
+            const uint32_t on = attn2::elect_lane();
+            const uint32_t page_bytes = 128u << a.shift;  // of half the head dimension
+            uint32_t st = is_v, ph = 1;                   // place in the ring, its phase
             uint32_t qph = 3;                             // a bit per slot
             int bits = 0;
             bool ok = true;
             const Unit* u;
             for (int i = 0; ok && (u = next_unit(i)); ++i) {
-                const int b = u->b, head = u->head, pair = u->pair, t0 = u->t0, n = u->n, end = u->L + a.n, split = u->split;
-                const bool fix = needs_fix(*u, a.n);
+                const int b = u->b, head = u->head, pair = u->pair, t0 = u->t0, end = u->L + a.n;
+                const int n = attn2::uniform_of(u->n);
+                const bool split = kSingle || u->split, fix = is_v && needs_fix(*u, a.n);
                 unit_read(i);
                 if (n == 0) continue;
                 auto load_q = [&](int s) {
@@ -203,33 +218,37 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 };
                 const int32_t* ids = a.table + (int64_t)b * a.width;
                 const int pages = (end + (1 << a.shift) - 1) >> a.shift;
-                auto load_id = [&](int j) {               // of this lane's page in tile j
-                    const int x = (t0 + j) * per + pg;
-                    return pg < per && x < pages ? __ldg(ids + x) : -1;
+                auto load_id = [&](int j) {               // lane x: of page x of tile j
+                    const int x = (t0 + j) * per + lane;
+                    return lane < per && x < pages ? __ldg(ids + x) : -1;
                 };
                 int id = load_id(0);
-                auto load_kv = [&](const CUtensorMap* map, int boxes, int z, int y, bool repair) {
-                    const bool free = attn2::wait_for(BAR_AT(empty, st), ph, abort_flag);
-                    ok = ok && __all_sync(0xffffffffu, free);
-                    if (ok) {
-                        const uint32_t bar = repair ? BAR_AT(v_last, st) : BAR_AT(full, st);
-                        if (lane == 0) mbar_expect_tx(bar, box_bytes * (uint32_t)boxes);
-                        __syncwarp();
-                        if (lane < boxes) tma_load_3d(s32(sR + st * kTile + half * kBox) + (pg << (7 + a.shift)), map, bar, 64 * half, y, z);
-                    }
-                    if (++st == kStages) { st = 0; ph ^= 1u; }
-                };
-                load_q(0);
+                if (!is_v) load_q(0);
                 for (int j = 0; ok && j < n; ++j) {
-                    const int boxes = 2 * min(per, pages - (t0 + j) * per);
+                    const int count = attn2::uniform_of(min(per, pages - (t0 + j) * per));
                     const bool bad = id < 0 || id >= a.N;
-                    if (bad && lane < boxes) bits = EAGLE_DEV_CAPACITY;
+                    if (bad && lane < count) bits = EAGLE_DEV_CAPACITY;
                     // a page that does not exist: the place behind a page's last row, which reads as zeros
                     const int z = bad ? 0 : id * a.Hkv + head, y = bad ? 1 << a.shift : 0;
                     if (j + 1 < n) id = load_id(j + 1);
-                    load_kv(&map_k, boxes, z, y, false);
-                    if (j == 0 && !split) load_q(1);
-                    load_kv(&map_v, boxes, z, y, fix && j == n - 1);
+                    const bool free = attn2::wait_for(BAR_AT(empty, st), ph, abort_flag);
+                    ok = __all_sync(0xffffffffu, free);
+                    if (ok) {
+                        const uint32_t bar = fix && j == n - 1 ? BAR_AT(v_last, st) : BAR_AT(full, st);
+                        const uint32_t to = s32(sR) + st * kTile;
+                        if (on) mbar_expect_tx(bar, 2u * page_bytes * (uint32_t)count);
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < kKeys / 16; ++x) {
+                            if (x >= count) break;
+                            const int zx = __shfl_sync(0xffffffffu, z, x), yx = __shfl_sync(0xffffffffu, y, x);
+                            tma_load_3d_if(on, to + x * page_bytes, map, bar, 0, yx, zx);
+                            tma_load_3d_if(on, to + x * page_bytes + kBox, map, bar, 64, yx, zx);
+                        }
+                    }
+                    st += 2;
+                    if (st >= kStages) { st -= kStages; ph ^= 1u; }
+                    if (!is_v && j == 0 && !split) load_q(1);
                 }
             }
             if (bits) flag_error(a.dev_status, bits);
@@ -289,7 +308,8 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             };
             const Unit* u;
             for (int i = 0; ok && (u = next_unit(i)); ++i) {
-                const int n = attn2::uniform_of(u->n), split = attn2::uniform_of(u->split);
+                const int n = attn2::uniform_of(u->n);
+                const bool split = kSingle || attn2::uniform_of(u->split);
                 unit_read(i);
                 if (n == 0) continue;
                 // step x.  Both slots see every tile: slot x & 1, PV of tile x / 2 - 1, QK of tile x / 2.
@@ -308,38 +328,18 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 umma_commit(BAR(drain));
                 attn2::wait_drain(BAR(drain));
             }
-        } else if (warp == 2) {
-            // ---------------- V rows behind the tree's last ----------------
-            uint32_t r = 0, phases = 0;                   // phases: a bit per stage
-            const Unit* u;
-            for (int i = 0; (u = next_unit(i)); ++i) {
-                const int n = u->n, first = u->L + a.n - (u->t0 + n - 1) * kKeys;
-                const bool fix = needs_fix(*u, a.n);
-                unit_read(i);
-                r += 2 * n;
-                if (!fix) continue;
-                const uint32_t st = (r - 1) % kStages;
-                const bool got = attn2::wait_for(BAR_AT(v_last, st), (phases >> st) & 1u, abort_flag);
-                phases ^= 1u << st;
-                if (!__all_sync(0xffffffffu, got)) break;
-                uint8_t* v = sR + st * kTile;
-                for (int row = first + (lane >> 4); row < kKeys; row += 2)
-                    *reinterpret_cast<uint4*>(v + ((lane >> 3) & 1) * kBox + row * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                attn2::fence_async_shared();
-                __syncwarp();
-                attn2::arrive_if(lane == 0, BAR_AT(full, st));
-            }
         } else {
-            // ---------------- the cut ----------------
+            // ---------------- the cut; V rows behind the tree's last ----------------
             const attn2::Cut cut = attn2::make_cut(a, gridDim.x);
             const bool mine = (int)blockIdx.x < cut.ctas;
             int pos = mine ? cut.begin(blockIdx.x) : 0, base = 0, b = 0;
             const int end = mine ? cut.begin(blockIdx.x + 1) : 0;
             int tree_of = -1, bits = 0, parent[2] = {-1, -1};         // of nodes lane and lane + 32
-            bool bad_tree = false, have = true;
-            for (int i = 0; have; ++i) {
+            bool bad_tree = false;
+            // tells the roles unit i, or that there is none: then false
+            auto tell = [&](int i) {
                 attn2::Segment s;
-                have = false;
+                bool have = false;
                 while (!have && pos < end) {
                     s = attn2::segment_at(a, pos, end, b, base);
                     pos = s.start + s.weight * (s.T + kUnitCost);
@@ -357,7 +357,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                     bad_tree = __any_sync(0xffffffffu, bad);
                 }
                 const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) break;
+                if (!__all_sync(0xffffffffu, got)) return false;
                 Unit* u = &sh->info[i % kInfo];
                 if (!have) {
                     if (lane == 0) u->head = -1;
@@ -379,6 +379,30 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 }
                 __syncwarp();
                 attn2::arrive_if(lane == 0, BAR_AT(info_full, i % kInfo));
+                return have;
+            };
+            // units are told kInfo - 1 ahead of the one whose V tile is looked after
+            bool more = tell(0);
+            if (more) more = tell(1);
+            uint32_t r = 0, phases = 0;                   // places in the ring so far; a bit per stage
+            const Unit* u;
+            for (int i = 0; (u = next_unit(i)); ++i) {
+                const int n = u->n, first = u->L + a.n - (u->t0 + n - 1) * kKeys;
+                const bool fix = needs_fix(*u, a.n);
+                unit_read(i);
+                if (more) more = tell(i + 2);
+                r += 2 * n;
+                if (!fix) continue;
+                const uint32_t st = (r - 1) % kStages;
+                const bool got = attn2::wait_for(BAR_AT(v_last, st), (phases >> st) & 1u, abort_flag);
+                phases ^= 1u << st;
+                if (!__all_sync(0xffffffffu, got)) break;
+                uint8_t* v = sR + st * kTile;
+                for (int row = first + (lane >> 4); row < kKeys; row += 2)
+                    *reinterpret_cast<uint4*>(v + ((lane >> 3) & 1) * kBox + row * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                attn2::fence_async_shared();
+                __syncwarp();
+                attn2::arrive_if(lane == 0, BAR_AT(full, st));
             }
             if (bits && lane == 0) flag_error(a.dev_status, bits);
         }
@@ -397,7 +421,8 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         bool ok = true;
         const Unit* u;
         for (int i = 0; ok && (u = next_unit(i)); ++i) {
-            const int n = u->n, split = u->split, t0 = u->t0, part = u->part, L = u->L;
+            const int n = u->n, t0 = u->t0, part = u->part, L = u->L;
+            const bool split = kSingle || u->split;
             const int row_tile = u->pair * 2 + (split ? 0 : slot), node = row_tile * a.P + p;
             const bool valid = p < a.P && node < a.n;
             unsigned long long anc = 0;                   // the node and its ancestors
