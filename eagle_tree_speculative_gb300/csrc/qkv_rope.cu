@@ -7,17 +7,28 @@
 // overflow is whole turns; the upper 32 bits are the angle to 2^-32 of a turn (its fraction was rounded
 // to 2^-53 of itself: 2^-29 of a turn at position 2^24).
 //
-// Layout.  A task is a token, or a part of its heads where there are few tokens; a warp takes one at
-// a time.  Eight lanes a head, four heads at once: a lane has two chunks of 8 elements (16 bytes)
-// that hold both elements of its pairs, so nothing is exchanged for the rotation and three shuffles do the norm.
-// The token's 64 angles are computed by the warp once, two a lane, and go through shared memory.
+// Layout.  Eight lanes a head, a group of four heads at once: a lane has two chunks of 8 elements (16 bytes) that
+// hold both elements of its pairs, so nothing is exchanged for the rotation and three shuffles do the norm.  The
+// token's 64 angles are computed by the warp once, two a lane, and go through shared memory.
+// The last tokens' groups are shared out to the warps alike, so a single token is worked on by as many as it has
+// groups and a call ends everywhere at once.  Each warp has kAhead groups on their way into shared memory, of this token and the next (cp.async;
+// a lane reads only what it copied itself, so nothing waits for other lanes): registers would hold two.
+#include <type_traits>
+
+#include "attn2_common.cuh"
 #include "paged_common.cuh"
-#include "tc_common.cuh"
 
 namespace eagle {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+// Blocks of an SM: 16 warps for the calls that are over soon, 12 for those that stream (us with 12 / 16 / 20: 24 ragged
+// prompts, 16610 tokens of 32 / 8 heads, 73.5 / 81.1 / 86.9; 64 trees of 60 nodes 19.1 / 18.2 / 23.0).
+constexpr int kBlocks = 4, kBlocksLong = 3;
+constexpr int kLongTokens = 4;                    // tokens a warp from which a call is long
+constexpr int kAhead = 8;                         // groups of four heads (1 KB) that a warp has on their way
+constexpr int kRopeSmem = kWarps * (kAhead * 1024 + 64 * (int)sizeof(float2));
+static_assert(kBlocks * (kRopeSmem + 1024) <= 233472, "shared memory of an SM");
 
 struct RopeArgs {
     const uint16_t *q, *k, *v, *q_weight, *k_weight;
@@ -27,7 +38,6 @@ struct RopeArgs {
     const int32_t* page_table;
     int T, B, n, Hq, Hkv, half;                   // half: rot_dim / 2 pairs
     int N, shift, P;
-    int parts, quads;                             // tasks of a token, groups of four heads a task
     float eps;
     int64_t q_stride, k_stride, v_stride;
     int32_t* dev_status;
@@ -37,186 +47,277 @@ struct RopeArgs {
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    float lo, hi;
+    attn2::unf2(v, lo, hi);
+    return pack2(lo, hi);
+}
+
 // The sum of squares of the eight lanes' 16 elements each.
-__device__ __forceinline__ float sum_squares(const float (&x)[16], float by) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ float sum_squares(const uint64_t (&x)[8]) {
+    uint64_t s[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float y = x[e] * by;
-        s[e & 3] = fmaf(y, y, s[e & 3]);
-    }
-    float t = (s[0] + s[1]) + (s[2] + s[3]);
+    for (int e = 0; e < 8; ++e) s[e & 1] = attn2::fma2(x[e], x[e], s[e & 1]);
+    float lo, hi;
+    attn2::unf2(attn2::add2(s[0], s[1]), lo, hi);
+    float t = lo + hi;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
 }
 
-template <bool kPairs2>                           // pairs (2i, 2i + 1), else (i, i + rot_dim / 2)
-__global__ void __launch_bounds__(kWarps * 32) qkv_rope_kernel(RopeArgs a) {
-    __shared__ float2 s_turn[kWarps][64];
+// 16 bytes of global into shared memory, behind this thread's back; kLeft: groups that may still be on their way.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kLeft) : "memory");
+}
+
+// kPairs2: pairs (2i, 2i + 1), else (i, i + rot_dim / 2).  kWhole: rot_dim is the head dimension
+template <bool kPairs2, bool kWhole>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs a) {
+    extern __shared__ uint4 s_all[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t task = (int64_t)blockIdx.x * kWarps + warp;
-    const int t = (int)(task / a.parts), part = (int)(task - (int64_t)t * a.parts);
-    if (t >= a.T) return;
+    // a lane reads what it has copied itself: its two chunks of each of the warp's groups
+    uint4* raw = s_all + warp * (kAhead * 64) + lane;                 // [kAhead][2][32]
+    float2* turns = reinterpret_cast<float2*>(s_all + kWarps * (kAhead * 64)) + warp * 64;
 
-    // ---- the token's sequence, its row there and its position ----
-    int b = -1, row = 0, ahead = 0, rows = 0;
-    if (a.parent) {
-        b = t / a.n;
-        row = t - b * a.n;
-        rows = a.n;
-        int depth[2];
-        if (!paged::tree_depths(a.parent + (int64_t)b * a.n, a.n, depth)) {
-            if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_BAD_TREE);
-            return;
-        }
-        const int d0 = __shfl_sync(0xffffffffu, depth[0], row & 31), d1 = __shfl_sync(0xffffffffu, depth[1], row & 31);
-        ahead = row < 32 ? d0 : d1;
-    } else {
-        bool bad = false;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int i = min(b0 + lane, a.B - 1), c0 = a.cu[i], c1 = a.cu[i + 1];
-            bad |= c0 < 0 || c1 < c0 || c1 > a.T;
-            const unsigned in = __ballot_sync(0xffffffffu, c0 <= t && t < c1);
-            if (b < 0 && in) {
-                const int l = __ffs(in) - 1;
-                b = b0 + l;
-                const int first = __shfl_sync(0xffffffffu, c0, l);
-                row = ahead = t - first;
-                rows = __shfl_sync(0xffffffffu, c1, l) - first;
+    // ---- what is alike for all tokens: the lane's chunks, the angles a position turns by ----
+    const int c = lane & 7;
+    // Pairs of halves: the first m = half / 8 lanes have chunks c and c + m, the others those from 2 m on, in two runs.
+    const int m = a.half >> 3;
+    const bool pairs = c < m;
+    const int p0 = kPairs2 || pairs ? c : c + m, p1 = !kPairs2 && pairs ? c + m : c + 8;
+    const bool turned0 = kPairs2 ? p0 < (a.half >> 2) : pairs, turned1 = kPairs2 ? p1 < (a.half >> 2) : pairs;
+    const int q_quads = (a.Hq + 3) >> 2, k_quads = (a.Hkv + 3) >> 2;
+    const int total = q_quads + k_quads * (a.page_table ? 2 : 1);
+
+    // ---- the warp's groups: every warps-th token, as long as there is one for each warp, then an equal share of
+    // the groups that the last tokens have ----
+    const int warps = gridDim.x * kWarps, w = blockIdx.x * kWarps + warp, rounds = a.T / warps;
+    const int64_t rest = (int64_t)(a.T - rounds * warps) * total, begin = rest * w / warps;
+    const int tail = (int)(rest * (w + 1) / warps - begin);
+    const int tail_t = rounds * warps + (int)(begin / total), tail_y = (int)(begin % total);
+    // a token's place in this order: which one, its first group here, rounds to come (it included; 0: in the tail)
+    struct Place {
+        int t, y, rounds;
+    };
+    auto start = [&] { return rounds > 0 ? Place{w, 0, rounds} : Place{tail_t, tail_y, 0}; };
+    auto following = [&](const Place& p) {
+        if (p.rounds > 1) return Place{p.t + warps, 0, p.rounds - 1};
+        return p.rounds == 1 ? Place{tail_t, tail_y, 0} : Place{p.t + 1, 0, 0};
+    };
+    int left = rounds * total + tail;
+    if (left == 0) return;
+    // A token's groups are q's, then k's, then v's.  What is copied next: group next_y of a token, whose head for
+    // this lane lies at `next` (a kind's last group may lack heads: those lanes copy its first one again)
+    Place copy = start();
+    int next_left = left, next_y = copy.y, next_end = next_y, next_h = 0, next_heads = 0;
+    const uint16_t *next = nullptr, *next_base = nullptr;
+    uint32_t copy_at = s32(raw), read_at = 0;     // places in the ring
+    const uint32_t copy_begin = copy_at, copy_end = copy_at + kAhead * 1024;
+    auto copy_next = [&]() {
+        if (next_left > 0) {
+            --next_left;
+            if (next_y == next_end) {             // a kind's first group
+                if (next_y == total) {
+                    copy = following(copy);
+                    next_y = copy.y;
+                }
+                const int kind = next_y < q_quads ? 0 : next_y < q_quads + k_quads ? 1 : 2, y0 = kind == 0 ? 0 : kind == 1 ? q_quads : q_quads + k_quads;
+                next_end = kind == 0 ? q_quads : y0 + k_quads;
+                next_heads = kind == 0 ? a.Hq : a.Hkv;
+                next_base = kind == 0 ? a.q + copy.t * a.q_stride : kind == 1 ? a.k + copy.t * a.k_stride : a.v + copy.t * a.v_stride;
+                next_h = 4 * (next_y - y0) + (lane >> 3);
+                next = next_base + next_h * kHeadDim;
             }
+            const uint16_t* src = next_h < next_heads ? next : next_base;
+            copy16_async(copy_at, src + 8 * p0);
+            copy16_async(copy_at + 512, src + 8 * p1);
+            next += 4 * kHeadDim;
+            next_h += 4;
+            ++next_y;
         }
-        if (__any_sync(0xffffffffu, bad)) {
-            if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
-            return;
-        }
-        if (b < 0) return;                        // a token of no sequence
-    }
-    const int held = a.pos[b];
-    const int64_t room = a.page_table ? (int64_t)a.P << a.shift : 0x7fffffffLL;
-    if (held < 0 || held + (int64_t)rows > room) {
-        if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
-        return;
-    }
-    int id = -1, in_page = 0;
-    if (a.page_table) {
-        const int at = held + row;
-        id = a.page_table[(int64_t)b * a.P + (at >> a.shift)];
-        in_page = at & ((1 << a.shift) - 1);
-        if (id < 0 || id >= a.N) {
-            if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
-            id = -1;
-        }
-    }
+        copy_commit();                            // (behind the last one: empty groups)
+        copy_at += 1024;
+        if (copy_at == copy_end) copy_at = copy_begin;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i) copy_next();
 
-    // ---- the token's turns ----
+    unsigned long long frac[2];                   // of pairs lane and lane + 32, in turns
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = lane + 32 * h;
-        float2 turn = make_float2(1.f, 0.f);
-        if (i < a.half) {
-            const double f = (double)a.inv_freq[i] * 0.15915494309189533577;
-            const unsigned long long frac = (unsigned long long)((f - floor(f)) * 18446744073709551616.0);
-            const int angle = (int)((frac * (unsigned)(held + ahead)) >> 32);
-            sincospif((float)angle * 0x1p-31f, &turn.y, &turn.x);
-        }
-        s_turn[warp][i] = turn;
+        const double f = i < a.half ? (double)a.inv_freq[i] * 0.15915494309189533577 : 0.0;
+        frac[h] = (unsigned long long)((f - floor(f)) * 18446744073709551616.0);
     }
-    __syncwarp();
-
-    // ---- the lane's chunks, and its pairs' turns ----
-    const int c = lane & 7;
-    // pairs of halves: chunks c and c + half / 8; lanes without pairs share what lies behind rot_dim
-    const bool pairs = c < (a.half >> 3);
-    const int p0 = kPairs2 || pairs ? c : 2 * c, p1 = kPairs2 ? c + 8 : pairs ? c + (a.half >> 3) : 2 * c + 1;
-    const bool turned0 = kPairs2 ? p0 < (a.half >> 2) : pairs, turned1 = kPairs2 ? p1 < (a.half >> 2) : pairs;
-    float2 turn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        turn[e] = s_turn[warp][kPairs2 ? (e < 4 ? 4 * c + e : 32 + 4 * c + e - 4) : 8 * c + e];
-
-    const int q_quads = (a.Hq + 3) >> 2, k_quads = (a.Hkv + 3) >> 2;
-    const int total = q_quads + k_quads * (a.page_table ? 2 : 1);
-    const int end = min(total, (part + 1) * a.quads);
-    uint4 w0, w1;
-    int kind = -1;
-    for (int y = part * a.quads; y < end; ++y) {
-        const int now = y < q_quads ? 0 : y < q_quads + k_quads ? 1 : 2;
-        const int h = 4 * (y - (now > 0 ? q_quads : 0) - (now > 1 ? k_quads : 0)) + (lane >> 3);
-        const bool on = h < (now == 0 ? a.Hq : a.Hkv);
-        const uint16_t* src = now == 0 ? a.q + t * a.q_stride : now == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-        const uint4* x = reinterpret_cast<const uint4*>(src + (int64_t)(on ? h : 0) * kHeadDim);
-        const uint4 r0 = x[p0], r1 = x[p1];
-        if (now == 2) {
-            if (on && id >= 0) {
-                uint4* dst = reinterpret_cast<uint4*>(a.v_pages + paged::row_at(id, h, in_page, a.Hkv, a.shift));
-                dst[p0] = r0;
-                dst[p1] = r1;
-            }
-            continue;
+    // sequences, 32 at a time; the first ones stay in registers
+    int c0 = 0, c1 = 0;
+    if (a.cu) {
+        bool bad = false;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int i = min(b0 + lane, a.B - 1), x0 = a.cu[i], x1 = a.cu[i + 1];
+            bad |= x0 < 0 || x1 < x0 || x1 > a.T;
+            if (b0 == 0) { c0 = x0; c1 = x1; }
         }
-        const uint16_t* weight = now == 0 ? a.q_weight : a.k_weight;
-        if (now != kind) {
-            kind = now;
+        if (__any_sync(0xffffffffu, bad)) {
+            if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
+            copy_wait<0>();
+            return;
+        }
+    }
+    int tree_of = -1, depth[2] = {0, 0};
+    bool tree_ok = false;
+
+    for (Place at = start(); left > 0; at = following(at)) {
+        const int t = at.t, first = at.y, end = min(total, first + left);
+        left -= end - first;
+        // ---- the token's sequence, its row there and its position ----
+        int b = -1, row = 0, ahead = 0, rows = 0;
+        bool skip = false;
+        if (a.parent) {
+            b = t / a.n;
+            row = t - b * a.n;
+            rows = a.n;
+            if (b != tree_of) {
+                tree_of = b;
+                tree_ok = paged::tree_depths(a.parent + (int64_t)b * a.n, a.n, depth);
+                if (!tree_ok && lane == 0) flag_error(a.dev_status, EAGLE_DEV_BAD_TREE);
+            }
+            skip = !tree_ok;
+            const int d0 = __shfl_sync(0xffffffffu, depth[0], row & 31), d1 = __shfl_sync(0xffffffffu, depth[1], row & 31);
+            ahead = row < 32 ? d0 : d1;
+        } else {
+            int x0 = c0, x1 = c1;
+            for (int b0 = 0; b0 < a.B && b < 0; b0 += 32) {
+                if (b0 > 0) {
+                    const int i = min(b0 + lane, a.B - 1);
+                    x0 = a.cu[i];
+                    x1 = a.cu[i + 1];
+                }
+                const unsigned in = __ballot_sync(0xffffffffu, x0 <= t && t < x1);
+                if (in) {
+                    const int l = __ffs(in) - 1, begin = __shfl_sync(0xffffffffu, x0, l);
+                    b = b0 + l;
+                    row = ahead = t - begin;
+                    rows = __shfl_sync(0xffffffffu, x1, l) - begin;
+                }
+            }
+            skip = b < 0;                         // a token of no sequence
+        }
+        int id = -1, in_page = 0, held = 0;
+        if (!skip) {
+            held = a.pos[b];
+            const int64_t room = a.page_table ? (int64_t)a.P << a.shift : 0x7fffffffLL;
+            if (held < 0 || held + (int64_t)rows > room) {
+                if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
+                skip = true;
+            } else if (a.page_table) {
+                id = a.page_table[(int64_t)b * a.P + ((held + row) >> a.shift)];
+                in_page = (held + row) & ((1 << a.shift) - 1);
+                if (id < 0 || id >= a.N) {
+                    if (lane == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
+                    id = -1;
+                }
+            }
+        }
+
+        // ---- the token's turns: two a lane, through shared memory ----
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int angle = (int)((frac[h] * (unsigned)(held + ahead)) >> 32);
+            float2 turn;
+            sincospif((float)angle * 0x1p-31f, &turn.y, &turn.x);
+            turns[lane + 32 * h] = turn;
+        }
+        __syncwarp();
+        float2 turn[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            turn[e] = turns[kPairs2 ? (e < 4 ? 4 * c + e : 32 + 4 * c + e - 4) : 8 * c + e];
+        __syncwarp();
+
+        // ---- the heads, kind by kind ----
+        for (int y = first; y < end;) {
+            const int kind = y < q_quads ? 0 : y < q_quads + k_quads ? 1 : 2, y0 = kind == 0 ? 0 : kind == 1 ? q_quads : q_quads + k_quads;
+            const int stop = min(end, kind == 0 ? q_quads : y0 + k_quads), heads = kind == 0 ? a.Hq : a.Hkv;
+            int h = 4 * (y - y0) + (lane >> 3);
+            uint16_t* packed = kind == 0 ? a.q_out + ((int64_t)t * a.Hq + h) * kHeadDim
+                                         : kind == 1 && a.k_out ? a.k_out + ((int64_t)t * a.Hkv + h) * kHeadDim : nullptr;
+            uint16_t* page = kind > 0 && id >= 0 ? (kind == 1 ? a.k_pages : a.v_pages) + paged::row_at(id, h, in_page, a.Hkv, a.shift) : nullptr;
+            const uint16_t* weight = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+            uint4 w0, w1;
             if (weight) {
                 w0 = reinterpret_cast<const uint4*>(weight)[p0];
                 w1 = reinterpret_cast<const uint4*>(weight)[p1];
             }
-        }
-        const uint32_t in[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-        float f[16];
+#pragma unroll 1
+            for (; y < stop; ++y, h += 4, packed += packed ? 4 * kHeadDim : 0, page += page ? (int64_t)(4 * kHeadDim) << a.shift : 0) {
+                copy_wait<kAhead - 1>();
+                const uint4 r0 = raw[read_at], r1 = raw[read_at + 32];
+                read_at = read_at == (kAhead - 1) * 64 ? 0 : read_at + 64;
+                copy_next();                      // into the place that has just been read
+                if (skip) continue;
+                uint32_t o[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+                if (kind < 2) {
+                    uint64_t f[8];                // pairs of neighbours
 #pragma unroll
-        for (int e = 0; e < 8; ++e) { f[2 * e] = lo_of(in[e]); f[2 * e + 1] = hi_of(in[e]); }
-        if (weight) {
-            const float sum = sum_squares(f, 1.f);
-            float r = rsqrtf(fmaf(sum, 1.f / kHeadDim, a.eps));
-            if (__any_sync(0xffffffffu, !(sum < 3e38f))) {
-                // squares beyond fp32: those heads once more, by 2^-80 (beside which eps is nothing)
-                const float small = sum_squares(f, 0x1p-80f);
-                if (!(sum < 3e38f)) {
-                    r = rsqrtf(small * (1.f / kHeadDim));
+                    for (int e = 0; e < 8; ++e) f[e] = attn2::f2(lo_of(o[e]), hi_of(o[e]));
+                    if (weight) {
+                        const float sum = sum_squares(f);
+                        float by = rsqrtf(fmaf(sum, 1.f / kHeadDim, a.eps));
+                        if (__any_sync(0xffffffffu, !(sum < 3e38f))) {
+                            // squares beyond fp32: those heads once more, by 2^-80 (beside which eps is nothing)
+                            uint64_t g[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] *= 0x1p-80f;
+                            for (int e = 0; e < 8; ++e) g[e] = attn2::mul2(f[e], attn2::f2(0x1p-80f, 0x1p-80f));
+                            const float small = sum_squares(g);
+                            if (!(sum < 3e38f)) {
+                                by = rsqrtf(small * (1.f / kHeadDim));
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) f[e] = g[e];
+                            }
+                        }
+                        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        const uint64_t by2 = attn2::f2(by, by);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = attn2::mul2(f[e], attn2::mul2(attn2::f2(lo_of(w[e]), hi_of(w[e])), by2));
+                    }
+                    // (what is not turned does not meet its neighbour's infinities either)
+                    if constexpr (kPairs2) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float x, z;
+                            attn2::unf2(f[e], x, z);
+                            const bool turned = kWhole || (e < 4 ? turned0 : turned1);
+                            o[e] = turned ? pack2(x * turn[e].x - z * turn[e].y, z * turn[e].x + x * turn[e].y) : pack2(x, z);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 u = turn[2 * e], z = turn[2 * e + 1];
+                            const uint64_t cs = attn2::f2(u.x, z.x), sn = attn2::f2(u.y, z.y), ns = attn2::f2(-u.y, -z.y);
+                            const bool turned = kWhole || turned0;
+                            o[e] = pack_pair(turned ? attn2::fma2(f[e], cs, attn2::mul2(f[4 + e], ns)) : f[e]);
+                            o[4 + e] = pack_pair(turned ? attn2::fma2(f[4 + e], cs, attn2::mul2(f[e], sn)) : f[4 + e]);
+                        }
+                    }
+                }
+                if (h >= heads) continue;
+                const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
+                if (packed) {
+                    reinterpret_cast<uint4*>(packed)[p0] = o0;
+                    reinterpret_cast<uint4*>(packed)[p1] = o1;
+                }
+                if (page) {
+                    reinterpret_cast<uint4*>(page)[p0] = o0;
+                    reinterpret_cast<uint4*>(page)[p1] = o1;
                 }
             }
-            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[2 * e] *= r * lo_of(w[e]);
-                f[2 * e + 1] *= r * hi_of(w[e]);
-            }
-        }
-        uint32_t o[8];
-        if constexpr (kPairs2) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                o[e] = pack2(f[2 * e] * turn[e].x - f[2 * e + 1] * turn[e].y, f[2 * e + 1] * turn[e].x + f[2 * e] * turn[e].y);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 u = turn[2 * e], z = turn[2 * e + 1];
-                o[e] = pack2(f[2 * e] * u.x - f[8 + 2 * e] * u.y, f[2 * e + 1] * z.x - f[9 + 2 * e] * z.y);
-                o[4 + e] = pack2(f[8 + 2 * e] * u.x + f[2 * e] * u.y, f[9 + 2 * e] * z.x + f[2 * e + 1] * z.y);
-            }
-        }
-        // what is not turned does not meet its neighbour's infinities either
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!turned0) o[e] = pack2(f[2 * e], f[2 * e + 1]);
-            if (!turned1) o[4 + e] = pack2(f[8 + 2 * e], f[9 + 2 * e]);
-        }
-        if (!on) continue;
-        const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
-        uint16_t* packed = now == 0 ? a.q_out + ((int64_t)t * a.Hq + h) * kHeadDim
-                                    : a.k_out ? a.k_out + ((int64_t)t * a.Hkv + h) * kHeadDim : nullptr;
-        if (packed) {
-            reinterpret_cast<uint4*>(packed)[p0] = o0;
-            reinterpret_cast<uint4*>(packed)[p1] = o1;
-        }
-        if (now == 1 && id >= 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.k_pages + paged::row_at(id, h, in_page, a.Hkv, a.shift));
-            dst[p0] = o0;
-            dst[p1] = o1;
         }
     }
 }
@@ -244,6 +345,7 @@ extern "C" eagle_status eagle_qkv_rope(const void* q, const void* k, const void*
         if (!paged::page_ok(page) || (int64_t)N * Hkv * page > paged::kMaxPool || (int64_t)P * page > paged::kMaxRows)
             return EAGLE_ERR_SHAPE;
     }
+    if (T > 0x3fffffff) return EAGLE_ERR_SHAPE;         // 32-bit places
     if (B == 0 || T == 0) return EAGLE_OK;              // nothing read or written
     if (!q || !k || !inv_freq || !pos || !q_out || !cu == !parent) return EAGLE_ERR_INVALID_ARG;
     if (pages ? !(k_pages && v_pages && page_table && v) : !k_out) return EAGLE_ERR_INVALID_ARG;
@@ -267,17 +369,23 @@ extern "C" eagle_status eagle_qkv_rope(const void* q, const void* k, const void*
     a.eps = eps;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.dev_status = dev_status;
-    // few tokens: a token's heads are spread over as many warps as fill the device
-    const int total = (Hq + 3) / 4 + (Hkv + 3) / 4 * (pages ? 2 : 1);
-    const int64_t want = (int64_t)cached_sm_count() * 16 / T;
-    a.parts = (int)(want < 1 ? 1 : want < total ? want : total);
-    a.quads = (total + a.parts - 1) / a.parts;
-    a.parts = (total + a.quads - 1) / a.quads;
-    const int64_t blocks = ((int64_t)T * a.parts + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffffLL) return EAGLE_ERR_SHAPE;
+    const int sms = cached_sm_count();
+    const bool is_long = T >= (int64_t)sms * kBlocksLong * kWarps * kLongTokens;
+    const int64_t groups = ((Hq + 3) / 4 + (Hkv + 3) / 4 * (pages ? 2 : 1)) * (int64_t)T, most = (int64_t)sms * (is_long ? kBlocksLong : kBlocks);
+    const int64_t need = (groups + kWarps - 1) / kWarps;
+    const unsigned blocks = (unsigned)(need < most ? need : most);
+    if (groups / (most * kWarps) > 0x3fffffff) return EAGLE_ERR_SHAPE;      // a warp counts its own
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (interleaved) qkv_rope_kernel<true><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a);
-    else qkv_rope_kernel<false><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a);
+    auto launch = [&](auto pairs2, auto whole) {
+        constexpr auto kernel = qkv_rope_kernel<decltype(pairs2)::value, decltype(whole)::value>;
+        if (!raise_smem_limit<kernel>(kRopeSmem)) return false;
+        kernel<<<blocks, kWarps * 32, kRopeSmem, s>>>(a);
+        return true;
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (!(interleaved ? rot_dim == kHeadDim ? launch(yes, yes) : launch(yes, no) : rot_dim == kHeadDim ? launch(no, yes) : launch(no, no)))
+        return EAGLE_ERR_CUDA;
     EAGLE_CHECK_LAUNCH();
     return EAGLE_OK;
 }

@@ -466,7 +466,7 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *   y = w * x / sqrt(mean x^2 + eps)          (y = x where w is NULL)
  *   the pairs (y_i, y_{i + r/2}), or (y_2i, y_{2i+1}) with `interleaved`, i < r/2 = rot_dim/2,
  *   are turned by the angle position * inv_freq[i]; elements from rot_dim on stay.
- * One rounding, to bf16, at the end.  Sequence b holds pos[b] rows already.  Its new tokens
+ * One rounding, to bf16, at the end.  T below 2^30.  Sequence b holds pos[b] rows already.  Its new tokens
  * are either rows cu[b] .. cu[b+1]-1 (packed, positions pos[b] + t) or, with parent, the n
  * nodes of a draft tree (T = B * n; position pos[b] + depth of the node: nodes of one depth
  * share it).  Token t of a sequence is cache row pos[b] + t in either case.
