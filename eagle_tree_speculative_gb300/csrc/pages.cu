@@ -19,23 +19,27 @@ namespace eagle {
 namespace {
 
 // ---------------- assignment ----------------
-constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 
-// The workspace, in 32-bit words: per slot (kSlotWords), per CTA of the cluster (the free pages of
-// its part), fresh page numbers, and a table of what slots keep.
+// The workspace: what is known of each slot, the copies, the number of copies, the free pages in each CTA's part of
+// refs, fresh page numbers, and a table of what slots keep.
 struct Slot {
     int fresh;                                    // pages it needs
     int from, rows;                               // a page to copy, how many rows of it; rows = 0: none
-    int to;
     int length;                                   // its rows
     int bad;
+};
+struct Copy {
+    int from, to, rows, pad;
 };
 constexpr int kMaxCluster = 8;
 
 struct AssignArgs {
     int32_t *table, *held, *refs, *kv_len;
     const int32_t *grow, *src;
-    Slot* slots;
+    Copy* copies;                                 // [B]
+    Slot* slots;                                  // [B]
+    int32_t* copy_count;
     int32_t* free_count;                          // [kMaxCluster]
     int32_t* free_ids;                            // [min(N, B P)]
     int32_t* kept;                                // [B][P]
@@ -45,7 +49,7 @@ struct AssignArgs {
 
 size_t assign_words(int B, int N, int P) {
     const int64_t cells = (int64_t)B * P;
-    return (size_t)B * (sizeof(Slot) / 4) + kMaxCluster + (size_t)(N < cells ? N : cells) + (size_t)cells;
+    return (size_t)B * ((sizeof(Copy) + sizeof(Slot)) / 4) + 1 + kMaxCluster + (size_t)(N < cells ? N : cells) + (size_t)cells;
 }
 
 // Warp-wide: the slot that goes on in the page in which s's rows end: s itself, else the first of those that
@@ -64,6 +68,8 @@ __device__ __forceinline__ bool goes_on(const AssignArgs& a, int b, int s) {
 template <int CS>
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) {
     __shared__ int s_sum[kPlanWarps];
+    // the copying kernel may be launched meanwhile; it waits for this one itself
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
     const int page = 1 << a.shift;
@@ -156,12 +162,14 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
 
     // ---- can it be done? ----
     bool bad = false;
-    int64_t fresh = 0;                            // at most B * P < 2^31, see the host side
+    int fresh = 0, copies = 0;                    // fresh: at most B * P < 2^30
     for (int b = tid; b < a.B; b += kPlanThreads) {
         bad |= __ldcg(&a.slots[b].bad) != 0;
         fresh += __ldcg(&a.slots[b].fresh);
+        copies += __ldcg(&a.slots[b].rows) != 0;
     }
-    const int total = block_sum((int)fresh);
+    const int total = block_sum(fresh);
+    if (rank == 0) copies = block_sum(copies);
     int before = 0, there = 0;                    // free pages of lower parts, of all
     for (int r = 0; r < CS; ++r) {
         const int x = __ldcg(a.free_count + r);
@@ -169,12 +177,13 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
         there += x;
     }
     if (__syncthreads_or(bad) || total > there) {       // alike in every CTA
-        if (rank == 0 && tid == 0) flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
-        // no copies: the second kernel reads the slots
-        all_sync();
-        for (int b = rank * kPlanThreads + tid; b < a.B; b += CS * kPlanThreads) a.slots[b].rows = 0;
+        if (rank == 0 && tid == 0) {
+            flag_error(a.dev_status, EAGLE_DEV_CAPACITY);
+            *a.copy_count = 0;
+        }
         return;
     }
+    if (rank == 0 && tid == 0) *a.copy_count = copies;
 
     // ---- (2) the first `total` free pages ----
     for (int p0 = r0; p0 < r1 && before < total; p0 += kPlanThreads) {
@@ -196,9 +205,14 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
 
     // ---- (3) tables and counts ----
     for (int b = rank * kPlanWarps + warp; b < a.B; b += CS * kPlanWarps) {
-        int at = 0;                               // fresh pages of the slots before
-        for (int x = lane; x < b; x += 32) at += __ldcg(&a.slots[x].fresh);
+        int at = 0, copy = 0;                     // fresh pages and copies of the slots before
+        for (int x = lane; x < b; x += 32) {
+            at += __ldcg(&a.slots[x].fresh);
+            copy += __ldcg(&a.slots[x].rows) != 0;
+        }
         at = __reduce_add_sync(0xffffffffu, at);
+        copy = __reduce_add_sync(0xffffffffu, copy);
+        const int rows = __ldcg(&a.slots[b].rows), from = __ldcg(&a.slots[b].from);
         const int s = a.src ? a.src[b] : b;
         const int length = __ldcg(&a.slots[b].length), had = a.held[b], full = length >> a.shift;
         const int need = (int)(((int64_t)length + a.grow[b] + page - 1) >> a.shift);
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
                 if (id >= 0) atomicAdd(a.refs + id, 1);
                 if (was >= 0) atomicAdd(a.refs + was, -1);
             }
-            if (t == full && t < need) a.slots[b].to = id;
+            if (t == full && t < need && rows) a.copies[copy] = Copy{from, id, rows, 0};
         }
         __syncwarp();
         if (lane == 0) {
@@ -229,23 +243,32 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
     }
 }
 
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 256, kCopyWarps = kCopyThreads / 32;
+constexpr int kCopyBlocks = 4;                    // of an SM
+constexpr int kCopyAhead = 8;                     // 16-byte loads of a lane on their way
 
-// One unit is a slot's page in one layer, K or V: the first `rows` rows of each head.
-__global__ void __launch_bounds__(kCopyThreads)
-pages_copy_kernel(uint16_t* k, uint16_t* v, const Slot* slots, int n_layers, int B, int N, int Hkv, int shift) {
-    const int64_t units = (int64_t)B * n_layers * 2;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int b = (int)(u % B);
-        const int rows = slots[b].rows;
-        if (rows == 0) continue;
-        const int layer = (int)(u / (2 * B)), from = slots[b].from, to = slots[b].to;
-        uint16_t* base = ((u / B) & 1 ? v : k) + (((int64_t)layer * N * Hkv) << shift) * kHeadDim;
-        const uint4* src = reinterpret_cast<const uint4*>(base + paged::row_at(from, 0, 0, Hkv, shift));
-        uint4* dst = reinterpret_cast<uint4*>(base + paged::row_at(to, 0, 0, Hkv, shift));
-        const int chunks = rows * (kHeadDim / 8), per = (kHeadDim / 8) << shift;
-        for (int h = 0; h < Hkv; ++h)
-            for (int c = threadIdx.x; c < chunks; c += kCopyThreads) dst[h * per + c] = src[h * per + c];
+// A warp takes a copy's rows of one layer, K or V, and head at a time: they lie in one piece.
+__global__ void __launch_bounds__(kCopyThreads, kCopyBlocks)
+pages_copy_kernel(uint16_t* k, uint16_t* v, const Copy* copies, const int32_t* count, int n_layers, int N, int Hkv, int shift) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int lane = threadIdx.x & 31, per = n_layers * 2 * Hkv;
+    const int64_t units = (int64_t)__ldcg(count) * per;
+    for (int64_t u = (int64_t)blockIdx.x * kCopyWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kCopyWarps) {
+        const int i = (int)(u / per), part = (int)(u - (int64_t)i * per), h = part % Hkv, layer = part / (2 * Hkv);
+        const int4 c = __ldcg(reinterpret_cast<const int4*>(copies + i));
+        uint16_t* base = ((part / Hkv) & 1 ? v : k) + (((int64_t)layer * N * Hkv) << shift) * kHeadDim;
+        const uint4* src = reinterpret_cast<const uint4*>(base + paged::row_at(c.x, h, 0, Hkv, shift)) + lane;
+        uint4* dst = reinterpret_cast<uint4*>(base + paged::row_at(c.y, h, 0, Hkv, shift)) + lane;
+        const int chunks = c.z * (kHeadDim / 8);
+        for (int x0 = 0; x0 < chunks; x0 += 32 * kCopyAhead) {
+            uint4 x[kCopyAhead];
+#pragma unroll
+            for (int y = 0; y < kCopyAhead; ++y)
+                if (x0 + 32 * y + lane < chunks) x[y] = src[x0 + 32 * y];
+#pragma unroll
+            for (int y = 0; y < kCopyAhead; ++y)
+                if (x0 + 32 * y + lane < chunks) dst[x0 + 32 * y] = x[y];
+        }
     }
 }
 
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(kCommitThreads) pages_commit_kernel(CommitArgs
 eagle_status check_pages(int n_layers, int B, int N, int Hkv, int page, int head_dim, int P) {
     if (n_layers < 0 || B < 0 || N < 1 || Hkv < 1 || P < 1) return EAGLE_ERR_INVALID_ARG;
     if (head_dim != kHeadDim || !paged::page_ok(page) || (int64_t)N * Hkv * page > paged::kMaxPool ||
-        (int64_t)P * page > paged::kMaxRows || (int64_t)B * P > 0x3fffffff)
+        (int64_t)P * page > paged::kMaxRows || (int64_t)B * P > 0x3fffffff || (int64_t)n_layers * Hkv > 0x3fffffff)
         return EAGLE_ERR_SHAPE;
     return EAGLE_OK;
 }
@@ -364,8 +387,10 @@ extern "C" eagle_status eagle_pages_assign(void* k_pages, void* v_pages, int32_t
     AssignArgs a;
     a.table = page_table; a.held = held; a.refs = refs; a.kv_len = kv_len;
     a.grow = grow; a.src = src;
-    a.slots = static_cast<Slot*>(workspace);
-    a.free_count = reinterpret_cast<int32_t*>(a.slots + B);
+    a.copies = static_cast<Copy*>(workspace);
+    a.slots = reinterpret_cast<Slot*>(a.copies + B);
+    a.copy_count = reinterpret_cast<int32_t*>(a.slots + B);
+    a.free_count = a.copy_count + 1;
     a.free_ids = a.free_count + kMaxCluster;
     a.kept = a.free_ids + (N < (int64_t)B * P ? N : (int64_t)B * P);
     a.B = B; a.N = N; a.P = P; a.shift = paged::page_shift(page);
@@ -374,10 +399,19 @@ extern "C" eagle_status eagle_pages_assign(void* k_pages, void* v_pages, int32_t
     const cudaError_t e = launch_clustered(pages_plan_kernel<kMaxCluster>, 1, kMaxCluster, kPlanThreads, 0, s, a);
     if (e != cudaSuccess) return EAGLE_ERR_CUDA;
     if (n_layers > 0) {
-        const int64_t units = (int64_t)B * n_layers * 2, most = 8LL * cached_sm_count();
-        pages_copy_kernel<<<(unsigned)(units < most ? units : most), kCopyThreads, 0, s>>>(
-            static_cast<uint16_t*>(k_pages), static_cast<uint16_t*>(v_pages), a.slots, n_layers, B, N, Hkv, a.shift);
-        EAGLE_CHECK_LAUNCH();
+        const int64_t blocks = ((int64_t)B * n_layers * 2 * Hkv + kCopyWarps - 1) / kCopyWarps, most = (int64_t)kCopyBlocks * cached_sm_count();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+        cfg.blockDim = dim3(kCopyThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, static_cast<uint16_t*>(k_pages), static_cast<uint16_t*>(v_pages),
+                               (const Copy*)a.copies, (const int32_t*)a.copy_count, n_layers, N, Hkv, a.shift) != cudaSuccess)
+            return EAGLE_ERR_CUDA;
     }
     return EAGLE_OK;
 }
