@@ -501,30 +501,44 @@ def paged_cache(n_layers, n_pages, Hkv, page, B, max_pages, d=128, device="cuda"
     return (*pages, table, *(torch.zeros(m, dtype=torch.int32, device=device) for m in (B, n_pages)))
 
 
-def _page_shape(fn, k_pages, dims):
-    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
-        raise TypeError("k_pages must be a CUDA tensor")
-    if k_pages.dim() != dims:
-        raise ValueError(f"{fn}: k_pages must be {'[n_layers, ' if dims == 5 else '['}N, Hkv, page, d]")
-    return k_pages.shape
+def _dims(fn, t, name, n, what):
+    """The shape of a tensor of n dimensions."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != n:
+        raise ValueError(f"{fn}: {name} must be {what}")
+    return t.shape
 
 
-def _table_shape(fn, page_table):
-    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
-        raise TypeError("page_table must be a CUDA tensor")
-    if page_table.dim() != 2:
-        raise ValueError(f"{fn}: page_table must be [B, P]")
-    return page_table.shape
+_PAGES, _LAYER = "[n_layers, N, Hkv, page, d]", "[N, Hkv, page, d]"
 
 
-def _workspace(fn, dev, workspace, need, stream, device):
-    """(tensor or None, bytes): the caller's workspace, or one of `need` bytes."""
-    if workspace is None:
-        return (_empty(need, torch.uint8, device, stream) if need else None), need
-    _dev(workspace, "workspace")
-    if workspace.get_device() != dev:
-        raise ValueError(f"{fn}: workspace is on {workspace.device}, other tensors on cuda:{dev}")
-    return workspace, workspace.numel() * workspace.element_size()
+def _launch_with_workspace(fn, dev, stream, workspace, need, head, tail):
+    """_launch with (workspace, its bytes) between the arguments of head and tail: the caller's, or
+    `need` bytes of the stream's pool.  Those go back to it as soon as the call is enqueued, for
+    work behind it on that stream: half the time of a tensor, in calls of a few microseconds."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        if workspace.get_device() != dev:
+            raise ValueError(f"{fn}: workspace is on {workspace.device}, other tensors on cuda:{dev}")
+        size = workspace.numel() * workspace.element_size()
+        return _launch(fn, dev, stream, (*head, workspace.data_ptr(), size, *tail))
+    if not need:
+        return _launch(fn, dev, stream, (*head, None, 0, *tail))
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _launch_with_workspace(fn, dev, stream, None, need, head, tail)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, raw)
+    try:
+        _launch(fn, dev, stream, (*head, ptr, need, *tail))
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ptr)
+
+
+@functools.lru_cache(maxsize=256)
+def _pages_workspace_size(B, N, P) -> int:
+    return pages_workspace_size(B, N, P)
 
 
 def pages_workspace_size(B, N, P) -> int:
@@ -538,20 +552,17 @@ def eagle_pages_assign(k_pages, v_pages, page_table, held, refs, kv_len, grow, s
     (int32) are updated in place; rows of pages that are shared no longer are copied in every
     layer of k_pages / v_pages [n_layers,N,Hkv,page,d] bf16.  All or nothing: see dev_status."""
     fn = "eagle_pages_assign"
-    nl, N, Hkv, page, d = _page_shape(fn, k_pages, 5)
-    B, P = _table_shape(fn, page_table)
+    nl, N, Hkv, page, d = shape = _dims(fn, k_pages, "k_pages", 5, _PAGES)
+    B, P = table = _dims(fn, page_table, "page_table", 2, "[B, P]")
     dev, i32, bf16 = k_pages.get_device(), torch.int32, torch.bfloat16
-    _args(fn, dev, ((k_pages, "k_pages", bf16, k_pages.shape), (v_pages, "v_pages", bf16, k_pages.shape),
-                    (page_table, "page_table", i32, (B, P)), (held, "held", i32, (B,)),
-                    (refs, "refs", i32, (N,)), (kv_len, "kv_len", i32, (B,)), (grow, "grow", i32, (B,))))
-    if src is not None:
-        _args(fn, dev, ((src, "src", i32, (B,)),))
-    need = pages_workspace_size(B, N, P) if workspace is None else 0
-    workspace, ws_bytes = _workspace(fn, dev, workspace, need, stream, k_pages.device)
-    _launch(fn, dev, stream, (
+    specs = ((k_pages, "k_pages", bf16, shape), (v_pages, "v_pages", bf16, shape),
+             (page_table, "page_table", i32, table), (held, "held", i32, (B,)), (refs, "refs", i32, (N,)),
+             (kv_len, "kv_len", i32, (B,)), (grow, "grow", i32, (B,)))
+    _args(fn, dev, specs if src is None else (*specs, (src, "src", i32, (B,))))
+    _launch_with_workspace(fn, dev, stream, workspace, _pages_workspace_size(B, N, P), (
         k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), held.data_ptr(), refs.data_ptr(),
-        kv_len.data_ptr(), grow.data_ptr(), _ptr(src), nl, B, N, Hkv, page, d, P, _ptr(workspace), ws_bytes,
-        _status_ptr(fn, dev, dev_status)))
+        kv_len.data_ptr(), grow.data_ptr(), _ptr(src), nl, B, N, Hkv, page, d, P),
+        (_status_ptr(fn, dev, dev_status),))
 
 
 def eagle_pages_commit(k_pages, v_pages, page_table, kv_len, path, accept_len, max_depth,
@@ -559,8 +570,8 @@ def eagle_pages_commit(k_pages, v_pages, page_table, kv_len, path, accept_len, m
     """Moves the accepted path's rows behind the committed ones in every layer of the pages
     [n_layers,N,Hkv,page,d] bf16; kv_len is advanced in place, or into kv_len_out."""
     fn = "eagle_pages_commit"
-    nl, N, Hkv, page, d = _page_shape(fn, k_pages, 5)
-    B, P = _table_shape(fn, page_table)
+    nl, N, Hkv, page, d = _dims(fn, k_pages, "k_pages", 5, _PAGES)
+    B, P = _dims(fn, page_table, "page_table", 2, "[B, P]")
     kv_len_out = kv_len if kv_len_out is None else kv_len_out
     D, dev, i32, bf16 = int(max_depth), k_pages.get_device(), torch.int32, torch.bfloat16
     _args(fn, dev, ((k_pages, "k_pages", bf16, k_pages.shape), (v_pages, "v_pages", bf16, k_pages.shape),
@@ -602,8 +613,8 @@ def eagle_qkv_rope(q, k, v, inv_freq, pos, cu=None, parent=None, q_weight=None, 
     N = page = P = sv = 0
     pages = k_pages is not None or v_pages is not None or page_table is not None
     if pages:
-        N, _, page, _ = _page_shape(fn, k_pages, 4)
-        P = _table_shape(fn, page_table)[1]
+        N, _, page, _ = _dims(fn, k_pages, "k_pages", 4, _LAYER)
+        P = _dims(fn, page_table, "page_table", 2, "[B, P]")[1]
         sv = _token_rows(fn, v, "v")
         if v.shape != k.shape or v.get_device() != dev:
             raise ValueError(f"{fn}: v must be like k")
@@ -650,22 +661,20 @@ def eagle_tree_attn_paged(q, k_pages, v_pages, page_table, kv_len, parent, scale
     if q.dim() != 4:
         raise ValueError(f"{fn}: q must be [B, n, Hq, d]")
     B, n, Hq, d = q.shape
-    N, Hkv, page, _ = _page_shape(fn, k_pages, 4)
-    P, dev = _table_shape(fn, page_table)[1], q.get_device()
+    N, Hkv, page, _ = _dims(fn, k_pages, "k_pages", 4, _LAYER)
+    P, dev = _dims(fn, page_table, "page_table", 2, "[B, P]")[1], q.get_device()
     bf16, i32 = torch.bfloat16, torch.int32
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
     _args(fn, dev, ((k_pages, "k_pages", bf16, (N, Hkv, page, d)), (v_pages, "v_pages", bf16, (N, Hkv, page, d)),
                     (page_table, "page_table", i32, (B, P)), (kv_len, "kv_len", i32, (B,)),
                     (parent, "parent", i32, (B, n)), (out, "out", bf16, q.shape)))
-    need = _tree_attn_paged_workspace_size(dev, B, n, Hq, Hkv, d, page, P) if workspace is None else 0
-    workspace, ws_bytes = _workspace(fn, dev, workspace, need, stream, q.device)
-    _launch(fn, dev, stream, (
+    _launch_with_workspace(fn, dev, stream, workspace, _tree_attn_paged_workspace_size(dev, B, n, Hq, Hkv, d, page, P), (
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
-        parent.data_ptr(), out.data_ptr(), B, n, Hq, Hkv, d, N, page, P, scale, _ptr(workspace), ws_bytes,
-        _status_ptr(fn, dev, dev_status)))
+        parent.data_ptr(), out.data_ptr(), B, n, Hq, Hkv, d, N, page, P, scale),
+        (_status_ptr(fn, dev, dev_status),))
     return out
 
 
