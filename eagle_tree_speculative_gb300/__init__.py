@@ -83,6 +83,10 @@ def _empty(shape, dtype, device, stream):
     return t
 
 
+def _empty_like(t, stream):
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _status(dev_status, device):
     if dev_status is None:
         return None
@@ -667,7 +671,7 @@ def eagle_tree_attn_paged(q, k_pages, v_pages, page_table, kv_len, parent, scale
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
+        out = _empty_like(q, stream)
     _args(fn, dev, ((k_pages, "k_pages", bf16, (N, Hkv, page, d)), (v_pages, "v_pages", bf16, (N, Hkv, page, d)),
                     (page_table, "page_table", i32, (B, P)), (kv_len, "kv_len", i32, (B,)),
                     (parent, "parent", i32, (B, n)), (out, "out", bf16, q.shape)))
