@@ -101,7 +101,7 @@ constexpr int kMergeMaxParts = 1024;              // at most one per CTA of the 
 
 template <int kLanes, class A>
 __device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const int* places, int parts) {
-    constexpr int kEach = 32 / kLanes;
+    constexpr int kEach = 32 / kLanes, kBatch = kEach == 1 ? 8 : 1;   // parts on their way at a time
     const int lane = threadIdx.x & 31, l = lane % kLanes;
     const int rows = a.unit_rows(s.pair), per_block = kMergeWarps * kEach;
     for (int row0 = blockIdx.y * per_block + (threadIdx.x >> 5) * kEach; row0 < rows; row0 += gridDim.y * per_block) {
@@ -139,16 +139,25 @@ __device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const i
 #pragma unroll
             for (int k = 0; k < kEach; ++k) {
                 const int first = p0 + k * kLanes, count = min(kLanes, parts - first);
-#pragma unroll 4
-                for (int p = 0; p < count; ++p) {
-                    const float wp = __shfl_sync(0xffffffffu, w[k], p, kLanes);
-                    const int place = places[first + p];
-                    if (place < 0) continue;
-                    const float4* x = reinterpret_cast<const float4*>(a.ws_o + ((int64_t)place * a.rows + row) * kHeadDim) + l;
+#pragma unroll 1
+                for (int q0 = 0; q0 < count; q0 += kBatch) {
+                    float4 z[kBatch][kEach];
+                    bool there[kBatch];
 #pragma unroll
-                    for (int c = 0; c < kEach; ++c) {
-                        const float4 z = x[c * kLanes];
-                        o[c].x += z.x * wp; o[c].y += z.y * wp; o[c].z += z.z * wp; o[c].w += z.w * wp;
+                    for (int q = 0; q < kBatch; ++q) {
+                        const int place = q0 + q < count ? places[first + q0 + q] : -1;
+                        there[q] = place >= 0;
+                        const float4* x = reinterpret_cast<const float4*>(a.ws_o + ((int64_t)max(place, 0) * a.rows + row) * kHeadDim) + l;
+#pragma unroll
+                        for (int c = 0; c < kEach; ++c)
+                            if (there[q]) z[q][c] = x[c * kLanes];
+                    }
+#pragma unroll
+                    for (int q = 0; q < kBatch; ++q) {
+                        const float wp = __shfl_sync(0xffffffffu, w[k], (q0 + q) % kLanes, kLanes);
+#pragma unroll
+                        for (int c = 0; c < kEach; ++c)
+                            if (there[q]) { o[c].x += z[q][c].x * wp; o[c].y += z[q][c].y * wp; o[c].z += z[q][c].z * wp; o[c].w += z[q][c].w * wp; }
                     }
                 }
             }
