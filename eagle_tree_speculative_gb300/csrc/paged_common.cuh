@@ -8,7 +8,9 @@ namespace eagle {
 namespace paged {
 
 constexpr int64_t kMaxPool = 0x7fffffffLL;        // N * Hkv * page: rows of all pages and heads, as 32-bit places
-constexpr int64_t kMaxRows = 1LL << 30;           // P * page: rows of a sequence in 32 bits, with a tile to spare
+// P * page: rows of a sequence.  The attention goes through them in 2^20 tiles of 3 500 cycles at most, during which the
+// roles that are done with them wait; waits give up from 2^32 cycles on.
+constexpr int64_t kMaxRows = 1LL << 27;
 
 inline bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 inline int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }

@@ -32,7 +32,7 @@ struct Slot {
 struct Copy {
     int from, to, rows, pad;
 };
-constexpr int kMaxCluster = 8;
+constexpr int kCluster = 8;
 
 struct AssignArgs {
     int32_t *table, *held, *refs, *kv_len;
@@ -40,7 +40,7 @@ struct AssignArgs {
     Copy* copies;                                 // [B]
     Slot* slots;                                  // [B]
     int32_t* copy_count;
-    int32_t* free_count;                          // [kMaxCluster]
+    int32_t* free_count;                          // [kCluster]
     int32_t* free_ids;                            // [min(N, B P)]
     int32_t* kept;                                // [B][P]
     int B, N, P, shift;
@@ -49,7 +49,7 @@ struct AssignArgs {
 
 size_t assign_words(int B, int N, int P) {
     const int64_t cells = (int64_t)B * P;
-    return (size_t)B * ((sizeof(Copy) + sizeof(Slot)) / 4) + 1 + kMaxCluster + (size_t)(N < cells ? N : cells) + (size_t)cells;
+    return (size_t)B * ((sizeof(Copy) + sizeof(Slot)) / 4) + 1 + kCluster + (size_t)(N < cells ? N : cells) + (size_t)cells;
 }
 
 // Warp-wide: the slot that goes on in the page in which s's rows end: s itself, else the first of those that
@@ -65,18 +65,14 @@ __device__ __forceinline__ bool goes_on(const AssignArgs& a, int b, int s) {
     return true;
 }
 
-template <int CS>
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) {
     __shared__ int s_sum[kPlanWarps];
     // the copying kernel may be launched meanwhile; it waits for this one itself
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
+    const int rank = (int)cg::this_cluster().block_rank();
     const int page = 1 << a.shift;
-    auto all_sync = [] {
-        if constexpr (CS > 1) cg::this_cluster().sync();
-        else __syncthreads();
-    };
+    auto all_sync = [] { cg::this_cluster().sync(); };
     auto block_sum = [&](int x) {                 // of every thread; for every thread
         x = __reduce_add_sync(0xffffffffu, x);
         __syncthreads();
@@ -88,7 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
     };
 
     // ---- (1) what each slot keeps and needs; how many pages are free ----
-    for (int b = rank * kPlanWarps + warp; b < a.B; b += CS * kPlanWarps) {
+    for (int b = rank * kPlanWarps + warp; b < a.B; b += kCluster * kPlanWarps) {
         const int s = a.src ? a.src[b] : b;
         Slot y = {};
         const int had = a.held[b], grow = a.grow[b];
@@ -153,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
         y.bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) a.slots[b] = y;
     }
-    const int per = (a.N + CS - 1) / CS, r0 = min(a.N, rank * per), r1 = min(a.N, r0 + per);
+    const int per = (a.N + kCluster - 1) / kCluster, r0 = min(a.N, rank * per), r1 = min(a.N, r0 + per);
     int mine = 0;
     for (int p = r0 + tid; p < r1; p += kPlanThreads) mine += a.refs[p] == 0;
     const int frees = block_sum(mine);
@@ -171,7 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
     const int total = block_sum(fresh);
     if (rank == 0) copies = block_sum(copies);
     int before = 0, there = 0;                    // free pages of lower parts, of all
-    for (int r = 0; r < CS; ++r) {
+    for (int r = 0; r < kCluster; ++r) {
         const int x = __ldcg(a.free_count + r);
         before += r < rank ? x : 0;
         there += x;
@@ -204,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
     all_sync();
 
     // ---- (3) tables and counts ----
-    for (int b = rank * kPlanWarps + warp; b < a.B; b += CS * kPlanWarps) {
+    for (int b = rank * kPlanWarps + warp; b < a.B; b += kCluster * kPlanWarps) {
         int at = 0, copy = 0;                     // fresh pages and copies of the slots before
         for (int x = lane; x < b; x += 32) {
             at += __ldcg(&a.slots[x].fresh);
@@ -393,12 +389,12 @@ extern "C" eagle_status eagle_pages_assign(void* k_pages, void* v_pages, int32_t
     a.slots = reinterpret_cast<Slot*>(a.copies + B);
     a.copy_count = reinterpret_cast<int32_t*>(a.slots + B);
     a.free_count = a.copy_count + 1;
-    a.free_ids = a.free_count + kMaxCluster;
+    a.free_ids = a.free_count + kCluster;
     a.kept = a.free_ids + (N < (int64_t)B * P ? N : (int64_t)B * P);
     a.B = B; a.N = N; a.P = P; a.shift = paged::page_shift(page);
     a.dev_status = dev_status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_clustered(pages_plan_kernel<kMaxCluster>, 1, kMaxCluster, kPlanThreads, 0, s, a);
+    const cudaError_t e = launch_clustered(pages_plan_kernel, 1, kCluster, kPlanThreads, 0, s, a);
     if (e != cudaSuccess) return EAGLE_ERR_CUDA;
     if (n_layers > 0) {
         const int64_t blocks = ((int64_t)B * n_layers * 2 * Hkv + kCopyWarps - 1) / kCopyWarps, most = (int64_t)kCopyBlocks * cached_sm_count();

@@ -421,7 +421,7 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *   page_table int32 [B, P]: row r of sequence b lies in page page_table[b][r / page],
  *            row r % page, in every layer.  Entries behind the pages that a sequence
  *            holds may hold anything.
- * N * Hkv * page below 2^31, P * page up to 2^30, B * P below 2^30.
+ * N * Hkv * page below 2^31, P * page up to 2^27, B * P below 2^30.
  *
  * eagle_pages_assign -- which pages each of B slots holds, and the rows that this needs
  * copied: room for new rows, forks, reorders, ends.  Slot b goes on with what slot
