@@ -1068,7 +1068,8 @@ def run_reference(args, rank, world):
 
 
 KERNEL_CASES = ("gemm", "topk", "fused", "attn", "verify", "verify_filtered", "compact",
-                "softmax", "ttt", "prompt", "attn_kv8", "append_kv8", "commit_kv8")
+                "softmax", "ttt", "prompt", "attn_kv8", "append_kv8", "commit_kv8", "attn_paged",
+                "rope_paged", "assign_paged", "commit_paged")
 
 
 def kernel_case(name, reps):
@@ -1092,6 +1093,10 @@ def kernel_case(name, reps):
       append_kv8  those prompts' rows quantised into the 8-bit cache, one layer
       commit_kv8  the path of `compact` committed into an 8-bit cache, 32 layers, B=4, lengths
                inside blocks that hold rows (from the second repetition on at their final scale)
+      attn_paged  tree attention over pages of 64 rows, the shape of `attn`
+      rope_paged  norms, rotation and rows into those pages, of 8 packed prompts of 2048 tokens
+      assign_paged  a prompt of 2040 rows continued in 8 slots, 32 layers (its last page copied)
+      commit_paged  the path of `compact` over pages, 32 layers, B=4
     """
     import torch
 
@@ -1239,6 +1244,62 @@ def kernel_case(name, reps):
         acc = torch.full((B,), 6, dtype=torch.int32, device=dev)
         fn = lambda: E.eagle_kv8_commit(kt, vt, k8, v8, ks, vs, kv_len, path, acc,  # noqa: E731
                                         c.depth, kv_len_out=new_len, dev_status=st)
+    elif name == "attn_paged":
+        B, page = c.B, 64
+        _, _, _, par, _ = expanded(8)
+        parent = par.repeat(B // 8, 1).contiguous()
+        P = -(-(c.L + c.n) // page)
+        kp, vp = (normal((B * P, c.Hkv, page, c.head_dim), 1.0, torch.bfloat16) for _ in range(2))
+        table = torch.randperm(B * P, generator=g, device=dev).int().view(B, P)
+        q = normal((B, c.n, c.Hq, c.head_dim), 1.0, torch.bfloat16)
+        kv_len = torch.full((B,), c.L, dtype=torch.int32, device=dev)
+        out = torch.empty_like(q)
+        ws = E.tree_attn_paged_workspace_size(B, c.n, c.Hq, c.Hkv, c.head_dim, page, P)
+        wsb = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+        fn = lambda: E.eagle_tree_attn_paged(q, kp, vp, table, kv_len, parent,  # noqa: E731
+                                             out=out, workspace=wsb, dev_status=st)
+    elif name == "rope_paged":
+        B, S, page = 8, 2048, 64
+        x = normal((B * S, (c.Hq + 2 * c.Hkv) * c.head_dim), 1.0, torch.bfloat16)
+        q, k, v = (y.unflatten(1, (-1, c.head_dim)) for y in
+                   x.split([c.Hq * c.head_dim, c.Hkv * c.head_dim, c.Hkv * c.head_dim], 1))
+        kp, vp, table, held, refs = E.paged_cache(1, B * S // page, c.Hkv, page, B, S // page, device=dev)
+        pos = torch.zeros(B, dtype=torch.int32, device=dev)
+        E.eagle_pages_assign(kp, vp, table, held, refs, pos, torch.full_like(pos, S))
+        cu = torch.arange(B + 1, dtype=torch.int32, device=dev) * S
+        w = normal((c.head_dim,), 1.0, torch.bfloat16)
+        f = 10000.0 ** -(torch.arange(0, c.head_dim, 2, device=dev) / c.head_dim)
+        q_out, k_out = (torch.empty(B * S, h, c.head_dim, dtype=torch.bfloat16, device=dev)
+                        for h in (c.Hq, c.Hkv))
+        fn = lambda: E.eagle_qkv_rope(q, k, v, f, pos, cu=cu, q_weight=w, k_weight=w,  # noqa: E731
+                                      k_pages=kp[0], v_pages=vp[0], page_table=table, q_out=q_out,
+                                      k_out=k_out, dev_status=st)
+    elif name == "assign_paged":
+        B, L, page = 8, 2040, 64
+        kp, vp, table, held, refs = E.paged_cache(c.n_layers, 64, c.Hkv, page, B, 40, device=dev)
+        kp.normal_(generator=g)
+        vp.normal_(generator=g)
+        kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
+        grow = torch.ones_like(kv_len)
+        first = torch.tensor([L] + [0] * (B - 1), dtype=torch.int32, device=dev)
+        E.eagle_pages_assign(kp, vp, table, held, refs, kv_len, first)
+        kv_len.copy_(first)
+        src = torch.zeros_like(kv_len)
+        fn = lambda: E.eagle_pages_assign(kp, vp, table, held, refs, kv_len, grow,  # noqa: E731
+                                          src=src, dev_status=st)
+    elif name == "commit_paged":
+        B, page = 4, 64
+        P = -(-c.Lmax // page)
+        kp, vp = (normal((c.n_layers, B * P, c.Hkv, page, c.head_dim), 1.0, torch.bfloat16)
+                  for _ in range(2))
+        table = torch.randperm(B * P, generator=g, device=dev).int().view(B, P)
+        kv_len = torch.full((B,), c.L, dtype=torch.int32, device=dev)
+        new_len = torch.empty_like(kv_len)
+        path = torch.full((B, c.depth + 1), -1, dtype=torch.int32, device=dev)
+        path[:, :7] = torch.tensor([0, 2, 5, 9, 14, 20, 27], dtype=torch.int32)
+        acc = torch.full((B,), 6, dtype=torch.int32, device=dev)
+        fn = lambda: E.eagle_pages_commit(kp, vp, table, kv_len, path, acc, c.depth,  # noqa: E731
+                                          kv_len_out=new_len, dev_status=st)
     else:
         raise ValueError(name)
     fn()                                   # warm-up (first-call set-up stays untimed)
