@@ -270,9 +270,11 @@ pages_copy_kernel(uint16_t* k, uint16_t* v, const Copy* copies, const int32_t* c
 
 // ---------------- commit ----------------
 // Threads of a CTA, eight of which look after a sequence: what is waited for is memory, so many warps, as long as all
-// CTAs have an SM of their own (one sequence, 32 layers: 6.1 us with 256, 5.4 with 512, 5.2 with 1024; 64 sequences: 11.5,
-// 12.4, 21.5).
-constexpr int kCommitFew = 1024, kCommitMany = 256, kCommitCluster = 8;
+// CTAs have an SM of their own (64 sequences, 32 layers: 12.1 us with 256, 21.1 with 512; one: 5.2 with 512, 6.1 with 256).
+// A warp has the rows of kCommitUnits (layer, K or V, kv head)s on their way at once (1 / 2 / 4 / 8: 64 sequences that
+// are in HBM 23 / 21 / 25 / 35 us, 16 sequences of 60 moved rows 25.4 / 22.8 / 24.4 / 48.8).
+constexpr int kCommitFew = 512, kCommitMany = 256, kCommitCluster = 8;
+constexpr int kCommitUnits = 2;
 
 struct CommitArgs {
     uint16_t *k, *v;
@@ -327,22 +329,33 @@ __global__ void __launch_bounds__(kCommitFew) pages_commit_kernel(CommitArgs a) 
     __syncthreads();
     const int moves = s_moves;
     const int units = moves ? a.n_layers * 2 * a.Hkv : 0;            // (layer, K|V, kv head)
-    for (int u = rank * warps + warp; u < units; u += kCommitCluster * warps) {
-        const int h = u % a.Hkv, layer = u / (2 * a.Hkv);
-        uint4* base = reinterpret_cast<uint4*>(((u / a.Hkv) & 1 ? a.v : a.k)) +
+    const int stride = kCommitCluster * warps;
+    for (int u0 = rank * warps + warp; u0 < units; u0 += kCommitUnits * stride) {
+        uint4* base[kCommitUnits];
+#pragma unroll
+        for (int i = 0; i < kCommitUnits; ++i) {
+            const int u = min(u0 + i * stride, units - 1), h = u % a.Hkv, layer = u / (2 * a.Hkv);
+            base[i] = reinterpret_cast<uint4*>(((u / a.Hkv) & 1 ? a.v : a.k)) +
                       ((((int64_t)layer * a.N * a.Hkv + h) << a.shift) * (kHeadDim / 8)) + (lane & 15);
+        }
         for (int m0 = 0; m0 < moves; m0 += 8) {                      // four pairs of rows a round
-            uint4 x[4];
+            uint4 x[kCommitUnits][4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int m = m0 + 2 * y + (lane >> 4);
-                if (m < moves) x[y] = base[(int64_t)s_from[m] * (kHeadDim / 8)];
+                const int64_t from = m < moves ? (int64_t)s_from[m] * (kHeadDim / 8) : -1;
+#pragma unroll
+                for (int i = 0; i < kCommitUnits; ++i)
+                    if (from >= 0 && u0 + i * stride < units) x[i][y] = base[i][from];
             }
             __syncwarp();
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int m = m0 + 2 * y + (lane >> 4);
-                if (m < moves) base[(int64_t)s_to[m] * (kHeadDim / 8)] = x[y];
+                const int64_t to = m < moves ? (int64_t)s_to[m] * (kHeadDim / 8) : -1;
+#pragma unroll
+                for (int i = 0; i < kCommitUnits; ++i)
+                    if (to >= 0 && u0 + i * stride < units) base[i][to] = x[i][y];
             }
             __syncwarp();
         }
