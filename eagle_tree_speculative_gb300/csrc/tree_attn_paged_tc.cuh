@@ -19,6 +19,14 @@
 //
 // MMA order and barriers are those of prompt_attn_tc.cuh: PV of a slot's last tile, then its next QK, whose
 // commit also says that O holds that PV.
+//
+// Measured (with the merging kernel): 48 sequences of one node over 100 .. 30 000 rows, 64 / 8 heads, 209 us: 6.9 TB/s; 64
+// trees of 60 nodes over 4096 rows, 32 / 8 heads, 207 us: 5.6 TB/s, 1.25 PFLOP/s (the slab's kernel 0.296 ms), tensor
+// pipe 63% active; from pages that stay in L2 the trees take 187 us, so the chain of QK, softmax and PV per slot
+// (3 000 cycles a tile of 256 rows) and HBM (5.7 of 6.8 TB/s) bind it together.  Loads without the L2 policy:
+// 212 us; one loading warp for K and V: 219; L2 prefetches two to six tiles ahead: 220 to 285; P handed over in
+// halves: no change; merging by the warp that comes last, in this kernel: 250 (its code and registers).  With five
+// stages instead of six the ragged sequences take 248 us.
 #pragma once
 
 #include <cstddef>
@@ -44,8 +52,10 @@ template <bool kSingle> constexpr int kQTiles = kSingle ? 1 : kSlots;
 constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
 constexpr int kInfo = 3;                          // units in flight between the roles
-constexpr int kUnitCost = 2;                      // what a unit costs beside its tiles, in tiles
-constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles (and unit costs)
+// What a unit costs beside its tiles, in tiles.  us with 1 / 2 / 3 / 4: 16 ragged trees of 48 nodes 74 / 67 / 71 / 77, 48 ragged
+// sequences of one node 214 / 210 / 210 / 213, 64 equal trees alike.
+constexpr int kUnitCost = 2;
+constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles (and unit costs); 2 to 8 alike
 constexpr float kRescale = 8.f;                   // log2 units the maximum may grow by
 
 struct Args {
@@ -191,6 +201,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             // between the warps.  Neither can be two uses ahead on one, which its parity would not show: a
             // place two before has been waited for, and the products that freed it come behind the older use's.)
             const bool is_v = warp == 2;
+            const uint64_t policy = l2_policy_evict_first();
             const CUtensorMap* map = is_v ? &map_v : &map_k;
             const int per = kKeys >> a.shift;             // pages of a tile
             const uint32_t on = attn2::elect_lane();
@@ -242,8 +253,8 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                         for (int x = 0; x < kKeys / 16; ++x) {
                             if (x >= count) break;
                             const int zx = __shfl_sync(0xffffffffu, z, x), yx = __shfl_sync(0xffffffffu, y, x);
-                            tma_load_3d_if(on, to + x * page_bytes, map, bar, 0, yx, zx);
-                            tma_load_3d_if(on, to + x * page_bytes + kBox, map, bar, 64, yx, zx);
+                            tma_load_3d_hint_if(on, to + x * page_bytes, map, bar, 0, yx, zx, policy);
+                            tma_load_3d_hint_if(on, to + x * page_bytes + kBox, map, bar, 64, yx, zx, policy);
                         }
                     }
                     st += 2;
