@@ -92,9 +92,10 @@ __device__ __forceinline__ Segment segment_at(const A& a, int pos, int end, int&
 // Blocks (c, y): the unit whose first tile lies in piece c and whose last does not; its parts are piece c's
 // second place and the first places of the pieces behind it.  m is in log2 units and a part's l and O share one
 // factor, so a part weighs 2^(m - max m).  kLanes lanes look after a row, 32 / kLanes float4 of its O each, and in
-// the same way after 32 parts at a time, so that the parts' loads do not wait for one another: a warp
-// a row where there are few, else eight lanes (4 rows a warp: 151 units of 256 rows and two parts took 24 us with
-// a warp a row).  The launch may begin while the attention kernel ends; the partials are awaited below.
+// the same way after 32 parts at a time, so that the parts' loads do not wait for one another: a warp a row
+// where there are few, with many parts as a rule, else eight lanes, and as many blocks as registers leave room for (4
+// rows a warp: 151 units of 256 rows and two parts took 24 us with a warp a row, 10 with eight lanes, 6 less with 64
+// registers than with 74).  The launch may begin while the attention kernel ends; the partials are awaited below.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeFewRows = 64;                 // rows of a part up to which a warp takes one
 constexpr int kMergeMaxParts = 1024;              // at most one per CTA of the attention kernel
@@ -172,7 +173,7 @@ __device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const i
     }
 }
 
-template <class A>
+template <bool kFew, class A>                     // rows of a part up to kMergeFewRows
 __device__ __forceinline__ void merge_parts(const A& a, int grid) {
     __shared__ int s_place[kMergeMaxParts];
     __shared__ int s_parts;
@@ -197,16 +198,26 @@ __device__ __forceinline__ void merge_parts(const A& a, int grid) {
     }
     __syncthreads();
     await();
-    if (a.rows <= kMergeFewRows) merge_rows<32>(a, s, s_place, s_parts);
-    else merge_rows<8>(a, s, s_place, s_parts);
+    merge_rows<kFew ? 32 : 8>(a, s, s_place, s_parts);
 }
 
-// Blocks a piece takes for the rows of a part: a warp a row, or at most four, which fit on the device together with
-// those of the other pieces (64 trees of 60 nodes: 211.6 us with 4, 214.3 with 8 and the second half waiting).
-inline int merge_blocks(int rows) {
-    if (rows <= kMergeFewRows) return (rows + kMergeWarps - 1) / kMergeWarps;
-    const int y = (rows + 4 * kMergeWarps - 1) / (4 * kMergeWarps);
-    return y < 4 ? y : 4;
+// Launches the merging kernel of the rows' kind behind an attention kernel of `grid` CTAs.  Blocks a piece takes: a
+// warp a row, or at most four, which fit on the device together with those of the other pieces (64 trees of 60
+// nodes: 211.6 us with 4, 214.3 with 8 and the second half waiting).
+template <class A>
+inline cudaError_t launch_merge(void (*few)(A, int), void (*many)(A, int), const A& a, int grid, cudaStream_t stream) {
+    const bool is_few = a.rows <= kMergeFewRows;
+    const int per = kMergeWarps * (is_few ? 1 : 4), y = (a.rows + per - 1) / per;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(is_few || y < 4 ? y : 4));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, is_few ? few : many, a, grid);
 }
 
 }  // namespace attn2

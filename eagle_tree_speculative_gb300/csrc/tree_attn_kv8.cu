@@ -104,17 +104,7 @@ extern "C" eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     kv8_tc::tree_attn_kv8_kernel<<<grid, kv8_tc::kThreads, kv8_tc::kSmem, s>>>(mk, mv, a);
     EAGLE_CHECK_LAUNCH();
-    if (grid > 1) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)attn2::merge_blocks(a.rows));
-        cfg.blockDim = dim3(attn2::kMergeThreads);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, kv8_tc::tree_attn_kv8_merge_kernel, a, grid) != cudaSuccess) return EAGLE_ERR_CUDA;
-    }
+    if (grid > 1 && attn2::launch_merge(kv8_tc::tree_attn_kv8_merge_kernel<true>, kv8_tc::tree_attn_kv8_merge_kernel<false>, a, grid, s) != cudaSuccess)
+        return EAGLE_ERR_CUDA;
     return EAGLE_OK;
 }

@@ -1076,7 +1076,10 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #undef BAR_AT
 }
 
-__global__ void __launch_bounds__(attn2::kMergeThreads) tree_attn_kv8_merge_kernel(Args a, int grid) { attn2::merge_parts(a, grid); }
+template <bool kFew>
+__global__ void __launch_bounds__(attn2::kMergeThreads, kFew ? 1 : 4) tree_attn_kv8_merge_kernel(Args a, int grid) {
+    attn2::merge_parts<kFew>(a, grid);
+}
 
 }  // namespace kv8_tc
 }  // namespace eagle

@@ -123,17 +123,7 @@ extern "C" eagle_status eagle_tree_attn_paged(const void* q, const void* k_pages
         paged_tc::tree_attn_paged_kernel<false><<<grid, paged_tc::kThreads, paged_tc::kSmem, s>>>(mq, mk, mv, a);
     }
     EAGLE_CHECK_LAUNCH();
-    if (grid > 1) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)attn2::merge_blocks(a.rows));
-        cfg.blockDim = dim3(attn2::kMergeThreads);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, paged_tc::tree_attn_paged_merge_kernel, a, grid) != cudaSuccess) return EAGLE_ERR_CUDA;
-    }
+    if (grid > 1 && attn2::launch_merge(paged_tc::tree_attn_paged_merge_kernel<true>, paged_tc::tree_attn_paged_merge_kernel<false>, a, grid, s) != cudaSuccess)
+        return EAGLE_ERR_CUDA;
     return EAGLE_OK;
 }

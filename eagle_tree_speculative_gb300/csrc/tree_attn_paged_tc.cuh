@@ -591,7 +591,10 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 #undef BAR_AT
 }
 
-__global__ void __launch_bounds__(attn2::kMergeThreads) tree_attn_paged_merge_kernel(Args a, int grid) { attn2::merge_parts(a, grid); }
+template <bool kFew>
+__global__ void __launch_bounds__(attn2::kMergeThreads, kFew ? 1 : 4) tree_attn_paged_merge_kernel(Args a, int grid) {
+    attn2::merge_parts<kFew>(a, grid);
+}
 
 }  // namespace paged_tc
 }  // namespace eagle
