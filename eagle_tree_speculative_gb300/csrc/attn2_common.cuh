@@ -249,6 +249,19 @@ __device__ __forceinline__ void rescale_row(uint32_t addr, float alpha) {
     tmem_wait_st();
 }
 
+// 32 bytes in one store (p at a multiple of 32), or in two of 16.  Threads that write a row each take a store's
+// lines one after the other, so half as many stores take half the time.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // Shared-memory writes become visible to the tensor cores and TMA.
 __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");

@@ -60,7 +60,7 @@ int paged_grid(int64_t positions, int n, int G) {
     return (int)(pieces < 1 ? 1 : pieces < sms ? pieces : sms);
 }
 size_t paged_workspace(int grid, int rows) {
-    return (size_t)grid * 2 * rows * (kHeadDim * sizeof(float) + sizeof(float2));
+    return (size_t)grid * 2 * rows * (kHeadDim * sizeof(float) + sizeof(float2)) + 16;      // 16: a workspace at an odd multiple
 }
 
 bool paged_shape_ok(int n, int Hq, int Hkv, int head_dim, int page, int P) {
@@ -104,7 +104,8 @@ extern "C" eagle_status eagle_tree_attn_paged(const void* q, const void* k_pages
     if (grid > 1 && (!workspace || ws_bytes < paged_workspace(grid, a.rows))) return EAGLE_ERR_CAPACITY;
     a.table = page_table; a.kv_len = kv_len; a.parent = parent;
     a.out = static_cast<uint16_t*>(out);
-    a.ws_o = static_cast<float*>(workspace);
+    a.ws_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~static_cast<uintptr_t>(31));
+    a.out_whole = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     a.ws_ml = reinterpret_cast<float2*>(a.ws_o + (size_t)grid * 2 * a.rows * kHeadDim);
     a.B = B; a.n = n; a.Hq = Hq; a.Hkv = Hkv; a.G = G; a.P = paged_tc::kRows / G;
     a.N = N; a.shift = paged::page_shift(page); a.width = P;

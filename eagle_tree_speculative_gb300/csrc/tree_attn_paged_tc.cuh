@@ -63,11 +63,12 @@ struct Args {
     const int32_t* kv_len;
     const int32_t* parent;
     uint16_t* out;
-    float* ws_o;                                  // [grid][2][rows][128]
+    float* ws_o;                                  // [grid][2][rows][128], at a multiple of 32 bytes
     float2* ws_ml;                                // [grid][2][rows]
     int B, n, Hq, Hkv, G, P;                      // P: nodes of a row tile
     int N, shift, width;                          // pages; log2 of a page's rows; entries of a table row
     int rows;                                     // rows of a part
+    bool out_whole;                               // out at a multiple of 32 bytes
     float scale_log2;
     int32_t* dev_status;
 
@@ -557,18 +558,21 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                             o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), w0, __uint_as_float(o1[e]) * w1));
                     }
                     if (valid && part < 0) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kHeadDim + c);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) w[k] = pack2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                            dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int k = 0; k < 8; ++k) w[k] = pack2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            attn2::store32(a.out + at * kHeadDim + c + e, w, a.out_whole);
                         }
                     } else if (valid) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(a.ws_o + place * kHeadDim + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = o[e + k];
+                            attn2::store32(a.ws_o + place * kHeadDim + c + e, w, true);
+                        }
                     }
                     __syncwarp();
                 }

@@ -231,6 +231,20 @@ def test_a_caller_s_workspace():
         E.eagle_tree_attn_paged(q, c["kp"][0], c["vp"][0], c["table"], c["len"], s["parent"], workspace=ws[:need - 16])
 
 
+@pytest.mark.parametrize("L", [40, 9000])
+def test_results_and_scratch_at_odd_multiples_of_16_bytes(L):
+    E = _E()
+    q, kp, vp = _bf16((2, 3, 8, D), 1).cuda(), _bf16((160, 2, 64, D), 2).cuda(), _bf16((160, 2, 64, D), 3).cuda()
+    table, lens = _dev(np.arange(320).reshape(2, 160) % 160), _dev([L, L - 7])
+    parent = _dev([[-1, 0, 1]] * 2)
+    want = E.eagle_tree_attn_paged(q, kp, vp, table, lens, parent)
+    need = E.tree_attn_paged_workspace_size(2, 3, 8, 2, D, 64, 160)
+    room, ws = torch.zeros(q.numel() + 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
+    out = room[8:].view(q.shape)
+    E.eagle_tree_attn_paged(q, kp, vp, table, lens, parent, out=out, workspace=ws[16:])
+    assert out.data_ptr() % 32 == 16 and torch.equal(out, want) and not bool(room[:8].any())
+
+
 def test_what_the_binding_refuses():
     E = _E()
     s = _step_inputs(5)
