@@ -249,9 +249,23 @@ __device__ __forceinline__ void rescale_row(uint32_t addr, float alpha) {
     tmem_wait_st();
 }
 
-// 32 bytes in one store (p at a multiple of 32), or in two of 16.  Threads that write a row each take a store's
-// lines one after the other, so half as many stores take half the time.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool whole) {
+// Four lanes with four units of 8 words each: afterwards place k of lane j (mod 4) holds unit j of lane k.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[32], int lane) {
+#pragma unroll
+    for (int step = 1; step <= 2; ++step) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int u = step == 1 ? i / 8 * 2 : i / 8, lo = 8 * u + i % 8, hi = lo + 8 * step;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[lo] : w[hi], step);
+            if (up) w[lo] = got;
+            else w[hi] = got;
+        }
+    }
+}
+
+// 32 bytes in one store (p at a multiple of 32), or in two of 16.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool whole) {
     if (whole) {
         asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
                      "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])

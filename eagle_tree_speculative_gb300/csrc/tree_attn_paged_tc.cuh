@@ -543,9 +543,8 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             }
             if (!idle) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-                for (int c = 0; c < kHeadDim; c += 32) {
-                    uint32_t o[32];
+                // 32 columns of O, both slots' where the row's tiles were dealt to them
+                auto load_o = [&](int c, uint32_t (&o)[32]) {
                     if (n > 0) tmem_ld32(o_addr + c, o);
                     else
 #pragma unroll
@@ -557,24 +556,41 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                         for (int e = 0; e < 32; ++e)
                             o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), w0, __uint_as_float(o1[e]) * w1));
                     }
-                    if (valid && part < 0) {
+                };
+                // Four lanes exchange what they have of their rows, so that they store 128 bytes of one of them at a time
+                const unsigned rows4 = __ballot_sync(0xffffffffu, valid) >> (lane & 28);
+                if (part < 0) {
+                    uint16_t* to[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 16) {
-                            uint32_t w[8];
+                    for (int k = 0; k < 4; ++k)
+                        to[k] = a.out + __shfl_sync(0xffffffffu, at, (lane & 28) + k) * kHeadDim + 16 * (lane & 3);
+#pragma unroll 1
+                    for (int c = 0; c < kHeadDim; c += 64) {
+                        uint32_t o[32], w[32];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) w[k] = pack2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                            attn2::store32(a.out + at * kHeadDim + c + e, w, a.out_whole);
+                        for (int h = 0; h < 2; ++h) {
+                            load_o(c + 32 * h, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[16 * h + e] = pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
                         }
-                    } else if (valid) {
+                        attn2::transpose4(w, lane);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) w[k] = o[e + k];
-                            attn2::store32(a.ws_o + place * kHeadDim + c + e, w, true);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            if ((rows4 >> k) & 1u) attn2::store32(to[k] + c, w + 8 * k, a.out_whole);
+                        __syncwarp();
                     }
-                    __syncwarp();
+                } else {
+                    float* to = a.ws_o + (place - (lane & 3)) * kHeadDim + 8 * (lane & 3);
+#pragma unroll 1
+                    for (int c = 0; c < kHeadDim; c += 32) {
+                        uint32_t o[32];
+                        load_o(c, o);
+                        attn2::transpose4(o, lane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if ((rows4 >> k) & 1u) attn2::store32(to + k * kHeadDim + c, o + 8 * k, true);
+                        __syncwarp();
+                    }
                 }
                 if (valid && part >= 0) a.ws_ml[place] = make_float2(m, l);
             }
