@@ -21,12 +21,12 @@
 // commit also says that O holds that PV.
 //
 // Measured (with the merging kernel): 48 sequences of one node over 100 .. 30 000 rows, 64 / 8 heads, 209 us: 6.9 TB/s; 64
-// trees of 60 nodes over 4096 rows, 32 / 8 heads, 207 us: 5.6 TB/s, 1.25 PFLOP/s (the slab's kernel 0.296 ms), tensor
-// pipe 63% active; from pages that stay in L2 the trees take 187 us, so the chain of QK, softmax and PV per slot
-// (3 000 cycles a tile of 256 rows) and HBM (5.7 of 6.8 TB/s) bind it together.  Loads without the L2 policy:
-// 212 us; one loading warp for K and V: 219; L2 prefetches two to six tiles ahead: 220 to 285; P handed over in
-// halves: no change; merging by the warp that comes last, in this kernel: 250 (its code and registers).  With five
-// stages instead of six the ragged sequences take 248 us.
+// trees of 60 nodes over 4096 rows, 32 / 8 heads, 202 us: 5.7 TB/s, 1.28 PFLOP/s (the slab's kernel 0.296 ms), tensor
+// pipe 65% active; from pages that stay in L2 the trees take 187 us, so the chain of QK, softmax and PV per slot
+// (3 000 cycles a tile of 256 rows) and HBM (5.7 of 6.8 TB/s) bind it together.  Tried, us of these trees: loads
+// without the L2 policy 5 more; one loading warp for K and V 4 more; L2 prefetches two to six tiles ahead 10 to 75
+// more; P handed over in halves no change; merging by the warp that comes last, in this kernel, 40 more (its
+// code and registers).  With five stages instead of six the ragged sequences take 248 us.
 #pragma once
 
 #include <cstddef>
@@ -52,10 +52,13 @@ template <bool kSingle> constexpr int kQTiles = kSingle ? 1 : kSlots;
 constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
 constexpr int kInfo = 3;                          // units in flight between the roles
-// What a unit costs beside its tiles, in tiles.  us with 1 / 2 / 3 / 4: 16 ragged trees of 48 nodes 74 / 67 / 71 / 77, 48 ragged
-// sequences of one node 214 / 210 / 210 / 213, 64 equal trees alike.
+// What a unit costs beside its tiles, in tiles.  us with 1 / 2 / 3: 16 ragged trees of 48 nodes 61 / 59 / 64, of 16 nodes 35 /
+// 30 / 32, 48 ragged sequences of one node 215 / 211 / 212, 64 equal trees alike.
 constexpr int kUnitCost = 2;
-constexpr int kMinTiles = 3;                      // a CTA's piece is at least so many tiles (and unit costs); 2 to 8 alike
+// A CTA's piece is at least so many tiles (and unit costs).  us with 3 / 4 / 5 / 6 / 7, few units only: one tree of 60 nodes over
+// 4096 rows 27.1 / 26.1 / 22.6 / 26.0 / 23.6, two 28.7 / 28.1 / 25.5 / 27.3 / 24.5, one over 1000 rows 20.7 / 21.6 / 23.4 /
+// 23.5 / 23.0; one sequence of one node over 4000 rows 13.8 / 13.5 / 14.6 / 15.0 / 15.6; large batches alike.
+constexpr int kMinTiles = 5;
 constexpr float kRescale = 8.f;                   // log2 units the maximum may grow by
 
 struct Args {
