@@ -198,20 +198,27 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
             const int d0 = __shfl_sync(0xffffffffu, depth[0], row & 31), d1 = __shfl_sync(0xffffffffu, depth[1], row & 31);
             ahead = row < 32 ? d0 : d1;
         } else {
-            int x0 = c0, x1 = c1;
-            for (int b0 = 0; b0 < a.B && b < 0; b0 += 32) {
-                if (b0 > 0) {
-                    const int i = min(b0 + lane, a.B - 1);
-                    x0 = a.cu[i];
-                    x1 = a.cu[i + 1];
+            int x0 = c0, x1 = c1, b0 = 0;
+            if (a.B > 32 && t >= __shfl_sync(0xffffffffu, c1, 31)) {
+                // behind the first 32: the last place of cu with at most t, a 32nd of what is left each time
+                int lo = 32, len = a.B - 31;      // in cu[lo .. lo + len), whose first is at most t
+                while (len > 1) {
+                    const int step = (len + 31) >> 5, x = lane * step;
+                    const unsigned upto = __ballot_sync(0xffffffffu, x < len && a.cu[lo + min(x, len - 1)] <= t);
+                    const int skipped = (31 - __clz(upto)) * step;
+                    lo += skipped;
+                    len = min(step, len - skipped);
                 }
-                const unsigned in = __ballot_sync(0xffffffffu, x0 <= t && t < x1);
-                if (in) {
-                    const int l = __ffs(in) - 1, begin = __shfl_sync(0xffffffffu, x0, l);
-                    b = b0 + l;
-                    row = ahead = t - begin;
-                    rows = __shfl_sync(0xffffffffu, x1, l) - begin;
-                }
+                b0 = lo;
+                x0 = lo < a.B ? a.cu[lo] : 0;
+                x1 = lo < a.B ? a.cu[lo + 1] : 0;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, x0 <= t && t < x1);
+            if (in) {
+                const int l = __ffs(in) - 1, begin = __shfl_sync(0xffffffffu, x0, l);
+                b = b0 + l;                       // (one sequence's place in all lanes: l is 0)
+                row = ahead = t - begin;
+                rows = __shfl_sync(0xffffffffu, x1, l) - begin;
             }
             skip = b < 0;                         // a token of no sequence
         }

@@ -182,6 +182,15 @@ def test_rope_many_tokens_and_sequences():
     _rope(lens, [int(x) for x in rng.integers(0, 50, 90)], 2, 1, 9, page=16)
 
 
+@pytest.mark.parametrize("B", [33, 34, 63, 64, 65, 100, 1025, 1057])
+def test_rope_finds_a_token_s_sequence(B):
+    """Sequences behind the first 32, most of them empty; rows of nobody before the first and behind the last."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(1, 4, B) * (rng.random(B) < (0.9 if B < 100 else 0.2))]
+    cu = [3] + list(3 + np.cumsum(lens))
+    _rope(lens, [int(x) for x in rng.integers(0, 900, B)], 1, 1, B, dest="packed", cu=cu, T=int(cu[-1]) + 5)
+
+
 def test_rope_large_call():
     """Several thousand tokens: on a sample of them."""
     E = _E()
