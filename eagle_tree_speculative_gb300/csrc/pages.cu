@@ -33,6 +33,7 @@ struct Copy {
     int from, to, rows, pad;
 };
 constexpr int kCluster = 8;
+constexpr int kMaxSlots = 1 << 16;                // a slot looks through those before it
 
 struct AssignArgs {
     int32_t *table, *held, *refs, *kv_len;
@@ -57,10 +58,15 @@ size_t assign_words(int B, int N, int P) {
 __device__ __forceinline__ bool goes_on(const AssignArgs& a, int b, int s) {
     if (!a.src || b == s) return true;
     const int lane = threadIdx.x & 31;
-    if (__ldcg(a.src + s) == s) return false;
-    for (int x0 = 0; x0 < b; x0 += 32) {
-        const int x = x0 + lane;
-        if (__any_sync(0xffffffffu, x < b && __ldcg(a.src + x) == s)) return false;
+    if (a.src[s] == s) return false;
+    for (int x0 = 0; x0 < b; x0 += 128) {         // four loads on their way at a time
+        bool other = false;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int x = x0 + 32 * y + lane;
+            other |= x < b && a.src[x] == s;
+        }
+        if (__any_sync(0xffffffffu, other)) return false;
     }
     return true;
 }
@@ -200,14 +206,18 @@ __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) 
     all_sync();
 
     // ---- (3) tables and counts ----
+    int seen = 0, fresh_seen = 0, copies_seen = 0;    // fresh pages and copies of the slots before `seen`
     for (int b = rank * kPlanWarps + warp; b < a.B; b += kCluster * kPlanWarps) {
-        int at = 0, copy = 0;                     // fresh pages and copies of the slots before
-        for (int x = lane; x < b; x += 32) {
-            at += __ldcg(&a.slots[x].fresh);
-            copy += __ldcg(&a.slots[x].rows) != 0;
+        int f = 0, c = 0;
+        for (int x = seen + lane; x < b; x += 32) {
+            f += __ldcg(&a.slots[x].fresh);
+            c += __ldcg(&a.slots[x].rows) != 0;
         }
-        at = __reduce_add_sync(0xffffffffu, at);
-        copy = __reduce_add_sync(0xffffffffu, copy);
+        fresh_seen += __reduce_add_sync(0xffffffffu, f);
+        copies_seen += __reduce_add_sync(0xffffffffu, c);
+        seen = b;
+        int at = fresh_seen;
+        const int copy = copies_seen;
         const int rows = __ldcg(&a.slots[b].rows), from = __ldcg(&a.slots[b].from);
         const int s = a.src ? a.src[b] : b;
         const int length = __ldcg(&a.slots[b].length), had = a.held[b], full = length >> a.shift;
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(kCommitFew) pages_commit_kernel(CommitArgs a) 
 
 eagle_status check_pages(int n_layers, int B, int N, int Hkv, int page, int head_dim, int P) {
     if (n_layers < 0 || B < 0 || N < 1 || Hkv < 1 || P < 1) return EAGLE_ERR_INVALID_ARG;
-    if (head_dim != kHeadDim || !paged::page_ok(page) || (int64_t)N * Hkv * page > paged::kMaxPool ||
+    if (head_dim != kHeadDim || B > kMaxSlots || !paged::page_ok(page) || (int64_t)N * Hkv * page > paged::kMaxPool ||
         (int64_t)P * page > paged::kMaxRows || (int64_t)B * P > 0x3fffffff || (int64_t)n_layers * Hkv > 0x3fffffff)
         return EAGLE_ERR_SHAPE;
     return EAGLE_OK;
@@ -379,7 +389,7 @@ eagle_status check_pages(int n_layers, int B, int N, int Hkv, int page, int head
 using namespace eagle;
 
 extern "C" size_t eagle_pages_workspace_size(int B, int N, int P) {
-    if (B < 1 || N < 1 || P < 1 || (int64_t)B * P > 0x3fffffff) return 0;
+    if (B < 1 || B > kMaxSlots || N < 1 || P < 1 || (int64_t)B * P > 0x3fffffff) return 0;
     return assign_words(B, N, P) * 4;
 }
 

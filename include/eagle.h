@@ -421,7 +421,8 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *   page_table int32 [B, P]: row r of sequence b lies in page page_table[b][r / page],
  *            row r % page, in every layer.  Entries behind the pages that a sequence
  *            holds may hold anything.
- * N * Hkv * page below 2^31, P * page up to 2^27, B * P below 2^30.
+ * N * Hkv * page below 2^31, P * page up to 2^27, B * P below 2^30; assign and commit: B up
+ * to 65536.
  *
  * eagle_pages_assign -- which pages each of B slots holds, and the rows that this needs
  * copied: room for new rows, forks, reorders, ends.  Slot b goes on with what slot
@@ -503,7 +504,8 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *          calls that may run at the same time need one each.
  * Rows 0 .. L + n - 1 must be finite (a row that a node does not see is multiplied with a
  * zero weight, which does not cancel NaN); what lies behind them in a page is not used,
- * whatever it holds.  Hq / Hkv <= 128.
+ * whatever it holds.  Hq / Hkv <= 128; B * Hkv * (row tiles of 128 / (Hq / Hkv) nodes, an even
+ * number if more than one) * (ceil(P * page / 128) + 2) below 2^31.
  * Device errors: an invalid tree, kv_len[b] < 0 or kv_len[b] + n > P * page sets a
  * dev_status bit and writes zeros for that sequence; a page outside [0, N) sets
  * EAGLE_DEV_CAPACITY and its rows count as zeros.

@@ -69,6 +69,14 @@ def test_commit_refusals(L, change, status):
     assert _call(L.eagle_pages_commit, COMMIT, COMMIT_OK, **change) == status
 
 
+def test_slots_that_a_call_can_have(L):
+    many = dict(B=(1 << 16) + 1, P=1)
+    assert _call(L.eagle_pages_assign, ASSIGN, ASSIGN_OK, **many) == SHAPE
+    assert _call(L.eagle_pages_commit, COMMIT, COMMIT_OK, **many) == SHAPE
+    assert _call(L.eagle_pages_commit, COMMIT, COMMIT_OK, B=(1 << 30) - 1, P=1) == SHAPE
+    assert L.eagle_pages_workspace_size(1 << 16, 9, 1) > 0 and L.eagle_pages_workspace_size((1 << 16) + 1, 9, 1) == 0
+
+
 NO_PAGES = dict(kp=None, vp=None, table=None, v=None, N=0, page=0, P=0, vs=0)
 
 
