@@ -19,7 +19,9 @@ namespace eagle {
 namespace {
 
 // ---------------- assignment ----------------
-constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
+// Threads of a CTA: a warp a slot in calls of up to kPlanFew / 32 * kCluster slots, whose barriers cost less (us with
+// 256 / 512 / 1024, growing: 64 slots 6.6 / 7.1 / 8.4, 96 8.4 / 7.1 / 8.4, 256 13.7 / 9.8 / 9.0, 1024 39.5 / 24.5 / 20.8).
+constexpr int kPlanFew = 256, kPlanMany = 512;
 
 // The workspace: what is known of each slot, the copies, the number of copies, the free pages in each CTA's part of
 // refs, fresh page numbers, and a table of what slots keep.
@@ -71,7 +73,9 @@ __device__ __forceinline__ bool goes_on(const AssignArgs& a, int b, int s) {
     return true;
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) pages_plan_kernel(AssignArgs a) {
+    constexpr int kPlanWarps = kPlanThreads / 32;
     __shared__ int s_sum[kPlanWarps];
     // the copying kernel may be launched meanwhile; it waits for this one itself
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -417,7 +421,8 @@ extern "C" eagle_status eagle_pages_assign(void* k_pages, void* v_pages, int32_t
     a.B = B; a.N = N; a.P = P; a.shift = paged::page_shift(page);
     a.dev_status = dev_status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_clustered(pages_plan_kernel, 1, kCluster, kPlanThreads, 0, s, a);
+    const cudaError_t e = B <= kCluster * (kPlanFew / 32) ? launch_clustered(pages_plan_kernel<kPlanFew>, 1, kCluster, kPlanFew, 0, s, a)
+                                                          : launch_clustered(pages_plan_kernel<kPlanMany>, 1, kCluster, kPlanMany, 0, s, a);
     if (e != cudaSuccess) return EAGLE_ERR_CUDA;
     if (n_layers > 0) {
         const int64_t blocks = ((int64_t)B * n_layers * 2 * Hkv + kCopyWarps - 1) / kCopyWarps, most = (int64_t)kCopyBlocks * cached_sm_count();
