@@ -349,19 +349,30 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             const bool mine = (int)blockIdx.x < cut.ctas;
             int pos = mine ? cut.begin(blockIdx.x) : 0, base = 0, b = 0;
             const int end = mine ? cut.begin(blockIdx.x + 1) : 0;
-            int tree_of = -1, bits = 0, parent[2] = {-1, -1};         // of nodes lane and lane + 32
-            bool bad_tree = false;
+            const int pairs = (a.row_tiles() + 1) / 2;
+            attn2::Segment s;
+            int told_of = -1, L = 0, bits = 0, parent[2] = {-1, -1};  // of nodes lane and lane + 32
+            bool zero = false;
             // tells the roles unit i, or that there is none: then false
             auto tell = [&](int i) {
-                attn2::Segment s;
                 bool have = false;
                 while (!have && pos < end) {
-                    s = attn2::segment_at(a, pos, end, b, base);
+                    if (told_of >= 0 && (s.pair + 1 < pairs || s.head + 1 < a.Hkv)) {
+                        // the sequence's next unit: nothing has to be looked up, which would take longer than a tile
+                        s.head += s.pair + 1 == pairs;
+                        s.pair = s.pair + 1 == pairs ? 0 : s.pair + 1;
+                        s.start = pos;
+                        s.t0 = 0;
+                        s.t1 = min(s.T, attn2::tiles_before<Args>(pos, s.weight, end));
+                    } else {
+                        s = attn2::segment_at(a, pos, end, b, base);
+                    }
                     pos = s.start + s.weight * (s.T + kUnitCost);
                     have = s.t0 < s.t1;
                 }
-                if (have && s.b != tree_of) {
-                    tree_of = s.b;
+                if (have && s.b != told_of) {
+                    told_of = s.b;
+                    L = a.kv_len[s.b];
                     bool bad = false;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -369,7 +380,9 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                         parent[h] = x < a.n ? a.parent[(int64_t)s.b * a.n + x] : 0;
                         bad |= x < a.n && (x == 0 ? parent[h] != -1 : (parent[h] < 0 || parent[h] >= x));
                     }
-                    bad_tree = __any_sync(0xffffffffu, bad);
+                    const bool bad_len = a.bad_length(L), bad_tree = __any_sync(0xffffffffu, bad);
+                    zero = bad_len || bad_tree;
+                    bits |= (bad_len ? EAGLE_DEV_CAPACITY : 0) | (bad_tree ? EAGLE_DEV_BAD_TREE : 0);
                 }
                 const bool got = attn2::wait_for(BAR_AT(info_empty, i % kInfo), (((uint32_t)i / kInfo) & 1u) ^ 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) return false;
@@ -377,10 +390,6 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 if (!have) {
                     if (lane == 0) u->head = -1;
                 } else {
-                    const int L = a.kv_len[s.b];
-                    const bool bad_len = a.bad_length(L), zero = bad_len || bad_tree;
-                    if (zero && s.head == 0 && s.pair == 0 && s.t0 == 0)
-                        bits |= (bad_len ? EAGLE_DEV_CAPACITY : 0) | (bad_tree ? EAGLE_DEV_BAD_TREE : 0);
                     u->parent[lane] = (uint8_t)parent[0];
                     u->parent[lane + 32] = (uint8_t)parent[1];
                     if (lane == 0) {
