@@ -17,8 +17,7 @@
 // and zeroes V rows behind the tree's last (never written: a zero weight does not cancel NaN), warps 4-11
 // are the softmax.
 //
-// MMA order and barriers are those of prompt_attn_tc.cuh: PV of a slot's last tile, then its next QK, whose
-// commit also says that O holds that PV.
+// MMA order: PV of a slot's last tile, then its next QK, whose commit also says that O holds that PV.
 //
 // Measured (with the merging kernel): 48 sequences of one node over 100 .. 30 000 rows, 64 / 8 heads, 209 us: 6.9 TB/s; 64
 // trees of 60 nodes over 4096 rows, 32 / 8 heads, 202 us: 5.7 TB/s, 1.28 PFLOP/s (the slab's kernel 0.296 ms), tensor
@@ -282,26 +281,31 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 st += 2;
                 if (st >= kStages) { st -= kStages; ph ^= 1u; }
             };
-            // O of slot s += P V of the next V tile, then S = Q K^T of the next K tile.  opens, closes: the
-            // tiles' first, last use; qs: the slot whose Q it is
-            auto step = [&](int s, int qs, bool pv, bool pv_first, bool pv_last, bool qk, bool qk_first, bool qk_last, bool opens, bool closes) {
+            // O of slot s += P V of the next V tile, then S = Q K^T of the next K tile.  qs: the slot whose Q it is;
+            // first, last: of the unit's tiles in the slot (PV), of its Q (QK); opens, closes: the tile's first, last use
+            struct Use {
+                bool on, first, last, opens, closes;
+            };
+            auto step = [&](int s, int qs, Use pv, Use qk) {
                 const uint32_t scol = tm + (uint32_t)(s << 7), ocol = scol + 256;
-                if (pv) {
-                    if (opens) wait(BAR_AT(full, vs), vp);
+                if (pv.on) {
+                    if (pv.opens) wait(BAR_AT(full, vs), vp);
                     wait(BAR_AT(p_full, s), pph >> s);
                     pph ^= 1u << s;
                     tc_fence_after();
                     const uint32_t dv = dv0 + ((vs * kTile) >> 4);
-                    uint32_t acc = pv_first ? 0u : 1u;
+                    uint32_t acc = pv.first ? 0u : 1u;
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k) {
                         attn2::mma_ts(on, ocol, scol + 8 * k, dv + ((k * 16 * 128) >> 4), kIdescPV, acc);
                         acc = 1u;
                     }
+                    // (the unit's result must not wait for the next one's Q)
+                    if (pv.last) attn2::commit_if(leader, BAR_AT(o_full, s));
                 }
-                if (qk) {
-                    if (opens) wait(BAR_AT(full, ks), kp);
-                    if (qk_first) {
+                if (qk.on) {
+                    if (qk.opens) wait(BAR_AT(full, ks), kp);
+                    if (qk.first) {
                         wait(BAR_AT(q_full, qs), qph >> qs);
                         qph ^= 1u << qs;
                     }
@@ -314,30 +318,43 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                     }
                     attn2::commit_if(leader, BAR_AT(s_full, s));
                 }
-                attn2::commit_if(leader && pv && pv_last, BAR_AT(o_full, s));
-                attn2::commit_if(leader && qk && qk_last, BAR_AT(q_empty, qs));
-                attn2::commit_if(leader && pv && closes, BAR_AT(empty, vs));
-                attn2::commit_if(leader && qk && closes, BAR_AT(empty, ks));
-                if (pv && closes) advance(vs, vp);
-                if (qk && closes) advance(ks, kp);
+                attn2::commit_if(leader && qk.on && qk.last, BAR_AT(q_empty, qs));
+                attn2::commit_if(leader && pv.on && pv.closes, BAR_AT(empty, vs));
+                attn2::commit_if(leader && qk.on && qk.closes, BAR_AT(empty, ks));
+                if (pv.on && pv.closes) advance(vs, vp);
+                if (qk.on && qk.closes) advance(ks, kp);
             };
-            const Unit* u;
-            for (int i = 0; ok && (u = next_unit(i)); ++i) {
-                const int n = attn2::uniform_of(u->n);
-                const bool split = kSingle || attn2::uniform_of(u->split);
-                unit_read(i);
-                if (n == 0) continue;
-                // step x.  Both slots see every tile: slot x & 1, PV of tile x / 2 - 1, QK of tile x / 2.
-                // Tiles in turn: PV of tile x - 2, QK of tile x, both slot x & 1's.
-                const int steps = split ? n + 2 : 2 * n + 2;
+            // A unit of a single tile leaves its PV to the steps of the next ones, in which the slots go on taking turns,
+            // so that such units follow one another without a gap (1024 sequences of one node over 1 .. 100 rows, 64 /
+            // 8 heads: 197 to 130 us); behind longer ones that gained nothing.  The last units' PV, and that before a
+            // unit without tiles (whose rows the softmax cannot write before), have steps of their own.
+            int turn = 0, owed = 0;                       // the slot that is next; a bit per slot that owes PV
+            for (int i = 0;; ++i) {
+                const Unit* u = ok ? next_unit(i) : nullptr;
+                int n = 0;
+                bool split = kSingle;
+                if (u) {
+                    n = attn2::uniform_of(u->n);
+                    split = kSingle || attn2::uniform_of(u->split);
+                    unit_read(i);
+                }
+                const bool one = split && n == 1;
+                turn = attn2::uniform_of(turn);
+                owed = attn2::uniform_of(owed);
+                // step x.  Both slots see every tile: PV of tile x / 2 - 1, QK of tile x / 2.  Tiles in turn: PV of
+                // tile x - 2, QK of tile x.  The first two: what is owed.
+                const int steps = one ? 1 : n == 0 ? 2 : split ? n + 2 : 2 * n + 2;
 #pragma unroll 1
                 for (int x = 0; x < steps && __all_sync(0xffffffffu, ok); ++x) {
-                    const int s = x & 1, j = split ? x : x >> 1, back = split ? 2 : 1;
-                    const bool pv = j >= back && j - back < n, qk = j < n;
-                    // (a slot's first PV is that of its first tile, its last that behind which it has no QK)
-                    step(s, split ? 0 : s, pv, j < 2 * back, j >= n, qk, j == 0, j == n - 1, split || s == 0, split || s == 1);
+                    const int s = (turn + x) & 1, j = split ? x : x >> 1, back = split ? 2 : 1;
+                    const bool early = x < 2, opens = split || !(x & 1), closes = split || (x & 1);
+                    step(s, split ? 0 : s, Use{!early || ((owed >> s) & 1), early || j < 2 * back, early || j >= n, early || opens, early || closes},
+                         Use{j < n, j == 0, j == n - 1, opens, closes});
                 }
+                owed = one ? owed | 1 << turn : 0;
+                turn = one ? turn ^ 1 : 0;
                 ok = __all_sync(0xffffffffu, ok);
+                if (!u) break;
             }
             if (leader) {
                 umma_commit(BAR(drain));
@@ -442,6 +459,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         const float sc = a.scale_log2;
         const uint64_t sc2 = attn2::f2(sc, sc);
         uint32_t tiles_done = 0, units_done = 0, merges = 0;
+        int turn = 0;                                     // the slot that has a unit's first tile
         bool ok = true;
         const Unit* u;
         for (int i = 0; ok && (u = next_unit(i)); ++i) {
@@ -462,7 +480,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             float mref = -INFINITY;
             uint64_t l2 = 0;                              // two partial sums
             int mine = 0;                                 // tiles of this slot
-            for (int t = split ? slot : 0; t < n; t += split ? 2 : 1, ++mine) {
+            for (int t = split ? slot ^ turn : 0; t < n; t += split ? 2 : 1, ++mine) {
                 const bool got = attn2::wait_for(BAR_AT(s_full, slot), tiles_done & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 ++tiles_done;
@@ -525,6 +543,9 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 ++units_done;
                 tc_fence_after();
             }
+            const bool one = split && n == 1;
+            const int writer = one ? turn : 0;            // who writes a single row tile
+            turn = one ? turn ^ 1 : 0;
             float la, lb;
             attn2::unf2(l2, la, lb);
             float l = la + lb, m = mref, w0 = 1.f, w1 = 0.f;             // weights of the slots' O
@@ -550,7 +571,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 w0 = exp2f(mref - mb);
                 w1 = exp2f(other.x - mb);
                 l = l * w0 + other.y * w1;
-            } else if (split && slot == 1) {
+            } else if (split && slot != writer) {
                 continue;
             }
             if (!idle) {
