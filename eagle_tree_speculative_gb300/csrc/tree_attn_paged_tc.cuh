@@ -302,6 +302,9 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                     }
                     // (the unit's result must not wait for the next one's Q)
                     if (pv.last) attn2::commit_if(leader, BAR_AT(o_full, s));
+                    // The V tile's place: behind PV where pairs of row tiles read it (16 ragged trees of 48 nodes 60 to
+                    // 55 us, longer ones 122 to 101), else behind QK (48 ragged sequences of one node 210 to 208 us).
+                    if (!kSingle) attn2::commit_if(leader && pv.closes, BAR_AT(empty, vs));
                 }
                 if (qk.on) {
                     if (qk.opens) wait(BAR_AT(full, ks), kp);
@@ -319,7 +322,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                     attn2::commit_if(leader, BAR_AT(s_full, s));
                 }
                 attn2::commit_if(leader && qk.on && qk.last, BAR_AT(q_empty, qs));
-                attn2::commit_if(leader && pv.on && pv.closes, BAR_AT(empty, vs));
+                if (kSingle) attn2::commit_if(leader && pv.on && pv.closes, BAR_AT(empty, vs));
                 attn2::commit_if(leader && qk.on && qk.closes, BAR_AT(empty, ks));
                 if (pv.on && pv.closes) advance(vs, vp);
                 if (qk.on && qk.closes) advance(ks, kp);
