@@ -51,12 +51,12 @@ template <bool kSingle> constexpr int kQTiles = kSingle ? 1 : kSlots;
 constexpr int kBox = 128 * 64 * 2;                // 16 KB: 128 rows x 64 dims
 constexpr int kTile = 2 * kBox;                   // 32 KB: Q of a slot, or a K or V tile
 constexpr int kInfo = 3;                          // units in flight between the roles
-// What a unit costs beside its tiles, in tiles.  us with 1 / 2 / 3: 16 ragged trees of 48 nodes 61 / 59 / 64, of 16 nodes 35 /
-// 30 / 32, 48 ragged sequences of one node 215 / 211 / 212, 64 equal trees alike.
+// What a unit costs beside its tiles, in tiles.  us with 1 / 2 / 3: 16 ragged trees of 48 nodes 63 / 55 / 58, of 16 nodes 32 /
+// 30 / 30, 48 ragged sequences of one node 214 / 210 / 211, 64 equal trees alike.
 constexpr int kUnitCost = 2;
-// A CTA's piece is at least so many tiles (and unit costs).  us with 3 / 4 / 5 / 6 / 7, few units only: one tree of 60 nodes over
-// 4096 rows 27.1 / 26.1 / 22.6 / 26.0 / 23.6, two 28.7 / 28.1 / 25.5 / 27.3 / 24.5, one over 1000 rows 20.7 / 21.6 / 23.4 /
-// 23.5 / 23.0; one sequence of one node over 4000 rows 13.8 / 13.5 / 14.6 / 15.0 / 15.6; large batches alike.
+// A CTA's piece is at least so many tiles (and unit costs).  us with 3 / 4 / 5 / 6, few units only: one tree of 60 nodes over
+// 4096 rows 26.5 / 25.6 / 23.0 / 25.9, two 27.9 / 27.7 / 25.7 / 27.2, eight over 500 .. 1000 rows 25.2 / 24.6 / 26.0 / 26.4;
+// one sequence of one node over 4000 rows 13.6 / 13.1 / 14.7 / 15.0; large batches alike.
 constexpr int kMinTiles = 5;
 constexpr float kRescale = 8.f;                   // log2 units the maximum may grow by
 
@@ -82,7 +82,7 @@ struct Args {
         return bad_length(L) ? 1 : (L + n + kKeys - 1) / kKeys;
     }
     // a pair's missing row tile counts too: its key tiles take as long as two row tiles' (a tile's bytes, not its
-    // products, are what a single row tile waits for; 16 ragged trees of 48 nodes, 64 / 8 heads: 67 against 87 us)
+    // products, are what a single row tile waits for; 16 ragged trees of 48 nodes, 64 / 8 heads: 67 us against 87, where both were measured)
     __device__ int row_tiles() const { return n <= P ? 1 : (n + 2 * P - 1) / (2 * P) * 2; }
     __device__ int unit_rows(int pair) const {
         const int left = n - pair * 2 * P;        // nodes from the pair's first on

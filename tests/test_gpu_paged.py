@@ -355,6 +355,22 @@ def test_refused_sequences_are_zeros_and_the_others_are_not():
     _attn([50, 60, 300], 5, 4, 2, 16, 11, status=CAPACITY, change=page)       # its rows count as zeros
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,page", [(1, 16, 16, 16), (1, 40, 20, 128), (16, 20, 20, 32), (20, 64, 8, 64), (33, 16, 8, 16)])
+def test_many_short_units_of_a_cta(n, Hq, Hkv, page):
+    """Units of one tile, of two and of three next to one another, and refused sequences between them: more than a few a CTA."""
+    rng = np.random.default_rng(n + Hq)
+    B = 150 if n < 20 else 80
+    L = [int(x) for x in rng.choice([0, 1, 60, 90, 127 - n, 128 - n, 129 - n, 200, 300], B, p=[.1, .2, .1, .2, .1, .1, .1, .05, .05])]
+
+    def change(table, parent, L, q, kp, vp, N):
+        for b in rng.choice(B, 12, replace=False):
+            L[b] = -1 if b % 2 else table.shape[1] * page
+        for b in (7, 8, 9, 10):
+            L[b] = -5
+    _attn(L, n, Hq, Hkv, page, n, status=CAPACITY, change=change)
+    _attn([min(max(x, 0), 128 - n) for x in L], n, Hq, Hkv, page, n + 1)
+
+
 def test_replayed_graph_and_two_streams():
     E = _E()
     args, out = _attn([900, 30, 4000], 9, 8, 2, 16, 12)
