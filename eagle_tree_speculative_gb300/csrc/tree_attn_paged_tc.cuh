@@ -21,7 +21,7 @@
 //
 // Measured (with the merging kernel): 48 sequences of one node over 100 .. 30 000 rows, 64 / 8 heads, 209 us: 6.9 TB/s; 64
 // trees of 60 nodes over 4096 rows, 32 / 8 heads, 202 us: 5.7 TB/s, 1.28 PFLOP/s (the slab's kernel 0.296 ms), tensor
-// pipe 65% active; from pages that stay in L2 the trees take 187 us, so the chain of QK, softmax and PV per slot
+// pipe 70% active; from pages that stay in L2 the trees take 187 us, so the chain of QK, softmax and PV per slot
 // (3 000 cycles a tile of 256 rows) and HBM (5.7 of 6.8 TB/s) bind it together.  Tried, us of these trees: loads
 // without the L2 policy 5 more; one loading warp for K and V 4 more; L2 prefetches two to six tiles ahead 10 to 75
 // more; P handed over in halves no change; merging by the warp that comes last, in this kernel, 40 more (its
