@@ -45,6 +45,7 @@ struct RopeArgs {
     int N, shift, P;
     float eps;
     int64_t q_stride, k_stride, v_stride;
+    uint32_t none;                                // 0, which the compiler does not know
     int32_t* dev_status;
 };
 
@@ -71,10 +72,9 @@ __device__ __forceinline__ float sum_squares(const uint64_t (&x)[8]) {
     return t;
 }
 
-// 16 bytes of global into shared memory, behind this thread's back, not before `after` is known; kLeft: groups that may
-// still be on their way.
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t after) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src), "r"(after) : "memory");
+// 16 bytes of global into shared memory, behind this thread's back; kLeft: groups that may still be on their way.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int kLeft>
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
     const uint16_t *next = nullptr, *next_base = nullptr;
     uint32_t copy_at = s32(raw), read_at = 0;     // places in the ring
     const uint32_t copy_begin = copy_at, copy_end = copy_at + kAhead * 1024;
-    auto copy_next = [&](uint32_t after) {
+    // (zero: the copy begins when it is known)
+    auto copy_next = [&](uint32_t zero) {
         if (next_left > 0) {
             --next_left;
             if (next_y == next_end) {             // a kind's first group
@@ -141,8 +142,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
                 next = next_base + next_h * kHeadDim;
             }
             const uint16_t* src = next_h < next_heads ? next : next_base;
-            copy16_async(copy_at, src + 8 * p0, after);
-            copy16_async(copy_at + 512, src + 8 * p1, after);
+            copy16_async(copy_at + zero, src + 8 * p0);
+            copy16_async(copy_at + zero + 512, src + 8 * p1);
             next += 4 * kHeadDim;
             next_h += 4;
             ++next_y;
@@ -274,11 +275,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
                 const uint4 r0 = raw[read_at], r1 = raw[read_at + 32];
                 read_at = read_at == (kAhead - 1) * 64 ? 0 : read_at + 64;
                 uint32_t o[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-                // the next copy goes into the place that was read, once what was read is there
-                uint32_t used = 0;
+                // The next copy goes into the place that was read.  Nothing orders it behind the reads, so its address is
+                // made of what they brought: it cannot begin before that is in registers.
+                uint32_t read = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) used |= o[e];
-                copy_next(used);
+                for (int e = 0; e < 8; ++e) read |= o[e];
+                copy_next(read & a.none);
                 if (skip) continue;
                 if (kind < 2) {
                     uint64_t f[8];                // pairs of neighbours
@@ -385,6 +387,7 @@ extern "C" eagle_status eagle_qkv_rope(const void* q, const void* k, const void*
     a.N = N; a.shift = pages ? paged::page_shift(page) : 0; a.P = P;
     a.eps = eps;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.none = 0;
     a.dev_status = dev_status;
     const int sms = cached_sm_count();
     const bool is_long = T >= (int64_t)sms * kBlocksLong * kWarps * kLongTokens;
