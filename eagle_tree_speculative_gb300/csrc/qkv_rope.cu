@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
                         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                         const uint64_t by2 = attn2::f2(by, by);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = attn2::mul2(f[e], attn2::mul2(attn2::f2(lo_of(w[e]), hi_of(w[e])), by2));
+                        for (int e = 0; e < 8; ++e)       // (w * by may leave fp32)
+                            f[e] = attn2::mul2(attn2::mul2(f[e], by2), attn2::f2(lo_of(w[e]), hi_of(w[e])));
                     }
                     // (what is not turned does not meet its neighbour's infinities either)
                     if constexpr (kPairs2) {
