@@ -288,15 +288,18 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
                     for (int e = 0; e < 8; ++e) f[e] = attn2::f2(lo_of(o[e]), hi_of(o[e]));
                     if (weight) {
                         const float sum = sum_squares(f);
-                        float by = rsqrtf(fmaf(sum, 1.f / kHeadDim, a.eps));
-                        if (__any_sync(0xffffffffu, !(sum < 3e38f))) {
-                            // squares beyond fp32: those heads once more, by 2^-80 (beside which eps is nothing)
+                        const float mean = fmaf(sum, 1.f / kHeadDim, a.eps);
+                        float by = rsqrtf(mean);
+                        const bool far = !(mean > 1e-30f && mean < 3e38f);
+                        if (__any_sync(0xffffffffu, far)) {
+                            // squares at the ends of fp32 or beyond: those heads once more, by 2^60 or 2^-80
+                            const float to = mean < 1.f ? 0x1p60f : 0x1p-80f;
                             uint64_t g[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) g[e] = attn2::mul2(f[e], attn2::f2(0x1p-80f, 0x1p-80f));
-                            const float small = sum_squares(g);
-                            if (!(sum < 3e38f)) {
-                                by = rsqrtf(small * (1.f / kHeadDim));
+                            for (int e = 0; e < 8; ++e) g[e] = attn2::mul2(f[e], attn2::f2(to, to));
+                            const float moved = sum_squares(g);
+                            if (far) {
+                                by = rsqrtf(fmaf(moved, 1.f / kHeadDim, a.eps * to * to));
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) f[e] = g[e];
                             }

@@ -50,3 +50,10 @@ def _norms(size, weight, eps, seed=1):
 def test_weights_far_from_one_over_heads_far_from_one(size, weight, eps):
     """The factor of a head times its weight leaves fp32 where the normed head times its weight does not."""
     _norms(size, weight, eps)
+
+
+@pytest.mark.parametrize("size,eps", [(2.0 ** 62, 2.0 ** 123), (2.0 ** 66, 2.0 ** 127), (1.0, 2.0 ** 127), (2.0 ** -70, 2.0 ** -140),
+                                      (2.0 ** -75, 2.0 ** -149), (2.0 ** -50, 2.0 ** -100), (2.0 ** -52, 2.0 ** -101)])
+def test_eps_beside_squares_at_the_ends_of_fp32(size, eps):
+    """Squares that overflow beside an eps that counts, squares that are denormal or zero beside one that does not."""
+    _norms(size, 1.0, eps)
