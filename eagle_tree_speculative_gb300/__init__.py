@@ -611,7 +611,7 @@ def eagle_qkv_rope(q, k, v, inv_freq, pos, cu=None, parent=None, q_weight=None, 
     B, n = pos.numel(), 0
     if parent is not None:
         _dev(parent, "parent", i32)
-        n = T // B if B else 0
+        n = T // B if B else parent.shape[1] if parent.dim() == 2 else 0
     specs = [(pos, "pos", i32, (B,)), (inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),)),
              (cu, "cu", i32, (B + 1,)) if parent is None else (parent, "parent", i32, (B, n))]
     N = page = P = sv = 0

@@ -57,3 +57,17 @@ def test_weights_far_from_one_over_heads_far_from_one(size, weight, eps):
 def test_eps_beside_squares_at_the_ends_of_fp32(size, eps):
     """Squares that overflow beside an eps that counts, squares that are denormal or zero beside one that does not."""
     _norms(size, 1.0, eps)
+
+
+@pytest.mark.parametrize("n", [0, 1, 9])
+def test_an_empty_batch_of_trees(n):
+    E = _E()
+    q, k = (torch.empty(0, H, D, dtype=torch.bfloat16, device="cuda") for H in (4, 2))
+    kp, vp, table, _, _ = E.paged_cache(1, 5, 2, 16, 0, 3)
+    parent = _dev(np.zeros((0, n)))
+    a, b = E.eagle_qkv_rope(q, k, None, _freq().cuda(), _dev([]), parent=parent)
+    assert a.shape == q.shape and b.shape == k.shape
+    a, b = E.eagle_qkv_rope(q, k, k, _freq().cuda(), _dev([]), parent=parent, k_pages=kp[0], v_pages=vp[0], page_table=table)
+    assert a.shape == q.shape and b is None
+    with pytest.raises((TypeError, ValueError)):
+        E.eagle_qkv_rope(q, k, None, _freq().cuda(), _dev([]), parent=_dev([]))
