@@ -91,18 +91,66 @@ __device__ __forceinline__ Segment segment_at(const A& a, int pos, int end, int&
 // ---------------- merging of cut units ----------------
 // Blocks (c, y): the unit whose first tile lies in piece c and whose last does not; its parts are piece c's
 // second place and the first places of the pieces behind it.  m is in log2 units and a part's l and O share one
-// factor, so a part weighs 2^(m - max m).  kLanes lanes look after a row, 32 / kLanes float4 of its O each, and in
-// the same way after 32 parts at a time, so that the parts' loads do not wait for one another: a warp a row
-// where there are few, with many parts as a rule, else eight lanes, and as many blocks as registers leave room for (4
-// rows a warp: 151 units of 256 rows and two parts took 24 us with a warp a row, 10 with eight lanes, 6 less with 64
-// registers than with 74).  The launch may begin while the attention kernel ends; the partials are awaited below.
+// factor, so a part weighs 2^(m - max m).  A row's parts are looked after 32 at a time, so that their loads do not wait
+// for one another: by a warp where rows are few (as a rule with many parts), else by eight lanes, 32 / 8 float4 of its O
+// each, and as many blocks as registers leave room for (4 rows a warp: 151 units of 256 rows and two parts took 24 us
+// with a warp a row, 10 with eight lanes, 6 less with 64 registers than with 74).  Few rows' parts have their places in
+// registers, one a lane; many rows' are listed once a block (with that list for few rows too, 48 ragged sequences of one
+// node over the 8-bit cache take 160.3 us instead of 158.7, one of 20 011 rows over pages 19.0 instead of 18.5).  The
+// launch may begin while the attention kernel ends; the partials are awaited below.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeFewRows = 64;                 // rows of a part up to which a warp takes one
 constexpr int kMergeMaxParts = 1024;              // at most one per CTA of the attention kernel
 
-template <int kLanes, class A>
-__device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const int* places, int parts) {
-    constexpr int kEach = 32 / kLanes, kBatch = kEach == 1 ? 8 : 1;   // parts on their way at a time
+// A warp a row.  place_of(p): piece p's part, -1: it has none, -2: none from there on; first: that of piece c + lane.
+template <class A, class PlaceOf>
+__device__ __forceinline__ void merge_few(const A& a, const Segment& s, int c, int first, PlaceOf place_of) {
+    constexpr int kBatch = 8;                     // parts on their way at a time
+    const int lane = threadIdx.x & 31, rows = a.unit_rows(s.pair);
+    for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
+        float m = -INFINITY, sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = c;; p0 += 32) {
+            const int place = p0 == c ? first : place_of(p0 + lane);
+            const float2 ml = place >= 0 ? a.ws_ml[(int64_t)place * a.rows + row] : make_float2(-INFINITY, 0.f);
+            float top = ml.x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float mn = fmaxf(m, top), at = mn == -INFINITY ? 0.f : mn;
+            const float w = exp2f(ml.x - at), wo = exp2f(m - at);
+            m = mn;
+            sum = sum * wo + warp_sum(ml.y * w);
+            o.x *= wo; o.y *= wo; o.z *= wo; o.w *= wo;
+            const unsigned there = __ballot_sync(0xffffffffu, place >= 0);
+            const int parts = 32 - __clz(there);          // up to the last one that is there
+#pragma unroll 1
+            for (int q0 = 0; q0 < parts; q0 += kBatch) {  // (of 32, so q0 + q stays below)
+                float4 z[kBatch];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const int from = __shfl_sync(0xffffffffu, place, q0 + q);
+                    if ((there >> (q0 + q)) & 1u)
+                        z[q] = reinterpret_cast<const float4*>(a.ws_o + ((int64_t)from * a.rows + row) * kHeadDim)[lane];
+                }
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const float wp = __shfl_sync(0xffffffffu, w, q0 + q);
+                    if ((there >> (q0 + q)) & 1u) { o.x += z[q].x * wp; o.y += z[q].y * wp; o.z += z[q].z * wp; o.w += z[q].w * wp; }
+                }
+            }
+            if (__any_sync(0xffffffffu, place == -2)) break;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t to = a.out_row(s.b, s.head, s.pair, row);
+        if (to < 0) continue;                             // nobody's row
+        reinterpret_cast<uint2*>(a.out + to * kHeadDim)[lane] = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    }
+}
+
+// Eight lanes a row; places: of the parts, -1: none.
+template <class A>
+__device__ __forceinline__ void merge_many(const A& a, const Segment& s, const int* places, int parts) {
+    constexpr int kLanes = 8, kEach = 32 / kLanes;
     const int lane = threadIdx.x & 31, l = lane % kLanes;
     const int rows = a.unit_rows(s.pair), per_block = kMergeWarps * kEach;
     for (int row0 = blockIdx.y * per_block + (threadIdx.x >> 5) * kEach; row0 < rows; row0 += gridDim.y * per_block) {
@@ -141,25 +189,16 @@ __device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const i
             for (int k = 0; k < kEach; ++k) {
                 const int first = p0 + k * kLanes, count = min(kLanes, parts - first);
 #pragma unroll 1
-                for (int q0 = 0; q0 < count; q0 += kBatch) {
-                    float4 z[kBatch][kEach];
-                    bool there[kBatch];
+                for (int q = 0; q < count; ++q) {
+                    const int place = places[first + q];
+                    const float4* x = reinterpret_cast<const float4*>(a.ws_o + ((int64_t)max(place, 0) * a.rows + row) * kHeadDim) + l;
+                    const float wp = __shfl_sync(0xffffffffu, w[k], q, kLanes);
+                    if (place < 0) continue;
+                    float4 z[kEach];
 #pragma unroll
-                    for (int q = 0; q < kBatch; ++q) {
-                        const int place = q0 + q < count ? places[first + q0 + q] : -1;
-                        there[q] = place >= 0;
-                        const float4* x = reinterpret_cast<const float4*>(a.ws_o + ((int64_t)max(place, 0) * a.rows + row) * kHeadDim) + l;
+                    for (int c = 0; c < kEach; ++c) z[c] = x[c * kLanes];
 #pragma unroll
-                        for (int c = 0; c < kEach; ++c)
-                            if (there[q]) z[q][c] = x[c * kLanes];
-                    }
-#pragma unroll
-                    for (int q = 0; q < kBatch; ++q) {
-                        const float wp = __shfl_sync(0xffffffffu, w[k], (q0 + q) % kLanes, kLanes);
-#pragma unroll
-                        for (int c = 0; c < kEach; ++c)
-                            if (there[q]) { o[c].x += z[q][c].x * wp; o[c].y += z[q][c].y * wp; o[c].z += z[q][c].z * wp; o[c].w += z[q][c].w * wp; }
-                    }
+                    for (int c = 0; c < kEach; ++c) { o[c].x += z[c].x * wp; o[c].y += z[c].y * wp; o[c].z += z[c].z * wp; o[c].w += z[c].w * wp; }
                 }
             }
         }
@@ -175,8 +214,6 @@ __device__ __forceinline__ void merge_rows(const A& a, const Segment& s, const i
 
 template <bool kFew, class A>                     // rows of a part up to kMergeFewRows
 __device__ __forceinline__ void merge_parts(const A& a, int grid) {
-    __shared__ int s_place[kMergeMaxParts];
-    __shared__ int s_parts;
     const Cut cut = make_cut(a, grid);
     const int c = blockIdx.x;
     // A block that has nothing to merge awaits the attention kernel too: a kernel launched next
@@ -187,18 +224,30 @@ __device__ __forceinline__ void merge_parts(const A& a, int grid) {
     int b = 0, base = 0;
     const Segment s = segment_at(a, end - 1, end, b, base);
     if (s.start < begin || s.t1 >= s.T) { await(); return; }   // it begins earlier, or is whole
-    if (threadIdx.x == 0) s_parts = cut.ctas - c;
-    __syncthreads();
-    for (int p = c + threadIdx.x; p < cut.ctas; p += kMergeThreads) {
-        // piece p's part of the unit, whose first tile is piece c's; -1: it holds none of its tiles
+    // piece p's part of the unit, whose first tile is piece c's; -1: it holds none of its tiles, -2: nor do those behind it
+    auto place_of = [&](int p) {
+        if (p >= cut.ctas) return -2;
         const int t0 = p == c ? 0 : tiles_before<A>(s.start, s.weight, cut.begin(p));
         const int t1 = p + 1 < cut.ctas ? tiles_before<A>(s.start, s.weight, cut.begin(p + 1)) : s.T;
-        s_place[p - c] = t0 < min(t1, s.T) ? p * 2 + (p == c) : -1;
-        if (t0 >= s.T) atomicMin(&s_parts, p - c);
+        return t0 >= s.T ? -2 : t0 < min(t1, s.T) ? p * 2 + (p == c) : -1;
+    };
+    if constexpr (kFew) {
+        const int first = place_of(c + (int)(threadIdx.x & 31));
+        await();
+        merge_few(a, s, c, first, place_of);
+    } else {
+        __shared__ int s_place[kMergeMaxParts];
+        __shared__ int s_parts;
+        if (threadIdx.x == 0) s_parts = cut.ctas - c;
+        __syncthreads();
+        for (int p = c + threadIdx.x; p < cut.ctas; p += kMergeThreads) {
+            s_place[p - c] = place_of(p);
+            if (s_place[p - c] == -2) atomicMin(&s_parts, p - c);
+        }
+        __syncthreads();
+        await();
+        merge_many(a, s, s_place, s_parts);
     }
-    __syncthreads();
-    await();
-    merge_rows<kFew ? 32 : 8>(a, s, s_place, s_parts);
 }
 
 // Launches the merging kernel of the rows' kind behind an attention kernel of `grid` CTAs.  Blocks a piece takes: a
