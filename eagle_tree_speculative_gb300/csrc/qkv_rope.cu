@@ -11,7 +11,7 @@
 // hold both elements of its pairs, so nothing is exchanged for the rotation and three shuffles do the norm.  The
 // token's 64 angles are computed by the warp once, two a lane, and go through shared memory.
 // The last tokens' groups are shared out to the warps alike, so a single token is worked on by as many as it has
-// groups and a call ends everywhere at once.  Each warp has kAhead groups on their way into shared memory, of this
+// groups and a call ends everywhere at once.  Each warp has kAhead - 1 groups on their way into shared memory, of this
 // token and the next (cp.async; a lane reads only what it copied itself, so nothing waits for other lanes):
 // registers would hold two.
 //
@@ -31,7 +31,7 @@ constexpr int kWarps = 4;
 // prompts, 16610 tokens of 32 / 8 heads, 73.5 / 81.1 / 86.9; 64 trees of 60 nodes 19.1 / 18.2 / 23.0).
 constexpr int kBlocks = 4, kBlocksLong = 3;
 constexpr int kLongTokens = 4;                    // tokens a warp from which a call is long
-constexpr int kAhead = 8;                         // groups of four heads (1 KB) that a warp has on their way
+constexpr int kAhead = 8;                         // places of groups of four heads (1 KB); all but one on their way
 constexpr int kRopeSmem = kWarps * (kAhead * 1024 + 64 * (int)sizeof(float2));
 static_assert(kBlocks * (kRopeSmem + 1024) <= 233472, "shared memory of an SM");
 
@@ -45,7 +45,6 @@ struct RopeArgs {
     int N, shift, P;
     float eps;
     int64_t q_stride, k_stride, v_stride;
-    uint32_t none;                                // 0, which the compiler does not know
     int32_t* dev_status;
 };
 
@@ -125,8 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
     const uint16_t *next = nullptr, *next_base = nullptr;
     uint32_t copy_at = s32(raw), read_at = 0;     // places in the ring
     const uint32_t copy_begin = copy_at, copy_end = copy_at + kAhead * 1024;
-    // (zero: the copy begins when it is known)
-    auto copy_next = [&](uint32_t zero) {
+    auto copy_next = [&] {
         if (next_left > 0) {
             --next_left;
             if (next_y == next_end) {             // a kind's first group
@@ -142,8 +140,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
                 next = next_base + next_h * kHeadDim;
             }
             const uint16_t* src = next_h < next_heads ? next : next_base;
-            copy16_async(copy_at + zero, src + 8 * p0);
-            copy16_async(copy_at + zero + 512, src + 8 * p1);
+            copy16_async(copy_at, src + 8 * p0);
+            copy16_async(copy_at + 512, src + 8 * p1);
             next += 4 * kHeadDim;
             next_h += 4;
             ++next_y;
@@ -153,7 +151,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
         if (copy_at == copy_end) copy_at = copy_begin;
     };
 #pragma unroll 1
-    for (int i = 0; i < kAhead; ++i) copy_next(0u);
+    for (int i = 0; i < kAhead - 1; ++i) copy_next();
 
     unsigned long long frac[2];                   // of pairs lane and lane + 32, in turns
 #pragma unroll
@@ -271,16 +269,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qkv_rope_kernel(RopeArgs
             }
 #pragma unroll 1
             for (; y < stop; ++y, h += 4, packed += packed ? 4 * kHeadDim : 0, page += page ? (int64_t)(4 * kHeadDim) << a.shift : 0) {
-                copy_wait<kAhead - 1>();
+                copy_wait<kAhead - 2>();
                 const uint4 r0 = raw[read_at], r1 = raw[read_at + 32];
                 read_at = read_at == (kAhead - 1) * 64 ? 0 : read_at + 64;
                 uint32_t o[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-                // The next copy goes into the place that was read.  Nothing orders it behind the reads, so its address is
-                // made of what they brought: it cannot begin before that is in registers.
-                uint32_t read = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) read |= o[e];
-                copy_next(read & a.none);
+                // The next copy goes into the place that was read a group ago: what came from there is in stores by now, or
+                // nobody's.  What was read just now need not be in registers yet, and nothing orders a copy behind that.
+                copy_next();
                 if (skip) continue;
                 if (kind < 2) {
                     uint64_t f[8];                // pairs of neighbours
@@ -391,7 +386,6 @@ extern "C" eagle_status eagle_qkv_rope(const void* q, const void* k, const void*
     a.N = N; a.shift = pages ? paged::page_shift(page) : 0; a.P = P;
     a.eps = eps;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
-    a.none = 0;
     a.dev_status = dev_status;
     const int sms = cached_sm_count();
     const bool is_long = T >= (int64_t)sms * kBlocksLong * kWarps * kLongTokens;
