@@ -6,8 +6,8 @@
 // its beginning and its output cost).  The host refuses sizes with 2^31 positions or more.
 //
 // A, the kernel's arguments, has B, Hkv, kUnitCost, kMinTiles (the least piece), tiles_of(b), row_tiles(),
-// unit_rows(pair), out_row(b, head, pair, row) (-1: nobody's), out, and the parts: ws_o [grid][2][rows][128],
-// ws_ml [grid][2][rows], rows.
+// unit_rows(pair), out_row(b, head, pair, row) (-1: nobody's), out, the parts: ws_o [grid][2][rows][128],
+// ws_ml [grid][2][rows], rows, and how few rows are merged: kFewRows, kFewBatch.
 #pragma once
 
 #include "attn2_common.cuh"
@@ -96,16 +96,16 @@ __device__ __forceinline__ Segment segment_at(const A& a, int pos, int end, int&
 // each, and as many blocks as registers leave room for (4 rows a warp: 151 units of 256 rows and two parts took 24 us
 // with a warp a row, 10 with eight lanes, 6 less with 64 registers than with 74).  Few rows' parts have their places in
 // registers, one a lane; many rows' are listed once a block (with that list for few rows too, 48 ragged sequences of one
-// node over the 8-bit cache take 160.3 us instead of 158.7, one of 20 011 rows over pages 19.0 instead of 18.5).  The
+// node over the 8-bit cache take 160.0 us instead of 158.4, one of 20 011 rows over pages 18.9 instead of 17.9).  The
 // launch may begin while the attention kernel ends; the partials are awaited below.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeFewRows = 64;                 // rows of a part up to which a warp takes one
 constexpr int kMergeMaxParts = 1024;              // at most one per CTA of the attention kernel
 
 // A warp a row.  place_of(p): piece p's part, -1: it has none, -2: none from there on; first: that of piece c + lane.
 template <class A, class PlaceOf>
 __device__ __forceinline__ void merge_few(const A& a, const Segment& s, int c, int first, PlaceOf place_of) {
-    constexpr int kBatch = 8;                     // parts on their way at a time
+    constexpr int kBatch = A::kFewBatch;          // parts on their way at a time
+    static_assert(32 % kBatch == 0, "batches of 32 parts");
     const int lane = threadIdx.x & 31, rows = a.unit_rows(s.pair);
     for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < rows; row += gridDim.y * kMergeWarps) {
         float m = -INFINITY, sum = 0.f;
@@ -212,7 +212,7 @@ __device__ __forceinline__ void merge_many(const A& a, const Segment& s, const i
     }
 }
 
-template <bool kFew, class A>                     // rows of a part up to kMergeFewRows
+template <bool kFew, class A>                     // rows of a part up to A::kFewRows
 __device__ __forceinline__ void merge_parts(const A& a, int grid) {
     const Cut cut = make_cut(a, grid);
     const int c = blockIdx.x;
@@ -255,7 +255,7 @@ __device__ __forceinline__ void merge_parts(const A& a, int grid) {
 // nodes: 211.6 us with 4, 214.3 with 8 and the second half waiting).
 template <class A>
 inline cudaError_t launch_merge(void (*few)(A, int), void (*many)(A, int), const A& a, int grid, cudaStream_t stream) {
-    const bool is_few = a.rows <= kMergeFewRows;
+    const bool is_few = a.rows <= A::kFewRows;
     const int per = kMergeWarps * (is_few ? 1 : 4), y = (a.rows + per - 1) / per;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(is_few || y < 4 ? y : 4));

@@ -90,6 +90,11 @@ constexpr int kSpread = 8;
 // 8 heads, 2048 rows 22.7 / 23.7 / 23.2 / 25.2 / 27.8; one head, 30 000 rows 41.6 / 37 / 35.5 / 31.4 / 31; two trees of
 // 12 nodes 23.2 / 27.3 / 25.7 / 26.2 / 29.3; large batches alike.
 constexpr int kMinTiles = 3;
+// Merging: a warp takes a row up to so many rows of a part, with so many parts on their way, in so many blocks an SM.  us
+// with a warp / eight lanes a row: 48 sequences of 100 .. 30 000 rows, G = 8, 32 rows of a part 170.2 / 171.4, 48 182.4 /
+// 180.2, 64 180.9 / 179.4, 96 209 / 205; one sequence alike.  With 8 parts on their way in 3 blocks 32 rows take 171.5 us,
+// in 2 (no limit on registers) 172.7.
+constexpr int kFewRows = 32, kFewBatch = 4, kFewBlocks = 4;
 
 struct Args {
     const uint16_t* q;
@@ -109,6 +114,7 @@ struct Args {
 
     // what the cut and the merging kernel ask for
     static constexpr int kUnitCost = kv8_tc::kUnitCost, kMinTiles = kv8_tc::kMinTiles;
+    static constexpr int kFewRows = kv8_tc::kFewRows, kFewBatch = kv8_tc::kFewBatch;
     __device__ int tiles_of(int b) const {        // key tiles of a sequence, the tree's the last
         const int L = kv_len[b];
         return (L < 0 || L > Lmax) ? 1 : (L + kKeys - 1) / kKeys + 1;
@@ -1077,7 +1083,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 }
 
 template <bool kFew>
-__global__ void __launch_bounds__(attn2::kMergeThreads, kFew ? 1 : 4) tree_attn_kv8_merge_kernel(Args a, int grid) {
+__global__ void __launch_bounds__(attn2::kMergeThreads, kFew ? kFewBlocks : 4) tree_attn_kv8_merge_kernel(Args a, int grid) {
     attn2::merge_parts<kFew>(a, grid);
 }
 

@@ -58,6 +58,12 @@ constexpr int kUnitCost = 2;
 // 4096 rows 26.5 / 25.6 / 23.0 / 25.9, two 27.9 / 27.7 / 25.7 / 27.2, eight over 500 .. 1000 rows 25.2 / 24.6 / 26.0 / 26.4;
 // one sequence of one node over 4000 rows 13.6 / 13.1 / 14.7 / 15.0; large batches alike.
 constexpr int kMinTiles = 5;
+// Merging: a warp takes a row up to so many rows of a part, with so many parts on their way, in so many blocks an SM.  us
+// with a warp / eight lanes a row, G = 4 or 8: one sequence of 20 011 rows, 32 rows of a part 22.2 / 25.0, 48 23.2 / 25.8,
+// 64 24.1 / 25.2, 96 28.4 / 26.6; 48 sequences of 100 .. 30 000 rows, 32 rows 217 / 216, 48 218 / 216, 64 222 / 218, 96
+// 232 / 218.  With 4 parts on their way one sequence of one node takes 18.9 us, with 8 18.2; with 2 blocks an SM (no
+// limit on registers) the ragged sequences of 64 rows take 225 us, with 3 222.
+constexpr int kFewRows = 64, kFewBatch = 8, kFewBlocks = 3;
 constexpr float kRescale = 8.f;                   // log2 units the maximum may grow by
 
 struct Args {
@@ -76,6 +82,7 @@ struct Args {
 
     // what the cut and the merging kernel ask for
     static constexpr int kUnitCost = paged_tc::kUnitCost, kMinTiles = paged_tc::kMinTiles;
+    static constexpr int kFewRows = paged_tc::kFewRows, kFewBatch = paged_tc::kFewBatch;
     __device__ bool bad_length(int L) const { return L < 0 || L + (int64_t)n > (int64_t)width << shift; }
     __device__ int tiles_of(int b) const {        // a sequence that is refused has one, of zeros
         const int L = kv_len[b];
@@ -648,7 +655,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
 }
 
 template <bool kFew>
-__global__ void __launch_bounds__(attn2::kMergeThreads, kFew ? 1 : 4) tree_attn_paged_merge_kernel(Args a, int grid) {
+__global__ void __launch_bounds__(attn2::kMergeThreads, kFew ? kFewBlocks : 4) tree_attn_paged_merge_kernel(Args a, int grid) {
     attn2::merge_parts<kFew>(a, grid);
 }
 
