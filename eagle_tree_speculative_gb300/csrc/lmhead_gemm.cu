@@ -22,7 +22,7 @@
 // Tiles are visited M-fastest so the CTAs working on one 256-column slab of W
 // run together and share it through L2: W is read from HBM about once.
 // Every mbarrier wait is bounded (about two seconds); on expiry the kernel sets
-// EAGLE_DEV_TIMEOUT, stops issuing work, drains its MMAs and frees TMEM.
+// EAGLE_DEV_TIMEOUT, stops issuing work, drains its MMAs, lets its copies land and frees TMEM.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -220,7 +220,7 @@ lmhead_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0 && *abort_flag) flag_error(g.dev_status, EAGLE_DEV_TIMEOUT);
+    if (threadIdx.x == 0 && *abort_flag) report_timeout(g.dev_status);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
@@ -333,7 +333,7 @@ __global__ void wait_selftest_kernel(int32_t* dev_status, long long max_cycles) 
     }
     if (over && (threadIdx.x & 31) == 0) atomicAdd(&given_up, 1);
     __syncthreads();
-    if (threadIdx.x == 0 && given_up == 3 && abort_flag) flag_error(dev_status, EAGLE_DEV_TIMEOUT);
+    if (threadIdx.x == 0 && given_up == 3 && abort_flag) report_timeout(dev_status);
 }
 
 }  // namespace

@@ -12,6 +12,8 @@
 
 #include <mutex>
 
+#include "common.cuh"
+
 namespace eagle {
 
 constexpr long long kTimeoutCycles = 4000000000LL;   // about two seconds at 2 GHz
@@ -56,6 +58,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             }
         }
     }
+}
+
+// The end of a CTA whose waits gave up, for one thread: products have been drained, but copies may still be on their way
+// into the CTA's shared memory, which is another's once it has returned.  Copies take microseconds; which ones are not
+// there nobody has kept, so all get a millisecond.
+constexpr long long kLandCycles = 1LL << 21;
+__device__ __forceinline__ void report_timeout(int32_t* dev_status) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kLandCycles) {}
+    flag_error(dev_status, EAGLE_DEV_TIMEOUT);
 }
 
 // cuTensorMapEncodeTiled from the driver, looked up once per process (thread-safe);

@@ -1073,7 +1073,7 @@ tree_attn_kv8_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         if (again()) pass(std::true_type{});
     }
     __syncthreads();
-    if (tid == 0 && *abort_flag) flag_error(a.dev_status, EAGLE_DEV_TIMEOUT);
+    if (tid == 0 && *abort_flag) report_timeout(a.dev_status);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, attn2::kTmemCols);

@@ -645,7 +645,7 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         }
     }
     __syncthreads();
-    if (tid == 0 && *abort_flag) flag_error(a.dev_status, EAGLE_DEV_TIMEOUT);
+    if (tid == 0 && *abort_flag) report_timeout(a.dev_status);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, attn2::kTmemCols);
