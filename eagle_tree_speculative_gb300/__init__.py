@@ -554,7 +554,8 @@ def eagle_pages_assign(k_pages, v_pages, page_table, held, refs, kv_len, grow, s
     """Room for grow [B] rows behind each sequence's kv_len [B], after slot b went on with what
     slot src[b] held (None: its own; -1: nothing).  page_table [B,P], held [B], refs [N] and kv_len
     (int32) are updated in place; rows of pages that are shared no longer are copied in every
-    layer of k_pages / v_pages [n_layers,N,Hkv,page,d] bf16.  All or nothing: see dev_status."""
+    layer of k_pages / v_pages [n_layers,N,Hkv,page,d] bf16.  All or nothing: a refused call sets
+    dev_status and leaves the old table, with which the calls behind it go on (see eagle.h)."""
     fn = "eagle_pages_assign"
     nl, N, Hkv, page, d = shape = _dims(fn, k_pages, "k_pages", 5, _PAGES)
     B, P = table = _dims(fn, page_table, "page_table", 2, "[B, P]")

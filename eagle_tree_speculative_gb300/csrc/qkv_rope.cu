@@ -15,8 +15,9 @@
 // token and the next (cp.async; a lane reads only what it copied itself, so nothing waits for other lanes):
 // registers would hold two.
 //
-// Measured: 24 ragged prompts, 16610 tokens of 32 / 8 heads with norms, rows packed and into pages, 75 us: 5.9 TB/s, 87%
-// of the measured copy; 64 trees of 60 nodes into pages 18 us (5.2 TB/s).  Bound: HBM; short calls the chain
+// Measured: 24 ragged prompts, 16610 tokens of 32 / 8 heads with norms, rows packed and into pages, 75 us, 77 with other
+// rows and pages in between: 5.7 TB/s, 85% of the measured copy; 64 trees of 60 nodes into pages 17.6 us where their 94 MB
+// stay in L2, 22 from HBM (4.3 TB/s).  Bound: HBM; short calls, and those of a token or two a warp, the chain
 // of dependent reads before a token's first output (place, page, angle).
 #include <type_traits>
 
@@ -28,7 +29,7 @@ namespace {
 
 constexpr int kWarps = 4;
 // Blocks of an SM: 16 warps for the calls that are over soon, 12 for those that stream (us with 12 / 16 / 20: 24 ragged
-// prompts, 16610 tokens of 32 / 8 heads, 73.5 / 81.1 / 86.9; 64 trees of 60 nodes 19.1 / 18.2 / 23.0).
+// prompts, 16610 tokens of 32 / 8 heads, 73.5 / 81.1 / 86.9; 64 trees of 60 nodes, in L2, 19.1 / 18.2 / 23.0).
 constexpr int kBlocks = 4, kBlocksLong = 3;
 constexpr int kLongTokens = 4;                    // tokens a warp from which a call is long
 constexpr int kAhead = 8;                         // places of groups of four heads (1 KB); all but one on their way

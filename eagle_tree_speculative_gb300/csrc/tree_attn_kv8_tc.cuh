@@ -41,9 +41,9 @@
 // digits of the tree's rows; V rows behind the last key become zeros there (whatever bits lie in them: a zero weight
 // does not cancel NaN).
 //
-// Measured: 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 0.267 ms (the bf16 cache's kernel:
+// Measured: 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 0.263 ms (the bf16 cache's kernel:
 // 0.296 ms from twice the bytes); tensor pipe 50% active, 646 MB read.  48 sequences of one node over
-// 100 .. 30 000 rows, 64 / 8 heads: 162 us, 3.8 TB/s.  With a second pass over every unit 0.58 ms and 350 us.
+// 100 .. 30 000 rows, 64 / 8 heads: 158.5 us, 3.8 TB/s.  With a second pass over every unit 0.58 ms and 350 us.
 // Bound: the chain of QK, softmax and PV per slot and the MMA warp's control, about 3 800 cycles per 256
 // rows x 128 keys, and 20 to 30 thousand cycles at a unit's ends; neither HBM nor the tensor pipe is full.
 // ptxas: 616 bytes of spill stores, 700 of loads, 200 bytes of stack, most of them in the warps of 64

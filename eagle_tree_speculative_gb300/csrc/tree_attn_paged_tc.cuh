@@ -19,10 +19,11 @@
 //
 // MMA order: PV of a slot's last tile, then its next QK, whose commit also says that O holds that PV.
 //
-// Measured (with the merging kernel): 48 sequences of one node over 100 .. 30 000 rows, 64 / 8 heads, 209 us: 6.9 TB/s; 64
-// trees of 60 nodes over 4096 rows, 32 / 8 heads, 202 us: 5.7 TB/s, 1.28 PFLOP/s (the slab's kernel 0.296 ms), tensor
-// pipe 70% active; from pages that stay in L2 the trees take 187 us, so the chain of QK, softmax and PV per slot
-// (3 000 cycles a tile of 256 rows) and HBM (5.7 of 6.8 TB/s) bind it together.  Tried, us of these trees: loads
+// Measured (with the merging kernel): 48 sequences of one node over 100 .. 30 000 rows, 64 / 8 heads, 209 .. 215 us: 6.9 ..
+// 6.7 TB/s; 64 trees of 60 nodes over 4096 rows, 32 / 8 heads, 196 .. 210 us replayed one behind the other (5.9 .. 5.5 TB/s,
+// 1.31 .. 1.23 PFLOP/s; the slab's kernel 296), 207 .. 221 with other caches read in between, up to 237 (4.9 TB/s, 1.09
+// PFLOP/s) in turn with other work; tensor pipe 70% active; from pages that stay in L2 187 .. 191, so the chain of QK, softmax
+// and PV per slot (3 000 cycles a tile of 256 rows) and HBM bind the trees together.  Tried, us of these trees: loads
 // without the L2 policy 5 more; one loading warp for K and V 4 more; L2 prefetches two to six tiles ahead 10 to 75
 // more; P handed over in halves no change; merging by the warp that comes last, in this kernel, 40 more (its
 // code and registers).  With five stages instead of six the ragged sequences take 248 us.
@@ -89,7 +90,8 @@ struct Args {
         return bad_length(L) ? 1 : (L + n + kKeys - 1) / kKeys;
     }
     // a pair's missing row tile counts too: its key tiles take as long as two row tiles' (a tile's bytes, not its
-    // products, are what a single row tile waits for; 16 ragged trees of 48 nodes, 64 / 8 heads: 67 us against 87, where both were measured)
+    // products, are what a single row tile waits for; three draws of 16 ragged trees of 48 nodes, 64 / 8 heads, 54 / 89 / 73
+    // us, counted by its rows 60 / 104 / 81)
     __device__ int row_tiles() const { return n <= P ? 1 : (n + 2 * P - 1) / (2 * P) * 2; }
     __device__ int unit_rows(int pair) const {
         const int left = n - pair * 2 * P;        // nodes from the pair's first on
@@ -335,8 +337,8 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
                 if (qk.on && qk.closes) advance(ks, kp);
             };
             // A unit of a single tile leaves its PV to the steps of the next ones, in which the slots go on taking turns,
-            // so that such units follow one another without a gap (1024 sequences of one node over 1 .. 100 rows, 64 /
-            // 8 heads: 197 to 130 us); behind longer ones that gained nothing.  The last units' PV, and that before a
+            // so that such units follow one another without a gap (64 / 8 heads: 1024 sequences of one node over 1 .. 100
+            // rows 194 to 128 us, 256 over 100 .. 400 rows 78 to 72); behind longer ones that gained nothing.  The last units' PV, and that before a
             // unit without tiles (whose rows the softmax cannot write before), have steps of their own.
             int turn = 0, owed = 0;                       // the slot that is next; a bit per slot that owes PV
             for (int i = 0;; ++i) {

@@ -422,7 +422,8 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *            row r % page, in every layer.  Entries behind the pages that a sequence
  *            holds may hold anything.
  * N * Hkv * page below 2^31, P * page up to 2^27, B * P below 2^30; assign and commit: B up
- * to 65536.
+ * to 65536.  Pages, rows (q, k, v and their outputs, out), weights and workspaces are 16-byte
+ * aligned.
  *
  * eagle_pages_assign -- which pages each of B slots holds, and the rows that this needs
  * copied: room for new rows, forks, reorders, ends.  Slot b goes on with what slot
@@ -442,6 +443,7 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *   refs   int32 [N]  how many slots hold each page, updated (all 0: an empty cache)
  *   kv_len int32 [B]  committed rows, updated      grow int32 [B], >= 0
  *   src    int32 [B] or NULL
+ *   n_layers 0: the numbers alone
  *   workspace / ws_bytes: device scratch of at least eagle_pages_workspace_size(B, N, P)
  *            bytes; no initialisation needed.  Two calls that may run at the same time
  *            need one each.
@@ -449,6 +451,18 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  * or grow negative, kv_len beyond the pages held, more than P pages needed, or a page
  * outside [0, N) among those looked at (EAGLE_DEV_CAPACITY as well) leave everything as it
  * was.  refs and the table have to agree; that is not checked.
+ * The calls behind a refused one on the stream, or in the graph, go on with what was there
+ * before, forks and ends not done.  Rows for which there are no pages are refused by them too
+ * where the table has no entry (-1), and no slot writes into a page that others hold -- except
+ * where kv_len was cut back into a shared page: only an assignment that is carried out gives
+ * the slot a page of its own there.  So the status has to be looked at before the next call
+ * that writes rows (eagle_qkv_rope, eagle_pages_commit) wherever lengths are cut back, and
+ * before anything is made of the results in any case.  Assignments that cannot be refused
+ * need no look: pages with refs = 0 are at least the sum of ceil((L % page + grow) / page), and
+ * all numbers are in range.
+ * Time: one warp a slot in one cluster of 8 CTAs, about 21 us for every 1024 slots; where most
+ * slots go on with another slot that nobody else goes on with, src is looked through for each
+ * (8192 slots 0.4 ms, 65536 20 ms).
  *
  * eagle_pages_commit -- eagle_kv_compact over pages.  For t = 0 .. a (a = accept_len[b]):
  * row L + path[b][t] moves to row L + t (L = kv_len[b]) in every layer and kv head, for K
@@ -457,8 +471,8 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  * of at least the tree's nodes before the step).
  *   kv_len int32 [B]   kv_len_out int32 [B], may be kv_len   path int32 [B, D+1]
  *   accept_len int32 [B]
- * Sequences with accept_len < 0 are skipped (kv_len_out = kv_len).  Device errors, the
- * sequence being skipped: a > D, rows beyond P * page or a page outside [0, N),
+ * Sequences with accept_len < 0 are skipped (kv_len_out = kv_len).  n_layers = 0 is a no-op:
+ * kv_len_out is not written either.  Device errors, the sequence being skipped: a > D, rows beyond P * page or a page outside [0, N),
  * EAGLE_DEV_CAPACITY; a path not starting at 0 or not increasing, EAGLE_DEV_BAD_TREE.
  *
  * eagle_qkv_rope -- from a layer's projections to its attention: norms of the queries' and
