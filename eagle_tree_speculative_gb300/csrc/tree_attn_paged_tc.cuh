@@ -338,8 +338,9 @@ tree_attn_paged_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
             };
             // A unit of a single tile leaves its PV to the steps of the next ones, in which the slots go on taking turns,
             // so that such units follow one another without a gap (64 / 8 heads: 1024 sequences of one node over 1 .. 100
-            // rows 194 to 128 us, 256 over 100 .. 400 rows 78 to 72); behind longer ones that gained nothing.  The last units' PV, and that before a
-            // unit without tiles (whose rows the softmax cannot write before), have steps of their own.
+            // rows 194 to 128 us, 256 over 100 .. 400 rows 78 to 72); behind longer ones that gained nothing.  The last
+            // units' PV, and that before a unit without tiles (whose rows the softmax cannot write before), have steps of
+            // their own.
             int turn = 0, owed = 0;                       // the slot that is next; a bit per slot that owes PV
             for (int i = 0;; ++i) {
                 const Unit* u = ok ? next_unit(i) : nullptr;

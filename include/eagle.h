@@ -472,8 +472,9 @@ eagle_status eagle_tree_attn_kv8(const void* q, const void* k8, const void* v8,
  *   kv_len int32 [B]   kv_len_out int32 [B], may be kv_len   path int32 [B, D+1]
  *   accept_len int32 [B]
  * Sequences with accept_len < 0 are skipped (kv_len_out = kv_len).  n_layers = 0 is a no-op:
- * kv_len_out is not written either.  Device errors, the sequence being skipped: a > D, rows beyond P * page or a page outside [0, N),
- * EAGLE_DEV_CAPACITY; a path not starting at 0 or not increasing, EAGLE_DEV_BAD_TREE.
+ * kv_len_out is not written either.  Device errors, the sequence being skipped: a > D, rows
+ * beyond P * page or a page outside [0, N), EAGLE_DEV_CAPACITY; a path not starting at 0 or not
+ * increasing, EAGLE_DEV_BAD_TREE.
  *
  * eagle_qkv_rope -- from a layer's projections to its attention: norms of the queries' and
  * keys' heads, the rotation by position, and the rows into pages, in one pass.
